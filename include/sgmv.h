@@ -359,6 +359,109 @@ int sgmv_group_rows(const int32_t* row_ids, int32_t num_rows, int32_t num_adapte
                     int32_t* perm, int32_t* seg_indptr, int32_t* adapter_ids,
                     int32_t* num_segments, void* stream);
 
+/*
+ * The projections around the adapters: a base model with 4-bit weights, the
+ * gated feed-forward block, and rotary positions.  These calls follow the
+ * conventions above (device pointers, row-major arrays of one dtype, float32
+ * sums, enqueue-only) and need no workspace.
+ */
+
+/*
+ * 4-bit weights.  W [out_features, in_features] is held as codes 0..15, one
+ * scale per group of group_size consecutive input features of a row, and
+ * optionally one zero point 0..15 per group (8 without):
+ *     W[n, k] = scales[n, k / group_size] * (code[n, k] - zero[n, k / group_size]).
+ * A user's arrays: codes [out_features, ceil(in_features / 2)] bytes, input
+ * feature 2 j in the low and 2 j + 1 in the high half of byte j; scales
+ * [out_features, groups] in the activations' dtype; zeros [out_features,
+ * groups] bytes, or NULL; groups = ceil(in_features / group_size).
+ * group_size is any multiple of 32 (the last group of a row may be shorter).
+ *
+ * q4_pack lays them out once for the matrix cores, into caller-owned,
+ * 16-byte aligned device arrays: tiles (q4_tiles_bytes), scales
+ * (q4_groups_padded elements of dtype) and, when zeros is given, zero
+ * points (q4_groups_padded bytes).  The calls below read only these.
+ */
+typedef struct {
+    const void* tiles;
+    const void* scales;
+    const uint8_t* zeros;  /* NULL: every zero point is 8 */
+} sgmv_q4_weight;
+
+size_t q4_tiles_bytes(int32_t out_features, int32_t in_features);
+size_t q4_groups_padded(int32_t out_features, int32_t in_features, int32_t group_size);
+int q4_pack(void* tiles, void* packed_scales, uint8_t* packed_zeros, const uint8_t* codes,
+            const void* scales, const uint8_t* zeros, int32_t out_features, int32_t in_features,
+            int32_t group_size, int32_t dtype, void* stream);
+
+/*
+ * y = round(x W^T + bias): x [num_rows, in_features], y [num_rows,
+ * out_features] (overwritten), bias [out_features] or NULL.  Up to 256 rows
+ * (any number in float32) the codes enter the products exactly and the
+ * scales multiply float32 sums per group; beyond that fp16 and bf16 round
+ * each scaled weight once to dtype first.  An infinity in x gives a
+ * non-finite row (NaN where the products alone would give an infinity).
+ */
+int q4_linear(void* y, const void* x, const sgmv_q4_weight* w, const void* bias, int32_t num_rows,
+              int32_t out_features, int32_t in_features, int32_t group_size, int32_t dtype,
+              void* stream);
+
+/*
+ * Gated feed-forward block: h = round(act(g) * u) with g = x Wg^T + gate_add
+ * and u = x Wu^T + up_add, both products, the activation and the product in
+ * one kernel.  gate_add, up_add [num_rows, out_features] or NULL: what the
+ * rows' adapters add before the activation (lora_apply_multi on zeros).
+ * q4_gated_ffn takes 4-bit weights of one group size, gated_ffn plain ones
+ * [out_features, in_features].
+ *
+ * gated_ffn also stores g and u, rounded to dtype, into g_saved and u_saved
+ * [num_rows, out_features] when these are not NULL; gated_ffn_backward takes
+ * them with dh = dL/dh and computes
+ *     dg = dh * u * act'(g),  du = dh * act(g)   (also the addends' gradients)
+ *     dx = dg Wg + du Wu,  dWg = dg^T x,  dWu = du^T x
+ * with dg and du rounded to dtype between the steps.  dx, or dWg and dWu,
+ * may be NULL and are then not computed; dg and du are needed.  With
+ * num_rows == 0 the weights' gradients are zero.  act' of relu at 0 is 0.
+ */
+typedef enum {
+    SGMV_ACT_SILU = 0,
+    SGMV_ACT_GELU = 1,      /* by the error function */
+    SGMV_ACT_GELU_TANH = 2,
+    SGMV_ACT_RELU = 3,
+    SGMV_ACT_SIGMOID = 4
+} sgmv_act_t;
+
+int q4_gated_ffn(void* h, const void* x, const sgmv_q4_weight* gate, const sgmv_q4_weight* up,
+                 const void* gate_add, const void* up_add, int32_t num_rows, int32_t out_features,
+                 int32_t in_features, int32_t group_size, int32_t act, int32_t dtype, void* stream);
+int gated_ffn(void* h, void* g_saved, void* u_saved, const void* x, const void* Wg, const void* Wu,
+              const void* gate_add, const void* up_add, int32_t num_rows, int32_t in_features,
+              int32_t out_features, int32_t act, int32_t dtype, void* stream);
+int gated_ffn_backward(void* dx, void* dWg, void* dWu, void* dg, void* du, const void* dh,
+                       const void* x, const void* Wg, const void* Wu, const void* g, const void* u,
+                       int32_t num_rows, int32_t in_features, int32_t out_features, int32_t act,
+                       int32_t dtype, void* stream);
+
+/*
+ * Rotary positions on q [num_rows, q_heads, head_dim] and k [num_rows,
+ * k_heads, head_dim] (either may have no heads): pair j of the first
+ * rotary_dim elements of every head, elements (j, j + rotary_dim / 2) or,
+ * interleaved, (2 j, 2 j + 1), is turned by positions[row] * inv_freq[j]
+ * radians and scaled by magnitude; the other elements are copied.  With
+ * `inverse` it turns back (the gradients' form).
+ *
+ * positions: int32 or int64 (position_bytes 4 or 8); inv_freq: rotary_dim / 2
+ * doubles.  Angles are formed in float64.  strides: HOST array of eight
+ * element strides, for q {in row, in head, out row, out head} and then for
+ * k; the last dimension is dense.  The outputs may be the inputs themselves
+ * (equal pointers and strides) and must not overlap them otherwise.
+ * rotary_dim is even, at most head_dim and 1024.
+ */
+int rope(void* q_out, void* k_out, const void* q, const void* k, const void* positions,
+         int32_t position_bytes, const double* inv_freq, float magnitude, int32_t num_rows,
+         int32_t q_heads, int32_t k_heads, int32_t head_dim, int32_t rotary_dim,
+         const int64_t* strides, int32_t interleaved, int32_t inverse, int32_t dtype, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

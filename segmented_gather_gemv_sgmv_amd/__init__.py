@@ -75,6 +75,18 @@ ABI = [
     ("lora_linear_workspace_bytes", _sz, [_i32, _i32, _i32, _i32, _i32, _i32]),
     ("lora_linear", ctypes.c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32,
                                    _i32, _i32, _i32, _f32, _i32, _vp, _sz, _vp]),
+    ("q4_tiles_bytes", _sz, [_i32, _i32]),
+    ("q4_groups_padded", _sz, [_i32, _i32, _i32]),
+    ("q4_pack", ctypes.c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _vp]),
+    ("q4_linear", ctypes.c_int, [_vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _i32, _vp]),
+    ("q4_gated_ffn", ctypes.c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _i32,
+                                    _i32, _vp]),
+    ("gated_ffn", ctypes.c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32,
+                                 _i32, _vp]),
+    ("gated_ffn_backward", ctypes.c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
+                                          _i32, _i32, _i32, _i32, _i32, _vp]),
+    ("rope", ctypes.c_int, [_vp, _vp, _vp, _vp, _vp, _i32, _vp, _f32, _i32, _i32, _i32, _i32, _i32,
+                            _vp, _i32, _i32, _i32, _vp]),
 ]
 
 
@@ -502,7 +514,14 @@ def group_rows(row_ids, num_adapters: int, out=None):
     return perm, seg, ids, count
 
 
+# The projections around the adapters (these modules use the helpers above).
+from .gated import gated_ffn, gated_ffn_backward  # noqa: E402
+from .q4 import Q4Weight, q4_gated_ffn, q4_linear, q4_pack  # noqa: E402
+from .rotary import RopePlan, rope, rope_frequencies, rope_plan  # noqa: E402
+
 __all__ = [
+    "gated_ffn", "gated_ffn_backward", "q4_pack", "q4_linear", "q4_gated_ffn", "Q4Weight",
+    "rope", "rope_plan", "rope_frequencies", "RopePlan",
     "lora_linear", "lora_linear_workspace_bytes",
     "build_segments", "group_rows", "lora_apply_multi", "lora_apply_multi_workspace_bytes",
     "load_adapter",

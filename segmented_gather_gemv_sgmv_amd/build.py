@@ -2,8 +2,9 @@
 
     python -m segmented_gather_gemv_sgmv_amd.build
 
-compiles ``csrc/sgmv_api.hip`` (which includes the kernel headers) with
-hipcc into ``libsgmv.so`` next to this file.  Cross-compiles without a GPU.
+compiles the sources of the C ABI (``csrc/*.hip``, which include the kernel
+headers) side by side with hipcc and links them into ``libsgmv.so`` next to
+this file.  Cross-compiles without a GPU.
 """
 from __future__ import annotations
 
@@ -16,7 +17,9 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIBRARY = os.path.join(PKG, "libsgmv.so")
-SOURCES = [os.path.join(CSRC, "sgmv_api.hip")]
+SOURCES = [os.path.join(CSRC, f) for f in ("sgmv_api.hip", "q4_api.hip", "ffn_api.hip",
+                                           "rope_api.hip")]
+OBJECTS = os.path.join(PKG, "_build")
 ARCH = "gfx950"
 
 HIPCC_FLAGS = [
@@ -38,13 +41,35 @@ def hipcc() -> str:
     return path if os.path.exists(path) else "hipcc"
 
 
+def _object(source: str, tag: str) -> str:
+    return os.path.join(OBJECTS, os.path.basename(source)[:-len(".hip")] + tag + ".o")
+
+
+def _compile_and_link(jobs, verbose: bool):
+    """jobs: (flags, output, tag).  Every source of every job is compiled at
+    the same time, then each job's objects are linked."""
+    os.makedirs(OBJECTS, exist_ok=True)
+    procs = []
+    for flags, output, tag in jobs:
+        for src in SOURCES:
+            cmd = [hipcc(), *[f for f in flags if f != "-shared"], "-I", INCLUDE, "-I", CSRC, "-c",
+                   "-o", _object(src, tag), src]
+            if verbose:
+                print(" ".join(cmd), flush=True)
+            procs.append(subprocess.Popen(cmd))
+    codes = [p.wait() for p in procs]
+    if any(codes):
+        raise subprocess.CalledProcessError(max(codes, key=abs), "hipcc")
+    for flags, output, tag in jobs:
+        cmd = [hipcc(), *flags, "-o", output + ".tmp", *[_object(src, tag) for src in SOURCES]]
+        if verbose:
+            print(" ".join(cmd), flush=True)
+        subprocess.run(cmd, check=True)
+        os.replace(output + ".tmp", output)
+
+
 def build(output: str = LIBRARY, extra_flags=(), verbose: bool = False) -> str:
-    tmp = output + ".tmp"
-    cmd = [hipcc(), *HIPCC_FLAGS, *extra_flags, "-I", INCLUDE, "-I", CSRC, "-o", tmp, *SOURCES]
-    if verbose:
-        print(" ".join(cmd), flush=True)
-    subprocess.run(cmd, check=True)
-    os.replace(tmp, output)
+    _compile_and_link([([*HIPCC_FLAGS, *extra_flags], output, "")], verbose)
     return output
 
 
@@ -88,30 +113,13 @@ def sources_mtime() -> float:
 
 
 def build_asan(output: str = ASAN_LIBRARY, verbose: bool = False) -> str:
-    tmp = output + ".tmp"
-    cmd = [hipcc(), *ASAN_FLAGS, "-I", INCLUDE, "-I", CSRC, "-o", tmp, *SOURCES]
-    if verbose:
-        print(" ".join(cmd), flush=True)
-    subprocess.run(cmd, check=True)
-    os.replace(tmp, output)
+    _compile_and_link([(ASAN_FLAGS, output, "_asan")], verbose)
     return output
 
 
 def build_all(verbose: bool = False) -> None:
     """The library and its host-sanitizer variant, compiled side by side."""
-    cmd_main = [hipcc(), *HIPCC_FLAGS, "-I", INCLUDE, "-I", CSRC, "-o", LIBRARY + ".tmp", *SOURCES]
-    cmd_asan = [hipcc(), *ASAN_FLAGS, "-I", INCLUDE, "-I", CSRC, "-o", ASAN_LIBRARY + ".tmp",
-                *SOURCES]
-    procs = []
-    for cmd in (cmd_main, cmd_asan):
-        if verbose:
-            print(" ".join(cmd), flush=True)
-        procs.append(subprocess.Popen(cmd))
-    codes = [p.wait() for p in procs]
-    if any(codes):
-        raise subprocess.CalledProcessError(max(codes), "hipcc")
-    os.replace(LIBRARY + ".tmp", LIBRARY)
-    os.replace(ASAN_LIBRARY + ".tmp", ASAN_LIBRARY)
+    _compile_and_link([(HIPCC_FLAGS, LIBRARY, ""), (ASAN_FLAGS, ASAN_LIBRARY, "_asan")], verbose)
 
 
 if __name__ == "__main__":

@@ -1,0 +1,173 @@
+// ffn_api.hip -- C ABI of the gated feed-forward block (declared in
+// include/sgmv.h): argument checks and kernel choice.
+#include "proj_launch.hpp"
+
+namespace {
+
+using namespace sgmv;
+
+// Rows up to which the forward streams the weights through the rows kernel.
+constexpr int kFfnRowsMax = 64;
+
+int check_ffn(int R, int H, int I, int act, int dtype) {
+    if (!known_dtype(dtype)) return SGMV_ERR_BAD_DTYPE;
+    if (R < 0 || H < 1 || I < 1 || !known_act(act)) return SGMV_ERR_BAD_SHAPE;
+    return SGMV_OK;
+}
+
+template <typename DT, int MT>
+int run_rows(const RowsArgs& a, hipStream_t st) {
+    launch(&rows_kernel<DT, PlainSrc<DT>, MT, 1, 1, true>,
+           dim3((unsigned)ceil_div(a.N, 16), (unsigned)ceil_div(a.R, 16 * MT)), dim3(kRowsThreads),
+           st, a);
+    return launch_status();
+}
+
+template <typename DT>
+int run_forward(const RowsArgs& a, hipStream_t st) {
+    if (a.R <= kFfnRowsMax) {
+        if (a.R <= 16) return run_rows<DT, 1>(a, st);
+        if (a.R <= 32) return run_rows<DT, 2>(a, st);
+        return run_rows<DT, 4>(a, st);
+    }
+    TileArgs t{};
+    t.a[0] = a.x;
+    t.lda = a.K;
+    t.b[0] = a.m[0].w;
+    t.b[1] = a.m[1].w;
+    t.ldb = a.K;
+    t.out[0] = a.y;
+    for (int q = 0; q < 2; ++q) {
+        t.add[q] = a.add[q];
+        t.save[q] = a.save[q];
+    }
+    t.M = a.R;
+    t.N = a.N;
+    t.K = a.K;
+    t.batches = 1;
+    t.avec = a.xvec;
+    t.bvec = a.wvec;
+    t.yvec = a.yvec;
+    t.act = a.act;
+    return launch_tiles_any<DT, kAlongK, kAlongK, 1, true>(t, a.xvec && a.wvec, st);
+}
+
+struct GradArgs {
+    void *dx, *dWg, *dWu, *dg, *du;
+    const void *dh, *x, *Wg, *Wu, *g, *u;
+    int R, H, I, act;
+};
+
+template <typename DT>
+int run_backward(const GradArgs& b, hipStream_t st) {
+    using T = typename DT::storage;
+    constexpr int PK = PieceOps<DT>::kPK;
+    if (b.R > 0) {
+        const long long n = (long long)b.R * b.I;
+        const int vec = aligned16(b.dg) && aligned16(b.du) && aligned16(b.dh) && aligned16(b.g) &&
+                        aligned16(b.u);
+        const long long blocks = std::min<long long>(ceil_div(n, 256 * DT::kVec), 4096);
+        launch(&gated_grad_kernel<DT>, dim3((unsigned)blocks), dim3(256), st, (T*)b.dg, (T*)b.du,
+               (const T*)b.dh, (const T*)b.g, (const T*)b.u, n, b.act, vec);
+        int rc = launch_status();
+        if (rc != SGMV_OK) return rc;
+    }
+    const bool hvec = b.H % PK == 0, ivec = b.I % PK == 0;
+    const bool gvec = ivec && aligned16(b.dg) && aligned16(b.du);
+    if (b.dx && b.R > 0) {
+        // dx = dg Wg + du Wu: two segments of K = I, the weights across K.
+        TileArgs t{};
+        t.a[0] = b.dg;
+        t.a[1] = b.du;
+        t.lda = b.I;
+        t.b[0] = b.Wg;
+        t.b[1] = b.Wu;
+        t.ldb = b.H;
+        t.out[0] = b.dx;
+        t.M = b.R;
+        t.N = b.H;
+        t.K = b.I;
+        t.batches = 1;
+        t.avec = gvec;
+        t.bvec = hvec && aligned16(b.Wg) && aligned16(b.Wu);
+        t.yvec = b.H % 4 == 0 && aligned16(b.dx);
+        const int rc = launch_tiles_any<DT, kAlongK, kAcrossK, 2, false>(t, t.avec && t.bvec, st);
+        if (rc != SGMV_OK) return rc;
+    }
+    if (b.dWg) {
+        // dWg = dg^T x and dWu = du^T x: K = rows, both operands across K.
+        TileArgs t{};
+        t.a[0] = b.dg;
+        t.a[1] = b.du;
+        t.lda = b.I;
+        t.b[0] = b.x;
+        t.b[1] = b.x;
+        t.ldb = b.H;
+        t.out[0] = b.dWg;
+        t.out[1] = b.dWu;
+        t.M = b.I;
+        t.N = b.H;
+        t.K = b.R;
+        t.batches = 2;
+        t.avec = gvec;
+        t.bvec = hvec && aligned16(b.x);
+        t.yvec = b.H % 4 == 0 && aligned16(b.dWg) && aligned16(b.dWu);
+        return launch_tiles_any<DT, kAcrossK, kAcrossK, 1, false>(t, t.avec && t.bvec, st);
+    }
+    return SGMV_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int gated_ffn(void* h, void* g_saved, void* u_saved, const void* x, const void* Wg, const void* Wu,
+              const void* gate_add, const void* up_add, int32_t num_rows, int32_t in_features,
+              int32_t out_features, int32_t act, int32_t dtype, void* stream) {
+    const int rc = check_ffn(num_rows, in_features, out_features, act, dtype);
+    if (rc != SGMV_OK) return rc;
+    if (num_rows == 0) return SGMV_OK;
+    if (!h || !x || !Wg || !Wu) return SGMV_ERR_NULL_PTR;
+    const int pk = piece_elems(dtype);
+    RowsArgs a{};
+    a.y = h;
+    a.x = x;
+    a.m[0].w = Wg;
+    a.m[1].w = Wu;
+    a.add[0] = gate_add;
+    a.add[1] = up_add;
+    a.save[0] = g_saved;
+    a.save[1] = u_saved;
+    a.R = num_rows;
+    a.N = out_features;
+    a.K = in_features;
+    a.kblocks = (int)ceil_div(in_features, 16 * pk);
+    a.act = act;
+    a.xvec = in_features % pk == 0 && aligned16(x);
+    a.wvec = in_features % pk == 0 && aligned16(Wg) && aligned16(Wu);
+    a.yvec = out_features % 4 == 0 && aligned16(h) && aligned16(g_saved) && aligned16(u_saved) &&
+             aligned16(gate_add) && aligned16(up_add);
+    const hipStream_t st = (hipStream_t)stream;
+    if (dtype == SGMV_F32) return run_forward<F32>(a, st);
+    if (dtype == SGMV_F16) return run_forward<F16>(a, st);
+    return run_forward<BF16>(a, st);
+}
+
+int gated_ffn_backward(void* dx, void* dWg, void* dWu, void* dg, void* du, const void* dh,
+                       const void* x, const void* Wg, const void* Wu, const void* g, const void* u,
+                       int32_t num_rows, int32_t in_features, int32_t out_features, int32_t act,
+                       int32_t dtype, void* stream) {
+    const int rc = check_ffn(num_rows, in_features, out_features, act, dtype);
+    if (rc != SGMV_OK) return rc;
+    if ((dWg == nullptr) != (dWu == nullptr)) return SGMV_ERR_NULL_PTR;
+    if (num_rows > 0 && (!dg || !du || !dh || !g || !u || (dx && (!Wg || !Wu)) || (dWg && !x)))
+        return SGMV_ERR_NULL_PTR;
+    const GradArgs b{dx, dWg, dWu, dg, du, dh, x, Wg, Wu, g, u, num_rows, in_features, out_features,
+                     act};
+    const hipStream_t st = (hipStream_t)stream;
+    if (dtype == SGMV_F32) return run_backward<F32>(b, st);
+    if (dtype == SGMV_F16) return run_backward<F16>(b, st);
+    return run_backward<BF16>(b, st);
+}
+
+}  // extern "C"

@@ -1,0 +1,223 @@
+// proj_device.hpp -- device-side pieces shared by the base projections'
+// kernels (proj_rows.hpp, proj_tile.hpp): matrix-core products of 16-byte
+// operand pieces for every element type, guarded piece loads, the
+// activations of the gated block with their derivatives, and the unpacking
+// of 4-bit weight codes.
+#pragma once
+
+#include <type_traits>
+
+#include "sgmv_device.hpp"
+
+namespace sgmv {
+
+// One operand piece is 16 bytes per lane: lane (lr, lg) = (lane % 16, lane / 16)
+// holds kPK consecutive K of row (or column) lr, starting at lg * kPK.  A
+// piece of the wave therefore covers 4 kPK values of K.  16-bit types take
+// one MFMA of K = 32; float32 takes four of K = 4, MFMA e multiplying
+// element e of every lane's piece.  Both operands use the same order of K,
+// which is all a sum over K needs.
+typedef float acc4_t __attribute__((ext_vector_type(4)));
+
+template <typename DT>
+struct PieceOps;
+template <>
+struct PieceOps<F16> {
+    static constexpr int kPK = 8;
+    typedef _Float16 frag_t __attribute__((ext_vector_type(8)));
+    __device__ static __forceinline__ acc4_t mma(const uint4& a, const uint4& b, acc4_t c) {
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(frag_t, a),
+                                                      __builtin_bit_cast(frag_t, b), c, 0, 0, 0);
+    }
+};
+template <>
+struct PieceOps<BF16> {
+    static constexpr int kPK = 8;
+    typedef __bf16 frag_t __attribute__((ext_vector_type(8)));
+    __device__ static __forceinline__ acc4_t mma(const uint4& a, const uint4& b, acc4_t c) {
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(frag_t, a),
+                                                       __builtin_bit_cast(frag_t, b), c, 0, 0, 0);
+    }
+};
+template <>
+struct PieceOps<F32> {
+    static constexpr int kPK = 4;
+    __device__ static __forceinline__ acc4_t mma(const uint4& a, const uint4& b, acc4_t c) {
+        c = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(a.x), __uint_as_float(b.x), c, 0, 0, 0);
+        c = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(a.y), __uint_as_float(b.y), c, 0, 0, 0);
+        c = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(a.z), __uint_as_float(b.z), c, 0, 0, 0);
+        c = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(a.w), __uint_as_float(b.w), c, 0, 0, 0);
+        return c;
+    }
+};
+
+__device__ __forceinline__ uint2 load_pair(const void* p) {
+    return *reinterpret_cast<const uint2*>(p);
+}
+__device__ __forceinline__ void store_pair(void* p, const uint2& v) {
+    *reinterpret_cast<uint2*>(p) = v;
+}
+
+// Two floats to two packed 16-bit values, nearest-even (gfx950 has a packed
+// conversion to bf16; NaN stays NaN, overflow goes to infinity).
+template <typename DT>
+__device__ __forceinline__ uint32_t pack2_rne(float lo, float hi);
+template <>
+__device__ __forceinline__ uint32_t pack2_rne<F16>(float lo, float hi) {
+    return F16::pack2(lo, hi);
+}
+template <>
+__device__ __forceinline__ uint32_t pack2_rne<BF16>(float lo, float hi) {
+    typedef __bf16 b2_t __attribute__((ext_vector_type(2)));
+    const b2_t v = {(__bf16)lo, (__bf16)hi};
+    return __builtin_bit_cast(uint32_t, v);
+}
+
+// Elements [k, k + kPK) of a row, zero at and past K.  `vec`: the row is
+// 16-byte aligned and K a multiple of kPK, so the piece lies wholly inside
+// or wholly outside.
+template <typename DT>
+__device__ __forceinline__ uint4 load_piece(const typename DT::storage* row, int k, int K,
+                                            bool vec) {
+    constexpr int PK = PieceOps<DT>::kPK;
+    if (vec) return k < K ? load16(row + k) : make_uint4(0, 0, 0, 0);
+    union {
+        typename DT::storage e[PK];
+        uint4 u;
+    } p;
+    p.u = make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int i = 0; i < PK; ++i)
+        if (k + i < K) p.e[i] = row[k + i];
+    return p.u;
+}
+
+// Four consecutive elements at p (the first n valid): one 8- or 16-byte
+// access when `vec` (p aligned to it and n >= 4), element by element else.
+template <typename DT>
+__device__ __forceinline__ void load4f(const typename DT::storage* p, int n, bool vec, float* f) {
+    if (vec && n >= 4) {
+        if constexpr (DT::kBytes == 4) {
+            DT::unpack(load16(p), f);
+        } else {
+            const uint2 u = load_pair(p);
+            DT::unpack2(u.x, f);
+            DT::unpack2(u.y, f + 2);
+        }
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = i < n ? DT::load1(p + i) : 0.f;
+}
+template <typename DT>
+__device__ __forceinline__ void store4f(typename DT::storage* p, int n, bool vec, const float* f) {
+    if (vec && n >= 4) {
+        if constexpr (DT::kBytes == 4)
+            store16(p, DT::pack(f));
+        else
+            store_pair(p, make_uint2(pack2_rne<DT>(f[0], f[1]), pack2_rne<DT>(f[2], f[3])));
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (i < n) p[i] = DT::from_float(f[i]);
+}
+
+// ---------------------------------------------------------------------------
+// Activations a(g) of the gated block and their derivatives.  `act` is
+// uniform over the launch (SGMV_ACT_* of sgmv.h).
+// ---------------------------------------------------------------------------
+enum { kActSilu = 0, kActGelu = 1, kActGeluTanh = 2, kActRelu = 3, kActSigmoid = 4 };
+
+__device__ __forceinline__ float sigmoid_f(float g) { return 1.f / (1.f + __expf(-g)); }
+
+// tanh by the exponential, 1 - 2 / (e^(2 z) + 1): absolute error a few
+// 2^-24, which is what 1 + tanh needs; both limits are exact.
+__device__ __forceinline__ float tanh_f(float z) { return 1.f - 2.f / (__expf(2.f * z) + 1.f); }
+
+constexpr float kInvSqrt2 = 0.70710678118654752f;
+constexpr float kInvSqrt2Pi = 0.39894228040143268f;
+constexpr float kSqrt2OverPi = 0.79788456080286536f;
+constexpr float kGeluCubic = 0.044715f;
+
+__device__ __forceinline__ float act_value(int act, float g) {
+    switch (act) {
+        case kActSilu: return g * sigmoid_f(g);
+        case kActGelu: return g * 0.5f * erfcf(-g * kInvSqrt2);
+        case kActGeluTanh: return 0.5f * g * (1.f + tanh_f(kSqrt2OverPi * (g + kGeluCubic * g * g * g)));
+        case kActRelu: return g < 0.f ? 0.f : g;  // a NaN stays one
+        default: return sigmoid_f(g);
+    }
+}
+
+__device__ __forceinline__ void act_value_grad(int act, float g, float& a, float& d) {
+    switch (act) {
+        case kActSilu: {
+            const float s = sigmoid_f(g);
+            a = g * s;
+            d = s * (1.f + g * (1.f - s));
+            return;
+        }
+        case kActGelu: {
+            const float c = 0.5f * erfcf(-g * kInvSqrt2);
+            a = g * c;
+            d = c + g * __expf(-0.5f * g * g) * kInvSqrt2Pi;
+            return;
+        }
+        case kActGeluTanh: {
+            const float t = tanh_f(kSqrt2OverPi * (g + kGeluCubic * g * g * g));
+            a = 0.5f * g * (1.f + t);
+            d = 0.5f * (1.f + t) +
+                0.5f * g * (1.f - t * t) * kSqrt2OverPi * (1.f + 3.f * kGeluCubic * g * g);
+            return;
+        }
+        case kActRelu:
+            a = g < 0.f ? 0.f : g;
+            d = g > 0.f ? 1.f : 0.f;
+            return;
+        default: {
+            const float s = sigmoid_f(g);
+            a = s;
+            d = s * (1.f - s);
+            return;
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// 4-bit weight codes.  A packed dword holds the codes of one lane's operand
+// piece (8 consecutive K of one output feature): code 2 p in bits
+// [4 p, 4 p + 4) and code 2 p + 1 in bits [16 + 4 p, 16 + 4 p + 4), so that
+// one mask picks a pair that already sits in the two halves of a register.
+// Put into the top mantissa bits of 16.0 (ulp 2^-6 in fp16, 2^-3 in bf16),
+// a code q becomes the exact value 16 + q: a shift and an and-or per pair.
+// ---------------------------------------------------------------------------
+constexpr float kCodeBias = 16.f;
+
+template <typename DT>
+__device__ __forceinline__ uint4 codes_biased(uint32_t w) {
+    uint4 o;
+    if constexpr (std::is_same<DT, F16>::value) {
+        constexpr uint32_t m = 0x03C003C0u, b = 0x4C004C00u;
+        o.x = ((w << 6) & m) | b;
+        o.y = ((w << 2) & m) | b;
+        o.z = ((w >> 2) & m) | b;
+        o.w = ((w >> 6) & m) | b;
+    } else {
+        constexpr uint32_t m = 0x00780078u, b = 0x41804180u;
+        o.x = ((w << 3) & m) | b;
+        o.y = ((w >> 1) & m) | b;
+        o.z = ((w >> 5) & m) | b;
+        o.w = ((w >> 9) & m) | b;
+    }
+    return o;
+}
+
+// A piece of ones.
+template <typename DT>
+__device__ __forceinline__ uint4 ones_piece() {
+    const uint32_t o = std::is_same<DT, F16>::value ? 0x3C003C00u : 0x3F803F80u;
+    return make_uint4(o, o, o, o);
+}
+
+}  // namespace sgmv

@@ -1,0 +1,51 @@
+// proj_launch.hpp -- host-side choice of tile shape and launch of the tile
+// kernels, shared by the 4-bit and the gated entry points.
+#pragma once
+
+#include "proj_tile.hpp"
+#include "sgmv_host.hpp"
+
+#include <algorithm>
+
+namespace sgmv {
+
+using BigTile = TileShape<256, 256, 2, 4>;
+using MidTile = TileShape<128, 128, 2, 2>;
+
+inline long long ceil_div(long long a, long long b) { return (a + b - 1) / b; }
+
+// Sets the tile grid of `a` for output width `width` (both matrices' columns
+// for a gated call) and launches.
+template <typename DT, typename SH, int AL, int BL, int kSegs, bool kGated, bool kDma>
+int launch_tiles(TileArgs a, hipStream_t st) {
+    const long long tm = ceil_div(a.M, SH::BM);
+    const long long tn = ceil_div(a.N, kGated ? SH::BN / 2 : SH::BN);
+    const long long tiles = tm * tn * a.batches;
+    if (tiles > 0x7FFFFFFFll) return SGMV_ERR_UNSUPPORTED;
+    if (tiles == 0) return SGMV_OK;
+    a.tiles_m = (int)tm;
+    a.tiles_n = (int)tn;
+    a.tiles = (int)tiles;
+    launch(&tile_kernel<DT, SH, AL, BL, kSegs, kGated, kDma>, dim3((unsigned)tiles), dim3(SH::NT), st,
+           a);
+    return launch_status();
+}
+
+// 256 x 256 tiles once they make a tile per CU, 128 x 128 below that; the
+// register path (operands no 16-byte load fits) always takes the small ones.
+template <typename DT, int AL, int BL, int kSegs, bool kGated>
+int launch_tiles_any(const TileArgs& a, bool direct, hipStream_t st) {
+    if (!direct) return launch_tiles<DT, MidTile, AL, BL, kSegs, kGated, false>(a, st);
+    const long long big = ceil_div(a.M, 256) * ceil_div(a.N, kGated ? 128 : 256) * a.batches;
+    if (big >= 192) return launch_tiles<DT, BigTile, AL, BL, kSegs, kGated, true>(a, st);
+    return launch_tiles<DT, MidTile, AL, BL, kSegs, kGated, true>(a, st);
+}
+
+inline int elem_size(int dtype) { return dtype == SGMV_F32 ? 4 : 2; }
+inline int piece_elems(int dtype) { return dtype == SGMV_F32 ? 4 : 8; }
+inline bool known_dtype(int dtype) {
+    return dtype == SGMV_F32 || dtype == SGMV_F16 || dtype == SGMV_BF16;
+}
+inline bool known_act(int act) { return act >= SGMV_ACT_SILU && act <= SGMV_ACT_SIGMOID; }
+
+}  // namespace sgmv

@@ -1,0 +1,526 @@
+// proj_tile.hpp -- matrix products of many rows on the matrix cores: the
+// gated block's forward, its gradients with respect to x and to the weights,
+// and 4-bit projections of prompts.
+//
+// Bound: the MFMA rate.  A workgroup computes a BM x BN tile of
+// C[m][n] = sum_k A[m][k] B[n][k] in steps of 64 bytes of K (32 16-bit or 16
+// float32 values) through four LDS stages.  Full steps arrive by direct
+// global-to-LDS loads three steps ahead, so no register holds a tile in
+// flight and a step waits only for loads issued three steps before; what is
+// left of K past a multiple of four steps, and operands that no 16-byte load
+// fits, go through registers, zero filled.
+//
+// An operand lies in memory either along K (x, W as used by the forward) or
+// across it (the gradients' transposed operands): the latter keep their
+// layout in LDS and are transposed by the reads that feed the MFMAs
+// (ds_read_b64_tr_b16), so no transposed copy of a weight or of an
+// activation is ever written.
+#pragma once
+
+#include "proj_rows.hpp"
+
+namespace sgmv {
+
+enum { kAlongK = 0, kAcrossK = 1, kCodes = 2 };
+
+template <int BM_, int BN_, int WM_, int WN_>
+struct TileShape {
+    static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_;
+    static constexpr int NW = WM * WN;                 // waves
+    static constexpr int NT = NW * kWave;              // threads
+    static constexpr int TM = BM / (16 * WM), TN = BN / (16 * WN);  // MFMA tiles per wave
+};
+
+struct TileArgs {
+    // One product C = A B^T over K, or (kSegs == 2) the sum of two of the
+    // same shapes; `batches` == 2: two products a[z], b[z] -> out[z].
+    const void* a[2];
+    const void* b[2];
+    long long lda, ldb;   // elements between rows (kAlongK) or K (kAcrossK)
+    ProjWeight q[2];      // kCodes
+    void* out[2];         // [M, N]
+    const void* add[2];   // gated: addends [M, N]; else add[0] = bias [N]; or NULL
+    void* save[2];        // gated: g and u [M, N], or NULL
+    int M, N, K;          // gated: N columns of each matrix
+    int batches;
+    int tiles_m, tiles_n, tiles;
+    int avec, bvec, yvec; // 16-byte pieces of A / B; 4-element pieces of [M, N] arrays
+    int kblocks, group_steps, groups, act;
+    uint32_t group_magic;
+};
+
+// Where 16-byte piece p of K row k of an operand kept across K lies in its
+// LDS row.  A transposing read takes, per group of 16 lanes, 32 bytes of each
+// of four K rows; the 32-byte units of a row are permuted by its K so that the
+// 16 rows one read touches fall on different banks.
+template <typename DT, int COLS>
+struct AcrossLayout {
+    static constexpr int kRow = COLS * DT::kBytes;  // bytes of a K row
+    static constexpr int kUnits = kRow / 32;
+    static constexpr int kRowsPerLoad = 1024 / kRow;
+    static constexpr bool kPermute = DT::kBytes == 2;
+    __device__ static __forceinline__ int permute(int k) {
+        return kPermute ? ((k & 3) | (((k >> 3) & 3) << 2)) & (kUnits - 1) : 0;
+    }
+};
+
+// Byte offset of 16-byte slot s of stage row r of an operand kept along K:
+// slot s holds piece s ^ ((r >> 1) & 3), which spreads the 16 rows an MFMA
+// operand read touches over the banks.
+__device__ __forceinline__ int along_piece(int r, int s) { return s ^ ((r >> 1) & 3); }
+
+// MFMA operand (16 rows or columns from c0 on) out of a stage.
+template <typename DT, int LAYOUT, int COLS>
+struct StageReader {
+    int off;       // lane's byte offset
+    int f;         // AcrossLayout permutation of this lane's rows
+    __device__ __forceinline__ StageReader(int c0, int lr, int lg) {
+        if constexpr (LAYOUT != kAcrossK) {
+            off = (c0 + lr) * 64 + (along_piece(lr, lg) << 4);
+            f = 0;
+        } else if constexpr (DT::kBytes == 2) {
+            using L = AcrossLayout<DT, COLS>;
+            off = (lg * 8 + (lr >> 2)) * L::kRow + (lr & 3) * 8;
+            f = L::permute(lg * 8 + (lr >> 2)) ^ (c0 >> 4);
+        } else {
+            off = lg * 4 * (COLS * 4) + (c0 + lr) * 4;
+            f = 0;
+        }
+    }
+    __device__ __forceinline__ uint4 operator()(const uint8_t* st, int i) const {
+        if constexpr (LAYOUT != kAcrossK) {
+            return load16(st + off + i * 1024);
+        } else if constexpr (DT::kBytes == 2) {
+#if __HIP_DEVICE_COMPILE__
+            using L = AcrossLayout<DT, COLS>;
+            typedef short v4s __attribute__((ext_vector_type(4)));
+            typedef __attribute__((address_space(3))) v4s lds_v4s;
+            typedef __attribute__((address_space(3))) uint8_t lds_u8;
+            const uint8_t* p = st + off + ((f ^ i) << 5);
+            const v4s lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(lds_u8*)p);
+            const v4s hi =
+                __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(lds_u8*)(p + 4 * L::kRow));
+            const uint2 l = __builtin_bit_cast(uint2, lo), h = __builtin_bit_cast(uint2, hi);
+            return make_uint4(l.x, l.y, h.x, h.y);
+#else
+            return make_uint4(0, 0, 0, 0);
+#endif
+        } else {
+            const uint32_t* p = reinterpret_cast<const uint32_t*>(st + off + i * 64);
+            constexpr int r = COLS;  // dwords of a K row
+            return make_uint4(p[0], p[r], p[2 * r], p[3 * r]);
+        }
+    }
+};
+
+// Scaled weights of one lane's eight codes, each rounded once to the 16-bit
+// type: s (q - z).  The rows kernel keeps the scales out of the products and
+// rounds nothing here, but a tile of many rows would pay for that with a
+// multiply-add per accumulator and group; one rounding of a weight is what a
+// 16-bit copy of the same weight would carry, and its share of the result's
+// error is below that of the result's own rounding.
+template <typename DT>
+__device__ __forceinline__ uint4 scaled_codes(uint32_t w, float s, float z) {
+    if constexpr (std::is_same<DT, F16>::value) {
+        typedef _Float16 h2_t __attribute__((ext_vector_type(2)));
+        const uint4 b = codes_biased<F16>(w);
+        const h2_t zz = {(_Float16)(kCodeBias + z), (_Float16)(kCodeBias + z)};
+        const h2_t ss = {(_Float16)s, (_Float16)s};
+        auto one = [&](uint32_t v) {  // (16 + q) - (16 + z) is exact
+            return __builtin_bit_cast(uint32_t, (__builtin_bit_cast(h2_t, v) - zz) * ss);
+        };
+        return make_uint4(one(b.x), one(b.y), one(b.z), one(b.w));
+    } else {
+        const float c = -s * (kCodeBias + z);
+        auto one = [&](uint32_t v) {  // v: two bf16 values 16 + q
+            return pack2_rne<BF16>(__builtin_fmaf(__uint_as_float(v << 16), s, c),
+                                   __builtin_fmaf(__uint_as_float(v & 0xFFFF0000u), s, c));
+        };
+        const uint4 b = codes_biased<BF16>(w);
+        return make_uint4(one(b.x), one(b.y), one(b.z), one(b.w));
+    }
+}
+
+template <typename DT, typename SH, int AL, int BL, int kSegs, bool kGated, bool kDma>
+__global__ __launch_bounds__(SH::NT) void tile_kernel(TileArgs g) {
+    using T = typename DT::storage;
+    using Ops = PieceOps<DT>;
+    constexpr int BM = SH::BM, BN = SH::BN, TM = SH::TM, TN = SH::TN, NT = SH::NT, NW = SH::NW;
+    constexpr int B = DT::kBytes, PK = Ops::kPK;
+    constexpr int KE = 4 * PK;                 // K per step
+    constexpr int kStage = (BM + BN) * 64;     // bytes of a stage: A then B
+    static_assert(BL != kCodes || (B == 2 && AL == kAlongK), "codes feed 16-bit tiles along K");
+    static_assert(!kGated || TN % 2 == 0, "a gated wave holds both matrices' columns");
+    __shared__ __attribute__((aligned(16))) uint8_t s_st0[kStage];
+    __shared__ __attribute__((aligned(16))) uint8_t s_st1[kStage];
+    __shared__ __attribute__((aligned(16))) uint8_t s_st2[kStage];
+    __shared__ __attribute__((aligned(16))) uint8_t s_st3[kStage];
+
+    const int tid = threadIdx.x, lane = tid & (kWave - 1);
+    const int wid = __builtin_amdgcn_readfirstlane(tid / kWave);
+    const int lr = lane & 15, lg = lane >> 4;
+
+    // Tile of this workgroup.  Workgroup b runs on XCD b % 8: each XCD takes a
+    // contiguous range of the tile order, which walks groups of eight tile
+    // rows column by column, so that the tiles an XCD holds at one time share
+    // their operands in its L2.
+    int t = (int)blockIdx.x;
+    {
+        const int x = t & 7, per = g.tiles >> 3, rest = g.tiles & 7;
+        t = x * per + min(x, rest) + (t >> 3);
+    }
+    const int per_batch = g.tiles_m * g.tiles_n;
+    const int z = t / per_batch;
+    t -= z * per_batch;
+    const int group = t / (8 * g.tiles_n);
+    const int in_group = t - group * 8 * g.tiles_n;
+    const int rows_here = min(8, g.tiles_m - 8 * group);
+    const int m0 = (8 * group + in_group % rows_here) * BM;
+    const int tn = in_group / rows_here;
+    // Columns per tile: a gated tile holds BN / 2 of each matrix.
+    const int n0 = tn * (kGated ? BN / 2 : BN);
+    const int wr0 = (wid / SH::WN) * (16 * TM), wc = wid % SH::WN, wc0 = wc * (16 * TN);
+    const int M = g.M, N = g.N, K = g.K;
+
+    // Stage row r of B, gated: waves' column blocks of 16 TN rows, the first
+    // half of each from the gate's matrix and the second from the up matrix.
+    auto gated_row = [&](int r, int& which) {
+        const int blk = r / (16 * TN), in = r % (16 * TN);
+        which = in >= 8 * TN;
+        return n0 + blk * (8 * TN) + (which ? in - 8 * TN : in);
+    };
+
+    // 4-bit weights: unit u of this thread (one packed dword of a step) is
+    // lane (unit & 63) of n-tile unit / 64 of the stage.
+    constexpr int kUnits = BL == kCodes ? BN * 4 / NT : 1;
+    static_assert(BL != kCodes || kUnits * NT == BN * 4, "whole units per thread");
+    struct Codes {
+        uint4 w;
+        float s[4], z[4];
+    };
+    auto load_codes = [&](int kb, Codes(&c)[kUnits]) {
+        if constexpr (BL == kCodes) {
+            const int kbc = min(kb, g.kblocks - 1);
+#pragma unroll
+            for (int u = 0; u < kUnits; ++u) {
+                const int unit = tid + u * NT, l = unit & 63;
+                int which = 0;
+                const int row = kGated ? gated_row((unit >> 6) * 16, which) : n0 + (unit >> 6) * 16;
+                const int nt = min(row >> 4, ((N + 15) >> 4) - 1);
+                const ProjWeight& q = g.q[which];
+                c[u].w = load16((const uint4*)q.w + ((long long)nt * g.kblocks + kbc) * 64 + l);
+#pragma unroll
+                for (int s = 0; s < 4; ++s) {
+                    const int step = kbc * 4 + s;
+                    int gr = g.group_steps == 1 ? step : (int)__umulhi((uint32_t)step, g.group_magic);
+                    gr = min(gr, g.groups - 1);
+                    const long long gi = ((long long)nt * g.groups + gr) * 16 + (l & 15);
+                    c[u].s[s] = DT::load1((const T*)q.scales + gi);
+                    c[u].z[s] = q.zeros ? (float)q.zeros[gi] : 8.f;
+                }
+            }
+        }
+    };
+    auto store_codes = [&](uint8_t* st, const Codes(&c)[kUnits], int s) {
+        if constexpr (BL == kCodes) {
+#pragma unroll
+            for (int u = 0; u < kUnits; ++u) {
+                const int unit = tid + u * NT, l = unit & 63;
+                const int row = (unit >> 6) * 16 + (l & 15);
+                const uint32_t w = s == 0 ? c[u].w.x : s == 1 ? c[u].w.y : s == 2 ? c[u].w.z : c[u].w.w;
+                store16(st + BM * 64 + row * 64 + (along_piece(row, l >> 4) << 4),
+                        scaled_codes<DT>(w, c[u].s[s], c[u].z[s]));
+            }
+        }
+    };
+
+    acc4_t acc[TM][TN];
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+        for (int j = 0; j < TN; ++j) acc[i][j] = acc4_t{0.f, 0.f, 0.f, 0.f};
+
+    const StageReader<DT, AL, BM> rd_a(wr0, lr, lg);
+    const StageReader<DT, BL, BN> rd_b(wc0, lr, lg);
+    auto compute = [&](const uint8_t* st) {
+        uint4 b[TN];
+#pragma unroll
+        for (int j = 0; j < TN; ++j) b[j] = rd_b(st + BM * 64, j);
+#pragma unroll
+        for (int i = 0; i < TM; ++i) {
+            const uint4 a = rd_a(st, i);
+#pragma unroll
+            for (int j = 0; j < TN; ++j) acc[i][j] = Ops::mma(b[j], a, acc[i][j]);
+        }
+    };
+
+    // ---- K through registers, zero filled: four steps from kc on ------------
+    // Element e of an operand's stage: 16-byte slot e.
+    auto guarded = [&](auto layout, auto cols_c, const void* base, long long ld, int r0, int rows,
+                       int e, int kc, bool vec, int seg_or_batch) -> uint4 {
+        constexpr int L = decltype(layout)::value, COLS = decltype(cols_c)::value;
+        (void)seg_or_batch;
+        const T* p = (const T*)base;
+        if constexpr (L == kAlongK) {
+            const int row = e >> 2, k = kc + along_piece(row, e & 3) * PK;
+            if (r0 + row >= rows) return make_uint4(0, 0, 0, 0);
+            return load_piece<DT>(p + (long long)(r0 + row) * ld, k, K, vec);
+        } else {
+            using LY = AcrossLayout<DT, COLS>;
+            const int kr = e * 16 / LY::kRow, slot = (e * 16 % LY::kRow) / 16;
+            const int piece = (((slot >> 1) ^ LY::permute(kr)) << 1) | (slot & 1);
+            if (kc + kr >= K) return make_uint4(0, 0, 0, 0);
+            return load_piece<DT>(p + (long long)(kc + kr) * ld, r0 + piece * PK, rows, vec);
+        }
+    };
+    auto slow_steps = [&](int seg, int kc) {
+        const int which = kSegs == 2 ? seg : z;
+        constexpr int kA = BM * 4 / NT, kB = BL == kCodes ? 0 : BN * 4 / NT;
+        static_assert(kA * NT == BM * 4 && (BL == kCodes || kB * NT == BN * 4), "whole slots per thread");
+        constexpr int kBn = kB > 0 ? kB : 1;
+        uint4 ra[4][kA], rb[4][kBn];
+        Codes cc[kUnits];
+        if constexpr (BL == kCodes) load_codes(kc / 128, cc);
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+#pragma unroll
+            for (int u = 0; u < kA; ++u)
+                ra[s][u] = guarded(std::integral_constant<int, AL>{}, std::integral_constant<int, BM>{},
+                                   g.a[which], g.lda, m0, M, tid + u * NT, kc + s * KE, g.avec, 0);
+#pragma unroll
+            for (int u = 0; u < kB; ++u) {
+                const int e = tid + u * NT;
+                if constexpr (kGated) {
+                    int w2;
+                    const int row = gated_row(e >> 2, w2);
+                    const int k = kc + s * KE + along_piece(e >> 2, e & 3) * PK;
+                    rb[s][u] = row < N ? load_piece<DT>((const T*)g.b[w2] + (long long)row * g.ldb, k,
+                                                        K, g.bvec)
+                                       : make_uint4(0, 0, 0, 0);
+                } else {
+                    rb[s][u] = guarded(std::integral_constant<int, BL>{},
+                                       std::integral_constant<int, BN>{}, g.b[which], g.ldb, n0, N,
+                                       e, kc + s * KE, g.bvec, 0);
+                }
+            }
+        }
+        __syncthreads();  // the stages' last reads are done
+        auto put = [&](uint8_t* st, int s) {
+#pragma unroll
+            for (int u = 0; u < kA; ++u) store16(st + (tid + u * NT) * 16, ra[s][u]);
+#pragma unroll
+            for (int u = 0; u < kB; ++u) store16(st + BM * 64 + (tid + u * NT) * 16, rb[s][u]);
+            if constexpr (BL == kCodes) store_codes(st, cc, s);
+        };
+        put(s_st0, 0);
+        put(s_st1, 1);
+        put(s_st2, 2);
+        put(s_st3, 3);
+        __syncthreads();
+        compute(s_st0);
+        if (kc + KE < K) compute(s_st1);
+        if (kc + 2 * KE < K) compute(s_st2);
+        if (kc + 3 * KE < K) compute(s_st3);
+    };
+    const int k_full = kDma ? K / (4 * KE) * (4 * KE) : 0;  // K by direct loads
+    for (int seg = 0; seg < kSegs; ++seg)
+        for (int kc = k_full; kc < K; kc += 4 * KE) slow_steps(seg, kc);
+
+    // ---- full steps by direct loads -----------------------------------------
+    if constexpr (kDma) {
+        const int seg_steps = k_full / KE, nsteps = kSegs * seg_steps;
+        if (nsteps > 0) {
+            // Load u of wave w is load w * kLoads + u of the step: 16 stage rows
+            // of A, then of B, 1 KB each.  A wave's loads belong to one operand.
+            constexpr int kLA = BM / 16, kLB = BL == kCodes ? 0 : BN / 16;
+            constexpr int kLoads = (kLA + kLB) / NW;
+            static_assert(kLoads * NW == kLA + kLB && kLA % kLoads == 0, "whole loads per wave");
+            static_assert(2 * kLoads < 64, "the wait count fits vmcnt");
+            constexpr int kWaitSteps = (2 * kLoads & 15) | ((2 * kLoads >> 4) << 14) | 0x0070;
+            using lds_t = __attribute__((address_space(3))) void;
+            const bool is_a = wid * kLoads < kLA;
+            const int which = kSegs == 2 ? 0 : z;
+            const char* src[kLoads];
+            long long stride, jump = 0;  // bytes per step; from segment 0 to 1
+            auto along = [&](const void* base, long long ld, int row, int rows, int slot_row) {
+                const int slot = lane & 3;
+                return (const char*)base + ((long long)min(row, rows - 1) * ld +
+                                            along_piece(slot_row, slot) * PK) * B;
+            };
+            auto across = [&](auto cols_c, const void* base, long long ld, int c0, int cols, int load) {
+                using LY = AcrossLayout<DT, decltype(cols_c)::value>;
+                const int byte = lane * 16;
+                const int kr = load * LY::kRowsPerLoad + byte / LY::kRow;
+                const int slot = (byte % LY::kRow) / 16;
+                const int piece = (((slot >> 1) ^ LY::permute(kr)) << 1) | (slot & 1);
+                return (const char*)base + ((long long)kr * ld + min(c0 + piece * PK, cols - PK)) * B;
+            };
+            if (is_a) {
+                stride = AL == kAlongK ? 64 : KE * g.lda * B;
+                if (kSegs == 2) jump = (const char*)g.a[1] - (const char*)g.a[0];
+#pragma unroll
+                for (int u = 0; u < kLoads; ++u) {
+                    const int load = wid * kLoads + u;
+                    if constexpr (AL == kAlongK) {
+                        const int row = load * 16 + (lane >> 2);
+                        src[u] = along(g.a[which], g.lda, m0 + row, M, row);
+                    } else {
+                        src[u] = across(std::integral_constant<int, BM>{}, g.a[which], g.lda, m0, M, load);
+                    }
+                }
+            } else {
+                stride = BL == kAcrossK ? KE * g.ldb * B : 64;
+                if (kSegs == 2) jump = (const char*)g.b[1] - (const char*)g.b[0];
+#pragma unroll
+                for (int u = 0; u < kLoads; ++u) {
+                    const int load = wid * kLoads + u - kLA;
+                    const int row = load * 16 + (lane >> 2);
+                    if constexpr (kGated && BL == kAlongK) {
+                        int w2;
+                        const int gr = gated_row(row, w2);
+                        src[u] = along(g.b[w2], g.ldb, gr, N, row);
+                    } else if constexpr (BL == kAlongK) {
+                        src[u] = along(g.b[which], g.ldb, n0 + row, N, row);
+                    } else if constexpr (BL == kAcrossK) {
+                        src[u] = across(std::integral_constant<int, BN>{}, g.b[which], g.ldb, n0, N, load);
+                    }
+                }
+            }
+            auto issue = [&](uint8_t* st, int step) {
+                long long off = step * stride;
+                if (kSegs == 2 && step >= seg_steps) off = (step - seg_steps) * stride + jump;
+#pragma unroll
+                for (int u = 0; u < kLoads; ++u)
+                    __builtin_amdgcn_global_load_lds((const void*)(src[u] + off),
+                                                     (lds_t*)(st + (wid * kLoads + u) * 1024), 16, 0, 0);
+            };
+            Codes cur[kUnits], nxt[kUnits];
+            // Step c: its own loads have landed (the later two steps' stay in
+            // flight) and every wave is past step c - 1; then stage (c + 3) % 4
+            // takes step c + 3.  Past the last step loads re-read it into a
+            // stage no step reads.
+            auto step = [&](uint8_t* st, uint8_t* ahead, uint8_t* next, int c, int s) {
+                __builtin_amdgcn_s_waitcnt(kWaitSteps);
+                asm volatile("" ::: "memory");
+                __builtin_amdgcn_s_barrier();
+                asm volatile("" ::: "memory");
+                issue(ahead, min(c + 3, nsteps - 1));
+                if constexpr (BL == kCodes) {
+                    if (s < 3) store_codes(next, cur, s + 1);
+                    else store_codes(next, nxt, 0);
+                }
+                compute(st);
+            };
+            if constexpr (BL == kCodes) load_codes(0, cur);
+            __syncthreads();  // the register steps' last reads of the stages
+            issue(s_st0, 0);
+            issue(s_st1, min(1, nsteps - 1));
+            issue(s_st2, min(2, nsteps - 1));
+            if constexpr (BL == kCodes) store_codes(s_st0, cur, 0);
+            for (int c = 0; c < nsteps; c += 4) {
+                if constexpr (BL == kCodes) load_codes(c / 4 + 1, nxt);
+                step(s_st0, s_st3, s_st1, c, 0);
+                step(s_st1, s_st0, s_st2, c + 1, 1);
+                step(s_st2, s_st1, s_st3, c + 2, 2);
+                step(s_st3, s_st2, s_st0, c + 3, 3);
+                if constexpr (BL == kCodes) {
+#pragma unroll
+                    for (int u = 0; u < kUnits; ++u) cur[u] = nxt[u];
+                }
+            }
+            __builtin_amdgcn_s_waitcnt(0x0070);  // no load is left in flight to the stages
+        }
+    }
+
+    // ---- epilogue -------------------------------------------------------------
+    T* out = (T*)g.out[kSegs == 2 ? 0 : z];
+    constexpr int TNO = kGated ? TN / 2 : TN;
+#pragma unroll
+    for (int j = 0; j < TNO; ++j) {
+        const int n = n0 + wc * (16 * TNO) + 16 * j + 4 * lg;
+        if (n >= N) continue;
+        const int left = N - n;
+        float bias[4] = {0.f, 0.f, 0.f, 0.f};
+        if constexpr (!kGated) {
+            if (g.add[0]) load4f<DT>((const T*)g.add[0] + n, left, g.yvec, bias);
+        }
+#pragma unroll
+        for (int i = 0; i < TM; ++i) {
+            const int m = m0 + wr0 + 16 * i + lr;
+            if (m >= M) continue;
+            const long long at = (long long)m * N + n;
+            float o[4];
+            if constexpr (kGated) {
+                float v[2][4];
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) v[q][c] = acc[i][q * TNO + j][c];
+                    if (g.add[q]) {
+                        float b[4];
+                        load4f<DT>((const T*)g.add[q] + at, left, g.yvec, b);
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) v[q][c] += b[c];
+                    }
+                    if (g.save[q]) store4f<DT>((T*)g.save[q] + at, left, g.yvec, v[q]);
+                }
+#pragma unroll
+                for (int c = 0; c < 4; ++c) o[c] = act_value(g.act, v[0][c]) * v[1][c];
+            } else {
+#pragma unroll
+                for (int c = 0; c < 4; ++c) o[c] = acc[i][j][c] + bias[c];
+            }
+            store4f<DT>(out + at, left, g.yvec, o);
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// dg = dh u a'(g), du = dh a(g), element by element (three reads, two
+// writes).  n is the element count; `vec`: every array is 16-byte aligned.
+// ---------------------------------------------------------------------------
+template <typename DT>
+__global__ __launch_bounds__(256) void gated_grad_kernel(
+    typename DT::storage* __restrict__ dg, typename DT::storage* __restrict__ du,
+    const typename DT::storage* __restrict__ dh, const typename DT::storage* __restrict__ gs,
+    const typename DT::storage* __restrict__ us, long long n, int act, int vec) {
+    constexpr int V = DT::kVec;
+    const long long stride = (long long)gridDim.x * 256 * V;
+    for (long long i = ((long long)blockIdx.x * 256 + threadIdx.x) * V; i < n; i += stride) {
+        float h[V], a[V], b[V];
+        const bool whole = vec && i + V <= n;
+        if (whole) {
+            DT::unpack(load16(dh + i), h);
+            DT::unpack(load16(gs + i), a);
+            DT::unpack(load16(us + i), b);
+        } else {
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+                const bool in = i + e < n;
+                h[e] = in ? DT::load1(dh + i + e) : 0.f;
+                a[e] = in ? DT::load1(gs + i + e) : 0.f;
+                b[e] = in ? DT::load1(us + i + e) : 0.f;
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+            float v, d;
+            act_value_grad(act, a[e], v, d);
+            a[e] = h[e] * b[e] * d;
+            b[e] = h[e] * v;
+        }
+        if (whole) {
+            store16(dg + i, DT::pack(a));
+            store16(du + i, DT::pack(b));
+        } else {
+#pragma unroll
+            for (int e = 0; e < V; ++e)
+                if (i + e < n) {
+                    dg[i + e] = DT::from_float(a[e]);
+                    du[i + e] = DT::from_float(b[e]);
+                }
+        }
+    }
+}
+
+}  // namespace sgmv

@@ -1,0 +1,84 @@
+// rope_api.hip -- C ABI of the rotary positions (declared in include/sgmv.h):
+// argument checks and the choice of kernel and grid.
+#include "sgmv_host.hpp"
+#include "rope.hpp"
+
+#include <algorithm>
+
+namespace {
+
+using namespace sgmv;
+
+template <typename DT>
+void launch_rope(const RopeArgs& a, bool vec, hipStream_t st) {
+    const dim3 grid((unsigned)((long long)a.rows * a.groups));
+    if (vec) launch(&rope_kernel<DT, true>, grid, dim3(kRopeThreads), st, a);
+    else launch(&rope_kernel<DT, false>, grid, dim3(kRopeThreads), st, a);
+}
+
+}  // namespace
+
+extern "C" int rope(void* q_out, void* k_out, const void* q, const void* k,
+                    const void* positions, int32_t position_bytes, const double* inv_freq,
+                    float magnitude, int32_t num_rows, int32_t q_heads, int32_t k_heads, int32_t head_dim,
+                    int32_t rotary_dim, const int64_t* strides, int32_t interleaved,
+                    int32_t inverse, int32_t dtype, void* stream) {
+    if (dtype != SGMV_F32 && dtype != SGMV_F16 && dtype != SGMV_BF16) return SGMV_ERR_BAD_DTYPE;
+    if (num_rows < 0 || q_heads < 0 || k_heads < 0 || head_dim < 1 || rotary_dim < 2 ||
+        rotary_dim > head_dim || (rotary_dim & 1) || (position_bytes != 4 && position_bytes != 8))
+        return SGMV_ERR_BAD_SHAPE;
+    if (rotary_dim > kRopeMaxRot) return SGMV_ERR_UNSUPPORTED;
+    const long long heads = (long long)q_heads + k_heads;
+    if (num_rows == 0 || heads == 0) return SGMV_OK;
+    if ((q_heads > 0 && (!q || !q_out)) || (k_heads > 0 && (!k || !k_out)) || !positions ||
+        !inv_freq || !strides)
+        return SGMV_ERR_NULL_PTR;
+    RopeArgs a{};
+    a.out[0] = q_out;
+    a.out[1] = k_out;
+    a.in[0] = q;
+    a.in[1] = k;
+    for (int w = 0; w < 2; ++w) {
+        a.in_row[w] = strides[4 * w];
+        a.in_head[w] = strides[4 * w + 1];
+        a.out_row[w] = strides[4 * w + 2];
+        a.out_head[w] = strides[4 * w + 3];
+    }
+    a.positions = positions;
+    a.wide_positions = position_bytes == 8;
+    a.freq = inv_freq;
+    a.mag = magnitude;
+    a.sign = inverse ? -1.f : 1.f;
+    a.rows = num_rows;
+    a.heads[0] = q_heads;
+    a.heads[1] = k_heads;
+    a.D = head_dim;
+    a.rot = rotary_dim;
+    a.interleaved = interleaved != 0;
+
+    const int V = dtype == SGMV_F32 ? 4 : 8;
+    bool vec = head_dim % V == 0 && (interleaved ? rotary_dim : rotary_dim / 2) % V == 0;
+    for (int w = 0; w < 2; ++w) {
+        if (a.heads[w] == 0) continue;
+        vec = vec && aligned16(a.in[w]) && aligned16(a.out[w]);
+        for (int s = 0; s < 4; ++s) vec = vec && strides[4 * w + s] % V == 0;
+    }
+    const int v = vec ? V : 1;
+    a.units = (interleaved ? (vec ? rotary_dim / V : rotary_dim / 2) : rotary_dim / 2 / v) +
+              (head_dim - rotary_dim) / v;
+    a.units_magic = (uint32_t)(((1ull << 32) + a.units - 1) / a.units);
+    // One workgroup per row once the rows fill the chip (4 per CU); with
+    // fewer rows the heads are split too, down to one pass of the workgroup.
+    const long long per_pass = std::max(1, kRopeThreads / a.units);
+    long long want = std::max(1ll, (1024ll + num_rows - 1) / num_rows);
+    long long hpg = std::max(per_pass, (heads + want - 1) / want);
+    hpg = std::min({hpg, heads, std::max(1ll, 65535ll / a.units)});
+    a.heads_per_group = (int)hpg;
+    a.groups = (int)((heads + hpg - 1) / hpg);
+    if ((long long)num_rows * a.groups > 0x7FFFFFFFll || a.units > 65535) return SGMV_ERR_UNSUPPORTED;
+    const hipStream_t st = (hipStream_t)stream;
+    if (dtype == SGMV_F32) launch_rope<F32>(a, vec, st);
+    else if (dtype == SGMV_F16) launch_rope<F16>(a, vec, st);
+    else launch_rope<BF16>(a, vec, st);
+    return launch_status();
+}

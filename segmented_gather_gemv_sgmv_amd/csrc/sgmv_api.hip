@@ -19,6 +19,7 @@
 #include <utility>
 
 #include "sgmv.h"
+#include "sgmv_host.hpp"
 #include "sgmv_device.hpp"
 #include "sgmv_gemv.hpp"
 #include "sgmv_fused.hpp"
@@ -563,44 +564,11 @@ long long wall_ticks_per_second() {
     return cache[dev];
 }
 
-bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
-
 int check_common(int num_segments, int num_rows, int num_adapters, int r, int dtype) {
     if (dtype != SGMV_F32 && dtype != SGMV_F16 && dtype != SGMV_BF16) return SGMV_ERR_BAD_DTYPE;
     if (num_segments < 0 || num_rows < 0 || num_adapters < 0) return SGMV_ERR_BAD_SHAPE;
     if (r < 1 || r > SGMV_MAX_RANK) return SGMV_ERR_BAD_SHAPE;
     return SGMV_OK;
-}
-
-// Launch bookkeeping: every launch goes through hipLaunchKernel, whose
-// return value describes that launch alone (hipGetLastError could also
-// report an older, unrelated error of the caller's).  The first failure of a
-// call is kept until launch_status() reads it; the last one stays readable
-// through sgmv_last_hip_error().
-thread_local hipError_t t_pending = hipSuccess;
-thread_local hipError_t t_last = hipSuccess;
-
-template <typename Tuple, size_t... I>
-void arg_pointers(Tuple& t, void** out, std::index_sequence<I...>) {
-    ((out[I] = (void*)&std::get<I>(t)), ...);
-}
-
-template <typename... KArgs, typename... Args>
-void launch(void (*kernel)(KArgs...), dim3 grid, dim3 block, hipStream_t st, Args&&... args) {
-    static_assert(sizeof...(KArgs) == sizeof...(Args), "argument count mismatch");
-    std::tuple<std::decay_t<KArgs>...> vals(static_cast<std::decay_t<KArgs>>(args)...);
-    void* ptrs[sizeof...(KArgs) > 0 ? sizeof...(KArgs) : 1];
-    arg_pointers(vals, ptrs, std::index_sequence_for<KArgs...>{});
-    const hipError_t e = hipLaunchKernel((const void*)kernel, grid, block, ptrs, 0, st);
-    if (e != hipSuccess && t_pending == hipSuccess) t_pending = e;
-}
-
-int launch_status() {
-    const hipError_t e = t_pending;
-    t_pending = hipSuccess;
-    if (e == hipSuccess) return SGMV_OK;
-    t_last = e;
-    return SGMV_ERR_HIP;
 }
 
 // Whether a call's shrink fits the mixed two-launch form's shrink half, as a

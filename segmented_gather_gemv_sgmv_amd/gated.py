@@ -1,0 +1,139 @@
+"""The gated feed-forward block, both projections in one kernel.
+
+    h = gated_ffn(x, Wg, Wu, act="silu")       # act(x Wg^T + gate_add) * (x Wu^T + up_add)
+
+Differentiable in x, both weights and both addends; gated_ffn_backward is
+the gradient step by itself.  The addends are what the rows' adapters
+contribute before the activation (lora_apply_multi on zeros), so that a batch
+of many adapters is served, and adapters over a frozen base are trained,
+through the same kernel.
+"""
+from __future__ import annotations
+
+from . import _check, _need, _stream_ptr, _torch, dtype_code, lib
+
+ACTIVATIONS = {"silu": 0, "gelu": 1, "gelu_tanh": 2, "relu": 3, "sigmoid": 4}
+
+
+def _act_code(act) -> int:
+    if act not in ACTIVATIONS:
+        raise ValueError(f"act must be one of {', '.join(ACTIVATIONS)}, got {act!r}")
+    return ACTIVATIONS[act]
+
+
+def _output(out, shape, like, name="out"):
+    if out is None:
+        return _torch().empty(shape, dtype=like.dtype, device=like.device)
+    _need(out, name, like.device, like.dtype, len(shape))
+    if tuple(out.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(out.shape)}")
+    return out
+
+
+def _addends(gate_add, up_add, shape, x):
+    """Data pointers of the two addends (None for None)."""
+    ptrs = []
+    for t, name in ((gate_add, "gate_add"), (up_add, "up_add")):
+        if t is not None:
+            _need(t, name, x.device, x.dtype, 2)
+            if tuple(t.shape) != shape:
+                raise ValueError(f"{name} must be {shape}, got {tuple(t.shape)}")
+        ptrs.append(None if t is None else t.data_ptr())
+    return ptrs
+
+
+def _check_weights(x, Wg, Wu):
+    _need(x, "x", x.device, None, 2)
+    _need(Wg, "Wg", x.device, x.dtype, 2)
+    _need(Wu, "Wu", x.device, x.dtype, 2)
+    if Wg.shape != Wu.shape or Wg.shape[1] != x.shape[1]:
+        raise ValueError(f"shape mismatch: x {tuple(x.shape)}, Wg {tuple(Wg.shape)}, "
+                         f"Wu {tuple(Wu.shape)}")
+    return x.shape[0], x.shape[1], Wg.shape[0]
+
+
+def _forward(x, Wg, Wu, act, gate_add, up_add, out, save):
+    torch = _torch()
+    R, H, I = _check_weights(x, Wg, Wu)
+    code = _act_code(act)
+    ga, ua = _addends(gate_add, up_add, (R, I), x)
+    out = _output(out, (R, I), x)
+    g = u = None
+    if save:
+        g, u = (torch.empty((R, I), dtype=x.dtype, device=x.device) for _ in range(2))
+    _check(lib().gated_ffn(out.data_ptr(), g.data_ptr() if save else None,
+                           u.data_ptr() if save else None, x.data_ptr(), Wg.data_ptr(),
+                           Wu.data_ptr(), ga, ua, R, H, I, code, dtype_code(x.dtype),
+                           _stream_ptr(x.device)), "gated_ffn")
+    return out, g, u
+
+
+def gated_ffn_backward(dh, x, Wg, Wu, g, u, act: str = "silu", need_dx=True, need_dw=True):
+    """Gradients of gated_ffn from dh = dL/dh and the saved g and u (its
+    pre-activations, addends included): returns ``(dx, dWg, dWu, dg, du)``,
+    dx or the weights' gradients None where not needed; dg and du are also
+    the addends' gradients."""
+    torch = _torch()
+    R, H, I = _check_weights(x, Wg, Wu)
+    code = _act_code(act)
+    for t, name in ((dh, "dh"), (g, "g"), (u, "u")):
+        _need(t, name, x.device, x.dtype, 2)
+        if tuple(t.shape) != (R, I):
+            raise ValueError(f"{name} must be {(R, I)}, got {tuple(t.shape)}")
+    new = lambda *shape: torch.empty(shape, dtype=x.dtype, device=x.device)
+    dg, du = new(R, I), new(R, I)
+    dx = new(R, H) if need_dx else None
+    dWg, dWu = (new(I, H), new(I, H)) if need_dw else (None, None)
+    ptr = lambda t: None if t is None else t.data_ptr()
+    _check(lib().gated_ffn_backward(ptr(dx), ptr(dWg), ptr(dWu), dg.data_ptr(), du.data_ptr(),
+                                    dh.data_ptr(), x.data_ptr(), Wg.data_ptr(), Wu.data_ptr(),
+                                    g.data_ptr(), u.data_ptr(), R, H, I, code, dtype_code(x.dtype),
+                                    _stream_ptr(x.device)), "gated_ffn_backward")
+    return dx, dWg, dWu, dg, du
+
+
+_function = None
+
+
+def _autograd_function():
+    """The autograd node (made on first use: this package imports torch late)."""
+    global _function
+    if _function is None:
+        torch = _torch()
+
+        class GatedFFN(torch.autograd.Function):
+            @staticmethod
+            def forward(ctx, x, Wg, Wu, gate_add, up_add, act):
+                h, g, u = _forward(x, Wg, Wu, act, gate_add, up_add, None, True)
+                ctx.save_for_backward(x, Wg, Wu, g, u)
+                ctx.act = act
+                return h
+
+            @staticmethod
+            @torch.autograd.function.once_differentiable
+            def backward(ctx, dh):
+                x, Wg, Wu, g, u = ctx.saved_tensors
+                want = ctx.needs_input_grad
+                dx, dWg, dWu, dg, du = gated_ffn_backward(
+                    dh.contiguous(), x, Wg, Wu, g, u, ctx.act, need_dx=want[0],
+                    need_dw=want[1] or want[2])
+                return (dx, dWg if want[1] else None, dWu if want[2] else None,
+                        dg if want[3] else None, du if want[4] else None, None)
+
+        _function = GatedFFN
+    return _function
+
+
+def gated_ffn(x, Wg, Wu, act: str = "silu", gate_add=None, up_add=None, out=None):
+    """h = act(x Wg^T + gate_add) * (x Wu^T + up_add), float32 sums, rounded
+    once.  x [R, in], Wg and Wu [hidden, in] (torch's linear layout), addends
+    [R, hidden] or None; ``act`` is silu, gelu, gelu_tanh, relu or sigmoid.
+    Under autograd the pre-activations are kept in x's dtype for the backward
+    pass; ``out`` (optional) receives h and is only for calls without it."""
+    torch = _torch()
+    inputs = (x, Wg, Wu, gate_add, up_add)
+    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in inputs):
+        if out is not None:
+            raise ValueError("out cannot be given where gradients are recorded")
+        return _autograd_function().apply(x, Wg, Wu, gate_add, up_add, act)
+    return _forward(x, Wg, Wu, act, gate_add, up_add, out, False)[0]

@@ -1,0 +1,195 @@
+"""Rotary positions on q and k.
+
+    plan = rope_plan(128, base=10000.0, layout="half", device="cuda")
+    q, k = rope(q, k, positions, plan)             # new tensors
+    rope(q, k, positions, plan, out=(q, k))        # in place
+
+q [R, q heads, D] and k [R, k heads, D] may be views of a fused projection's
+output (any row and head strides); the first ``rotary_dim`` elements of a
+head turn, the rest is copied.  Differentiable in q and k.
+"""
+from __future__ import annotations
+
+import ctypes
+import math
+
+from . import _check, _need, _stream_ptr, _torch, dtype_code, lib
+
+LAYOUTS = {"half": 0, "interleaved": 1}
+
+
+def rope_frequencies(rotary_dim: int, base: float = 10000.0, scaling=None):
+    """``(inv_freq, magnitude)``: rotary_dim / 2 radians per position (a list
+    of floats) and the factor on the rotated elements.
+
+    inv_freq[j] = base^(-2 j / rotary_dim), changed for contexts longer than
+    the trained one by ``scaling``, a dict with "kind" and "factor":
+      linear    every frequency divided by factor
+      ntk       base raised so that the slowest pair slows by factor and the
+                fastest keeps its frequency: base * factor^(r / (r - 2))
+      by_parts  pairs that turn at least "fast" (32) times within "context"
+                positions keep their frequency, those that turn at most
+                "slow" (1) times are divided by factor, a linear ramp over
+                the pair index between; magnitude = 0.1 ln(factor) + 1 unless
+                "magnitude" is given.
+    """
+    r = int(rotary_dim)
+    if r < 2 or r % 2:
+        raise ValueError(f"rotary_dim must be even and at least 2, got {rotary_dim}")
+    if not base > 0:
+        raise ValueError("base must be positive")
+    magnitude, kind, factor = 1.0, None, 1.0
+    if scaling is not None:
+        kind, factor = scaling.get("kind"), float(scaling.get("factor", 0.0))
+        if kind not in ("linear", "ntk", "by_parts"):
+            raise ValueError(f"scaling kind must be linear, ntk or by_parts, got {kind!r}")
+        if not factor > 0:
+            raise ValueError("scaling needs a positive factor")
+        if kind == "ntk" and r > 2:
+            base = base * factor ** (r / (r - 2))
+    freq = [base ** (-2.0 * j / r) for j in range(r // 2)]
+    if kind == "linear":
+        freq = [f / factor for f in freq]
+    elif kind == "by_parts":
+        context = float(scaling.get("context", 0))
+        if not context > 0:
+            raise ValueError("by_parts scaling needs the trained context")
+
+        def index(turns):  # (real-valued) element index of the pair turning this often
+            return r * math.log(context / (turns * 2 * math.pi)) / (2 * math.log(base))
+
+        lo = max(math.floor(index(float(scaling.get("fast", 32)))), 0)
+        hi = min(math.ceil(index(float(scaling.get("slow", 1)))), r - 1)
+        width = max(hi - lo, 1e-3)
+        ramp = [min(max((j - lo) / width, 0.0), 1.0) for j in range(r // 2)]
+        freq = [f * (1 - t) + f / factor * t for f, t in zip(freq, ramp)]
+        magnitude = float(scaling.get("magnitude", 0.1 * math.log(factor) + 1.0))
+    return freq, magnitude
+
+
+class RopePlan:
+    """Frequencies on the device and the layout of the pairs (rope_plan)."""
+
+    def __init__(self, inv_freq, magnitude, rotary_dim, layout):
+        self.inv_freq, self.magnitude = inv_freq, magnitude
+        self.rotary_dim, self.layout = rotary_dim, layout
+
+
+def rope_plan(rotary_dim: int, base: float = 10000.0, scaling=None, layout: str = "half",
+              device="cuda") -> RopePlan:
+    """Plan for rope: frequencies as in rope_frequencies, ``layout`` "half"
+    (element j pairs with j + rotary_dim / 2) or "interleaved" (2 j, 2 j + 1)."""
+    torch = _torch()
+    if layout not in LAYOUTS:
+        raise ValueError(f"layout must be half or interleaved, got {layout!r}")
+    freq, magnitude = rope_frequencies(rotary_dim, base, scaling)
+    inv_freq = torch.tensor(freq, dtype=torch.float64, device=device)
+    return RopePlan(inv_freq, magnitude, int(rotary_dim), layout)
+
+
+def _heads(t, name, like):
+    """Checks one of q, k: on like's device and dtype, dense last dimension."""
+    if not t.is_cuda or t.device != like.device:
+        raise ValueError(f"{name} must be on {like.device}, got {t.device}")
+    if t.dtype != like.dtype:
+        raise TypeError(f"{name} must be {like.dtype}, got {t.dtype}")
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be [rows, heads, head_dim], got {tuple(t.shape)}")
+    if t.shape[2] > 1 and t.numel() and t.stride(2) != 1:
+        raise ValueError(f"{name}'s last dimension must be dense")
+
+
+def _run(q, k, positions, plan, out, inverse):
+    torch = _torch()
+    first = q if q is not None else k
+    if first is None:
+        raise ValueError("q or k must be given")
+    dev = first.device
+    if not first.is_cuda:
+        raise ValueError(f"q and k must be on a GPU, got {dev}")
+    _heads(first, "q" if q is not None else "k", first)
+    R, _, D = first.shape
+    pair, outs, strides, counts = (q, k), [], [], []
+    for i, (t, name) in enumerate(zip(pair, ("q", "k"))):
+        if t is None:
+            outs.append(None)
+            strides += [0] * 4
+            counts.append(0)
+            continue
+        _heads(t, name, first)
+        if t.shape[0] != R or t.shape[2] != D:
+            raise ValueError(f"q and k disagree on rows or head_dim: {tuple(first.shape)}, "
+                             f"{tuple(t.shape)}")
+        o = out[i] if out is not None else None
+        if o is None:
+            o = torch.empty(t.shape, dtype=t.dtype, device=dev)
+        else:
+            _heads(o, f"out {name}", first)
+            if o.shape != t.shape:
+                raise ValueError(f"out {name} must be {tuple(t.shape)}, got {tuple(o.shape)}")
+        outs.append(o)
+        strides += [t.stride(0), t.stride(1), o.stride(0), o.stride(1)]
+        counts.append(t.shape[1])
+    if positions.dtype not in (torch.int32, torch.int64):
+        raise TypeError(f"positions must be int32 or int64, got {positions.dtype}")
+    _need(positions, "positions", dev, None, 1)
+    if positions.shape[0] != R:
+        raise ValueError(f"positions must be [{R}], got {tuple(positions.shape)}")
+    if plan.inv_freq.device != dev:
+        raise ValueError(f"the plan must be on {dev}, got {plan.inv_freq.device}")
+    if plan.rotary_dim > D:
+        raise ValueError(f"rotary_dim {plan.rotary_dim} exceeds head_dim {D}")
+    ptr = lambda t: None if t is None else t.data_ptr()
+    _check(lib().rope(ptr(outs[0]), ptr(outs[1]), ptr(q), ptr(k), positions.data_ptr(),
+                      positions.element_size(), plan.inv_freq.data_ptr(), plan.magnitude, R,
+                      counts[0], counts[1], D, plan.rotary_dim, (ctypes.c_int64 * 8)(*strides),
+                      LAYOUTS[plan.layout], int(inverse), dtype_code(first.dtype),
+                      _stream_ptr(dev)), "rope")
+    return tuple(outs)
+
+
+_function = None
+
+
+def _autograd_function():
+    """The autograd node (made on first use: this package imports torch late)."""
+    global _function
+    if _function is None:
+        torch = _torch()
+
+        class Rope(torch.autograd.Function):
+            @staticmethod
+            def forward(ctx, q, k, positions, plan):
+                ctx.save_for_backward(positions)
+                ctx.plan = plan
+                return _run(q, k, positions, plan, None, False)
+
+            @staticmethod
+            @torch.autograd.function.once_differentiable
+            def backward(ctx, dq, dk):
+                grads = [None, None]
+                dense = lambda t: t if t.stride(2) == 1 or t.shape[2] == 1 else t.contiguous()
+                use = [dense(t) if want else None
+                       for t, want in zip((dq, dk), ctx.needs_input_grad)]
+                if use[0] is not None or use[1] is not None:
+                    grads = _run(use[0], use[1], ctx.saved_tensors[0], ctx.plan, None, True)
+                return (*grads, None, None)
+
+        _function = Rope
+    return _function
+
+
+def rope(q, k, positions, plan: RopePlan, out=None, inverse: bool = False):
+    """``(q', k')``: every head's pairs turned by positions[row] * frequency
+    and scaled by the plan's magnitude, rounded once.  q or k may be None.
+    ``positions`` [R] int32 or int64.  ``out=(q, k)`` works in place (or into
+    other tensors, which must not overlap the inputs); ``inverse`` turns back,
+    which is what the gradients take."""
+    torch = _torch()
+    if not isinstance(plan, RopePlan):
+        raise TypeError("plan must be a RopePlan (see rope_plan)")
+    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in (q, k)):
+        if out is not None or inverse:
+            raise ValueError("out and inverse cannot be given where gradients are recorded")
+        return _autograd_function().apply(q, k, positions, plan)
+    return _run(q, k, positions, plan, out, inverse)
