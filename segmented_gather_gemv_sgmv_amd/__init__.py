@@ -108,6 +108,8 @@ def lib() -> ctypes.CDLL:
     runtime so that torch's streams and allocations are valid in its calls.
     Loaded the other way round, the process would hold two HIP runtimes."""
     global _lib_handle
+    if _lib_handle is not None:
+        return _lib_handle
     with _lib_lock:
         if _lib_handle is None:
             import torch  # noqa: F401  (see above)
@@ -133,21 +135,48 @@ def _check(code: int, what: str):
 
 # -- torch marshalling -----------------------------------------------------------
 
+# A decode call's kernel takes a few microseconds, so what the binding spends
+# per call is part of its latency: the module, the dtype codes and the raw
+# stream lookup are kept once found.
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
+
+
+_dtype_codes = {}
 
 
 def dtype_code(dtype) -> int:
-    torch = _torch()
-    codes = {torch.float32: SGMV_F32, torch.float16: SGMV_F16, torch.bfloat16: SGMV_BF16}
-    if dtype not in codes:
-        raise TypeError(f"unsupported dtype {dtype}; expected float32, float16 or bfloat16")
-    return codes[dtype]
+    code = _dtype_codes.get(dtype)
+    if code is None:
+        torch = _torch()
+        _dtype_codes.update({torch.float32: SGMV_F32, torch.float16: SGMV_F16,
+                             torch.bfloat16: SGMV_BF16})
+        code = _dtype_codes.get(dtype)
+        if code is None:
+            raise TypeError(f"unsupported dtype {dtype}; expected float32, float16 or bfloat16")
+    return code
+
+
+_raw_stream = None
 
 
 def _stream_ptr(device) -> int:
-    return _torch().cuda.current_stream(device).cuda_stream
+    """torch's current stream on ``device`` as a hipStream_t."""
+    global _raw_stream
+    if _raw_stream is None:
+        torch = _torch()
+        # The raw handle without building a Stream object, where torch has it.
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+            lambda index: torch.cuda.current_stream(index).cuda_stream)
+    index = device.index
+    return _raw_stream(_torch().cuda.current_device() if index is None else index)
 
 
 def _need(t, name, device, dtype=None, ndim=None):

@@ -23,7 +23,7 @@ def _act_code(act) -> int:
 
 def _output(out, shape, like, name="out"):
     if out is None:
-        return _torch().empty(shape, dtype=like.dtype, device=like.device)
+        return like.new_empty(shape)
     _need(out, name, like.device, like.dtype, len(shape))
     if tuple(out.shape) != tuple(shape):
         raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(out.shape)}")
@@ -53,14 +53,13 @@ def _check_weights(x, Wg, Wu):
 
 
 def _forward(x, Wg, Wu, act, gate_add, up_add, out, save):
-    torch = _torch()
     R, H, I = _check_weights(x, Wg, Wu)
     code = _act_code(act)
     ga, ua = _addends(gate_add, up_add, (R, I), x)
     out = _output(out, (R, I), x)
     g = u = None
     if save:
-        g, u = (torch.empty((R, I), dtype=x.dtype, device=x.device) for _ in range(2))
+        g, u = x.new_empty((R, I)), x.new_empty((R, I))
     _check(lib().gated_ffn(out.data_ptr(), g.data_ptr() if save else None,
                            u.data_ptr() if save else None, x.data_ptr(), Wg.data_ptr(),
                            Wu.data_ptr(), ga, ua, R, H, I, code, dtype_code(x.dtype),
@@ -73,17 +72,15 @@ def gated_ffn_backward(dh, x, Wg, Wu, g, u, act: str = "silu", need_dx=True, nee
     pre-activations, addends included): returns ``(dx, dWg, dWu, dg, du)``,
     dx or the weights' gradients None where not needed; dg and du are also
     the addends' gradients."""
-    torch = _torch()
     R, H, I = _check_weights(x, Wg, Wu)
     code = _act_code(act)
     for t, name in ((dh, "dh"), (g, "g"), (u, "u")):
         _need(t, name, x.device, x.dtype, 2)
         if tuple(t.shape) != (R, I):
             raise ValueError(f"{name} must be {(R, I)}, got {tuple(t.shape)}")
-    new = lambda *shape: torch.empty(shape, dtype=x.dtype, device=x.device)
-    dg, du = new(R, I), new(R, I)
-    dx = new(R, H) if need_dx else None
-    dWg, dWu = (new(I, H), new(I, H)) if need_dw else (None, None)
+    dg, du = x.new_empty((R, I)), x.new_empty((R, I))
+    dx = x.new_empty((R, H)) if need_dx else None
+    dWg, dWu = (x.new_empty((I, H)), x.new_empty((I, H))) if need_dw else (None, None)
     ptr = lambda t: None if t is None else t.data_ptr()
     _check(lib().gated_ffn_backward(ptr(dx), ptr(dWg), ptr(dWu), dg.data_ptr(), du.data_ptr(),
                                     dh.data_ptr(), x.data_ptr(), Wg.data_ptr(), Wu.data_ptr(),

@@ -73,6 +73,8 @@ class RopePlan:
     def __init__(self, inv_freq, magnitude, rotary_dim, layout):
         self.inv_freq, self.magnitude = inv_freq, magnitude
         self.rotary_dim, self.layout = rotary_dim, layout
+        self.device, self.ptr = inv_freq.device, inv_freq.data_ptr()
+        self.interleaved = LAYOUTS[layout]
 
 
 def rope_plan(rotary_dim: int, base: float = 10000.0, scaling=None, layout: str = "half",
@@ -87,65 +89,76 @@ def rope_plan(rotary_dim: int, base: float = 10000.0, scaling=None, layout: str 
     return RopePlan(inv_freq, magnitude, int(rotary_dim), layout)
 
 
-def _heads(t, name, like):
-    """Checks one of q, k: on like's device and dtype, dense last dimension."""
-    if not t.is_cuda or t.device != like.device:
-        raise ValueError(f"{name} must be on {like.device}, got {t.device}")
-    if t.dtype != like.dtype:
-        raise TypeError(f"{name} must be {like.dtype}, got {t.dtype}")
+_Strides = ctypes.c_int64 * 8
+
+
+def _heads(t, name, dev, dtype):
+    """Checks one of q, k and their outputs: place, type, dense last dimension."""
+    if not t.is_cuda or t.device != dev:
+        raise ValueError(f"{name} must be on {dev if t.is_cuda else 'a GPU'}, got {t.device}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.dim() != 3:
         raise ValueError(f"{name} must be [rows, heads, head_dim], got {tuple(t.shape)}")
-    if t.shape[2] > 1 and t.numel() and t.stride(2) != 1:
+    st = t.stride()
+    if st[2] != 1 and t.shape[2] > 1 and t.numel():
         raise ValueError(f"{name}'s last dimension must be dense")
+    return st
+
+
+def _one(t, name, o, dev, dtype, R, D):
+    """(output, its and t's pointers, strides, heads) of q or k."""
+    st = _heads(t, name, dev, dtype)
+    shape = t.shape
+    if shape[0] != R or shape[2] != D:
+        raise ValueError(f"q and k disagree on rows or head_dim: {(R, D)}, {tuple(shape)}")
+    if o is None:
+        o = t.new_empty(shape)
+        so = (shape[1] * D, D)
+    else:
+        so = _heads(o, "out " + name, dev, dtype)
+        if o.shape != shape:
+            raise ValueError(f"out {name} must be {tuple(shape)}, got {tuple(o.shape)}")
+    return o, o.data_ptr(), t.data_ptr(), (st[0], st[1], so[0], so[1]), shape[1]
+
+
+_ABSENT = (None, None, None, (0, 0, 0, 0), 0)
 
 
 def _run(q, k, positions, plan, out, inverse):
-    torch = _torch()
     first = q if q is not None else k
     if first is None:
         raise ValueError("q or k must be given")
-    dev = first.device
-    if not first.is_cuda:
-        raise ValueError(f"q and k must be on a GPU, got {dev}")
-    _heads(first, "q" if q is not None else "k", first)
+    dev, dtype = first.device, first.dtype
+    _heads(first, "q" if q is not None else "k", dev, dtype)
     R, _, D = first.shape
-    pair, outs, strides, counts = (q, k), [], [], []
-    for i, (t, name) in enumerate(zip(pair, ("q", "k"))):
-        if t is None:
-            outs.append(None)
-            strides += [0] * 4
-            counts.append(0)
-            continue
-        _heads(t, name, first)
-        if t.shape[0] != R or t.shape[2] != D:
-            raise ValueError(f"q and k disagree on rows or head_dim: {tuple(first.shape)}, "
-                             f"{tuple(t.shape)}")
-        o = out[i] if out is not None else None
-        if o is None:
-            o = torch.empty(t.shape, dtype=t.dtype, device=dev)
-        else:
-            _heads(o, f"out {name}", first)
-            if o.shape != t.shape:
-                raise ValueError(f"out {name} must be {tuple(t.shape)}, got {tuple(o.shape)}")
-        outs.append(o)
-        strides += [t.stride(0), t.stride(1), o.stride(0), o.stride(1)]
-        counts.append(t.shape[1])
-    if positions.dtype not in (torch.int32, torch.int64):
+    oq, ok = out if out is not None else (None, None)
+    q2, qo, qi, qs, hq = _one(q, "q", oq, dev, dtype, R, D) if q is not None else _ABSENT
+    k2, ko, ki, ks, hk = _one(k, "k", ok, dev, dtype, R, D) if k is not None else _ABSENT
+    wide = positions.element_size()
+    if positions.dtype not in _position_types():
         raise TypeError(f"positions must be int32 or int64, got {positions.dtype}")
     _need(positions, "positions", dev, None, 1)
     if positions.shape[0] != R:
         raise ValueError(f"positions must be [{R}], got {tuple(positions.shape)}")
-    if plan.inv_freq.device != dev:
-        raise ValueError(f"the plan must be on {dev}, got {plan.inv_freq.device}")
+    if plan.device != dev:
+        raise ValueError(f"the plan must be on {dev}, got {plan.device}")
     if plan.rotary_dim > D:
         raise ValueError(f"rotary_dim {plan.rotary_dim} exceeds head_dim {D}")
-    ptr = lambda t: None if t is None else t.data_ptr()
-    _check(lib().rope(ptr(outs[0]), ptr(outs[1]), ptr(q), ptr(k), positions.data_ptr(),
-                      positions.element_size(), plan.inv_freq.data_ptr(), plan.magnitude, R,
-                      counts[0], counts[1], D, plan.rotary_dim, (ctypes.c_int64 * 8)(*strides),
-                      LAYOUTS[plan.layout], int(inverse), dtype_code(first.dtype),
-                      _stream_ptr(dev)), "rope")
-    return tuple(outs)
+    _check(lib().rope(qo, ko, qi, ki, positions.data_ptr(), wide, plan.ptr, plan.magnitude, R, hq,
+                      hk, D, plan.rotary_dim, _Strides(*qs, *ks), plan.interleaved, int(inverse),
+                      dtype_code(dtype), _stream_ptr(dev)), "rope")
+    return q2, k2
+
+
+_types = None
+
+
+def _position_types():
+    global _types
+    if _types is None:
+        _types = (_torch().int64, _torch().int32)
+    return _types
 
 
 _function = None
