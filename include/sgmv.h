@@ -378,21 +378,19 @@ int sgmv_group_rows(const int32_t* row_ids, int32_t num_rows, int32_t num_adapte
  * group_size is any multiple of 32 (the last group of a row may be shorter).
  *
  * q4_pack lays them out once for the matrix cores, into caller-owned,
- * 16-byte aligned device arrays: tiles (q4_tiles_bytes), scales
- * (q4_groups_padded elements of dtype) and, when zeros is given, zero
- * points (q4_groups_padded bytes).  The calls below read only these.
+ * 16-byte aligned device arrays: tiles (q4_tiles_bytes) and meta, the scales
+ * and zero points (q4_meta_bytes).  The calls below read only these.
  */
 typedef struct {
     const void* tiles;
-    const void* scales;
-    const uint8_t* zeros;  /* NULL: every zero point is 8 */
+    const void* meta;
 } sgmv_q4_weight;
 
 size_t q4_tiles_bytes(int32_t out_features, int32_t in_features);
-size_t q4_groups_padded(int32_t out_features, int32_t in_features, int32_t group_size);
-int q4_pack(void* tiles, void* packed_scales, uint8_t* packed_zeros, const uint8_t* codes,
-            const void* scales, const uint8_t* zeros, int32_t out_features, int32_t in_features,
-            int32_t group_size, int32_t dtype, void* stream);
+size_t q4_meta_bytes(int32_t out_features, int32_t in_features, int32_t group_size, int32_t dtype);
+int q4_pack(void* tiles, void* meta, const uint8_t* codes, const void* scales,
+            const uint8_t* zeros, int32_t out_features, int32_t in_features, int32_t group_size,
+            int32_t dtype, void* stream);
 
 /*
  * y = round(x W^T + bias): x [num_rows, in_features], y [num_rows,

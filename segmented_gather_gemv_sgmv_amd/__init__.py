@@ -76,8 +76,8 @@ ABI = [
     ("lora_linear", ctypes.c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32,
                                    _i32, _i32, _i32, _f32, _i32, _vp, _sz, _vp]),
     ("q4_tiles_bytes", _sz, [_i32, _i32]),
-    ("q4_groups_padded", _sz, [_i32, _i32, _i32]),
-    ("q4_pack", ctypes.c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _vp]),
+    ("q4_meta_bytes", _sz, [_i32, _i32, _i32, _i32]),
+    ("q4_pack", ctypes.c_int, [_vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _vp]),
     ("q4_linear", ctypes.c_int, [_vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _i32, _vp]),
     ("q4_gated_ffn", ctypes.c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _i32,
                                     _i32, _vp]),

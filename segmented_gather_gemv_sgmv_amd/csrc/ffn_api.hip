@@ -15,20 +15,21 @@ int check_ffn(int R, int H, int I, int act, int dtype) {
     return SGMV_OK;
 }
 
-template <typename DT, int MT>
+template <typename DT, int XR, int MT, int NTW, int PD>
 int run_rows(const RowsArgs& a, hipStream_t st) {
-    launch(&rows_kernel<DT, PlainSrc<DT>, MT, 1, 1, true>,
-           dim3((unsigned)ceil_div(a.N, 16), (unsigned)ceil_div(a.R, 16 * MT)), dim3(kRowsThreads),
-           st, a);
+    launch(&rows_kernel<DT, PlainSrc<DT>, XR, MT, NTW, PD, 1, true>,
+           dim3((unsigned)ceil_div(a.N, 16 * NTW), (unsigned)ceil_div(a.R, 16 * MT)),
+           dim3(kRowsThreads), st, a);
     return launch_status();
 }
 
 template <typename DT>
 int run_forward(const RowsArgs& a, hipStream_t st) {
     if (a.R <= kFfnRowsMax) {
-        if (a.R <= 16) return run_rows<DT, 1>(a, st);
-        if (a.R <= 32) return run_rows<DT, 2>(a, st);
-        return run_rows<DT, 4>(a, st);
+        if (a.R <= 4) return run_rows<DT, 4, 1, 1, 2>(a, st);
+        if (a.R <= 16) return run_rows<DT, 16, 1, 1, 2>(a, st);
+        if (a.R <= 32) return run_rows<DT, 16, 2, 1, 2>(a, st);
+        return run_rows<DT, 16, 4, 1, 1>(a, st);
     }
     TileArgs t{};
     t.a[0] = a.x;
@@ -47,7 +48,8 @@ int run_forward(const RowsArgs& a, hipStream_t st) {
     t.batches = 1;
     t.avec = a.xvec;
     t.bvec = a.wvec;
-    t.yvec = a.yvec;
+    t.yvec = a.N % 4 == 0 && aligned16(a.y) && aligned16(a.add[0]) && aligned16(a.add[1]) &&
+             aligned16(a.save[0]) && aligned16(a.save[1]);
     t.act = a.act;
     return launch_tiles_any<DT, kAlongK, kAlongK, 1, true>(t, a.xvec && a.wvec, st);
 }
@@ -145,8 +147,6 @@ int gated_ffn(void* h, void* g_saved, void* u_saved, const void* x, const void* 
     a.act = act;
     a.xvec = in_features % pk == 0 && aligned16(x);
     a.wvec = in_features % pk == 0 && aligned16(Wg) && aligned16(Wu);
-    a.yvec = out_features % 4 == 0 && aligned16(h) && aligned16(g_saved) && aligned16(u_saved) &&
-             aligned16(gate_add) && aligned16(up_add);
     const hipStream_t st = (hipStream_t)stream;
     if (dtype == SGMV_F32) return run_forward<F32>(a, st);
     if (dtype == SGMV_F16) return run_forward<F16>(a, st);

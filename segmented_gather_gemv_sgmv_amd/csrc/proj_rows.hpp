@@ -5,12 +5,13 @@
 // (of one matrix, or of both of the gated block) and 16 * MT rows, and its
 // eight waves split K in blocks of four operand pieces, so every weight is
 // read once per 16 * MT rows, straight from memory into the MFMA operand
-// registers; the eight float32 partial tiles are added in a fixed order
-// through LDS.  Rows ride in the MFMA's 16 columns: a single row costs the
-// same matrix-core time as 16, which is far below the weights' stream time.
+// registers, PD blocks ahead of its use; the eight float32 partial tiles are
+// added in a fixed order through LDS.  Rows ride in the MFMA's 16 columns: a
+// single row costs the same matrix-core time as 16, which is far below the
+// weights' stream time.
 //
-// Weights are the first MFMA operand, so a lane ends with four consecutive
-// features of one row.
+// x is the first MFMA operand, so a lane's sums all belong to one output
+// feature, lane % 16, and a 4-bit weight's scale is one value per lane.
 #pragma once
 
 #include "proj_device.hpp"
@@ -20,12 +21,15 @@ namespace sgmv {
 constexpr int kRowsWaves = 8;
 constexpr int kRowsThreads = kRowsWaves * kWave;
 
-// One weight matrix: plain [N, K] (w), or 4-bit: packed tiles (w) with
-// scales [N / 16][groups][16] and zero points likewise (NULL: 8).
+// One weight matrix: plain [N, K] (w), or 4-bit: packed tiles (w) and their
+// scales (meta): per tile of 16 features by 128 K and feature, kFlushes = 1, 2
+// or 4 pairs of scale and biased zero point 16 + z, one for each 128, 64 or 32
+// of the tile's K (a longer group is repeated), so that a lane reads what it
+// needs for a tile beside it in one load.  A pair is two 16-bit values of the
+// activations' type in a dword, or two floats.
 struct ProjWeight {
     const void* w;
-    const void* scales;
-    const uint8_t* zeros;
+    const void* meta;
 };
 
 struct RowsArgs {
@@ -36,34 +40,27 @@ struct RowsArgs {
                           // else add[0] = bias [N] or NULL
     void* save[2];        // gated: where g and u are kept [R, N], or NULL
     int R, N, K;
-    int kblocks;          // ceil(K / (16 kPK))
-    int group_steps;      // 4-bit: steps of 32 K per group
-    uint32_t group_magic; // ceil(2^32 / group_steps)
-    int groups;           // 4-bit: groups per row
+    int kblocks;          // blocks of four pieces of K
     int act;
-    int xvec, wvec, yvec; // 16-byte pieces of x / of W; 4-element pieces of y and the addends
+    int xvec, wvec;       // 16-byte pieces of x / of W
 };
 
-// Plain weights: one K block is four 16-byte pieces of a row.
+// Plain weights: one K block is four 16-byte pieces of a row.  4-bit weights:
+// four steps of 32 codes; float32 rows enter as three bf16 terms (their 24
+// bits exactly).
 template <typename DT>
 struct PlainSrc {
     static constexpr bool kQ4 = false;
     static constexpr int kStepK = 4 * PieceOps<DT>::kPK;
-    static constexpr int kXP = 1;  // x pieces per step
+    static constexpr int kXL = 1;  // 16-byte loads of x per step
+    static constexpr int kXP = 1;  // MFMA operands of x per step
 };
-// 4-bit weights: one K block is four steps of 32 codes; float32 rows enter
-// as three bf16 terms (their 24 bits exactly), so kXP = 3.
 template <typename DT>
 struct Q4Src {
     static constexpr bool kQ4 = true;
     static constexpr int kStepK = 32;
-    static constexpr int kXP = 1;
-};
-template <>
-struct Q4Src<F32> {
-    static constexpr bool kQ4 = true;
-    static constexpr int kStepK = 32;
-    static constexpr int kXP = 3;
+    static constexpr int kXL = DT::kBytes / 2;
+    static constexpr int kXP = DT::kBytes == 4 ? 3 : 1;
 };
 
 // The 16-bit type whose MFMA takes the codes.
@@ -96,41 +93,72 @@ __device__ __forceinline__ void split3(const float* f, uint4* out) {
     for (int i = 0; i < 3; ++i) out[i] = make_uint4(t[i][0], t[i][1], t[i][2], t[i][3]);
 }
 
-// x for one step of 32 K (or one piece, plain weights).
-template <typename DT, typename Src>
-__device__ __forceinline__ void load_x_step(const typename DT::storage* row, int k0, int lg, int K,
-                                            bool vec, uint4* out) {
-    if constexpr (Src::kXP == 3) {
-        float f[8];
-        F32::unpack(load_piece<F32>(row, k0 + 8 * lg, K, vec), f);
-        F32::unpack(load_piece<F32>(row, k0 + 8 * lg + 4, K, vec), f + 4);
-        split3(f, out);
+// The scale and biased zero point of a 16-bit meta dword.
+template <typename DT>
+__device__ __forceinline__ void meta_values(uint32_t m, float& s, float& zb) {
+    float f[2];
+    DT::unpack2(m, f);
+    s = f[0];
+    zb = f[1];
+}
+
+// n dwords at p in one load (p aligned to 4 n bytes).
+template <int N>
+__device__ __forceinline__ void load_dwords(const void* p, uint32_t* out) {
+    if constexpr (N == 1) {
+        out[0] = *(const uint32_t*)p;
+    } else if constexpr (N == 2) {
+        const uint2 v = load_pair(p);
+        out[0] = v.x, out[1] = v.y;
     } else {
-        out[0] = load_piece<DT>(row, k0 + PieceOps<DT>::kPK * lg, K, vec);
+#pragma unroll
+        for (int i = 0; i < N / 4; ++i) {
+            const uint4 v = load16((const uint4*)p + i);
+            out[4 * i] = v.x, out[4 * i + 1] = v.y, out[4 * i + 2] = v.z, out[4 * i + 3] = v.w;
+        }
     }
 }
 
-// Four consecutive scales (features 4 lg .. 4 lg + 3 of an n-tile) as floats.
-template <typename DT>
-__device__ __forceinline__ void load_scales4(const void* scales, long long index, float* s) {
-    load4f<DT>((const typename DT::storage*)scales + index, 4, true, s);
+// Rotates each row of 16 lanes so that lanes 0..3 (0..7) receive what lanes
+// N .. N + 3 (N + 7) hold: DPP row_ror by 16 - N.
+template <int N>
+__device__ __forceinline__ uint4 row_down(const uint4& v) {
+    if constexpr (N == 0) {
+        return v;
+    } else {
+        auto one = [](uint32_t d) {
+            return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)d, 0x120 + 16 - N, 0xf, 0xf, false);
+        };
+        return make_uint4(one(v.x), one(v.y), one(v.z), one(v.w));
+    }
 }
 
+// XR: rows an x load brings.  16: lane lr loads row lr, one step per load.
+// With at most XR = 4 (8) rows, one load brings 4 (2) steps, lane lr taking row
+// lr % XR of step lr / XR, and a rotation moves a step's rows to the front
+// (the MFMA's other columns then hold other steps' rows, and are not stored):
+// x then costs a quarter (half) of the loads.
 // FL: steps per scale flush (4-bit): the group is a multiple of 32 FL.
-template <typename DT, typename Src, int MT, int NTW, int FL, bool kGated>
+template <typename DT, typename Src, int XR, int MT, int NTW, int PD, int FL, bool kGated>
 __global__ __launch_bounds__(kRowsThreads) void rows_kernel(RowsArgs a) {
     using T = typename DT::storage;
     using CT = typename CodeType<DT>::type;
     constexpr int NM = kGated ? 2 : 1;
-    constexpr int XP = Src::kXP;
+    constexpr int PK = PieceOps<DT>::kPK;
+    constexpr int XL = Src::kXL, XP = Src::kXP;
+    constexpr int kXLoads = XR == 16 ? 4 * XL : XR / 4;  // x loads per block and row tile
+    static_assert(XR == 16 || (MT == 1 && XL == 1), "packed x loads are for one row tile");
+    constexpr int kFlushes = 4 / FL;
+    constexpr int kMeta = kFlushes * DT::kBytes / 2;  // dwords of a lane's pairs per tile
+    constexpr int kWL = Src::kQ4 ? 1 : 4;      // weight loads per block and n-tile
     __shared__ __attribute__((aligned(16))) float s_part[kRowsWaves][NM * MT * NTW * 256];
 
-    const int tid = threadIdx.x, lane = tid & (kWave - 1), wid = tid / kWave;
+    const int tid = threadIdx.x, lane = tid & (kWave - 1);
+    const int wid = __builtin_amdgcn_readfirstlane(tid / kWave);
     const int lr = lane & 15, lg = lane >> 4;
     const int nt0 = (int)blockIdx.x * NTW;
     const int m0 = (int)blockIdx.y * (16 * MT);
     const int ntiles = (a.N + 15) / 16;
-    const T* x = (const T*)a.x;
 
     acc4_t acc[NM][MT][NTW];
 #pragma unroll
@@ -144,51 +172,117 @@ __global__ __launch_bounds__(kRowsThreads) void rows_kernel(RowsArgs a) {
     const T* xrow[MT];
 #pragma unroll
     for (int i = 0; i < MT; ++i)
-        xrow[i] = x + (long long)min(m0 + 16 * i + lr, a.R - 1) * a.K;
+        xrow[i] = (const T*)a.x + (long long)min(m0 + 16 * i + lr % XR, a.R - 1) * a.K;
+    const char* wbase[NM][NTW];
+    const char* mbase[NM][NTW];
+#pragma unroll
+    for (int q = 0; q < NM; ++q)
+#pragma unroll
+        for (int j = 0; j < NTW; ++j) {
+            if constexpr (Src::kQ4) {
+                const long long nt = min(nt0 + j, ntiles - 1);
+                wbase[q][j] = (const char*)a.m[q].w + nt * a.kblocks * 1024 + lane * 16;
+                mbase[q][j] = (const char*)a.m[q].meta + (nt * a.kblocks * 16 + lr) * (4 * kMeta);
+            } else {
+                wbase[q][j] = (const char*)a.m[q].w +
+                              (long long)min((nt0 + j) * 16 + lr, a.N - 1) * a.K * DT::kBytes;
+                mbase[q][j] = nullptr;
+            }
+        }
 
-    for (int kb = wid; kb < a.kblocks; kb += kRowsWaves) {
+    struct Block {
+        uint4 x[MT][kXLoads];
+        uint4 w[NM][NTW][kWL];
+        uint32_t meta[Src::kQ4 ? NM : 1][NTW][kMeta];
+    };
+    Block blk[PD];
+    // Blocks past the last re-read it (an L2 hit); they are not used.
+    auto load = [&](Block& b, int kb) {
+        kb = min(kb, a.kblocks - 1);
         const int k0 = kb * 4 * Src::kStepK;
+#pragma unroll
+        for (int q = 0; q < NM; ++q)
+#pragma unroll
+            for (int j = 0; j < NTW; ++j) {
+                if constexpr (Src::kQ4) {
+                    b.w[q][j][0] = load16(wbase[q][j] + (long long)kb * 1024);
+                    load_dwords<kMeta>(mbase[q][j] + (long long)kb * (64 * kMeta), b.meta[q][j]);
+                } else {
+#pragma unroll
+                    for (int s = 0; s < 4; ++s)
+                        b.w[q][j][s] = load_piece<DT>((const T*)wbase[q][j],
+                                                      k0 + s * Src::kStepK + PK * lg, a.K, a.wvec);
+                }
+            }
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int s = 0; s < kXLoads; ++s) {
+                if constexpr (XR == 16) {
+                    b.x[i][s] = load_piece<DT>(xrow[i], k0 + (s / XL) * Src::kStepK + XL * PK * lg + PK * (s % XL),
+                                               a.K, a.xvec);
+                } else {
+                    const int step = s * (16 / XR) + lr / XR;
+                    b.x[i][s] = load_piece<DT>(xrow[i], k0 + step * Src::kStepK + PK * lg, a.K, a.xvec);
+                }
+            }
+    };
+    auto compute = [&](const Block& b) {
         uint4 xv[4][MT][XP];
 #pragma unroll
-        for (int s = 0; s < 4; ++s)
+        for (int i = 0; i < MT; ++i) {
+            if constexpr (XR == 4) {
+                xv[0][i][0] = b.x[i][0];
+                xv[1][i][0] = row_down<4>(b.x[i][0]);
+                xv[2][i][0] = row_down<8>(b.x[i][0]);
+                xv[3][i][0] = row_down<12>(b.x[i][0]);
+            } else if constexpr (XR == 8) {
+                xv[0][i][0] = b.x[i][0];
+                xv[1][i][0] = row_down<8>(b.x[i][0]);
+                xv[2][i][0] = b.x[i][1];
+                xv[3][i][0] = row_down<8>(b.x[i][1]);
+            } else {
 #pragma unroll
-            for (int i = 0; i < MT; ++i)
-                load_x_step<DT, Src>(xrow[i], k0 + s * Src::kStepK, lg, a.K, a.xvec, xv[s][i]);
+                for (int s = 0; s < 4; ++s) {
+                    if constexpr (XP == 3) {
+                        float f[8];
+                        F32::unpack(b.x[i][2 * s], f);
+                        F32::unpack(b.x[i][2 * s + 1], f + 4);
+                        split3(f, xv[s][i]);
+                    } else {
+                        xv[s][i][0] = b.x[i][s];
+                    }
+                }
+            }
+        }
         if constexpr (Src::kQ4) {
-            // Sum of x over each flush, in every lane of the row's column: the
-            // codes enter biased by 16, which is taken out with the zero point.
-            acc4_t sx[4 / FL][MT];
+            // Sum of x over each flush, in every column: the codes enter biased
+            // by 16, which is taken out with the zero point.
 #pragma unroll
-            for (int f = 0; f < 4 / FL; ++f)
+            for (int f = 0; f < kFlushes; ++f) {
+                acc4_t sx[MT];
 #pragma unroll
                 for (int i = 0; i < MT; ++i) {
-                    sx[f][i] = acc4_t{0.f, 0.f, 0.f, 0.f};
+                    sx[i] = acc4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                     for (int s = 0; s < FL; ++s)
 #pragma unroll
                         for (int p = 0; p < XP; ++p)
-                            sx[f][i] = PieceOps<CT>::mma(ones_piece<CT>(), xv[f * FL + s][i][p], sx[f][i]);
+                            sx[i] = PieceOps<CT>::mma(xv[f * FL + s][i][p], ones_piece<CT>(), sx[i]);
                 }
 #pragma unroll
-            for (int q = 0; q < NM; ++q)
+                for (int q = 0; q < NM; ++q)
 #pragma unroll
-                for (int j = 0; j < NTW; ++j) {
-                    const int nt = min(nt0 + j, ntiles - 1);
-                    const uint4 wv =
-                        load16((const uint4*)a.m[q].w + ((long long)nt * a.kblocks + kb) * 64 + lane);
-                    const uint32_t wd[4] = {wv.x, wv.y, wv.z, wv.w};
-#pragma unroll
-                    for (int f = 0; f < 4 / FL; ++f) {
-                        const int step = kb * 4 + f * FL;
-                        int g = a.group_steps == 1 ? step : (int)__umulhi((uint32_t)step, a.group_magic);
-                        g = min(g, a.groups - 1);  // the last block may run past K
-                        const long long gi = ((long long)nt * a.groups + g) * 16 + 4 * lg;
-                        float sc[4], zp[4];
-                        load_scales4<DT>(a.m[q].scales, gi, sc);
-                        uint32_t zw = 0x08080808u;
-                        if (a.m[q].zeros) zw = *reinterpret_cast<const uint32_t*>(a.m[q].zeros + gi);
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) zp[e] = kCodeBias + (float)((zw >> (8 * e)) & 255u);
+                    for (int j = 0; j < NTW; ++j) {
+                        const uint4 wv = b.w[q][j][0];
+                        const uint32_t wd[4] = {wv.x, wv.y, wv.z, wv.w};
+                        float sc, zb;
+                        if constexpr (DT::kBytes == 2) {
+                            meta_values<DT>(b.meta[q][j][f], sc, zb);
+                        } else {
+                            sc = __uint_as_float(b.meta[q][j][2 * f]);
+                            zb = __uint_as_float(b.meta[q][j][2 * f + 1]);
+                        }
                         uint4 wp[FL];
 #pragma unroll
                         for (int s = 0; s < FL; ++s) wp[s] = codes_biased<CT>(wd[f * FL + s]);
@@ -199,31 +293,35 @@ __global__ __launch_bounds__(kRowsThreads) void rows_kernel(RowsArgs a) {
                             for (int s = 0; s < FL; ++s)
 #pragma unroll
                                 for (int p = 0; p < XP; ++p)
-                                    t = PieceOps<CT>::mma(wp[s], xv[f * FL + s][i][p], t);
+                                    t = PieceOps<CT>::mma(xv[f * FL + s][i][p], wp[s], t);
 #pragma unroll
                             for (int e = 0; e < 4; ++e)
-                                acc[q][i][j][e] += sc[e] * (t[e] - zp[e] * sx[f][i][e]);
+                                acc[q][i][j][e] += sc * (t[e] - zb * sx[i][e]);
                         }
+                        // One n-tile's products at a time: interleaved freely, their
+                        // partial sums spill.
+                        if constexpr (MT * NTW >= 4) __builtin_amdgcn_sched_barrier(0);
                     }
-                }
+            }
         } else {
 #pragma unroll
             for (int q = 0; q < NM; ++q)
 #pragma unroll
-                for (int j = 0; j < NTW; ++j) {
-                    const T* wrow = (const T*)a.m[q].w +
-                                    (long long)min((nt0 + j) * 16 + lr, a.N - 1) * a.K;
-                    uint4 wp[4];
+                for (int j = 0; j < NTW; ++j)
 #pragma unroll
                     for (int s = 0; s < 4; ++s)
-                        wp[s] = load_piece<DT>(wrow, k0 + s * Src::kStepK + PieceOps<DT>::kPK * lg,
-                                               a.K, a.wvec);
 #pragma unroll
-                    for (int i = 0; i < MT; ++i)
+                        for (int i = 0; i < MT; ++i)
+                            acc[q][i][j] = PieceOps<DT>::mma(xv[s][i][0], b.w[q][j][s], acc[q][i][j]);
+        }
+    };
 #pragma unroll
-                        for (int s = 0; s < 4; ++s)
-                            acc[q][i][j] = PieceOps<DT>::mma(wp[s], xv[s][i][0], acc[q][i][j]);
-                }
+    for (int d = 0; d < PD; ++d) load(blk[d], wid + d * kRowsWaves);
+    for (int kb = wid; kb < a.kblocks; kb += PD * kRowsWaves) {
+#pragma unroll
+        for (int d = 0; d < PD; ++d) {
+            if (kb + d * kRowsWaves < a.kblocks) compute(blk[d]);
+            load(blk[d], kb + (d + PD) * kRowsWaves);
         }
     }
 
@@ -239,46 +337,40 @@ __global__ __launch_bounds__(kRowsThreads) void rows_kernel(RowsArgs a) {
     __syncthreads();
     for (int e = tid; e < MT * NTW * 64; e += kRowsThreads) {
         const int tile = e >> 6, l = e & 63;  // tile = i * NTW + j
-        const int m = m0 + 16 * (tile / NTW) + (l & 15);
-        const int n = (nt0 + tile % NTW) * 16 + 4 * (l >> 4);
-        if (m >= a.R || n >= a.N) continue;
-        float v[NM][4];
+        const int mq = m0 + 16 * (tile / NTW) + 4 * (l >> 4);
+        const int n = (nt0 + tile % NTW) * 16 + (l & 15);
+        if (mq >= a.R || n >= a.N) continue;
+        acc4_t v[NM];
 #pragma unroll
         for (int q = 0; q < NM; ++q) {
-            acc4_t s = acc4_t{0.f, 0.f, 0.f, 0.f};
+            v[q] = acc4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int w = 0; w < kRowsWaves; ++w)
-                s += *reinterpret_cast<const acc4_t*>(&s_part[w][(q * MT * NTW + tile) * 256 + 4 * l]);
-#pragma unroll
-            for (int c = 0; c < 4; ++c) v[q][c] = s[c];
+                v[q] += *reinterpret_cast<const acc4_t*>(&s_part[w][(q * MT * NTW + tile) * 256 + 4 * l]);
         }
-        const long long at = (long long)m * a.N + n;
-        const int left = a.N - n;
-        float o[4];
-        if constexpr (kGated) {
+        float bias = 0.f;
+        if constexpr (!kGated) {
+            if (a.add[0]) bias = DT::load1((const T*)a.add[0] + n);
+        }
 #pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                if (a.add[q]) {
-                    float b[4];
-                    load4f<DT>((const T*)a.add[q] + at, left, a.yvec, b);
+        for (int c = 0; c < 4; ++c) {
+            if (mq + c >= a.R) break;
+            const long long at = (long long)(mq + c) * a.N + n;
+            float o;
+            if constexpr (kGated) {
+                float p[2];
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) v[q][c] += b[c];
+                for (int q = 0; q < 2; ++q) {
+                    p[q] = v[q][c];
+                    if (a.add[q]) p[q] += DT::load1((const T*)a.add[q] + at);
+                    if (a.save[q]) ((T*)a.save[q])[at] = DT::from_float(p[q]);
                 }
-                if (a.save[q]) store4f<DT>((T*)a.save[q] + at, left, a.yvec, v[q]);
+                o = act_value(a.act, p[0]) * p[1];
+            } else {
+                o = v[0][c] + bias;
             }
-#pragma unroll
-            for (int c = 0; c < 4; ++c) o[c] = act_value(a.act, v[0][c]) * v[1][c];
-        } else {
-#pragma unroll
-            for (int c = 0; c < 4; ++c) o[c] = v[0][c];
-            if (a.add[0]) {
-                float b[4];
-                load4f<DT>((const T*)a.add[0] + n, left, a.yvec, b);
-#pragma unroll
-                for (int c = 0; c < 4; ++c) o[c] += b[c];
-            }
+            ((T*)a.y)[at] = DT::from_float(o);
         }
-        store4f<DT>((T*)a.y + at, left, a.yvec, o);
     }
 }
 

@@ -45,8 +45,8 @@ struct TileArgs {
     int batches;
     int tiles_m, tiles_n, tiles;
     int avec, bvec, yvec; // 16-byte pieces of A / B; 4-element pieces of [M, N] arrays
-    int kblocks, group_steps, groups, act;
-    uint32_t group_magic;
+    int kblocks, flushes; // 4-bit: tiles of 128 K; pairs per feature and tile
+    int act;
 };
 
 // Where 16-byte piece p of K row k of an operand kept across K lies in its
@@ -120,23 +120,24 @@ struct StageReader {
 // 16-bit copy of the same weight would carry, and its share of the result's
 // error is below that of the result's own rounding.
 template <typename DT>
-__device__ __forceinline__ uint4 scaled_codes(uint32_t w, float s, float z) {
+__device__ __forceinline__ uint4 scaled_codes(uint32_t w, uint32_t meta) {
+    const uint4 b = codes_biased<DT>(w);
     if constexpr (std::is_same<DT, F16>::value) {
         typedef _Float16 h2_t __attribute__((ext_vector_type(2)));
-        const uint4 b = codes_biased<F16>(w);
-        const h2_t zz = {(_Float16)(kCodeBias + z), (_Float16)(kCodeBias + z)};
-        const h2_t ss = {(_Float16)s, (_Float16)s};
+        const h2_t m = __builtin_bit_cast(h2_t, meta);
+        const h2_t ss = {m.x, m.x}, zz = {m.y, m.y};
         auto one = [&](uint32_t v) {  // (16 + q) - (16 + z) is exact
             return __builtin_bit_cast(uint32_t, (__builtin_bit_cast(h2_t, v) - zz) * ss);
         };
         return make_uint4(one(b.x), one(b.y), one(b.z), one(b.w));
     } else {
-        const float c = -s * (kCodeBias + z);
+        float s, zb;
+        meta_values<BF16>(meta, s, zb);
+        const float c = -s * zb;  // exact: 8 by 8 significant bits
         auto one = [&](uint32_t v) {  // v: two bf16 values 16 + q
             return pack2_rne<BF16>(__builtin_fmaf(__uint_as_float(v << 16), s, c),
                                    __builtin_fmaf(__uint_as_float(v & 0xFFFF0000u), s, c));
         };
-        const uint4 b = codes_biased<BF16>(w);
         return make_uint4(one(b.x), one(b.y), one(b.z), one(b.w));
     }
 }
@@ -196,28 +197,26 @@ __global__ __launch_bounds__(SH::NT) void tile_kernel(TileArgs g) {
     static_assert(BL != kCodes || kUnits * NT == BN * 4, "whole units per thread");
     struct Codes {
         uint4 w;
-        float s[4], z[4];
+        uint32_t meta[4];  // scale and biased zero point of each step
     };
     auto load_codes = [&](int kb, Codes(&c)[kUnits]) {
         if constexpr (BL == kCodes) {
-            const int kbc = min(kb, g.kblocks - 1);
+            kb = min(kb, g.kblocks - 1);
 #pragma unroll
             for (int u = 0; u < kUnits; ++u) {
                 const int unit = tid + u * NT, l = unit & 63;
                 int which = 0;
                 const int row = kGated ? gated_row((unit >> 6) * 16, which) : n0 + (unit >> 6) * 16;
-                const int nt = min(row >> 4, ((N + 15) >> 4) - 1);
+                const long long nt = min(row >> 4, ((N + 15) >> 4) - 1);
                 const ProjWeight& q = g.q[which];
-                c[u].w = load16((const uint4*)q.w + ((long long)nt * g.kblocks + kbc) * 64 + l);
-#pragma unroll
-                for (int s = 0; s < 4; ++s) {
-                    const int step = kbc * 4 + s;
-                    int gr = g.group_steps == 1 ? step : (int)__umulhi((uint32_t)step, g.group_magic);
-                    gr = min(gr, g.groups - 1);
-                    const long long gi = ((long long)nt * g.groups + gr) * 16 + (l & 15);
-                    c[u].s[s] = DT::load1((const T*)q.scales + gi);
-                    c[u].z[s] = q.zeros ? (float)q.zeros[gi] : 8.f;
-                }
+                c[u].w = load16((const uint4*)q.w + (nt * g.kblocks + kb) * 64 + l);
+                const uint32_t* m =
+                    (const uint32_t*)q.meta + ((nt * g.kblocks + kb) * 16 + (l & 15)) * g.flushes;
+                // Step s uses pair s flushes / 4; the last ones repeat.
+                c[u].meta[0] = m[0];
+                c[u].meta[1] = m[g.flushes >> 2];
+                c[u].meta[2] = m[g.flushes >> 1];
+                c[u].meta[3] = m[g.flushes - 1];
             }
         }
     };
@@ -229,7 +228,7 @@ __global__ __launch_bounds__(SH::NT) void tile_kernel(TileArgs g) {
                 const int row = (unit >> 6) * 16 + (l & 15);
                 const uint32_t w = s == 0 ? c[u].w.x : s == 1 ? c[u].w.y : s == 2 ? c[u].w.z : c[u].w.w;
                 store16(st + BM * 64 + row * 64 + (along_piece(row, l >> 4) << 4),
-                        scaled_codes<DT>(w, c[u].s[s], c[u].z[s]));
+                        scaled_codes<DT>(w, c[u].meta[s]));
             }
         }
     };

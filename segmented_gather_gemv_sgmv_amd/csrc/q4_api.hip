@@ -6,14 +6,15 @@ namespace sgmv {
 
 // One thread per packed dword: the eight codes of lane `lane` of tile
 // (nt, kb), step s -- output feature 16 nt + lane % 16, K from 128 kb + 32 s
-// + 8 (lane / 16) on -- and, in the first grid rows, the scales and zero
-// points gathered per n-tile.  Codes past N or K are 0.
+// + 8 (lane / 16) on -- and, in the first threads, the pairs of scale and
+// biased zero point 16 + z (exact in every type) that go with the tiles
+// (ProjWeight).  Codes past N or K are 0.
 template <typename DT>
 __global__ __launch_bounds__(256) void q4_pack_kernel(
-    uint32_t* __restrict__ tiles, typename DT::storage* __restrict__ pscales,
-    uint8_t* __restrict__ pzeros, const uint8_t* __restrict__ codes,
-    const typename DT::storage* __restrict__ scales, const uint8_t* __restrict__ zeros, int N, int K,
-    int kblocks, int groups, long long dwords, long long metas) {
+    uint32_t* __restrict__ tiles, typename DT::storage* __restrict__ meta,
+    const uint8_t* __restrict__ codes, const typename DT::storage* __restrict__ scales,
+    const uint8_t* __restrict__ zeros, int N, int K, int kblocks, int groups, int group,
+    int flushes, long long dwords, long long metas) {
     const long long t = (long long)blockIdx.x * 256 + threadIdx.x;
     if (t < dwords) {
         const int s = (int)(t & 3), lane = (int)(t >> 2) & 63;
@@ -35,15 +36,18 @@ __global__ __launch_bounds__(256) void q4_pack_kernel(
         }
         tiles[t] = w;
     }
-    if (t < metas) {  // [N / 16][groups][16]
-        const long long row = t >> 4;
-        const long long nt = row / groups;
-        const int g = (int)(row - nt * groups);
-        const long long n = nt * 16 + (t & 15);
-        typename DT::storage sc = 0;
-        if (n < N) sc = scales[n * groups + g];
-        pscales[t] = sc;
-        if (pzeros) pzeros[t] = n < N ? (uint8_t)(zeros[n * groups + g] & 15u) : (uint8_t)0;
+    if (t < metas) {  // [N / 16][kblocks][16][flushes]
+        const long long cell = t / (16 * flushes);
+        const int in_cell = (int)(t - cell * 16 * flushes);
+        const long long nt = cell / kblocks;
+        const int kb = (int)(cell - nt * kblocks);
+        const long long n = nt * 16 + in_cell / flushes;
+        const int k = kb * 128 + in_cell % flushes * (128 / flushes);
+        const bool in = n < N && k < K;
+        const long long at = n * groups + k / group;
+        const int z = in && zeros ? zeros[at] & 15 : 8;
+        meta[2 * t] = in ? scales[at] : DT::from_float(0.f);
+        meta[2 * t + 1] = DT::from_float(kCodeBias + (float)z);
     }
 }
 
@@ -66,93 +70,106 @@ int check_q4(int N, int K, int group, int dtype) {
 }
 
 struct Q4Geometry {
-    int kblocks, groups, group_steps;
-    uint32_t magic;
     long long ntiles;
+    int kblocks, groups;
+    int flushes;  // scale pairs per feature and tile of 128 K
 };
 Q4Geometry geometry(int N, int K, int group) {
     Q4Geometry q;
-    q.kblocks = (int)ceil_div(K, 128);
-    // A group longer than the row is the row.
-    const int g = (int)std::min<long long>(group, ceil_div(K, 32) * 32);
-    q.groups = (int)ceil_div(K, g);
-    q.group_steps = g / 32;
-    q.magic = (uint32_t)(((1ull << 32) + q.group_steps - 1) / q.group_steps);
     q.ntiles = ceil_div(N, 16);
+    q.kblocks = (int)ceil_div(K, 128);
+    q.groups = (int)ceil_div(K, group);
+    q.flushes = group % 128 == 0 || group >= K ? 1 : group % 64 == 0 ? 2 : 4;
     return q;
 }
 
-template <typename DT, int MT, int FL, bool kGated>
+// A rows kernel of 16 MT rows and 16 NTW features per workgroup, PD blocks of
+// K ahead; XR as in rows_kernel.
+template <typename DT, int XR, int MT, int NTW, int PD, int FL, bool kGated>
 int run_rows(const RowsArgs& a, hipStream_t st) {
-    const long long gx = ceil_div(a.N, 16), gy = ceil_div(a.R, 16 * MT);
+    const long long gx = ceil_div(a.N, 16 * NTW), gy = ceil_div(a.R, 16 * MT);
     if (gy > 65535) return SGMV_ERR_UNSUPPORTED;
-    launch(&rows_kernel<DT, Q4Src<DT>, MT, 1, FL, kGated>, dim3((unsigned)gx, (unsigned)gy),
+    launch(&rows_kernel<DT, Q4Src<DT>, XR, MT, NTW, PD, FL, kGated>, dim3((unsigned)gx, (unsigned)gy),
            dim3(kRowsThreads), st, a);
     return launch_status();
 }
 
-template <typename DT, bool kGated>
-int run_rows_any(const RowsArgs& a, hipStream_t st) {
-    auto with_rows = [&](auto fl) {
-        constexpr int FL = decltype(fl)::value;
-        if (a.R <= 16) return run_rows<DT, 1, FL, kGated>(a, st);
-        if (a.R <= 32) return run_rows<DT, 2, FL, kGated>(a, st);
-        return run_rows<DT, 4, FL, kGated>(a, st);
-    };
-    if (a.group_steps % 4 == 0) return with_rows(std::integral_constant<int, 4>{});
-    if (a.group_steps % 2 == 0) return with_rows(std::integral_constant<int, 2>{});
-    return with_rows(std::integral_constant<int, 1>{});
+template <typename DT, int FL, bool kGated>
+int run_rows_fl(const RowsArgs& a, hipStream_t st) {
+    if constexpr (DT::kBytes == 4) {
+        if (a.R <= 16) return run_rows<DT, 16, 1, 1, 2, FL, kGated>(a, st);
+        return run_rows<DT, 16, 2, 1, 1, FL, kGated>(a, st);
+    } else {
+        // Two n-tiles per workgroup once that still gives every CU one.
+        const bool two = ceil_div(a.N, 16) >= 512;
+        if (a.R <= 4)
+            return two ? run_rows<DT, 4, 1, 2, 3, FL, kGated>(a, st)
+                       : run_rows<DT, 4, 1, 1, 4, FL, kGated>(a, st);
+        if (a.R <= 16)
+            return two ? run_rows<DT, 16, 1, 2, 2, FL, kGated>(a, st)
+                       : run_rows<DT, 16, 1, 1, 3, FL, kGated>(a, st);
+        if (a.R <= 32)
+            return two ? run_rows<DT, 16, 2, kGated ? 2 : 4, 1, FL, kGated>(a, st)
+                       : run_rows<DT, 16, 2, 1, 2, FL, kGated>(a, st);
+        return two ? run_rows<DT, 16, 4, kGated ? 2 : 4, 1, FL, kGated>(a, st)
+                   : run_rows<DT, 16, 4, 1, 1, FL, kGated>(a, st);
+    }
 }
 
 template <typename DT, bool kGated>
-int run_q4(const RowsArgs& a, hipStream_t st) {
+int run_rows_any(const RowsArgs& a, int flushes, hipStream_t st) {
+    if (flushes == 1) return run_rows_fl<DT, 4, kGated>(a, st);
+    if (flushes == 2) return run_rows_fl<DT, 2, kGated>(a, st);
+    return run_rows_fl<DT, 1, kGated>(a, st);
+}
+
+template <typename DT, bool kGated>
+int run_q4(const RowsArgs& a, int flushes, hipStream_t st) {
     if constexpr (DT::kBytes == 2) {
         if (a.R > kQ4RowsMax) {
             TileArgs t{};
             t.a[0] = a.x;
             t.lda = a.K;
-            t.q[0] = a.m[0];
-            t.q[1] = a.m[1];
             t.out[0] = a.y;
-            t.add[0] = a.add[0];
-            t.add[1] = a.add[1];
+            bool yvec = a.N % 4 == 0 && aligned16(a.y);
+            for (int q = 0; q < 2; ++q) {
+                t.q[q] = a.m[q];
+                t.add[q] = a.add[q];
+                yvec = yvec && aligned16(a.add[q]);
+            }
             t.M = a.R;
             t.N = a.N;
             t.K = a.K;
             t.batches = 1;
             t.avec = a.xvec;
-            t.yvec = a.yvec;
+            t.yvec = yvec;
             t.kblocks = a.kblocks;
-            t.group_steps = a.group_steps;
-            t.group_magic = a.group_magic;
-            t.groups = a.groups;
+            t.flushes = flushes;
             t.act = a.act;
             return launch_tiles_any<DT, kAlongK, kCodes, 1, kGated>(t, a.xvec != 0, st);
         }
     }
-    return run_rows_any<DT, kGated>(a, st);
+    return run_rows_any<DT, kGated>(a, flushes, st);
 }
 
 template <bool kGated>
-int run_q4_dtype(const RowsArgs& a, int dtype, hipStream_t st) {
-    if (dtype == SGMV_F32) return run_q4<F32, kGated>(a, st);
-    if (dtype == SGMV_F16) return run_q4<F16, kGated>(a, st);
-    return run_q4<BF16, kGated>(a, st);
+int run_q4_dtype(const RowsArgs& a, int group, int dtype, hipStream_t st) {
+    const int flushes = geometry(a.N, a.K, group).flushes;
+    if (dtype == SGMV_F32) return run_q4<F32, kGated>(a, flushes, st);
+    if (dtype == SGMV_F16) return run_q4<F16, kGated>(a, flushes, st);
+    return run_q4<BF16, kGated>(a, flushes, st);
 }
 
-void fill_common(RowsArgs& a, void* y, const void* x, int R, int N, int K, int group, int dtype) {
-    const Q4Geometry q = geometry(N, K, group);
+RowsArgs rows_args(void* y, const void* x, int R, int N, int K, int dtype) {
+    RowsArgs a{};
     a.y = y;
     a.x = x;
     a.R = R;
     a.N = N;
     a.K = K;
-    a.kblocks = q.kblocks;
-    a.group_steps = q.group_steps;
-    a.group_magic = q.magic;
-    a.groups = q.groups;
+    a.kblocks = (int)ceil_div(K, 128);
     a.xvec = aligned16(x) && K % piece_elems(dtype) == 0;
-    a.yvec = aligned16(y) && N % 4 == 0;
+    return a;
 }
 
 }  // namespace
@@ -164,29 +181,33 @@ size_t q4_tiles_bytes(int32_t out_features, int32_t in_features) {
     return (size_t)ceil_div(out_features, 16) * (size_t)ceil_div(in_features, 128) * 1024u;
 }
 
-size_t q4_groups_padded(int32_t out_features, int32_t in_features, int32_t group_size) {
-    if (out_features < 1 || in_features < 1 || group_size < 32 || group_size % 32 != 0) return 0;
-    return (size_t)ceil_div(out_features, 16) * 16u * (size_t)ceil_div(in_features, group_size);
+size_t q4_meta_bytes(int32_t out_features, int32_t in_features, int32_t group_size,
+                     int32_t dtype) {
+    if (out_features < 1 || in_features < 1 || group_size < 32 || group_size % 32 != 0 ||
+        !known_dtype(dtype))
+        return 0;
+    const Q4Geometry q = geometry(out_features, in_features, group_size);
+    return (size_t)q.ntiles * (size_t)q.kblocks * 16u * (size_t)q.flushes * 2u *
+           (size_t)elem_size(dtype);
 }
 
-int q4_pack(void* tiles, void* packed_scales, uint8_t* packed_zeros, const uint8_t* codes,
-            const void* scales, const uint8_t* zeros, int32_t out_features, int32_t in_features,
-            int32_t group_size, int32_t dtype, void* stream) {
+int q4_pack(void* tiles, void* meta, const uint8_t* codes, const void* scales,
+            const uint8_t* zeros, int32_t out_features, int32_t in_features, int32_t group_size,
+            int32_t dtype, void* stream) {
     const int rc = check_q4(out_features, in_features, group_size, dtype);
     if (rc != SGMV_OK) return rc;
-    if (!tiles || !packed_scales || !codes || !scales || (zeros && !packed_zeros))
-        return SGMV_ERR_NULL_PTR;
-    if (!zeros) packed_zeros = nullptr;
+    if (!tiles || !meta || !codes || !scales) return SGMV_ERR_NULL_PTR;
     const Q4Geometry q = geometry(out_features, in_features, group_size);
-    const long long dwords = q.ntiles * q.kblocks * 256, metas = q.ntiles * 16 * q.groups;
+    const long long dwords = q.ntiles * q.kblocks * 256, metas = q.ntiles * q.kblocks * 16 * q.flushes;
     const long long blocks = ceil_div(std::max(dwords, metas), 256);
     if (blocks > 0x7FFFFFFFll) return SGMV_ERR_UNSUPPORTED;
     auto run = [&](auto dt) {
         using DT = decltype(dt);
         using T = typename DT::storage;
         launch(&q4_pack_kernel<DT>, dim3((unsigned)blocks), dim3(256), (hipStream_t)stream,
-               (uint32_t*)tiles, (T*)packed_scales, packed_zeros, codes, (const T*)scales, zeros,
-               (int)out_features, (int)in_features, q.kblocks, q.groups, dwords, metas);
+               (uint32_t*)tiles, (T*)meta, codes, (const T*)scales, zeros,
+               (int)out_features, (int)in_features, q.kblocks, q.groups, (int)group_size,
+               q.flushes, dwords, metas);
     };
     if (dtype == SGMV_F32) run(F32{});
     else if (dtype == SGMV_F16) run(F16{});
@@ -201,14 +222,12 @@ int q4_linear(void* y, const void* x, const sgmv_q4_weight* w, const void* bias,
     if (rc != SGMV_OK) return rc;
     if (num_rows < 0) return SGMV_ERR_BAD_SHAPE;
     if (num_rows == 0) return SGMV_OK;
-    if (!y || !x || !w || !w->tiles || !w->scales) return SGMV_ERR_NULL_PTR;
-    if (!aligned16(w->tiles) || !aligned16(w->scales)) return SGMV_ERR_UNSUPPORTED;
-    RowsArgs a{};
-    fill_common(a, y, x, num_rows, out_features, in_features, group_size, dtype);
-    a.m[0] = ProjWeight{w->tiles, w->scales, w->zeros};
+    if (!y || !x || !w || !w->tiles || !w->meta) return SGMV_ERR_NULL_PTR;
+    if (!aligned16(w->tiles) || !aligned16(w->meta)) return SGMV_ERR_UNSUPPORTED;
+    RowsArgs a = rows_args(y, x, num_rows, out_features, in_features, dtype);
+    a.m[0] = ProjWeight{w->tiles, w->meta};
     a.add[0] = bias;
-    a.yvec = a.yvec && aligned16(bias);
-    return run_q4_dtype<false>(a, dtype, (hipStream_t)stream);
+    return run_q4_dtype<false>(a, group_size, dtype, (hipStream_t)stream);
 }
 
 int q4_gated_ffn(void* h, const void* x, const sgmv_q4_weight* gate, const sgmv_q4_weight* up,
@@ -218,20 +237,18 @@ int q4_gated_ffn(void* h, const void* x, const sgmv_q4_weight* gate, const sgmv_
     if (rc != SGMV_OK) return rc;
     if (num_rows < 0 || !known_act(act)) return SGMV_ERR_BAD_SHAPE;
     if (num_rows == 0) return SGMV_OK;
-    if (!h || !x || !gate || !up || !gate->tiles || !gate->scales || !up->tiles || !up->scales)
+    if (!h || !x || !gate || !up || !gate->tiles || !gate->meta || !up->tiles || !up->meta)
         return SGMV_ERR_NULL_PTR;
-    if (!aligned16(gate->tiles) || !aligned16(gate->scales) || !aligned16(up->tiles) ||
-        !aligned16(up->scales))
+    if (!aligned16(gate->tiles) || !aligned16(gate->meta) || !aligned16(up->tiles) ||
+        !aligned16(up->meta))
         return SGMV_ERR_UNSUPPORTED;
-    RowsArgs a{};
-    fill_common(a, h, x, num_rows, out_features, in_features, group_size, dtype);
-    a.m[0] = ProjWeight{gate->tiles, gate->scales, gate->zeros};
-    a.m[1] = ProjWeight{up->tiles, up->scales, up->zeros};
+    RowsArgs a = rows_args(h, x, num_rows, out_features, in_features, dtype);
+    a.m[0] = ProjWeight{gate->tiles, gate->meta};
+    a.m[1] = ProjWeight{up->tiles, up->meta};
     a.add[0] = gate_add;
     a.add[1] = up_add;
     a.act = act;
-    a.yvec = a.yvec && aligned16(gate_add) && aligned16(up_add);
-    return run_q4_dtype<true>(a, dtype, (hipStream_t)stream);
+    return run_q4_dtype<true>(a, group_size, dtype, (hipStream_t)stream);
 }
 
 }  // extern "C"

@@ -18,24 +18,19 @@ from .gated import _act_code, _addends, _output
 
 class _CWeight(ctypes.Structure):
     """sgmv_q4_weight of sgmv.h."""
-    _fields_ = [("tiles", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("zeros", ctypes.c_void_p)]
+    _fields_ = [("tiles", ctypes.c_void_p), ("meta", ctypes.c_void_p)]
 
 
 class Q4Weight:
     """A weight laid out by q4_pack: device arrays and the sizes they were
     made for.  Its dtype is that of the activations it multiplies."""
 
-    def __init__(self, tiles, scales, zeros, out_features, in_features, group_size):
-        self.tiles, self.scales, self.zeros = tiles, scales, zeros
+    def __init__(self, tiles, meta, dtype, out_features, in_features, group_size):
+        self.tiles, self.meta, self.dtype = tiles, meta, dtype
         self.out_features, self.in_features = out_features, in_features
         self.group_size = group_size
-        self._c = _CWeight(tiles.data_ptr(), scales.data_ptr(),
-                           None if zeros is None else zeros.data_ptr())
+        self._c = _CWeight(tiles.data_ptr(), meta.data_ptr())
         self._ptr = ctypes.addressof(self._c)
-
-    @property
-    def dtype(self):
-        return self.scales.dtype
 
     @property
     def device(self):
@@ -71,14 +66,11 @@ def q4_pack(codes, scales, zeros=None, group_size: int = 128, in_features: int =
     if N < 1:
         raise ValueError("a weight needs at least one output feature")
     tiles = torch.empty(lib().q4_tiles_bytes(N, K), dtype=torch.uint8, device=dev)
-    padded = lib().q4_groups_padded(N, K, G)
-    pscales = torch.empty(padded, dtype=scales.dtype, device=dev)
-    pzeros = None if zeros is None else torch.empty(padded, dtype=torch.uint8, device=dev)
-    _check(lib().q4_pack(tiles.data_ptr(), pscales.data_ptr(),
-                         None if pzeros is None else pzeros.data_ptr(), codes.data_ptr(),
-                         scales.data_ptr(), None if zeros is None else zeros.data_ptr(), N, K, G, dt,
+    meta = torch.empty(lib().q4_meta_bytes(N, K, G, dt), dtype=torch.uint8, device=dev)
+    _check(lib().q4_pack(tiles.data_ptr(), meta.data_ptr(), codes.data_ptr(), scales.data_ptr(),
+                         None if zeros is None else zeros.data_ptr(), N, K, G, dt,
                          _stream_ptr(dev)), "q4_pack")
-    return Q4Weight(tiles, pscales, pzeros, N, K, G)
+    return Q4Weight(tiles, meta, scales.dtype, N, K, G)
 
 
 def _check_weight(w, x, name):

@@ -20,7 +20,7 @@ def lib():
 
 def _weight(**kw):
     from segmented_gather_gemv_sgmv_amd.q4 import _CWeight
-    return _CWeight(kw.get("tiles", FAKE), kw.get("scales", FAKE), kw.get("zeros", None))
+    return _CWeight(kw.get("tiles", FAKE), kw.get("meta", FAKE))
 
 
 def _q4(lib, **kw):
@@ -39,7 +39,7 @@ def test_q4_linear_checks(lib):
     assert _q4(lib, K=(1 << 20) + 1) == 4
     assert _q4(lib, R=0, x=None, y=None, w=None) == 0
     for bad in (dict(y=None), dict(x=None), dict(w=None), dict(w=_weight(tiles=None)),
-                dict(w=_weight(scales=None))):
+                dict(w=_weight(meta=None))):
         assert _q4(lib, **bad) == 1, bad
     assert _q4(lib, w=_weight(tiles=FAKE + 4)) == 4
 
@@ -52,12 +52,13 @@ def test_q4_gated_and_pack_checks(lib):
                                                            64, act, dt, None)
     assert call(act=5) == 2 and call(act=-1) == 2 and call(dt=7) == 3
     assert call(g=None) == 1 and call(h=None) == 1
-    pack = lambda tiles=FAKE, zeros=None, pz=None, G=64: lib.q4_pack(
-        tiles, FAKE, pz, FAKE, FAKE, zeros, 64, 128, G, 1, None)
-    assert pack(tiles=None) == 1 and pack(zeros=FAKE) == 1 and pack(G=40) == 2
+    pack = lambda tiles=FAKE, meta=FAKE, G=64: lib.q4_pack(
+        tiles, meta, FAKE, FAKE, None, 64, 128, G, 1, None)
+    assert pack(tiles=None) == 1 and pack(meta=None) == 1 and pack(G=40) == 2
     assert lib.q4_tiles_bytes(17, 129) == 2 * 2 * 1024
-    assert lib.q4_groups_padded(17, 129, 64) == 32 * 3
-    assert lib.q4_tiles_bytes(0, 5) == 0 and lib.q4_groups_padded(4, 4, 31) == 0
+    assert lib.q4_meta_bytes(17, 129, 64, 1) == 2 * 2 * 16 * 2 * 4
+    assert lib.q4_meta_bytes(17, 129, 64, 0) == 2 * 2 * 16 * 2 * 8
+    assert lib.q4_tiles_bytes(0, 5) == 0 and lib.q4_meta_bytes(4, 4, 31, 1) == 0
 
 
 def test_gated_checks(lib):
