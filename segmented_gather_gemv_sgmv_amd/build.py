@@ -17,8 +17,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIBRARY = os.path.join(PKG, "libsgmv.so")
-SOURCES = [os.path.join(CSRC, f) for f in ("sgmv_api.hip", "q4_api.hip", "ffn_api.hip",
-                                           "rope_api.hip")]
+SOURCES = [os.path.join(CSRC, f) for f in ("sgmv_api.hip", "q4_api.hip", "q4_f32.hip", "q4_f16.hip",
+                                           "q4_bf16.hip", "ffn_api.hip", "rope_api.hip")]
 OBJECTS = os.path.join(PKG, "_build")
 ARCH = "gfx950"
 

@@ -26,6 +26,9 @@ int run_rows(const RowsArgs& a, hipStream_t st) {
 template <typename DT>
 int run_forward(const RowsArgs& a, hipStream_t st) {
     if (a.R <= kFfnRowsMax) {
+        if constexpr (DT::kBytes == 2) {
+            if (a.R > 4 && a.xvec && a.wvec) return run_strip<DT, PlainSrc<DT>, 1, true>(a, st);
+        }
         if (a.R <= 4) return run_rows<DT, 4, 1, 1, 2>(a, st);
         if (a.R <= 16) return run_rows<DT, 16, 1, 1, 2>(a, st);
         if (a.R <= 32) return run_rows<DT, 16, 2, 1, 2>(a, st);

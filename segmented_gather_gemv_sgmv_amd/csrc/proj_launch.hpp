@@ -2,6 +2,7 @@
 // kernels, shared by the 4-bit and the gated entry points.
 #pragma once
 
+#include "proj_strip.hpp"
 #include "proj_tile.hpp"
 #include "sgmv_host.hpp"
 
@@ -39,6 +40,41 @@ int launch_tiles_any(const TileArgs& a, bool direct, hipStream_t st) {
     const long long big = ceil_div(a.M, 256) * ceil_div(a.N, kGated ? 128 : 256) * a.batches;
     if (big >= 192) return launch_tiles<DT, BigTile, AL, BL, kSegs, kGated, true>(a, st);
     return launch_tiles<DT, MidTile, AL, BL, kSegs, kGated, true>(a, st);
+}
+
+template <typename DT, typename Src, int MT, int NTW, int KG, int NG, int S, int FL, bool kGated>
+int launch_strip(const RowsArgs& a, hipStream_t st) {
+    const long long gx = ceil_div(a.N, 16 * NTW * NG), gy = ceil_div(a.R, 16 * MT);
+    if (gy > 65535) return SGMV_ERR_UNSUPPORTED;
+    launch(&strip_kernel<DT, Src, MT, NTW, KG, NG, S, FL, kGated>, dim3((unsigned)gx, (unsigned)gy),
+           dim3(kRowsThreads), st, a);
+    return launch_status();
+}
+
+// The largest block of rows and features that still gives about three of four
+// CUs a workgroup.  Larger blocks read x and unpack weights less often; below
+// that many workgroups the idle CUs cost more (5120 -> 13824, 4-bit, bf16, 64
+// rows: 24.5 us on 432 workgroups of 32 x 64, 32.9 us on 108 of 64 x 128; 128
+// rows: 43.7 and 34.7 us).  S = 3 stages where a block's products are too few
+// to cover one x load (16 rows: 13.2 -> 12.2 us), two otherwise.
+template <typename DT, typename Src, int FL, bool kGated>
+int run_strip(const RowsArgs& a, hipStream_t st) {
+    // A gated wave holds both matrices' n-tiles: half as many features each.
+    constexpr int T = kGated ? 1 : 2;
+    auto fills = [&](int rows, int features) {
+        return ceil_div(a.R, rows) * ceil_div(a.N, features) >= 190;
+    };
+    if (a.R > 32) {
+        if (fills(64, 128 * T)) return launch_strip<DT, Src, 4, T, 1, 8, 2, FL, kGated>(a, st);
+        if (fills(64, 64 * T)) return launch_strip<DT, Src, 4, T, 2, 4, 2, FL, kGated>(a, st);
+    }
+    if (a.R > 16) {
+        if (!kGated && fills(32, 64)) return launch_strip<DT, Src, 2, T, 4, 2, 2, FL, kGated>(a, st);
+        if (fills(32, 32)) return launch_strip<DT, Src, 2, 1, 4, 2, 2, FL, kGated>(a, st);
+    }
+    if (!kGated && fills(16, 64)) return launch_strip<DT, Src, 1, T, 4, 2, 3, FL, kGated>(a, st);
+    if (fills(16, 32)) return launch_strip<DT, Src, 1, 1, 4, 2, 3, FL, kGated>(a, st);
+    return launch_strip<DT, Src, 1, 1, 8, 1, 3, FL, kGated>(a, st);
 }
 
 inline int elem_size(int dtype) { return dtype == SGMV_F32 ? 4 : 2; }

@@ -1,6 +1,6 @@
 // q4_api.hip -- C ABI of the 4-bit projections (declared in include/sgmv.h):
 // the one-time packing of a weight, argument checks and kernel choice.
-#include "proj_launch.hpp"
+#include "q4_run.hpp"
 
 namespace sgmv {
 
@@ -57,11 +57,6 @@ namespace {
 
 using namespace sgmv;
 
-// Rows up to which the rows kernel is taken (16-bit types; float32 has no
-// other): beyond, re-reading and unpacking the weight once per 64 rows costs
-// more than the tiles' fill and drain.
-constexpr int kQ4RowsMax = 256;
-
 int check_q4(int N, int K, int group, int dtype) {
     if (!known_dtype(dtype)) return SGMV_ERR_BAD_DTYPE;
     if (N < 1 || K < 1 || group < 32 || group % 32 != 0) return SGMV_ERR_BAD_SHAPE;
@@ -81,75 +76,6 @@ Q4Geometry geometry(int N, int K, int group) {
     q.groups = (int)ceil_div(K, group);
     q.flushes = group % 128 == 0 || group >= K ? 1 : group % 64 == 0 ? 2 : 4;
     return q;
-}
-
-// A rows kernel of 16 MT rows and 16 NTW features per workgroup, PD blocks of
-// K ahead; XR as in rows_kernel.
-template <typename DT, int XR, int MT, int NTW, int PD, int FL, bool kGated>
-int run_rows(const RowsArgs& a, hipStream_t st) {
-    const long long gx = ceil_div(a.N, 16 * NTW), gy = ceil_div(a.R, 16 * MT);
-    if (gy > 65535) return SGMV_ERR_UNSUPPORTED;
-    launch(&rows_kernel<DT, Q4Src<DT>, XR, MT, NTW, PD, FL, kGated>, dim3((unsigned)gx, (unsigned)gy),
-           dim3(kRowsThreads), st, a);
-    return launch_status();
-}
-
-template <typename DT, int FL, bool kGated>
-int run_rows_fl(const RowsArgs& a, hipStream_t st) {
-    if constexpr (DT::kBytes == 4) {
-        if (a.R <= 16) return run_rows<DT, 16, 1, 1, 2, FL, kGated>(a, st);
-        return run_rows<DT, 16, 2, 1, 1, FL, kGated>(a, st);
-    } else {
-        // Two n-tiles per workgroup once that still gives every CU one.
-        const bool two = ceil_div(a.N, 16) >= 512;
-        if (a.R <= 4)
-            return two ? run_rows<DT, 4, 1, 2, 3, FL, kGated>(a, st)
-                       : run_rows<DT, 4, 1, 1, 4, FL, kGated>(a, st);
-        if (a.R <= 16)
-            return two ? run_rows<DT, 16, 1, 2, 2, FL, kGated>(a, st)
-                       : run_rows<DT, 16, 1, 1, 3, FL, kGated>(a, st);
-        if (a.R <= 32)
-            return two ? run_rows<DT, 16, 2, kGated ? 2 : 4, 1, FL, kGated>(a, st)
-                       : run_rows<DT, 16, 2, 1, 2, FL, kGated>(a, st);
-        return two ? run_rows<DT, 16, 4, kGated ? 2 : 4, 1, FL, kGated>(a, st)
-                   : run_rows<DT, 16, 4, 1, 1, FL, kGated>(a, st);
-    }
-}
-
-template <typename DT, bool kGated>
-int run_rows_any(const RowsArgs& a, int flushes, hipStream_t st) {
-    if (flushes == 1) return run_rows_fl<DT, 4, kGated>(a, st);
-    if (flushes == 2) return run_rows_fl<DT, 2, kGated>(a, st);
-    return run_rows_fl<DT, 1, kGated>(a, st);
-}
-
-template <typename DT, bool kGated>
-int run_q4(const RowsArgs& a, int flushes, hipStream_t st) {
-    if constexpr (DT::kBytes == 2) {
-        if (a.R > kQ4RowsMax) {
-            TileArgs t{};
-            t.a[0] = a.x;
-            t.lda = a.K;
-            t.out[0] = a.y;
-            bool yvec = a.N % 4 == 0 && aligned16(a.y);
-            for (int q = 0; q < 2; ++q) {
-                t.q[q] = a.m[q];
-                t.add[q] = a.add[q];
-                yvec = yvec && aligned16(a.add[q]);
-            }
-            t.M = a.R;
-            t.N = a.N;
-            t.K = a.K;
-            t.batches = 1;
-            t.avec = a.xvec;
-            t.yvec = yvec;
-            t.kblocks = a.kblocks;
-            t.flushes = flushes;
-            t.act = a.act;
-            return launch_tiles_any<DT, kAlongK, kCodes, 1, kGated>(t, a.xvec != 0, st);
-        }
-    }
-    return run_rows_any<DT, kGated>(a, flushes, st);
 }
 
 template <bool kGated>
