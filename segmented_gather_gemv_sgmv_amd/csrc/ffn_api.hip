@@ -15,10 +15,10 @@ int check_ffn(int R, int H, int I, int act, int dtype) {
     return SGMV_OK;
 }
 
-template <typename DT, int XR, int MT, int NTW, int PD>
+template <typename DT, int XR, int MT, int PD>
 int run_rows(const RowsArgs& a, hipStream_t st) {
-    launch(&rows_kernel<DT, PlainSrc<DT>, XR, MT, NTW, PD, 1, true>,
-           dim3((unsigned)ceil_div(a.N, 16 * NTW), (unsigned)ceil_div(a.R, 16 * MT)),
+    launch(&rows_kernel<DT, PlainSrc<DT>, XR, MT, 1, PD, 1, true>,
+           dim3((unsigned)ceil_div(a.N, 16), (unsigned)ceil_div(a.R, 16 * MT)),
            dim3(kRowsThreads), st, a);
     return launch_status();
 }
@@ -26,13 +26,22 @@ int run_rows(const RowsArgs& a, hipStream_t st) {
 template <typename DT>
 int run_forward(const RowsArgs& a, hipStream_t st) {
     if (a.R <= kFfnRowsMax) {
+        if (a.R <= 4) return run_rows<DT, 4, 1, 2>(a, st);
+        if (a.R <= 16) return run_rows<DT, 16, 1, 2>(a, st);
         if constexpr (DT::kBytes == 2) {
-            if (a.R > 4 && a.xvec && a.wvec) return run_strip<DT, PlainSrc<DT>, 1, true>(a, st);
+            // From 17 rows on x goes through LDS; more features per workgroup
+            // while that still fills the chip.
+            if (a.xvec && a.wvec) {
+                using Src = PlainSrc<DT>;
+                const bool wide = ceil_div(a.N, 64) >= 128;
+                if (a.R <= 32)
+                    return wide ? launch_strip<DT, Src, 2, 1, 2, 4, 2, 1, true>(a, st)
+                                : launch_strip<DT, Src, 2, 1, 4, 2, 2, 1, true>(a, st);
+                return wide ? launch_strip<DT, Src, 4, 1, 2, 4, 2, 1, true>(a, st)
+                            : launch_strip<DT, Src, 4, 1, 4, 2, 2, 1, true>(a, st);
+            }
         }
-        if (a.R <= 4) return run_rows<DT, 4, 1, 1, 2>(a, st);
-        if (a.R <= 16) return run_rows<DT, 16, 1, 1, 2>(a, st);
-        if (a.R <= 32) return run_rows<DT, 16, 2, 1, 2>(a, st);
-        return run_rows<DT, 16, 4, 1, 1>(a, st);
+        return run_rows<DT, 16, 2, 1>(a, st);
     }
     TileArgs t{};
     t.a[0] = a.x;

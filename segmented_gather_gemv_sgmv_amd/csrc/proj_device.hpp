@@ -51,6 +51,9 @@ struct PieceOps<F32> {
     }
 };
 
+// What lanes past the end of K read in direct global-to-LDS loads.
+__device__ const uint4 g_zero_piece = {0, 0, 0, 0};
+
 __device__ __forceinline__ uint2 load_pair(const void* p) {
     return *reinterpret_cast<const uint2*>(p);
 }

@@ -17,7 +17,7 @@ inline long long ceil_div(long long a, long long b) { return (a + b - 1) / b; }
 
 // Sets the tile grid of `a` for output width `width` (both matrices' columns
 // for a gated call) and launches.
-template <typename DT, typename SH, int AL, int BL, int kSegs, bool kGated, bool kDma>
+template <typename DT, typename SH, int AL, int BL, int kSegs, bool kGated, bool kDma, int kFlushes>
 int launch_tiles(TileArgs a, hipStream_t st) {
     const long long tm = ceil_div(a.M, SH::BM);
     const long long tn = ceil_div(a.N, kGated ? SH::BN / 2 : SH::BN);
@@ -27,19 +27,19 @@ int launch_tiles(TileArgs a, hipStream_t st) {
     a.tiles_m = (int)tm;
     a.tiles_n = (int)tn;
     a.tiles = (int)tiles;
-    launch(&tile_kernel<DT, SH, AL, BL, kSegs, kGated, kDma>, dim3((unsigned)tiles), dim3(SH::NT), st,
-           a);
+    launch(&tile_kernel<DT, SH, AL, BL, kSegs, kGated, kDma, kFlushes>, dim3((unsigned)tiles),
+           dim3(SH::NT), st, a);
     return launch_status();
 }
 
 // 256 x 256 tiles once they make a tile per CU, 128 x 128 below that; the
 // register path (operands no 16-byte load fits) always takes the small ones.
-template <typename DT, int AL, int BL, int kSegs, bool kGated>
+template <typename DT, int AL, int BL, int kSegs, bool kGated, int kFlushes = 1>
 int launch_tiles_any(const TileArgs& a, bool direct, hipStream_t st) {
-    if (!direct) return launch_tiles<DT, MidTile, AL, BL, kSegs, kGated, false>(a, st);
+    if (!direct) return launch_tiles<DT, MidTile, AL, BL, kSegs, kGated, false, kFlushes>(a, st);
     const long long big = ceil_div(a.M, 256) * ceil_div(a.N, kGated ? 128 : 256) * a.batches;
-    if (big >= 192) return launch_tiles<DT, BigTile, AL, BL, kSegs, kGated, true>(a, st);
-    return launch_tiles<DT, MidTile, AL, BL, kSegs, kGated, true>(a, st);
+    if (big >= 192) return launch_tiles<DT, BigTile, AL, BL, kSegs, kGated, true, kFlushes>(a, st);
+    return launch_tiles<DT, MidTile, AL, BL, kSegs, kGated, true, kFlushes>(a, st);
 }
 
 template <typename DT, typename Src, int MT, int NTW, int KG, int NG, int S, int FL, bool kGated>

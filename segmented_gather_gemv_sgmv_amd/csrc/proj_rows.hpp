@@ -237,7 +237,7 @@ __global__ __launch_bounds__(kRowsThreads) void rows_kernel(RowsArgs a) {
 #pragma unroll
             for (int j = 0; j < NTW; ++j) {
                 if constexpr (Src::kQ4) {
-                    b.w[q][j][0] = load16(wbase[q][j] + (long long)kb * 1024);
+                    b.w[q][j][0] = load16_stream(wbase[q][j] + (long long)kb * 1024);
                     load_dwords<kMeta>(mbase[q][j] + (long long)kb * (64 * kMeta), b.meta[q][j]);
                 } else {
 #pragma unroll
@@ -343,13 +343,17 @@ __global__ __launch_bounds__(kRowsThreads) void rows_kernel(RowsArgs a) {
     };
 #pragma unroll
     for (int d = 0; d < PD; ++d) load(blk[d], wid + d * kRowsWaves);
-    for (int kb = wid; kb < a.kblocks; kb += PD * kRowsWaves) {
+    int kb = wid;
+    for (; kb + PD * kRowsWaves < a.kblocks; kb += PD * kRowsWaves) {
 #pragma unroll
         for (int d = 0; d < PD; ++d) {
-            if (kb + d * kRowsWaves < a.kblocks) compute(blk[d]);
+            compute(blk[d]);
             load(blk[d], kb + (d + PD) * kRowsWaves);
         }
     }
+#pragma unroll
+    for (int d = 0; d < PD; ++d)
+        if (kb + d * kRowsWaves < a.kblocks) compute(blk[d]);
 
     // ---- add the waves' partial tiles, finish, store -------------------------
 #pragma unroll

@@ -14,9 +14,6 @@
 
 namespace sgmv {
 
-// What lanes past the end of a row of x load.
-__device__ const uint4 g_zero_piece = {0, 0, 0, 0};
-
 template <typename DT, typename Src, int MT, int NTW, int KG, int NG, int S, int FL, bool kGated>
 __global__ __launch_bounds__(kRowsThreads) void strip_kernel(RowsArgs a) {
     using T = typename DT::storage;
@@ -105,7 +102,7 @@ __global__ __launch_bounds__(kRowsThreads) void strip_kernel(RowsArgs a) {
 #pragma unroll
             for (int j = 0; j < NTW; ++j) {
                 if constexpr (Src::kQ4) {
-                    b.w[q][j][0] = load16(wbase[q][j] + (long long)kb * 1024);
+                    b.w[q][j][0] = load16_stream(wbase[q][j] + (long long)kb * 1024);
                     load_dwords<kFlushes>(mbase[q][j] + (long long)kb * (64 * kFlushes), b.meta[q][j]);
                 } else {
 #pragma unroll

@@ -4,11 +4,11 @@
 //
 // Bound: the MFMA rate.  A workgroup computes a BM x BN tile of
 // C[m][n] = sum_k A[m][k] B[n][k] in steps of 64 bytes of K (32 16-bit or 16
-// float32 values) through four LDS stages.  Full steps arrive by direct
-// global-to-LDS loads three steps ahead, so no register holds a tile in
-// flight and a step waits only for loads issued three steps before; what is
-// left of K past a multiple of four steps, and operands that no 16-byte load
-// fits, go through registers, zero filled.
+// float32 values) through four LDS stages, filled by direct global-to-LDS
+// loads three steps ahead, so no register holds a tile in flight and a step
+// waits only for loads issued three steps before.  Lanes past the end of K load
+// a page of zeros.  Operands that no 16-byte load fits go through registers
+// instead (kDma false), several times slower.
 //
 // An operand lies in memory either along K (x, W as used by the forward) or
 // across it (the gradients' transposed operands): the latter keep their
@@ -45,7 +45,7 @@ struct TileArgs {
     int batches;
     int tiles_m, tiles_n, tiles;
     int avec, bvec, yvec; // 16-byte pieces of A / B; 4-element pieces of [M, N] arrays
-    int kblocks, flushes; // 4-bit: tiles of 128 K; pairs per feature and tile
+    int kblocks;          // 4-bit: tiles of 128 K
     int act;
 };
 
@@ -96,7 +96,9 @@ struct StageReader {
             typedef short v4s __attribute__((ext_vector_type(4)));
             typedef __attribute__((address_space(3))) v4s lds_v4s;
             typedef __attribute__((address_space(3))) uint8_t lds_u8;
-            const uint8_t* p = st + off + ((f ^ i) << 5);
+            int u = f;
+            asm("" : "+v"(u));  // recomputed per read: kept, the offsets would take a register each
+            const uint8_t* p = st + off + ((u ^ i) << 5);
             const v4s lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(lds_u8*)p);
             const v4s hi =
                 __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(lds_u8*)(p + 4 * L::kRow));
@@ -142,20 +144,23 @@ __device__ __forceinline__ uint4 scaled_codes(uint32_t w, uint32_t meta) {
     }
 }
 
-template <typename DT, typename SH, int AL, int BL, int kSegs, bool kGated, bool kDma>
+// kFlushes: scale pairs per feature and tile of 128 K (kCodes), else 1.
+template <typename DT, typename SH, int AL, int BL, int kSegs, bool kGated, bool kDma, int kFlushes>
 __global__ __launch_bounds__(SH::NT) void tile_kernel(TileArgs g) {
     using T = typename DT::storage;
     using Ops = PieceOps<DT>;
     constexpr int BM = SH::BM, BN = SH::BN, TM = SH::TM, TN = SH::TN, NT = SH::NT, NW = SH::NW;
     constexpr int B = DT::kBytes, PK = Ops::kPK;
     constexpr int KE = 4 * PK;                 // K per step
-    constexpr int kStage = (BM + BN) * 64;     // bytes of a stage: A then B
     static_assert(BL != kCodes || (B == 2 && AL == kAlongK), "codes feed 16-bit tiles along K");
     static_assert(!kGated || TN % 2 == 0, "a gated wave holds both matrices' columns");
-    __shared__ __attribute__((aligned(16))) uint8_t s_st0[kStage];
-    __shared__ __attribute__((aligned(16))) uint8_t s_st1[kStage];
-    __shared__ __attribute__((aligned(16))) uint8_t s_st2[kStage];
-    __shared__ __attribute__((aligned(16))) uint8_t s_st3[kStage];
+    // Four stages of 64 bytes of K for each operand.  They are arrays of their own,
+    // and every load names its array: the compiler, which orders LDS accesses
+    // after the direct loads into the same array, then needs no wait but ours.
+    __shared__ __attribute__((aligned(16))) uint8_t s_a0[BM * 64], s_b0[BN * 64];
+    __shared__ __attribute__((aligned(16))) uint8_t s_a1[BM * 64], s_b1[BN * 64];
+    __shared__ __attribute__((aligned(16))) uint8_t s_a2[BM * 64], s_b2[BN * 64];
+    __shared__ __attribute__((aligned(16))) uint8_t s_a3[BM * 64], s_b3[BN * 64];
 
     const int tid = threadIdx.x, lane = tid & (kWave - 1);
     const int wid = __builtin_amdgcn_readfirstlane(tid / kWave);
@@ -197,7 +202,7 @@ __global__ __launch_bounds__(SH::NT) void tile_kernel(TileArgs g) {
     static_assert(BL != kCodes || kUnits * NT == BN * 4, "whole units per thread");
     struct Codes {
         uint4 w;
-        uint32_t meta[4];  // scale and biased zero point of each step
+        uint32_t meta[kFlushes];
     };
     auto load_codes = [&](int kb, Codes(&c)[kUnits]) {
         if constexpr (BL == kCodes) {
@@ -210,25 +215,21 @@ __global__ __launch_bounds__(SH::NT) void tile_kernel(TileArgs g) {
                 const long long nt = min(row >> 4, ((N + 15) >> 4) - 1);
                 const ProjWeight& q = g.q[which];
                 c[u].w = load16((const uint4*)q.w + (nt * g.kblocks + kb) * 64 + l);
-                const uint32_t* m =
-                    (const uint32_t*)q.meta + ((nt * g.kblocks + kb) * 16 + (l & 15)) * g.flushes;
-                // Step s uses pair s flushes / 4; the last ones repeat.
-                c[u].meta[0] = m[0];
-                c[u].meta[1] = m[g.flushes >> 2];
-                c[u].meta[2] = m[g.flushes >> 1];
-                c[u].meta[3] = m[g.flushes - 1];
+                load_dwords<kFlushes>(
+                    (const uint32_t*)q.meta + ((nt * g.kblocks + kb) * 16 + (l & 15)) * kFlushes,
+                    c[u].meta);
             }
         }
     };
-    auto store_codes = [&](uint8_t* st, const Codes(&c)[kUnits], int s) {
+    auto store_codes = [&](uint8_t* sb, const Codes(&c)[kUnits], int s) {
         if constexpr (BL == kCodes) {
 #pragma unroll
             for (int u = 0; u < kUnits; ++u) {
                 const int unit = tid + u * NT, l = unit & 63;
                 const int row = (unit >> 6) * 16 + (l & 15);
                 const uint32_t w = s == 0 ? c[u].w.x : s == 1 ? c[u].w.y : s == 2 ? c[u].w.z : c[u].w.w;
-                store16(st + BM * 64 + row * 64 + (along_piece(row, l >> 4) << 4),
-                        scaled_codes<DT>(w, c[u].meta[s]));
+                store16(sb + row * 64 + (along_piece(row, l >> 4) << 4),
+                        scaled_codes<DT>(w, c[u].meta[s * kFlushes / 4]));
             }
         }
     };
@@ -241,24 +242,23 @@ __global__ __launch_bounds__(SH::NT) void tile_kernel(TileArgs g) {
 
     const StageReader<DT, AL, BM> rd_a(wr0, lr, lg);
     const StageReader<DT, BL, BN> rd_b(wc0, lr, lg);
-    auto compute = [&](const uint8_t* st) {
+    auto compute = [&](const uint8_t* sa, const uint8_t* sb) {
         uint4 b[TN];
 #pragma unroll
-        for (int j = 0; j < TN; ++j) b[j] = rd_b(st + BM * 64, j);
+        for (int j = 0; j < TN; ++j) b[j] = rd_b(sb, j);
 #pragma unroll
         for (int i = 0; i < TM; ++i) {
-            const uint4 a = rd_a(st, i);
+            const uint4 a = rd_a(sa, i);
 #pragma unroll
             for (int j = 0; j < TN; ++j) acc[i][j] = Ops::mma(b[j], a, acc[i][j]);
         }
     };
 
     // ---- K through registers, zero filled: four steps from kc on ------------
-    // Element e of an operand's stage: 16-byte slot e.
+    // What 16-byte slot e of an operand's stage holds.
     auto guarded = [&](auto layout, auto cols_c, const void* base, long long ld, int r0, int rows,
-                       int e, int kc, bool vec, int seg_or_batch) -> uint4 {
+                       int e, int kc, bool vec) -> uint4 {
         constexpr int L = decltype(layout)::value, COLS = decltype(cols_c)::value;
-        (void)seg_or_batch;
         const T* p = (const T*)base;
         if constexpr (L == kAlongK) {
             const int row = e >> 2, k = kc + along_piece(row, e & 3) * PK;
@@ -285,7 +285,7 @@ __global__ __launch_bounds__(SH::NT) void tile_kernel(TileArgs g) {
 #pragma unroll
             for (int u = 0; u < kA; ++u)
                 ra[s][u] = guarded(std::integral_constant<int, AL>{}, std::integral_constant<int, BM>{},
-                                   g.a[which], g.lda, m0, M, tid + u * NT, kc + s * KE, g.avec, 0);
+                                   g.a[which], g.lda, m0, M, tid + u * NT, kc + s * KE, g.avec);
 #pragma unroll
             for (int u = 0; u < kB; ++u) {
                 const int e = tid + u * NT;
@@ -299,132 +299,251 @@ __global__ __launch_bounds__(SH::NT) void tile_kernel(TileArgs g) {
                 } else {
                     rb[s][u] = guarded(std::integral_constant<int, BL>{},
                                        std::integral_constant<int, BN>{}, g.b[which], g.ldb, n0, N,
-                                       e, kc + s * KE, g.bvec, 0);
+                                       e, kc + s * KE, g.bvec);
                 }
             }
         }
         __syncthreads();  // the stages' last reads are done
-        auto put = [&](uint8_t* st, int s) {
+        auto put = [&](uint8_t* sa, uint8_t* sb, int s) {
 #pragma unroll
-            for (int u = 0; u < kA; ++u) store16(st + (tid + u * NT) * 16, ra[s][u]);
+            for (int u = 0; u < kA; ++u) store16(sa + (tid + u * NT) * 16, ra[s][u]);
 #pragma unroll
-            for (int u = 0; u < kB; ++u) store16(st + BM * 64 + (tid + u * NT) * 16, rb[s][u]);
-            if constexpr (BL == kCodes) store_codes(st, cc, s);
+            for (int u = 0; u < kB; ++u) store16(sb + (tid + u * NT) * 16, rb[s][u]);
+            if constexpr (BL == kCodes) store_codes(sb, cc, s);
         };
-        put(s_st0, 0);
-        put(s_st1, 1);
-        put(s_st2, 2);
-        put(s_st3, 3);
+        put(s_a0, s_b0, 0);
+        put(s_a1, s_b1, 1);
+        put(s_a2, s_b2, 2);
+        put(s_a3, s_b3, 3);
         __syncthreads();
-        compute(s_st0);
-        if (kc + KE < K) compute(s_st1);
-        if (kc + 2 * KE < K) compute(s_st2);
-        if (kc + 3 * KE < K) compute(s_st3);
+        compute(s_a0, s_b0);
+        if (kc + KE < K) compute(s_a1, s_b1);
+        if (kc + 2 * KE < K) compute(s_a2, s_b2);
+        if (kc + 3 * KE < K) compute(s_a3, s_b3);
     };
-    const int k_full = kDma ? K / (4 * KE) * (4 * KE) : 0;  // K by direct loads
-    for (int seg = 0; seg < kSegs; ++seg)
-        for (int kc = k_full; kc < K; kc += 4 * KE) slow_steps(seg, kc);
+    if constexpr (!kDma) {
+        for (int seg = 0; seg < kSegs; ++seg)
+            for (int kc = 0; kc < K; kc += 4 * KE) slow_steps(seg, kc);
+    }
 
-    // ---- full steps by direct loads -----------------------------------------
+    // ---- K by direct loads ----------------------------------------------------
     if constexpr (kDma) {
-        const int seg_steps = k_full / KE, nsteps = kSegs * seg_steps;
-        if (nsteps > 0) {
-            // Load u of wave w is load w * kLoads + u of the step: 16 stage rows
-            // of A, then of B, 1 KB each.  A wave's loads belong to one operand.
-            constexpr int kLA = BM / 16, kLB = BL == kCodes ? 0 : BN / 16;
-            constexpr int kLoads = (kLA + kLB) / NW;
-            static_assert(kLoads * NW == kLA + kLB && kLA % kLoads == 0, "whole loads per wave");
+        // Steps per segment, and in all: whole turns of the loops below.
+        constexpr int kTurn = BL == kCodes ? 8 : 4;
+        const int seg_steps = (K + KE - 1) / KE;
+        const int nsteps = (kSegs * seg_steps + kTurn - 1) / kTurn * kTurn;
+        {
+            // A load brings 1 KB: 16 stage rows of an operand along K, or the K rows
+            // that fit.  Wave w takes loads w, w + NW, ... of A and of B.
+            constexpr int kLA = BM / 16 / NW, kLB = BL == kCodes ? 0 : BN / 16 / NW;
+            constexpr int kLoads = kLA + kLB, kLBn = kLB > 0 ? kLB : 1;
+            static_assert(kLA * NW * 16 == BM && (BL == kCodes || kLB * NW * 16 == BN), "whole loads per wave");
             static_assert(2 * kLoads < 64, "the wait count fits vmcnt");
             constexpr int kWaitSteps = (2 * kLoads & 15) | ((2 * kLoads >> 4) << 14) | 0x0070;
             using lds_t = __attribute__((address_space(3))) void;
-            const bool is_a = wid * kLoads < kLA;
             const int which = kSegs == 2 ? 0 : z;
-            const char* src[kLoads];
-            long long stride, jump = 0;  // bytes per step; from segment 0 to 1
-            auto along = [&](const void* base, long long ld, int row, int rows, int slot_row) {
-                const int slot = lane & 3;
-                return (const char*)base + ((long long)min(row, rows - 1) * ld +
-                                            along_piece(slot_row, slot) * PK) * B;
-            };
-            auto across = [&](auto cols_c, const void* base, long long ld, int c0, int cols, int load) {
-                using LY = AcrossLayout<DT, decltype(cols_c)::value>;
-                const int byte = lane * 16;
-                const int kr = load * LY::kRowsPerLoad + byte / LY::kRow;
-                const int slot = (byte % LY::kRow) / 16;
-                const int piece = (((slot >> 1) ^ LY::permute(kr)) << 1) | (slot & 1);
-                return (const char*)base + ((long long)kr * ld + min(c0 + piece * PK, cols - PK)) * B;
-            };
-            if (is_a) {
-                stride = AL == kAlongK ? 64 : KE * g.lda * B;
-                if (kSegs == 2) jump = (const char*)g.a[1] - (const char*)g.a[0];
-#pragma unroll
-                for (int u = 0; u < kLoads; ++u) {
-                    const int load = wid * kLoads + u;
-                    if constexpr (AL == kAlongK) {
-                        const int row = load * 16 + (lane >> 2);
-                        src[u] = along(g.a[which], g.lda, m0 + row, M, row);
-                    } else {
-                        src[u] = across(std::integral_constant<int, BM>{}, g.a[which], g.lda, m0, M, load);
-                    }
-                }
-            } else {
-                stride = BL == kAcrossK ? KE * g.ldb * B : 64;
-                if (kSegs == 2) jump = (const char*)g.b[1] - (const char*)g.b[0];
-#pragma unroll
-                for (int u = 0; u < kLoads; ++u) {
-                    const int load = wid * kLoads + u - kLA;
+            // Lane's byte offset in load `load` of an operand from its tile's first row
+            // (along K) or first column (across K), and its first K within a step; past
+            // the end of the rows (columns) it reads the last.
+            auto source = [&](auto layout, auto cols_c, long long ld, int r0, int rows, int load,
+                              int& k) {
+                if constexpr (decltype(layout)::value == kAlongK) {
                     const int row = load * 16 + (lane >> 2);
-                    if constexpr (kGated && BL == kAlongK) {
-                        int w2;
-                        const int gr = gated_row(row, w2);
-                        src[u] = along(g.b[w2], g.ldb, gr, N, row);
-                    } else if constexpr (BL == kAlongK) {
-                        src[u] = along(g.b[which], g.ldb, n0 + row, N, row);
-                    } else if constexpr (BL == kAcrossK) {
-                        src[u] = across(std::integral_constant<int, BN>{}, g.b[which], g.ldb, n0, N, load);
-                    }
+                    k = along_piece(row, lane & 3) * PK;
+                    return (uint32_t)(min(row, rows - 1 - r0) * ld + k) * B;
+                } else {
+                    using LY = AcrossLayout<DT, decltype(cols_c)::value>;
+                    const int byte = lane * 16;
+                    k = load * LY::kRowsPerLoad + byte / LY::kRow;
+                    const int slot = (byte % LY::kRow) / 16;
+                    const int piece = (((slot >> 1) ^ LY::permute(k)) << 1) | (slot & 1);
+                    return (uint32_t)(k * ld + min(piece * PK, rows - PK - r0)) * B;
+                }
+            };
+            auto corner = [&](auto layout, const void* base, long long ld, int r0) {
+                return (const char*)base + (decltype(layout)::value == kAlongK ? r0 * ld : r0) * B;
+            };
+            using AL_t = std::integral_constant<int, AL>;
+            using BL_t = std::integral_constant<int, BL>;
+            uint32_t off_a[kLA], off_b[kLBn];
+            int ka[kLA], kb[kLBn];
+            const char *base_a, *base_b[kLBn];  // uniform over the wave
+            base_a = corner(AL_t{}, g.a[which], g.lda, m0);
+#pragma unroll
+            for (int u = 0; u < kLA; ++u)
+                off_a[u] = source(AL_t{}, std::integral_constant<int, BM>{}, g.lda, m0, M, wid + u * NW, ka[u]);
+#pragma unroll
+            for (int u = 0; u < kLB; ++u) {
+                const int load = wid + u * NW;
+                if constexpr (kGated) {
+                    // A load's 16 stage rows lie in one matrix.  Its rows may lie past
+                    // N altogether, so the corner is the first row that does not.
+                    int w2;
+                    const int row = gated_row(load * 16, w2), at = min(row, N - 1);
+                    base_b[u] = corner(BL_t{}, g.b[w2], g.ldb, at);
+                    const int r = load * 16 + (lane >> 2);
+                    kb[u] = along_piece(r, lane & 3) * PK;
+                    off_b[u] = (uint32_t)(min(lane >> 2, N - 1 - at) * g.ldb + kb[u]) * B;
+                } else {
+                    base_b[u] = corner(BL_t{}, g.b[which], g.ldb, n0);
+                    off_b[u] = source(BL_t{}, std::integral_constant<int, BN>{}, g.ldb, n0, N, load, kb[u]);
                 }
             }
-            auto issue = [&](uint8_t* st, int step) {
-                long long off = step * stride;
-                if (kSegs == 2 && step >= seg_steps) off = (step - seg_steps) * stride + jump;
-#pragma unroll
-                for (int u = 0; u < kLoads; ++u)
-                    __builtin_amdgcn_global_load_lds((const void*)(src[u] + off),
-                                                     (lds_t*)(st + (wid * kLoads + u) * 1024), 16, 0, 0);
+            const long long stride_a = AL == kAlongK ? 64 : KE * g.lda * B;  // bytes per step
+            const long long stride_b = BL == kAcrossK ? KE * g.ldb * B : 64;
+            const long long jump_a = kSegs == 2 ? (const char*)g.a[1] - (const char*)g.a[0] : 0;
+            const long long jump_b = kSegs == 2 ? (const char*)g.b[1] - (const char*)g.b[0] : 0;
+            // Buffer loads: the step's address is the (scalar) base, a lane adds its
+            // 32-bit offset, and a lane past the end of K takes an offset past the
+            // buffer's range, for which the load returns zeros.
+            auto load_lds = [](const char* base, int offset, uint8_t* to) {
+#if __HIP_DEVICE_COMPILE__  // the host pass does not know buffer resources
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(
+                    __builtin_amdgcn_make_buffer_rsrc((void*)base, (short)0, 0x7FFFFFFF, 0x00020000),
+                    (lds_t*)to, 16, offset, 0, 0, 0);
+#endif
             };
-            Codes cur[kUnits], nxt[kUnits];
-            // Step c: its own loads have landed (the later two steps' stay in
-            // flight) and every wave is past step c - 1; then stage (c + 3) % 4
-            // takes step c + 3.  Past the last step loads re-read it into a
-            // stage no step reads.
-            auto step = [&](uint8_t* st, uint8_t* ahead, uint8_t* next, int c, int s) {
-                __builtin_amdgcn_s_waitcnt(kWaitSteps);
-                asm volatile("" ::: "memory");
-                __builtin_amdgcn_s_barrier();
-                asm volatile("" ::: "memory");
-                issue(ahead, min(c + 3, nsteps - 1));
-                if constexpr (BL == kCodes) {
-                    if (s < 3) store_codes(next, cur, s + 1);
-                    else store_codes(next, nxt, 0);
+            // Load u of a step (A's, then B's).
+            auto issue1 = [&](uint8_t* sa, uint8_t* sb, int step, int u) {
+                long long ja = 0, jb = 0;
+                if (kSegs == 2 && step >= seg_steps) {
+                    step -= seg_steps;
+                    ja = jump_a;
+                    jb = jump_b;
                 }
-                compute(st);
+                const int k_left = K - step * KE;  // not positive past the last step
+                if (u < kLA) {
+                    const int o = ka[u < kLA ? u : 0] < k_left ? (int)off_a[u < kLA ? u : 0] : -16;
+                    load_lds(base_a + (ja + step * stride_a), o, sa + (wid + u * NW) * 1024);
+                } else {
+                    const int v = u >= kLA ? u - kLA : 0;
+                    const int o = kb[v] < k_left ? (int)off_b[v] : -16;
+                    load_lds(base_b[v] + (jb + step * stride_b), o, sb + (wid + v * NW) * 1024);
+                }
             };
-            if constexpr (BL == kCodes) load_codes(0, cur);
-            __syncthreads();  // the register steps' last reads of the stages
-            issue(s_st0, 0);
-            issue(s_st1, min(1, nsteps - 1));
-            issue(s_st2, min(2, nsteps - 1));
-            if constexpr (BL == kCodes) store_codes(s_st0, cur, 0);
-            for (int c = 0; c < nsteps; c += 4) {
-                if constexpr (BL == kCodes) load_codes(c / 4 + 1, nxt);
-                step(s_st0, s_st3, s_st1, c, 0);
-                step(s_st1, s_st0, s_st2, c + 1, 1);
-                step(s_st2, s_st1, s_st3, c + 2, 2);
-                step(s_st3, s_st2, s_st0, c + 3, 3);
-                if constexpr (BL == kCodes) {
+            auto issue = [&](uint8_t* sa, uint8_t* sb, int step) {
 #pragma unroll
-                    for (int u = 0; u < kUnits; ++u) cur[u] = nxt[u];
+                for (int u = 0; u < kLoads; ++u) issue1(sa, sb, step, u);
+            };
+            // Packed codes of two K blocks: a block's four steps unpack it while the
+            // next one loads.
+            Codes ca[kUnits], cb[kUnits];
+            auto fence = [] {
+                asm volatile("" ::: "memory");
+                __builtin_amdgcn_sched_barrier(0);
+            };
+            constexpr int kWaitReads = 0xC07F;  // lgkmcnt(0) alone
+            if constexpr (BL == kCodes) load_codes(0, ca);
+            issue(s_a0, s_b0, 0);
+            issue(s_a1, s_b1, 1);
+            issue(s_a2, s_b2, 2);
+            if constexpr (BL == kCodes) store_codes(s_b0, ca, 0);
+            if constexpr (NW == 8) {
+                // Two waves per SIMD, half a step apart: while waves 0-3 multiply,
+                // waves 4-7 read the operands of their next products from LDS, and
+                // the other way round, so that the matrix cores and the LDS are both
+                // kept busy (in step, all eight would read at the start of a step
+                // and the matrix cores wait).  Step c's reads of waves 0-3 are phase
+                // 2 c, those of waves 4-7 phase 2 c + 1, each wave's products the
+                // phase after; a barrier ends each phase.  The direct loads ride
+                // among the products, where their issue costs nothing: in step c,
+                // waves 0-3 (phase 2 c + 1) load step c + 3, whose stage was last
+                // read in phase 2 c - 1, and waves 4-7 (phase 2 c + 2) step c + 4,
+                // whose stage was last read in phase 2 c + 1.  A wave's own loads for
+                // step c + 1 have landed before the barrier that opens phase 2 c + 2:
+                // only those of two later steps may be in flight.
+                auto run = [&](auto lag) {
+                    constexpr bool kLag = decltype(lag)::value;
+                    auto step = [&](uint8_t* sa, uint8_t* sb, uint8_t* ahead_a, uint8_t* ahead_b,
+                                    uint8_t* next_b, int c, auto index,
+                                    const Codes(&cur)[kUnits], const Codes(&nxt)[kUnits]) {
+                        constexpr int s = decltype(index)::value;  // c % 4
+                        fence();
+                        uint4 a[TM], b[TN];
+#pragma unroll
+                        for (int j = 0; j < TN; ++j) b[j] = rd_b(sb, j);
+#pragma unroll
+                        for (int i = 0; i < TM; ++i) a[i] = rd_a(sa, i);
+                        if constexpr (BL == kCodes) {
+                            if (s < 3) store_codes(next_b, cur, s + 1);
+                            else store_codes(next_b, nxt, 0);
+                        }
+                        fence();
+                        constexpr int kLanded = kWaitSteps;
+                        __builtin_amdgcn_s_waitcnt(kLag ? kLanded : kWaitReads);
+                        __builtin_amdgcn_s_barrier();
+                        fence();
+                        __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+                        for (int i = 0; i < TM; ++i) {
+#pragma unroll
+                            for (int j = 0; j < TN; ++j) acc[i][j] = Ops::mma(b[j], a[i], acc[i][j]);
+#pragma unroll
+                            for (int u = kLoads * i / TM; u < kLoads * (i + 1) / TM; ++u) {
+                                __builtin_amdgcn_sched_barrier(0);
+                                if constexpr (kLag) issue1(sa, sb, c + 4, u);
+                                else issue1(ahead_a, ahead_b, c + 3, u);
+                                __builtin_amdgcn_sched_barrier(0);
+                            }
+                        }
+                        __builtin_amdgcn_s_setprio(0);
+                        fence();
+                        if constexpr (!kLag) __builtin_amdgcn_s_waitcnt(kLanded);
+                        __builtin_amdgcn_s_barrier();
+                        fence();
+                    };
+                    if constexpr (kLag) __builtin_amdgcn_s_barrier();
+                    auto four = [&](int c, Codes(&cur)[kUnits], Codes(&nxt)[kUnits]) {
+                        load_codes(c / 4 + 1, nxt);
+                        step(s_a0, s_b0, s_a3, s_b3, s_b1, c, std::integral_constant<int, 0>{}, cur, nxt);
+                        step(s_a1, s_b1, s_a0, s_b0, s_b2, c + 1, std::integral_constant<int, 1>{}, cur, nxt);
+                        step(s_a2, s_b2, s_a1, s_b1, s_b3, c + 2, std::integral_constant<int, 2>{}, cur, nxt);
+                        step(s_a3, s_b3, s_a2, s_b2, s_b0, c + 3, std::integral_constant<int, 3>{}, cur, nxt);
+                    };
+                    for (int c = 0; c < nsteps; c += kTurn) {
+                        four(c, ca, cb);
+                        if constexpr (kTurn == 8) four(c + 4, cb, ca);
+                    }
+                    if constexpr (!kLag) __builtin_amdgcn_s_barrier();
+                };
+                fence();
+                __builtin_amdgcn_s_waitcnt(kWaitSteps);
+                __builtin_amdgcn_s_barrier();
+                if (wid < 4) {
+                    run(std::false_type{});
+                } else {
+                    fence();
+                    issue(s_a3, s_b3, 3);
+                    run(std::true_type{});
+                }
+            } else {
+                // Step c: its own loads have landed (the later two steps' stay in
+                // flight) and every wave is past step c - 1; then stage (c + 3) % 4
+                // takes step c + 3 (zeros past the last).  Two workgroups share a CU
+                // and cover each other's waits.
+                auto step = [&](uint8_t* sa, uint8_t* sb, uint8_t* ahead_a, uint8_t* ahead_b, uint8_t* next_b, int c, int s,
+                                    const Codes(&cur)[kUnits], const Codes(&nxt)[kUnits]) {
+                    __builtin_amdgcn_s_waitcnt(kWaitSteps);
+                    asm volatile("" ::: "memory");
+                    __builtin_amdgcn_s_barrier();
+                    asm volatile("" ::: "memory");
+                    issue(ahead_a, ahead_b, c + 3);
+                    if constexpr (BL == kCodes) {
+                        if (s < 3) store_codes(next_b, cur, s + 1);
+                        else store_codes(next_b, nxt, 0);
+                    }
+                    compute(sa, sb);
+                };
+                auto four = [&](int c, Codes(&cur)[kUnits], Codes(&nxt)[kUnits]) {
+                    load_codes(c / 4 + 1, nxt);
+                    step(s_a0, s_b0, s_a3, s_b3, s_b1, c, 0, cur, nxt);
+                    step(s_a1, s_b1, s_a0, s_b0, s_b2, c + 1, 1, cur, nxt);
+                    step(s_a2, s_b2, s_a1, s_b1, s_b3, c + 2, 2, cur, nxt);
+                    step(s_a3, s_b3, s_a2, s_b2, s_b0, c + 3, 3, cur, nxt);
+                };
+                for (int c = 0; c < nsteps; c += kTurn) {
+                    four(c, ca, cb);
+                    if constexpr (kTurn == 8) four(c + 4, cb, ca);
                 }
             }
             __builtin_amdgcn_s_waitcnt(0x0070);  // no load is left in flight to the stages

@@ -61,9 +61,11 @@ int run_q4(const RowsArgs& a, int flushes, hipStream_t st) {
             t.avec = a.xvec;
             t.yvec = yvec;
             t.kblocks = a.kblocks;
-            t.flushes = flushes;
             t.act = a.act;
-            return launch_tiles_any<DT, kAlongK, kCodes, 1, kGated>(t, a.xvec != 0, st);
+            const bool direct = a.xvec != 0;
+            if (flushes == 1) return launch_tiles_any<DT, kAlongK, kCodes, 1, kGated, 1>(t, direct, st);
+            if (flushes == 2) return launch_tiles_any<DT, kAlongK, kCodes, 1, kGated, 2>(t, direct, st);
+            return launch_tiles_any<DT, kAlongK, kCodes, 1, kGated, 4>(t, direct, st);
         }
     }
     if (flushes == 1) return run_q4_rows<DT, 4, kGated>(a, st);
