@@ -162,6 +162,8 @@ __global__ __launch_bounds__(SH::NT) void tile_kernel(TileArgs g) {
     __shared__ __attribute__((aligned(16))) uint8_t s_a2[BM * 64], s_b2[BN * 64];
     __shared__ __attribute__((aligned(16))) uint8_t s_a3[BM * 64], s_b3[BN * 64];
 
+    __shared__ uint8_t s_unread[NW == 8 && kDma ? 256 * NW : 1];  // where prefetches land
+
     const int tid = threadIdx.x, lane = tid & (kWave - 1);
     const int wid = __builtin_amdgcn_readfirstlane(tid / kWave);
     const int lr = lane & 15, lg = lane >> 4;
@@ -403,6 +405,13 @@ __global__ __launch_bounds__(SH::NT) void tile_kernel(TileArgs g) {
                     (lds_t*)to, 16, offset, 0, 0, 0);
 #endif
             };
+            auto load_lds4 = [](const char* base, int offset, uint8_t* to) {
+#if __HIP_DEVICE_COMPILE__
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(
+                    __builtin_amdgcn_make_buffer_rsrc((void*)base, (short)0, 0x7FFFFFFF, 0x00020000),
+                    (lds_t*)to, 4, offset, 0, 0, 0);
+#endif
+            };
             // Load u of a step (A's, then B's).
             auto issue1 = [&](uint8_t* sa, uint8_t* sb, int step, int u) {
                 long long ja = 0, jb = 0;
@@ -421,6 +430,52 @@ __global__ __launch_bounds__(SH::NT) void tile_kernel(TileArgs g) {
                     load_lds(base_b[v] + (jb + step * stride_b), o, sb + (wid + v * NW) * 1024);
                 }
             };
+            // L2 prefetch, kAhead steps before a step is loaded, of 128-byte lines that
+            // hold two steps: one 4-byte load per line, into LDS that nobody reads.
+            // The tiles that an XCD holds at one time are eight tile rows by four tile
+            // columns (see the tile order above), so each workgroup fetches a quarter
+            // of its A lines and an eighth of its B lines, and the direct loads find
+            // all of them in L2.  Waves 0-3 fetch A's share, waves 4-7 B's.
+            constexpr int kAhead = 6;
+            constexpr bool kPrefetch = NW == 8;
+            const char* pf_base = base_a;
+            long long pf_stride = stride_a, pf_jump = jump_a;
+            int pf_off = -16, pf_k = 0;
+            if constexpr (kPrefetch) {
+                static_assert(BM == 256 && BN == 256, "256 lines per operand and two steps");
+                // Line `id` of a tile: row id along K; across K, line id % 4 of K row
+                // id / 4 (float32: its first half; a line holds one step then).
+                auto line = [&](auto layout, long long ld, int id, int rows_left) {
+                    if constexpr (decltype(layout)::value == kAlongK) return (int)(min(id, rows_left - 1) * ld) * B;
+                    pf_k = id >> 2;
+                    return (int)(pf_k * ld + min((id & 3) * (128 / B), rows_left - PK)) * B;
+                };
+                if (wid < 4) {
+                    if (lane < 16) pf_off = line(AL_t{}, g.lda, (tn & 3) * 64 + wid * 16 + lane, M - m0);
+                } else if constexpr (BL != kCodes) {
+                    const int first = (m0 / BM & 7) * 32 + (wid - 4) * 8;
+                    pf_base = base_b[0];
+                    pf_stride = stride_b;
+                    pf_jump = jump_b;
+                    if constexpr (kGated) {  // 8 stage rows lie in one matrix
+                        int w2;
+                        const int row = gated_row(first, w2), at = min(row, N - 1);
+                        pf_base = corner(BL_t{}, g.b[w2], g.ldb, at);
+                        if (lane < 8) pf_off = (int)(min(lane, N - 1 - at) * g.ldb) * B;
+                    } else if (lane < 8) {
+                        pf_off = line(BL_t{}, g.ldb, first + lane, N - n0);
+                    }
+                }
+            }
+            auto prefetch = [&](int step) {
+                long long at = 0;
+                if (kSegs == 2 && step >= seg_steps) {
+                    step -= seg_steps;
+                    at = pf_jump;
+                }
+                const int o = pf_k < K - step * KE ? pf_off : -16;
+                load_lds4(pf_base + (at + step * pf_stride), o, s_unread + 256 * wid);
+            };
             auto issue = [&](uint8_t* sa, uint8_t* sb, int step) {
 #pragma unroll
                 for (int u = 0; u < kLoads; ++u) issue1(sa, sb, step, u);
@@ -436,7 +491,7 @@ __global__ __launch_bounds__(SH::NT) void tile_kernel(TileArgs g) {
             if constexpr (BL == kCodes) load_codes(0, ca);
             issue(s_a0, s_b0, 0);
             issue(s_a1, s_b1, 1);
-            issue(s_a2, s_b2, 2);
+            if (NW != 8 || wid >= 4) issue(s_a2, s_b2, 2);
             if constexpr (BL == kCodes) store_codes(s_b0, ca, 0);
             if constexpr (NW == 8) {
                 // Two waves per SIMD, half a step apart: while waves 0-3 multiply,
@@ -445,17 +500,25 @@ __global__ __launch_bounds__(SH::NT) void tile_kernel(TileArgs g) {
                 // kept busy (in step, all eight would read at the start of a step
                 // and the matrix cores wait).  Step c's reads of waves 0-3 are phase
                 // 2 c, those of waves 4-7 phase 2 c + 1, each wave's products the
-                // phase after; a barrier ends each phase.  The direct loads ride
-                // among the products, where their issue costs nothing: in step c,
-                // waves 0-3 (phase 2 c + 1) load step c + 3, whose stage was last
-                // read in phase 2 c - 1, and waves 4-7 (phase 2 c + 2) step c + 4,
-                // whose stage was last read in phase 2 c + 1.  A wave's own loads for
-                // step c + 1 have landed before the barrier that opens phase 2 c + 2:
-                // only those of two later steps may be in flight.
+                // phase after; a barrier ends each phase.
+                //
+                // The direct loads ride among the products, two steps at a time, so
+                // that the halves of a 128-byte line are asked for together.  In an
+                // even step c, waves 0-3 (phase 2 c + 1) load steps c + 2 and c + 3,
+                // whose stages were last read in phases 2 c - 3 and 2 c - 1; in an odd
+                // step c, waves 4-7 (phase 2 c + 2) load steps c + 3 and c + 4, whose
+                // stages were last read in phases 2 c - 1 and 2 c + 1.  A wave's own
+                // loads for step c + 1 have landed before the barrier that opens phase
+                // 2 c + 2.  Issued after them by then, at least: in an even step the
+                // loads of two steps and one prefetch, in an odd step those of one.
+                //
+                // 4096 x 4096 -> 2 x 10240, bf16, per step of 32 K: 1.02 us without
+                // the pairs and the prefetch, 0.92 with the prefetch, 0.88 with both;
+                // the products and LDS reads alone 0.72.
                 auto run = [&](auto lag) {
                     constexpr bool kLag = decltype(lag)::value;
-                    auto step = [&](uint8_t* sa, uint8_t* sb, uint8_t* ahead_a, uint8_t* ahead_b,
-                                    uint8_t* next_b, int c, auto index,
+                    auto step = [&](uint8_t* sa, uint8_t* sb, uint8_t* even_a, uint8_t* even_b,
+                                    uint8_t* odd_a, uint8_t* odd_b, uint8_t* next_b, int c, auto index,
                                     const Codes(&cur)[kUnits], const Codes(&nxt)[kUnits]) {
                         constexpr int s = decltype(index)::value;  // c % 4
                         fence();
@@ -469,7 +532,8 @@ __global__ __launch_bounds__(SH::NT) void tile_kernel(TileArgs g) {
                             else store_codes(next_b, nxt, 0);
                         }
                         fence();
-                        constexpr int kLanded = kWaitSteps;
+                        constexpr int kAfter = (s % 2 == 0 ? 2 * kLoads : kLoads) + 1;
+                        constexpr int kLanded = (kAfter & 15) | ((kAfter >> 4) << 14) | 0x0070;
                         __builtin_amdgcn_s_waitcnt(kLag ? kLanded : kWaitReads);
                         __builtin_amdgcn_s_barrier();
                         fence();
@@ -478,15 +542,18 @@ __global__ __launch_bounds__(SH::NT) void tile_kernel(TileArgs g) {
                         for (int i = 0; i < TM; ++i) {
 #pragma unroll
                             for (int j = 0; j < TN; ++j) acc[i][j] = Ops::mma(b[j], a[i], acc[i][j]);
+                            if constexpr (s % 2 == (kLag ? 1 : 0)) {
 #pragma unroll
-                            for (int u = kLoads * i / TM; u < kLoads * (i + 1) / TM; ++u) {
-                                __builtin_amdgcn_sched_barrier(0);
-                                if constexpr (kLag) issue1(sa, sb, c + 4, u);
-                                else issue1(ahead_a, ahead_b, c + 3, u);
-                                __builtin_amdgcn_sched_barrier(0);
+                                for (int u = 2 * kLoads * i / TM; u < 2 * kLoads * (i + 1) / TM; ++u) {
+                                    __builtin_amdgcn_sched_barrier(0);
+                                    if (u < kLoads) issue1(even_a, even_b, c + (kLag ? 3 : 2), u);
+                                    else issue1(odd_a, odd_b, c + (kLag ? 4 : 3), u - kLoads);
+                                    __builtin_amdgcn_sched_barrier(0);
+                                }
                             }
                         }
                         __builtin_amdgcn_s_setprio(0);
+                        if constexpr (s % 2 == 0) prefetch(c + kAhead);
                         fence();
                         if constexpr (!kLag) __builtin_amdgcn_s_waitcnt(kLanded);
                         __builtin_amdgcn_s_barrier();
@@ -495,10 +562,12 @@ __global__ __launch_bounds__(SH::NT) void tile_kernel(TileArgs g) {
                     if constexpr (kLag) __builtin_amdgcn_s_barrier();
                     auto four = [&](int c, Codes(&cur)[kUnits], Codes(&nxt)[kUnits]) {
                         load_codes(c / 4 + 1, nxt);
-                        step(s_a0, s_b0, s_a3, s_b3, s_b1, c, std::integral_constant<int, 0>{}, cur, nxt);
-                        step(s_a1, s_b1, s_a0, s_b0, s_b2, c + 1, std::integral_constant<int, 1>{}, cur, nxt);
-                        step(s_a2, s_b2, s_a1, s_b1, s_b3, c + 2, std::integral_constant<int, 2>{}, cur, nxt);
-                        step(s_a3, s_b3, s_a2, s_b2, s_b0, c + 3, std::integral_constant<int, 3>{}, cur, nxt);
+                        // Pair of stages loaded in each step: 2, 3 by waves 0-3 in step
+                        // 0 and by waves 4-7 in step 3, 0, 1 in steps 2 and 1.
+                        step(s_a0, s_b0, s_a2, s_b2, s_a3, s_b3, s_b1, c, std::integral_constant<int, 0>{}, cur, nxt);
+                        step(s_a1, s_b1, s_a0, s_b0, s_a1, s_b1, s_b2, c + 1, std::integral_constant<int, 1>{}, cur, nxt);
+                        step(s_a2, s_b2, s_a0, s_b0, s_a1, s_b1, s_b3, c + 2, std::integral_constant<int, 2>{}, cur, nxt);
+                        step(s_a3, s_b3, s_a2, s_b2, s_a3, s_b3, s_b0, c + 3, std::integral_constant<int, 3>{}, cur, nxt);
                     };
                     for (int c = 0; c < nsteps; c += kTurn) {
                         four(c, ca, cb);
@@ -506,14 +575,16 @@ __global__ __launch_bounds__(SH::NT) void tile_kernel(TileArgs g) {
                     }
                     if constexpr (!kLag) __builtin_amdgcn_s_barrier();
                 };
+                // Step 0 has landed: after its loads came those of one or two steps.
                 fence();
-                __builtin_amdgcn_s_waitcnt(kWaitSteps);
+                __builtin_amdgcn_s_waitcnt((kLoads & 15) | 0x0070);
                 __builtin_amdgcn_s_barrier();
                 if (wid < 4) {
                     run(std::false_type{});
                 } else {
                     fence();
                     issue(s_a3, s_b3, 3);
+                    prefetch(4);
                     run(std::true_type{});
                 }
             } else {
