@@ -453,7 +453,7 @@ int gated_ffn_backward(void* dx, void* dWg, void* dWu, void* dg, void* du, const
  * element strides, for q {in row, in head, out row, out head} and then for
  * k; the last dimension is dense.  The outputs may be the inputs themselves
  * (equal pointers and strides) and must not overlap them otherwise.
- * rotary_dim is even, at most head_dim and 1024.
+ * rotary_dim is even and at most head_dim, head_dim at most 1024.
  */
 int rope(void* q_out, void* k_out, const void* q, const void* k, const void* positions,
          int32_t position_bytes, const double* inv_freq, float magnitude, int32_t num_rows,

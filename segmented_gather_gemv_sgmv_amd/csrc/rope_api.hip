@@ -9,11 +9,21 @@ namespace {
 
 using namespace sgmv;
 
+constexpr int kUnitsMost = 4;  // units per thread
+
+template <typename DT, bool kVec>
+void launch_rope(const RopeArgs& a, hipStream_t st) {
+    const dim3 grid((unsigned)((long long)a.rows * a.groups)), block(kRopeThreads);
+    const int each = (a.heads_per_group * a.units + kRopeThreads - 1) / kRopeThreads;
+    if (each <= 1) launch(&rope_kernel<DT, kVec, 1>, grid, block, st, a);
+    else if (each <= 2) launch(&rope_kernel<DT, kVec, 2>, grid, block, st, a);
+    else launch(&rope_kernel<DT, kVec, kUnitsMost>, grid, block, st, a);
+}
+
 template <typename DT>
 void launch_rope(const RopeArgs& a, bool vec, hipStream_t st) {
-    const dim3 grid((unsigned)((long long)a.rows * a.groups));
-    if (vec) launch(&rope_kernel<DT, true>, grid, dim3(kRopeThreads), st, a);
-    else launch(&rope_kernel<DT, false>, grid, dim3(kRopeThreads), st, a);
+    if (vec) launch_rope<DT, true>(a, st);
+    else launch_rope<DT, false>(a, st);
 }
 
 }  // namespace
@@ -27,7 +37,7 @@ extern "C" int rope(void* q_out, void* k_out, const void* q, const void* k,
     if (num_rows < 0 || q_heads < 0 || k_heads < 0 || head_dim < 1 || rotary_dim < 2 ||
         rotary_dim > head_dim || (rotary_dim & 1) || (position_bytes != 4 && position_bytes != 8))
         return SGMV_ERR_BAD_SHAPE;
-    if (rotary_dim > kRopeMaxRot) return SGMV_ERR_UNSUPPORTED;
+    if (head_dim > kRopeMaxDim) return SGMV_ERR_UNSUPPORTED;
     const long long heads = (long long)q_heads + k_heads;
     if (num_rows == 0 || heads == 0) return SGMV_OK;
     if ((q_heads > 0 && (!q || !q_out)) || (k_heads > 0 && (!k || !k_out)) || !positions ||
@@ -67,15 +77,17 @@ extern "C" int rope(void* q_out, void* k_out, const void* q, const void* k,
     a.units = (interleaved ? (vec ? rotary_dim / V : rotary_dim / 2) : rotary_dim / 2 / v) +
               (head_dim - rotary_dim) / v;
     a.units_magic = (uint32_t)(((1ull << 32) + a.units - 1) / a.units);
-    // One workgroup per row once the rows fill the chip (4 per CU); with
-    // fewer rows the heads are split too, down to one pass of the workgroup.
+    // One workgroup per row once the rows fill the chip (4 per CU); with fewer
+    // rows, and where a thread would hold more than kUnitsMost units, the heads are
+    // split too, down to one pass of the workgroup.
+    static_assert(kRopeMaxDim <= kRopeThreads * kUnitsMost, "a head fits a workgroup");
     const long long per_pass = std::max(1, kRopeThreads / a.units);
-    long long want = std::max(1ll, (1024ll + num_rows - 1) / num_rows);
+    const long long want = (1024ll + num_rows - 1) / num_rows;
     long long hpg = std::max(per_pass, (heads + want - 1) / want);
-    hpg = std::min({hpg, heads, std::max(1ll, 65535ll / a.units)});
+    hpg = std::min({hpg, heads, (long long)(kRopeThreads * kUnitsMost / a.units)});
     a.heads_per_group = (int)hpg;
     a.groups = (int)((heads + hpg - 1) / hpg);
-    if ((long long)num_rows * a.groups > 0x7FFFFFFFll || a.units > 65535) return SGMV_ERR_UNSUPPORTED;
+    if ((long long)num_rows * a.groups > 0x7FFFFFFFll) return SGMV_ERR_UNSUPPORTED;
     const hipStream_t st = (hipStream_t)stream;
     if (dtype == SGMV_F32) launch_rope<F32>(a, vec, st);
     else if (dtype == SGMV_F16) launch_rope<F16>(a, vec, st);

@@ -130,7 +130,8 @@ def _run(q, k, positions, plan, out, inverse):
     if first is None:
         raise ValueError("q or k must be given")
     dev, dtype = first.device, first.dtype
-    _heads(first, "q" if q is not None else "k", dev, dtype)
+    if first.dim() != 3:
+        raise ValueError(f"q and k must be [rows, heads, head_dim], got {tuple(first.shape)}")
     R, _, D = first.shape
     oq, ok = out if out is not None else (None, None)
     q2, qo, qi, qs, hq = _one(q, "q", oq, dev, dtype, R, D) if q is not None else _ABSENT
@@ -165,31 +166,41 @@ _function = None
 
 
 def _autograd_function():
-    """The autograd node (made on first use: this package imports torch late)."""
+    """The autograd node (made on first use: this package imports torch late).
+    The gradient of a rotation is the rotation back, itself differentiable."""
     global _function
     if _function is None:
         torch = _torch()
 
         class Rope(torch.autograd.Function):
             @staticmethod
-            def forward(ctx, q, k, positions, plan):
+            def forward(ctx, q, k, positions, plan, inverse):
                 ctx.save_for_backward(positions)
-                ctx.plan = plan
-                return _run(q, k, positions, plan, None, False)
+                ctx.plan, ctx.inverse = plan, inverse
+                return _run(q, k, positions, plan, None, inverse)
 
             @staticmethod
-            @torch.autograd.function.once_differentiable
             def backward(ctx, dq, dk):
-                grads = [None, None]
-                dense = lambda t: t if t.stride(2) == 1 or t.shape[2] == 1 else t.contiguous()
-                use = [dense(t) if want else None
-                       for t, want in zip((dq, dk), ctx.needs_input_grad)]
-                if use[0] is not None or use[1] is not None:
-                    grads = _run(use[0], use[1], ctx.saved_tensors[0], ctx.plan, None, True)
-                return (*grads, None, None)
+                positions, = ctx.saved_tensors
+                want_q, want_k = ctx.needs_input_grad[:2]
+                if want_q and dq.stride(2) != 1:
+                    dq = dq.contiguous()
+                if want_k and dk.stride(2) != 1:
+                    dk = dk.contiguous()
+                gq, gk = _turn(dq if want_q else None, dk if want_k else None, positions, ctx.plan,
+                               not ctx.inverse)
+                return gq, gk, None, None, None
 
         _function = Rope
     return _function
+
+
+def _turn(q, k, positions, plan, inverse):
+    """_run, recorded where gradients are."""
+    if _torch().is_grad_enabled() and ((q is not None and q.requires_grad) or
+                                       (k is not None and k.requires_grad)):
+        return (_function or _autograd_function()).apply(q, k, positions, plan, inverse)
+    return _run(q, k, positions, plan, None, inverse)
 
 
 def rope(q, k, positions, plan: RopePlan, out=None, inverse: bool = False):
@@ -198,11 +209,10 @@ def rope(q, k, positions, plan: RopePlan, out=None, inverse: bool = False):
     ``positions`` [R] int32 or int64.  ``out=(q, k)`` works in place (or into
     other tensors, which must not overlap the inputs); ``inverse`` turns back,
     which is what the gradients take."""
-    torch = _torch()
     if not isinstance(plan, RopePlan):
         raise TypeError("plan must be a RopePlan (see rope_plan)")
-    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in (q, k)):
-        if out is not None or inverse:
-            raise ValueError("out and inverse cannot be given where gradients are recorded")
-        return _autograd_function().apply(q, k, positions, plan)
+    if out is None:
+        return _turn(q, k, positions, plan, inverse)
+    if _torch().is_grad_enabled() and any(t is not None and t.requires_grad for t in (q, k)):
+        raise ValueError("out cannot be given where gradients are recorded")
     return _run(q, k, positions, plan, out, inverse)

@@ -168,6 +168,13 @@ def test_only_what_needs_gradients():
     assert torch.equal(gx, gy)
 
 
+def test_second_derivative_is_refused():
+    x, Wg, Wu, _, _, _ = _inputs(4, 40, 48, "f32", False)
+    h = sg.gated_ffn(x.requires_grad_(), Wg, Wu)
+    with pytest.raises(RuntimeError, match="once"):
+        torch.autograd.grad(h.sum(), [x], create_graph=True)
+
+
 def test_no_rows():
     x, Wg, Wu, _, _, _ = _inputs(4, 40, 48, "f16", False)
     x0 = x[:0].requires_grad_()

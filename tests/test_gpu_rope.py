@@ -190,4 +190,23 @@ def test_refusals():
     with pytest.raises(ValueError, match="rows, heads"):
         sg.rope(q[0], None, pos, plan)
     with pytest.raises(ValueError, match="recorded"):
-        sg.rope(q.clone().requires_grad_(), None, pos, plan, inverse=True)
+        sg.rope(q.clone().requires_grad_(), None, pos, plan, out=(torch.empty_like(q), None))
+
+
+def test_second_derivative():
+    """<rope(q), rope(q)> has the gradient 2 m^2 q on turned elements, 2 q on
+    the others; its own derivative is that factor again."""
+    gen = torch.Generator().manual_seed(5)
+    plan = sg.rope_plan(32, scaling=dict(kind="by_parts", factor=4.0, context=1024), device=DEV)
+    q = torch.randn(6, 2, 48, generator=gen).to(DEV).requires_grad_()
+    pos = torch.arange(6, device=DEV)
+    out, _ = sg.rope(q, None, pos, plan)
+    g, = torch.autograd.grad((out * out).sum(), [q], create_graph=True)
+    v = torch.randn(q.shape, generator=gen).to(DEV)
+    gg, = torch.autograd.grad(g, [q], v)
+    factor = torch.full((48,), 2.0, dtype=torch.float64)
+    factor[:32] *= plan.magnitude ** 2
+    # two rotations of float32 pairs each way: 4 x 8 roundings of the pair's size
+    want = v.double().cpu() * factor
+    size = v.double().cpu().abs().amax(-1, keepdim=True) * factor.max() * 2
+    check(gg, want, 32 * F32 * size.expand_as(want), "second derivative")
