@@ -396,8 +396,8 @@ int q4_pack(void* tiles, void* meta, const uint8_t* codes, const void* scales,
  * y = round(x W^T + bias): x [num_rows, in_features], y [num_rows,
  * out_features] (overwritten), bias [out_features] or NULL.  Up to 256 rows
  * (any number in float32) the codes enter the products exactly and the
- * scales multiply float32 sums per group; beyond that fp16 and bf16 round
- * each scaled weight once to dtype first.  An infinity in x gives a
+ * scales multiply float32 sums per group; beyond that fp16 and bf16 calls may
+ * round each scaled weight once to dtype first.  An infinity in x gives a
  * non-finite row (NaN where the products alone would give an infinity).
  */
 int q4_linear(void* y, const void* x, const sgmv_q4_weight* w, const void* bias, int32_t num_rows,

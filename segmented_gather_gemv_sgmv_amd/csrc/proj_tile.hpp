@@ -437,13 +437,12 @@ __global__ __launch_bounds__(SH::NT) void tile_kernel(TileArgs g) {
             // of its A lines and an eighth of its B lines, and the direct loads find
             // all of them in L2.  Waves 0-3 fetch A's share, waves 4-7 B's.
             constexpr int kAhead = 6;
-            constexpr bool kPrefetch = NW == 8;
+            constexpr bool kPrefetch = NW == 8 && BM == 256 && BN == 256;
             const char* pf_base = base_a;
             long long pf_stride = stride_a, pf_jump = jump_a;
             int pf_off = -16, pf_k = 0;
             if constexpr (kPrefetch) {
-                static_assert(BM == 256 && BN == 256, "256 lines per operand and two steps");
-                // Line `id` of a tile: row id along K; across K, line id % 4 of K row
+                // Line `id` of a tile (256 of two steps): row id along K; across K, line id % 4 of K row
                 // id / 4 (float32: its first half; a line holds one step then).
                 auto line = [&](auto layout, long long ld, int id, int rows_left) {
                     if constexpr (decltype(layout)::value == kAlongK) return (int)(min(id, rows_left - 1) * ld) * B;
@@ -532,7 +531,7 @@ __global__ __launch_bounds__(SH::NT) void tile_kernel(TileArgs g) {
                             else store_codes(next_b, nxt, 0);
                         }
                         fence();
-                        constexpr int kAfter = (s % 2 == 0 ? 2 * kLoads : kLoads) + 1;
+                        constexpr int kAfter = (s % 2 == 0 ? 2 * kLoads : kLoads) + (kPrefetch ? 1 : 0);
                         constexpr int kLanded = (kAfter & 15) | ((kAfter >> 4) << 14) | 0x0070;
                         __builtin_amdgcn_s_waitcnt(kLag ? kLanded : kWaitReads);
                         __builtin_amdgcn_s_barrier();
@@ -553,7 +552,7 @@ __global__ __launch_bounds__(SH::NT) void tile_kernel(TileArgs g) {
                             }
                         }
                         __builtin_amdgcn_s_setprio(0);
-                        if constexpr (s % 2 == 0) prefetch(c + kAhead);
+                        if constexpr (kPrefetch && s % 2 == 0) prefetch(c + kAhead);
                         fence();
                         if constexpr (!kLag) __builtin_amdgcn_s_waitcnt(kLanded);
                         __builtin_amdgcn_s_barrier();
@@ -584,7 +583,7 @@ __global__ __launch_bounds__(SH::NT) void tile_kernel(TileArgs g) {
                 } else {
                     fence();
                     issue(s_a3, s_b3, 3);
-                    prefetch(4);
+                    if constexpr (kPrefetch) prefetch(4);
                     run(std::true_type{});
                 }
             } else {

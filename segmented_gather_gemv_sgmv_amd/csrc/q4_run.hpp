@@ -8,9 +8,22 @@
 
 namespace sgmv {
 
-// Rows up to which 16-bit calls keep the codes exact in the products (rows and
-// strip kernels); beyond, tiles of scaled, once rounded weights.
-constexpr int kQ4RowsMax = 1024;
+// Whether a 16-bit call of R rows takes tiles (scaled weights, each rounded
+// once) instead of strips (exact codes, scales on float32 sums): by the times
+// they take per 4096 of K.  Strips run at a steady rate, 240 us for 4096 x 4096
+// outputs (350 with a scale per 32 K); for tiles see above, gated 256 x 256 tiles
+// taking 150 us a round.  Measured, 4096 x 4096 weights, bf16: 1024 rows 48 us by
+// strips, 52 by tiles; 1531 rows 78 and 73; 5120 -> 13824: 512 rows 134 and 95,
+// 2048 rows 506 and 300.  Calls of up to kQ4ExactRows rows never round.
+constexpr int kQ4ExactRows = 256;
+
+inline bool q4_takes_tiles(int R, int N, int flushes, bool gated) {
+    const int per = gated ? 2 : 1;  // matrices
+    const double outputs = (double)ceil_div(R, 32) * 32 * N * per / (4096. * 4096.);
+    const double big_us = big_tiles_us(ceil_div(R, 256) * ceil_div((long long)N * per, 256));
+    const double mid_us = mid_tiles_us(ceil_div(R, 128) * ceil_div((long long)N * per, 128));
+    return std::min(mid_us, gated ? big_us * 1.42 : big_us) < outputs * (flushes == 4 ? 350. : 240.);
+}
 
 // FL: 4, 2 or 1 steps of 32 K per scale (1, 2 or 4 flushes per tile of 128 K).
 template <typename DT, int XR, int MT, int PD, int FL, bool kGated>
@@ -26,10 +39,12 @@ template <typename DT, int FL, bool kGated>
 int run_q4_rows(const RowsArgs& a, hipStream_t st) {
     if constexpr (DT::kBytes == 2) {
         if (a.xvec) {
-            // x loads for at most four rows; as many workgroups as n-tiles, so only
-            // while these do not fill the chip several times over.
-            if (a.R <= 4 && ceil_div(a.N, 16) < 640)
-                return launch_q4_rows<DT, 4, 1, 3, FL, kGated>(a, st);
+            // x loads for at most four rows; as many workgroups as n-tiles, so a
+            // single matrix takes it only while these do not fill the chip several
+            // times over (one row, 5120 -> 13824: 12.6 us against 11.2 by strips;
+            // 4096 -> 11008: 7.8 against 8.5; gated 12.8 against 13.6).
+            if (a.R <= 4 && (kGated || ceil_div(a.N, 16) < 768))
+                return launch_q4_rows<DT, 4, 1, kGated ? 1 : FL == 1 ? 3 : 4, FL, kGated>(a, st);
             return run_strip<DT, Q4Src<DT>, FL, kGated>(a, st);
         }
         return a.R <= 16 ? launch_q4_rows<DT, 16, 1, 2, FL, kGated>(a, st)
@@ -43,7 +58,7 @@ int run_q4_rows(const RowsArgs& a, hipStream_t st) {
 template <typename DT, bool kGated>
 int run_q4(const RowsArgs& a, int flushes, hipStream_t st) {
     if constexpr (DT::kBytes == 2) {
-        if (a.R > kQ4RowsMax) {
+        if (a.R > kQ4ExactRows && (!a.xvec || q4_takes_tiles(a.R, a.N, flushes, kGated))) {
             TileArgs t{};
             t.a[0] = a.x;
             t.lda = a.K;

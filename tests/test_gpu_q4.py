@@ -18,7 +18,8 @@ SHAPES = [
     (130, 640, 80, 160), (256, 264, 40, 64),
 ]
 TILE_SHAPES = [(257, 640, 264, 128), (300, 200, 136, 64), (400, 333, 77, 32), (513, 1152, 129, 96),
-               (300, 64, 300, 32)]
+               (300, 64, 300, 32), (1100, 264, 4000, 128), (1100, 328, 4000, 64), (700, 136, 6000, 32),
+               (2100, 130, 100, 64), (900, 392, 1000, 32)]
 
 
 def _x(gen, R, K, dtype):
@@ -46,6 +47,31 @@ def test_rows(R, K, N, G, dt):
     _linear(R, K, N, G, dt, zeros=(R % 2 == 1), bias=(N % 2 == 0))
 
 
+# Wide enough that a workgroup's block of features is the largest, for every
+# block of rows the kernels have.
+WIDE_SHAPES = [(1, 200, 13000, 64), (4, 384, 11100, 128), (6, 520, 11000, 32), (16, 264, 2900, 64),
+               (20, 392, 11000, 128), (31, 200, 2800, 32), (40, 328, 11000, 64), (64, 136, 5500, 128),
+               (90, 264, 11000, 64), (128, 200, 11008, 128), (150, 72, 11008, 32), (256, 392, 8200, 64)]
+
+
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("R,K,N,G", WIDE_SHAPES)
+def test_wide_rows(R, K, N, G, dt):
+    _linear(R, K, N, G, dt, zeros=True, bias=True, seed=2)
+
+
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("R,K,N,G", WIDE_SHAPES)
+def test_wide_gated_rows(R, K, N, G, dt):
+    gen = torch.Generator().manual_seed(4)
+    dtype = DTYPES[dt]
+    wg, wu = (make_q4(gen, N, K, G, dtype, z, DEV) for z in (False, True))
+    x = _x(gen, R, K, dtype)
+    (g, dg), (u, du) = (q4_product(x, w, K, G, False) for w in (wg, wu))
+    h = sg.q4_gated_ffn(x, *(sg.q4_pack(*w, group_size=G, in_features=K) for w in (wg, wu)))
+    check(h, *gated_forward(g, u, dg, du, "silu", dtype), f"wide gated {R}x{K}->{N} G={G} {dt}")
+
+
 @pytest.mark.parametrize("dt", ["f16", "bf16", "f32"])
 @pytest.mark.parametrize("R,K,N,G", TILE_SHAPES)
 def test_tiles(R, K, N, G, dt):
@@ -61,7 +87,7 @@ def test_wide_tiles(dt):
 @pytest.mark.parametrize("dt", ["f16", "bf16", "f32"])
 @pytest.mark.parametrize("act", ["silu", "gelu", "gelu_tanh", "relu", "sigmoid"])
 @pytest.mark.parametrize("R,K,N,G", [(1, 256, 64, 128), (7, 136, 43, 32), (40, 520, 96, 64),
-                                     (300, 392, 200, 128)])
+                                     (300, 392, 200, 128), (600, 168, 5000, 64)])
 def test_gated(R, K, N, G, act, dt):
     gen = torch.Generator().manual_seed(3)
     dtype = DTYPES[dt]
