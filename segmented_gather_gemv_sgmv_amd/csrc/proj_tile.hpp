@@ -486,135 +486,86 @@ __global__ __launch_bounds__(SH::NT) void tile_kernel(TileArgs g) {
                 asm volatile("" ::: "memory");
                 __builtin_amdgcn_sched_barrier(0);
             };
-            constexpr int kWaitReads = 0xC07F;  // lgkmcnt(0) alone
             if constexpr (BL == kCodes) load_codes(0, ca);
             issue(s_a0, s_b0, 0);
             issue(s_a1, s_b1, 1);
-            if (NW != 8 || wid >= 4) issue(s_a2, s_b2, 2);
-            if constexpr (BL == kCodes) store_codes(s_b0, ca, 0);
-            if constexpr (NW == 8) {
-                // Two waves per SIMD, half a step apart: while waves 0-3 multiply,
-                // waves 4-7 read the operands of their next products from LDS, and
-                // the other way round, so that the matrix cores and the LDS are both
-                // kept busy (in step, all eight would read at the start of a step
-                // and the matrix cores wait).  Step c's reads of waves 0-3 are phase
-                // 2 c, those of waves 4-7 phase 2 c + 1, each wave's products the
-                // phase after; a barrier ends each phase.
-                //
-                // The direct loads ride among the products, two steps at a time, so
-                // that the halves of a 128-byte line are asked for together.  In an
-                // even step c, waves 0-3 (phase 2 c + 1) load steps c + 2 and c + 3,
-                // whose stages were last read in phases 2 c - 3 and 2 c - 1; in an odd
-                // step c, waves 4-7 (phase 2 c + 2) load steps c + 3 and c + 4, whose
-                // stages were last read in phases 2 c - 1 and 2 c + 1.  A wave's own
-                // loads for step c + 1 have landed before the barrier that opens phase
-                // 2 c + 2.  Issued after them by then, at least: in an even step the
-                // loads of two steps and one prefetch, in an odd step those of one.
-                //
-                // 4096 x 4096 -> 2 x 10240, bf16, per step of 32 K: 1.02 us without
-                // the pairs and the prefetch, 0.92 with the prefetch, 0.88 with both;
-                // the products and LDS reads alone 0.72.
-                auto run = [&](auto lag) {
-                    constexpr bool kLag = decltype(lag)::value;
-                    auto step = [&](uint8_t* sa, uint8_t* sb, uint8_t* even_a, uint8_t* even_b,
-                                    uint8_t* odd_a, uint8_t* odd_b, uint8_t* next_b, int c, auto index,
-                                    const Codes(&cur)[kUnits], const Codes(&nxt)[kUnits]) {
-                        constexpr int s = decltype(index)::value;  // c % 4
-                        fence();
-                        uint4 a[TM], b[TN];
-#pragma unroll
-                        for (int j = 0; j < TN; ++j) b[j] = rd_b(sb, j);
-#pragma unroll
-                        for (int i = 0; i < TM; ++i) a[i] = rd_a(sa, i);
-                        if constexpr (BL == kCodes) {
-                            if (s < 3) store_codes(next_b, cur, s + 1);
-                            else store_codes(next_b, nxt, 0);
-                        }
-                        fence();
-                        constexpr int kAfter = (s % 2 == 0 ? 2 * kLoads : kLoads) + (kPrefetch ? 1 : 0);
-                        constexpr int kLanded = (kAfter & 15) | ((kAfter >> 4) << 14) | 0x0070;
-                        __builtin_amdgcn_s_waitcnt(kLag ? kLanded : kWaitReads);
-                        __builtin_amdgcn_s_barrier();
-                        fence();
-                        __builtin_amdgcn_s_setprio(1);
-#pragma unroll
-                        for (int i = 0; i < TM; ++i) {
-#pragma unroll
-                            for (int j = 0; j < TN; ++j) acc[i][j] = Ops::mma(b[j], a[i], acc[i][j]);
-                            if constexpr (s % 2 == (kLag ? 1 : 0)) {
-#pragma unroll
-                                for (int u = 2 * kLoads * i / TM; u < 2 * kLoads * (i + 1) / TM; ++u) {
-                                    __builtin_amdgcn_sched_barrier(0);
-                                    if (u < kLoads) issue1(even_a, even_b, c + (kLag ? 3 : 2), u);
-                                    else issue1(odd_a, odd_b, c + (kLag ? 4 : 3), u - kLoads);
-                                    __builtin_amdgcn_sched_barrier(0);
-                                }
-                            }
-                        }
-                        __builtin_amdgcn_s_setprio(0);
-                        if constexpr (kPrefetch && s % 2 == 0) prefetch(c + kAhead);
-                        fence();
-                        if constexpr (!kLag) __builtin_amdgcn_s_waitcnt(kLanded);
-                        __builtin_amdgcn_s_barrier();
-                        fence();
-                    };
-                    if constexpr (kLag) __builtin_amdgcn_s_barrier();
-                    auto four = [&](int c, Codes(&cur)[kUnits], Codes(&nxt)[kUnits]) {
-                        load_codes(c / 4 + 1, nxt);
-                        // Pair of stages loaded in each step: 2, 3 by waves 0-3 in step
-                        // 0 and by waves 4-7 in step 3, 0, 1 in steps 2 and 1.
-                        step(s_a0, s_b0, s_a2, s_b2, s_a3, s_b3, s_b1, c, std::integral_constant<int, 0>{}, cur, nxt);
-                        step(s_a1, s_b1, s_a0, s_b0, s_a1, s_b1, s_b2, c + 1, std::integral_constant<int, 1>{}, cur, nxt);
-                        step(s_a2, s_b2, s_a0, s_b0, s_a1, s_b1, s_b3, c + 2, std::integral_constant<int, 2>{}, cur, nxt);
-                        step(s_a3, s_b3, s_a2, s_b2, s_a3, s_b3, s_b0, c + 3, std::integral_constant<int, 3>{}, cur, nxt);
-                    };
-                    for (int c = 0; c < nsteps; c += kTurn) {
-                        four(c, ca, cb);
-                        if constexpr (kTurn == 8) four(c + 4, cb, ca);
-                    }
-                    if constexpr (!kLag) __builtin_amdgcn_s_barrier();
-                };
-                // Step 0 has landed: after its loads came those of one or two steps.
+            issue(s_a2, s_b2, 2);
+            if constexpr (kPrefetch) prefetch(kAhead - 2);
+            if constexpr (BL == kCodes) {
+                store_codes(s_b0, ca, 0);
+                store_codes(s_b1, ca, 1);
+            }
+            // Step c multiplies stage c % 4.  Its B operands and first A operand are in
+            // registers when it begins (they were read in step c - 1); the other A
+            // operands are read at its start, behind the first products.  In its
+            // middle, with half of its products issued, comes the step's one
+            // barrier: this wave's own loads of step c + 1 have landed (only what was
+            // issued after them may be in flight) and so has every other wave's;
+            // and every wave is past its reads of stage (c - 1) % 4, which takes step
+            // c + 3.  The next step's first operands are then read behind the second
+            // half of the products, so that the matrix cores have work on both
+            // sides of the barrier.
+            constexpr int kAfter = kLoads + (kPrefetch ? 1 : 0);
+            constexpr int kLanded = (kAfter & 15) | ((kAfter >> 4) << 14) | (BL == kCodes ? 0x0070 : 0x0F70);
+            uint4 a0[2], b[2][TN];  // by parity of the step
+            auto step = [&](const uint8_t* sa, const uint8_t* next_a, const uint8_t* next_b,
+                            uint8_t* ahead_a, uint8_t* ahead_b, uint8_t* codes_b, int c, auto index,
+                            const Codes(&cur)[kUnits], const Codes(&nxt)[kUnits]) {
+                constexpr int s = decltype(index)::value;  // c % 4
+                constexpr int X = s & 1, Y = X ^ 1;
                 fence();
-                __builtin_amdgcn_s_waitcnt((kLoads & 15) | 0x0070);
+                uint4 a[TM];
+                a[0] = a0[X];
+#pragma unroll
+                for (int i = 1; i < TM; ++i) a[i] = rd_a(sa, i);
+                fence();
+#pragma unroll
+                for (int i = 0; i < TM / 2; ++i)
+#pragma unroll
+                    for (int j = 0; j < TN; ++j) acc[i][j] = Ops::mma(b[X][j], a[i], acc[i][j]);
+                fence();
+                __builtin_amdgcn_s_waitcnt(kLanded);
                 __builtin_amdgcn_s_barrier();
-                if (wid < 4) {
-                    run(std::false_type{});
-                } else {
-                    fence();
-                    issue(s_a3, s_b3, 3);
-                    if constexpr (kPrefetch) prefetch(4);
-                    run(std::true_type{});
-                }
-            } else {
-                // Step c: its own loads have landed (the later two steps' stay in
-                // flight) and every wave is past step c - 1; then stage (c + 3) % 4
-                // takes step c + 3 (zeros past the last).  Two workgroups share a CU
-                // and cover each other's waits.
-                auto step = [&](uint8_t* sa, uint8_t* sb, uint8_t* ahead_a, uint8_t* ahead_b, uint8_t* next_b, int c, int s,
-                                    const Codes(&cur)[kUnits], const Codes(&nxt)[kUnits]) {
-                    __builtin_amdgcn_s_waitcnt(kWaitSteps);
-                    asm volatile("" ::: "memory");
-                    __builtin_amdgcn_s_barrier();
-                    asm volatile("" ::: "memory");
-                    issue(ahead_a, ahead_b, c + 3);
-                    if constexpr (BL == kCodes) {
-                        if (s < 3) store_codes(next_b, cur, s + 1);
-                        else store_codes(next_b, nxt, 0);
+                fence();
+#pragma unroll
+                for (int j = 0; j < TN; ++j) b[Y][j] = rd_b(next_b, j);
+                a0[Y] = rd_a(next_a, 0);
+                fence();
+#pragma unroll
+                for (int i = TM / 2; i < TM; ++i) {
+#pragma unroll
+                    for (int j = 0; j < TN; ++j) acc[i][j] = Ops::mma(b[X][j], a[i], acc[i][j]);
+#pragma unroll
+                    for (int u = 2 * kLoads * (i - TM / 2) / TM; u < 2 * kLoads * (i + 1 - TM / 2) / TM; ++u) {
+                        fence();
+                        issue1(ahead_a, ahead_b, c + 3, u);
+                        fence();
                     }
-                    compute(sa, sb);
-                };
-                auto four = [&](int c, Codes(&cur)[kUnits], Codes(&nxt)[kUnits]) {
-                    load_codes(c / 4 + 1, nxt);
-                    step(s_a0, s_b0, s_a3, s_b3, s_b1, c, 0, cur, nxt);
-                    step(s_a1, s_b1, s_a0, s_b0, s_b2, c + 1, 1, cur, nxt);
-                    step(s_a2, s_b2, s_a1, s_b1, s_b3, c + 2, 2, cur, nxt);
-                    step(s_a3, s_b3, s_a2, s_b2, s_b0, c + 3, 3, cur, nxt);
-                };
-                for (int c = 0; c < nsteps; c += kTurn) {
-                    four(c, ca, cb);
-                    if constexpr (kTurn == 8) four(c + 4, cb, ca);
                 }
+                if constexpr (kPrefetch && s % 2 == 0) prefetch(c + kAhead);
+                if constexpr (BL == kCodes) {  // step c + 2, read after the next barrier
+                    if (s < 2) store_codes(codes_b, cur, s + 2);
+                    else store_codes(codes_b, nxt, s - 2);
+                }
+                fence();
+            };
+            auto four = [&](int c, Codes(&cur)[kUnits], Codes(&nxt)[kUnits]) {
+                load_codes(c / 4 + 1, nxt);
+                step(s_a0, s_a1, s_b1, s_a3, s_b3, s_b2, c, std::integral_constant<int, 0>{}, cur, nxt);
+                step(s_a1, s_a2, s_b2, s_a0, s_b0, s_b3, c + 1, std::integral_constant<int, 1>{}, cur, nxt);
+                step(s_a2, s_a3, s_b3, s_a1, s_b1, s_b0, c + 2, std::integral_constant<int, 2>{}, cur, nxt);
+                step(s_a3, s_a0, s_b0, s_a2, s_b2, s_b1, c + 3, std::integral_constant<int, 3>{}, cur, nxt);
+            };
+            fence();
+            __builtin_amdgcn_s_waitcnt(kWaitSteps);  // step 0 has landed
+            __builtin_amdgcn_s_barrier();
+            fence();
+#pragma unroll
+            for (int j = 0; j < TN; ++j) b[0][j] = rd_b(s_b0, j);
+            a0[0] = rd_a(s_a0, 0);
+            for (int c = 0; c < nsteps; c += kTurn) {
+                four(c, ca, cb);
+                if constexpr (kTurn == 8) four(c + 4, cb, ca);
             }
             __builtin_amdgcn_s_waitcnt(0x0070);  // no load is left in flight to the stages
         }
