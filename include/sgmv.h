@@ -420,6 +420,10 @@ int q4_linear(void* y, const void* x, const sgmv_q4_weight* w, const void* bias,
  * with dg and du rounded to dtype between the steps.  dx, or dWg and dWu,
  * may be NULL and are then not computed; dg and du are needed.  With
  * num_rows == 0 the weights' gradients are zero.  act' of relu at 0 is 0.
+ * Features beyond 2^20 return SGMV_ERR_UNSUPPORTED.
+ * workspace: for dx, at least gated_ffn_backward_workspace_bytes(...) bytes,
+ * 16-byte aligned, with the conventions of "Workspace" above: dx of few rows is
+ * summed in ranges of out_features, whose float32 sums stand there.
  */
 typedef enum {
     SGMV_ACT_SILU = 0,
@@ -435,10 +439,12 @@ int q4_gated_ffn(void* h, const void* x, const sgmv_q4_weight* gate, const sgmv_
 int gated_ffn(void* h, void* g_saved, void* u_saved, const void* x, const void* Wg, const void* Wu,
               const void* gate_add, const void* up_add, int32_t num_rows, int32_t in_features,
               int32_t out_features, int32_t act, int32_t dtype, void* stream);
+size_t gated_ffn_backward_workspace_bytes(int32_t num_rows, int32_t in_features,
+                                          int32_t out_features, int32_t dtype);
 int gated_ffn_backward(void* dx, void* dWg, void* dWu, void* dg, void* du, const void* dh,
                        const void* x, const void* Wg, const void* Wu, const void* g, const void* u,
                        int32_t num_rows, int32_t in_features, int32_t out_features, int32_t act,
-                       int32_t dtype, void* stream);
+                       int32_t dtype, void* workspace, size_t workspace_bytes, void* stream);
 
 /*
  * Rotary positions on q [num_rows, q_heads, head_dim] and k [num_rows,

@@ -84,7 +84,8 @@ ABI = [
     ("gated_ffn", ctypes.c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32,
                                  _i32, _vp]),
     ("gated_ffn_backward", ctypes.c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
-                                          _i32, _i32, _i32, _i32, _i32, _vp]),
+                                          _i32, _i32, _i32, _i32, _i32, _vp, _sz, _vp]),
+    ("gated_ffn_backward_workspace_bytes", _sz, [_i32, _i32, _i32, _i32]),
     ("rope", ctypes.c_int, [_vp, _vp, _vp, _vp, _vp, _i32, _vp, _f32, _i32, _i32, _i32, _i32, _i32,
                             _vp, _i32, _i32, _i32, _vp]),
 ]

@@ -12,6 +12,8 @@ constexpr int kFfnRowsMax = 64;
 int check_ffn(int R, int H, int I, int act, int dtype) {
     if (!known_dtype(dtype)) return SGMV_ERR_BAD_DTYPE;
     if (R < 0 || H < 1 || I < 1 || !known_act(act)) return SGMV_ERR_BAD_SHAPE;
+    // A tile's 256 rows are reached by 32-bit byte offsets from its first.
+    if (H > (1 << 20) || I > (1 << 20) || R > 0x7FFFFF00) return SGMV_ERR_UNSUPPORTED;
     return SGMV_OK;
 }
 
@@ -70,6 +72,8 @@ struct GradArgs {
     void *dx, *dWg, *dWu, *dg, *du;
     const void *dh, *x, *Wg, *Wu, *g, *u;
     int R, H, I, act;
+    float* workspace;  // of dx's sums, when they are taken in ranges
+    SumPlan sum;
 };
 
 template <typename DT>
@@ -101,11 +105,26 @@ int run_backward(const GradArgs& b, hipStream_t st) {
         t.M = b.R;
         t.N = b.H;
         t.K = b.I;
-        t.batches = 1;
+        t.batches = b.sum.ranges;
+        t.range_steps = b.sum.range_steps;
         t.avec = gvec;
         t.bvec = hvec && aligned16(b.Wg) && aligned16(b.Wu);
         t.yvec = b.H % 4 == 0 && aligned16(b.dx);
-        const int rc = launch_tiles_any<DT, kAlongK, kAcrossK, 2, false>(t, t.avec && t.bvec, st);
+        const bool direct = t.avec && t.bvec;
+        int rc;
+        if (b.sum.ranges == 1) {
+            rc = launch_tiles_any<DT, kAlongK, kAcrossK, 2, false>(t, direct, st);
+        } else {
+            t.partial = b.workspace;
+            t.partial_stride = b.sum.stride;
+            rc = launch_kind<DT, kAlongK, kAcrossK, 2, false>(
+                b.sum.kind, t, TileRange{0, t.M, 0, t.N}, direct, st);
+            if (rc != SGMV_OK) return rc;
+            const long long n = (long long)b.R * b.H;
+            launch(&join_kernel<DT>, dim3((unsigned)ceil_div(n, 1024)), dim3(256), st, (T*)b.dx,
+                   (const float*)b.workspace, b.sum.ranges, b.sum.stride, n, (int)aligned16(b.dx));
+            rc = launch_status();
+        }
         if (rc != SGMV_OK) return rc;
     }
     if (b.dWg) {
@@ -165,17 +184,30 @@ int gated_ffn(void* h, void* g_saved, void* u_saved, const void* x, const void* 
     return run_forward<BF16>(a, st);
 }
 
+size_t gated_ffn_backward_workspace_bytes(int32_t num_rows, int32_t in_features,
+                                          int32_t out_features, int32_t dtype) {
+    if (check_ffn(num_rows, in_features, out_features, SGMV_ACT_SILU, dtype) != SGMV_OK || num_rows == 0)
+        return 0;
+    const SumPlan p = plan_sum(num_rows, in_features, out_features, dtype);
+    return p.ranges == 1 ? 0 : (size_t)(p.ranges * p.stride) * sizeof(float);
+}
+
 int gated_ffn_backward(void* dx, void* dWg, void* dWu, void* dg, void* du, const void* dh,
                        const void* x, const void* Wg, const void* Wu, const void* g, const void* u,
                        int32_t num_rows, int32_t in_features, int32_t out_features, int32_t act,
-                       int32_t dtype, void* stream) {
+                       int32_t dtype, void* workspace, size_t workspace_bytes, void* stream) {
     const int rc = check_ffn(num_rows, in_features, out_features, act, dtype);
     if (rc != SGMV_OK) return rc;
     if ((dWg == nullptr) != (dWu == nullptr)) return SGMV_ERR_NULL_PTR;
     if (num_rows > 0 && (!dg || !du || !dh || !g || !u || (dx && (!Wg || !Wu)) || (dWg && !x)))
         return SGMV_ERR_NULL_PTR;
+    const size_t need =
+        dx ? gated_ffn_backward_workspace_bytes(num_rows, in_features, out_features, dtype) : 0;
+    if (need > 0 && (!workspace || workspace_bytes < need || !aligned16(workspace)))
+        return SGMV_ERR_WORKSPACE;
     const GradArgs b{dx, dWg, dWu, dg, du, dh, x, Wg, Wu, g, u, num_rows, in_features, out_features,
-                     act};
+                     act, (float*)workspace,
+                     plan_sum(num_rows, in_features, out_features, dtype)};
     const hipStream_t st = (hipStream_t)stream;
     if (dtype == SGMV_F32) return run_backward<F32>(b, st);
     if (dtype == SGMV_F16) return run_backward<F16>(b, st);

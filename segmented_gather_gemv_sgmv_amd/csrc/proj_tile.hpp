@@ -42,8 +42,12 @@ struct TileArgs {
     const void* add[2];   // gated: addends [M, N]; else add[0] = bias [N]; or NULL
     void* save[2];        // gated: g and u [M, N], or NULL
     int M, N, K;          // gated: N columns of each matrix
-    int batches;
-    int tiles_m, tiles_n, tiles;
+    int batches;          // kSegs == 2: ranges of K, each summed by workgroups of its own
+    int range_steps;      // kSegs == 2, direct loads: steps per range, a multiple of 4
+    float* partial;       // kSegs == 2: sums of the ranges, [batches][partial_stride]; or NULL
+    long long partial_stride;
+    int m_first, n_first;            // row and column (of each matrix) of the first tile
+    int tiles_m, tiles_n, tiles;     // of this launch
     int avec, bvec, yvec; // 16-byte pieces of A / B; 4-element pieces of [M, N] arrays
     int kblocks;          // 4-bit: tiles of 128 K
     int act;
@@ -183,10 +187,11 @@ __global__ __launch_bounds__(SH::NT) void tile_kernel(TileArgs g) {
     const int group = t / (8 * g.tiles_n);
     const int in_group = t - group * 8 * g.tiles_n;
     const int rows_here = min(8, g.tiles_m - 8 * group);
-    const int m0 = (8 * group + in_group % rows_here) * BM;
+    const int row8 = in_group % rows_here;  // tile row within the group
+    const int m0 = g.m_first + (8 * group + row8) * BM;
     const int tn = in_group / rows_here;
     // Columns per tile: a gated tile holds BN / 2 of each matrix.
-    const int n0 = tn * (kGated ? BN / 2 : BN);
+    const int n0 = g.n_first + tn * (kGated ? BN / 2 : BN);
     const int wr0 = (wid / SH::WN) * (16 * TM), wc = wid % SH::WN, wc0 = wc * (16 * TN);
     const int M = g.M, N = g.N, K = g.K;
 
@@ -324,8 +329,17 @@ __global__ __launch_bounds__(SH::NT) void tile_kernel(TileArgs g) {
         if (kc + 3 * KE < K) compute(s_a3, s_b3);
     };
     if constexpr (!kDma) {
-        for (int seg = 0; seg < kSegs; ++seg)
-            for (int kc = 0; kc < K; kc += 4 * KE) slow_steps(seg, kc);
+        const int seg_turns = (K + 4 * KE - 1) / (4 * KE);
+        int turn = 0, end = kSegs * seg_turns;
+        if constexpr (kSegs == 2) {
+            const int each = (end + g.batches - 1) / g.batches;  // turns per range
+            turn = z * each;
+            end = min(end, turn + each);
+        }
+        for (; turn < end; ++turn) {
+            const int seg = kSegs == 2 && turn >= seg_turns;
+            slow_steps(seg, (turn - seg * seg_turns) * 4 * KE);
+        }
     }
 
     // ---- K by direct loads ----------------------------------------------------
@@ -333,7 +347,12 @@ __global__ __launch_bounds__(SH::NT) void tile_kernel(TileArgs g) {
         // Steps per segment, and in all: whole turns of the loops below.
         constexpr int kTurn = BL == kCodes ? 8 : 4;
         const int seg_steps = (K + KE - 1) / KE;
-        const int nsteps = (kSegs * seg_steps + kTurn - 1) / kTurn * kTurn;
+        int nsteps = (kSegs * seg_steps + kTurn - 1) / kTurn * kTurn;
+        int step0 = 0;  // first step of this workgroup's range
+        if constexpr (kSegs == 2) {
+            step0 = z * g.range_steps;
+            nsteps = min(nsteps - step0, g.range_steps);
+        }
         {
             // A load brings 1 KB: 16 stage rows of an operand along K, or the K rows
             // that fit.  Wave w takes loads w, w + NW, ... of A and of B.
@@ -415,6 +434,7 @@ __global__ __launch_bounds__(SH::NT) void tile_kernel(TileArgs g) {
             // Load u of a step (A's, then B's).
             auto issue1 = [&](uint8_t* sa, uint8_t* sb, int step, int u) {
                 long long ja = 0, jb = 0;
+                step += step0;
                 if (kSegs == 2 && step >= seg_steps) {
                     step -= seg_steps;
                     ja = jump_a;
@@ -437,22 +457,29 @@ __global__ __launch_bounds__(SH::NT) void tile_kernel(TileArgs g) {
             // of its A lines and an eighth of its B lines, and the direct loads find
             // all of them in L2.  Waves 0-3 fetch A's share, waves 4-7 B's.
             constexpr int kAhead = 6;
-            constexpr bool kPrefetch = NW == 8 && BM == 256 && BN == 256;
+            constexpr bool kPrefetch = NW == 8;
             const char* pf_base = base_a;
             long long pf_stride = stride_a, pf_jump = jump_a;
             int pf_off = -16, pf_k = 0;
             if constexpr (kPrefetch) {
-                // Line `id` of a tile (256 of two steps): row id along K; across K, line id % 4 of K row
-                // id / 4 (float32: its first half; a line holds one step then).
-                auto line = [&](auto layout, long long ld, int id, int rows_left) {
-                    if constexpr (decltype(layout)::value == kAlongK) return (int)(min(id, rows_left - 1) * ld) * B;
-                    pf_k = id >> 2;
-                    return (int)(pf_k * ld + min((id & 3) * (128 / B), rows_left - PK)) * B;
+                // Line `id` of an operand's tile of COLS rows (columns), two steps being
+                // COLS lines: row id along K; across K, line id % (COLS / 64) of K row
+                // id / (COLS / 64) (float32: its first half; a line holds one step then).
+                auto line = [&](auto layout, auto cols_c, long long ld, int id, int rows_left) {
+                    if constexpr (decltype(layout)::value == kAlongK) {
+                        return (int)(min(id, rows_left - 1) * ld) * B;
+                    } else {
+                        constexpr int kLines = decltype(cols_c)::value / 64;
+                        pf_k = id / kLines;
+                        return (int)(pf_k * ld + min(id % kLines * (128 / B), rows_left - PK)) * B;
+                    }
                 };
                 if (wid < 4) {
-                    if (lane < 16) pf_off = line(AL_t{}, g.lda, (tn & 3) * 64 + wid * 16 + lane, M - m0);
+                    if (lane < BM / 16)
+                        pf_off = line(AL_t{}, std::integral_constant<int, BM>{}, g.lda,
+                                      (tn & 3) * (BM / 4) + wid * (BM / 16) + lane, M - m0);
                 } else if constexpr (BL != kCodes) {
-                    const int first = (m0 / BM & 7) * 32 + (wid - 4) * 8;
+                    const int first = row8 * (BN / 8) + (wid - 4) * (BN / 32);
                     pf_base = base_b[0];
                     pf_stride = stride_b;
                     pf_jump = jump_b;
@@ -460,14 +487,15 @@ __global__ __launch_bounds__(SH::NT) void tile_kernel(TileArgs g) {
                         int w2;
                         const int row = gated_row(first, w2), at = min(row, N - 1);
                         pf_base = corner(BL_t{}, g.b[w2], g.ldb, at);
-                        if (lane < 8) pf_off = (int)(min(lane, N - 1 - at) * g.ldb) * B;
-                    } else if (lane < 8) {
-                        pf_off = line(BL_t{}, g.ldb, first + lane, N - n0);
+                        if (lane < BN / 32) pf_off = (int)(min(lane, N - 1 - at) * g.ldb) * B;
+                    } else if (lane < BN / 32) {
+                        pf_off = line(BL_t{}, std::integral_constant<int, BN>{}, g.ldb, first + lane, N - n0);
                     }
                 }
             }
             auto prefetch = [&](int step) {
                 long long at = 0;
+                step += step0;
                 if (kSegs == 2 && step >= seg_steps) {
                     step -= seg_steps;
                     at = pf_jump;
@@ -609,7 +637,10 @@ __global__ __launch_bounds__(SH::NT) void tile_kernel(TileArgs g) {
 #pragma unroll
                 for (int c = 0; c < 4; ++c) o[c] = acc[i][j][c] + bias[c];
             }
-            store4f<DT>(out + at, left, g.yvec, o);
+            if (kSegs == 2 && g.partial)
+                store4f<F32>(g.partial + z * g.partial_stride + at, left, N % 4 == 0, o);
+            else
+                store4f<DT>(out + at, left, g.yvec, o);
         }
     }
 }
@@ -660,6 +691,28 @@ __global__ __launch_bounds__(256) void gated_grad_kernel(
                 }
         }
     }
+}
+
+// ---------------------------------------------------------------------------
+// y = the sum of `count` arrays of n float32 sums, in their order, rounded
+// once.  `stride` floats apart, a multiple of 4, each 16-byte aligned; `vec`: y
+// is too.  The sums were written just before and are mostly read from the
+// caches.
+// ---------------------------------------------------------------------------
+template <typename DT>
+__global__ __launch_bounds__(256) void join_kernel(typename DT::storage* __restrict__ y,
+                                                   const float* __restrict__ parts, int count,
+                                                   long long stride, long long n, int vec) {
+    const long long i = ((long long)blockIdx.x * 256 + threadIdx.x) * 4;
+    if (i >= n) return;
+    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int c = 0; c < count; ++c) {
+        float v[4];
+        F32::unpack(load16(parts + c * stride + i), v);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sum[e] += v[e];
+    }
+    store4f<DT>(y + i, (int)min(n - i, 4ll), vec, sum);
 }
 
 }  // namespace sgmv

@@ -20,9 +20,8 @@ constexpr int kQ4ExactRows = 256;
 inline bool q4_takes_tiles(int R, int N, int flushes, bool gated) {
     const int per = gated ? 2 : 1;  // matrices
     const double outputs = (double)ceil_div(R, 32) * 32 * N * per / (4096. * 4096.);
-    const double big_us = big_tiles_us(ceil_div(R, 256) * ceil_div((long long)N * per, 256));
-    const double mid_us = mid_tiles_us(ceil_div(R, 128) * ceil_div((long long)N * per, 128));
-    return std::min(mid_us, gated ? big_us * 1.42 : big_us) < outputs * (flushes == 4 ? 350. : 240.);
+    const double us = plan_tiles(R, N, 1, gated, true).us;
+    return us < outputs * (flushes == 4 ? 350. : 240.);
 }
 
 // FL: 4, 2 or 1 steps of 32 K per scale (1, 2 or 4 flushes per tile of 128 K).

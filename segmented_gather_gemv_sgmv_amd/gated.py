@@ -82,10 +82,16 @@ def gated_ffn_backward(dh, x, Wg, Wu, g, u, act: str = "silu", need_dx=True, nee
     dx = x.new_empty((R, H)) if need_dx else None
     dWg, dWu = (x.new_empty((I, H)), x.new_empty((I, H))) if need_dw else (None, None)
     ptr = lambda t: None if t is None else t.data_ptr()
+    ws, ws_bytes = None, 0
+    if need_dx:
+        ws_bytes = lib().gated_ffn_backward_workspace_bytes(R, H, I, dtype_code(x.dtype))
+        if ws_bytes:
+            ws = x.new_empty(ws_bytes, dtype=_torch().uint8)
     _check(lib().gated_ffn_backward(ptr(dx), ptr(dWg), ptr(dWu), dg.data_ptr(), du.data_ptr(),
                                     dh.data_ptr(), x.data_ptr(), Wg.data_ptr(), Wu.data_ptr(),
                                     g.data_ptr(), u.data_ptr(), R, H, I, code, dtype_code(x.dtype),
-                                    _stream_ptr(x.device)), "gated_ffn_backward")
+                                    ptr(ws), ws_bytes, _stream_ptr(x.device)),
+           "gated_ffn_backward")
     return dx, dWg, dWu, dg, du
 
 

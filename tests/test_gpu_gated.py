@@ -120,6 +120,39 @@ def test_wide_tiles(dt):
                      "wide " + dt)
 
 
+# dx of few tiles and a long sum, taken in ranges: whole and ragged tiles, a
+# last range that is shorter, sizes no vector fits, more ranges than tile rows.
+@pytest.mark.parametrize("dt", ["f16", "bf16", "f32"])
+@pytest.mark.parametrize("R,H,I", [(32, 256, 4096), (300, 136, 2008), (90, 333, 1501), (1, 8, 9000),
+                                   (257, 1000, 2744)])
+def test_sums_in_ranges(R, H, I, dt):
+    x, Wg, Wu, ag, au, dh = _inputs(R, H, I, dt, True, seed=7)
+    assert sg.lib().gated_ffn_backward_workspace_bytes(R, H, I, sg.dtype_code(x.dtype)) > 0
+    leaves = [t.requires_grad_() for t in (x, ag, au)]
+    h = sg.gated_ffn(x, Wg, Wu, gate_add=ag, up_add=au)
+    grads = torch.autograd.grad(h, leaves, dh, retain_graph=True)
+    with torch.no_grad():
+        _check_grads(x, Wg, Wu, ag, au, dh, "silu", dict(zip(("dx", "dg", "du"), grads)),
+                     f"ranges {R}x{H}->{I} {dt}")
+    assert torch.equal(torch.autograd.grad(h, leaves, dh)[0], grads[0])
+
+
+# Outputs of a little more than a round of 256 x 256 tiles, whose rest takes
+# smaller ones: by columns (forward), by rows (the weights' gradients).
+@pytest.mark.parametrize("dt", ["f16", "bf16", "f32"])
+@pytest.mark.parametrize("R,H,I", [(4200, 72, 2200), (70, 4040, 2312), (2050, 40, 8 * 555)])
+def test_rest_tiles(R, H, I, dt):
+    x, Wg, Wu, ag, au, dh = _inputs(R, H, I, dt, True, seed=8)
+    leaves = [t.requires_grad_() for t in (x, Wg, Wu, ag, au)]
+    h = sg.gated_ffn(x, Wg, Wu, gate_add=ag, up_add=au)
+    grads = torch.autograd.grad(h, leaves, dh)
+    with torch.no_grad():
+        g, eg, u, eu = _pre(x, Wg, Wu, ag, au)
+        check(h, *gated_forward(g, u, eg, eu, "silu", x.dtype), f"rest {R}x{H}->{I} {dt}")
+        _check_grads(x, Wg, Wu, ag, au, dh, "silu",
+                     dict(zip(("dx", "dWg", "dWu", "dg", "du"), grads)), f"rest {R}x{H}->{I} {dt}")
+
+
 def test_gradients_against_differences():
     x, Wg, Wu, ag, au, dh = _inputs(6, 40, 24, "f32", True, seed=3)
     leaves = [t.requires_grad_() for t in (x, Wg, Wu, ag, au)]

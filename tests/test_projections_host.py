@@ -66,12 +66,20 @@ def test_gated_checks(lib):
         h, None, None, x, FAKE, FAKE, None, None, R, H, I, act, dt, None)
     assert fwd(dt=4) == 3 and fwd(H=0) == 2 and fwd(I=-1) == 2 and fwd(R=-2) == 2 and fwd(act=9) == 2
     assert fwd(h=None) == 1 and fwd(x=None) == 1 and fwd(R=0, h=None) == 0
+    assert fwd(H=(1 << 20) + 1) == 4 and fwd(I=(1 << 20) + 1) == 4
 
-    def bwd(dWg=FAKE, dWu=FAKE, dg=FAKE, x=FAKE, R=4, dt=1):
+    def bwd(dWg=FAKE, dWu=FAKE, dg=FAKE, x=FAKE, R=4, H=64, I=64, dt=1, ws=FAKE, ws_bytes=1 << 30):
         return lib.gated_ffn_backward(FAKE, dWg, dWu, dg, FAKE, FAKE, x, FAKE, FAKE, FAKE, FAKE, R,
-                                      64, 64, 0, dt, None)
+                                      H, I, 0, dt, ws, ws_bytes, None)
     assert bwd(dt=-1) == 3 and bwd(R=-1) == 2
     assert bwd(dWg=None) == 1 and bwd(dWu=None) == 1 and bwd(dg=None) == 1 and bwd(x=None) == 1
+    need = lib.gated_ffn_backward_workspace_bytes(300, 256, 4096, 1)
+    assert need >= 2 * 300 * 256 * 4 and need % (300 * 256 * 4) == 0
+    big = dict(R=300, H=256, I=4096)
+    assert bwd(ws=None, **big) == 5 and bwd(ws_bytes=need - 1, **big) == 5 and bwd(ws=FAKE + 4, **big) == 5
+    sizes = lib.gated_ffn_backward_workspace_bytes
+    assert sizes(0, 256, 4096, 1) == 0 and sizes(300, 0, 4096, 1) == 0 and sizes(300, 256, 4096, 7) == 0
+    assert sizes(8192, 8192, 4096, 1) == 0  # fills the chip by itself
 
 
 def test_rope_checks(lib):
