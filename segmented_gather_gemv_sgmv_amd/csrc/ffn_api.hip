@@ -6,8 +6,17 @@ namespace {
 
 using namespace sgmv;
 
-// Rows up to which the forward streams the weights through the rows kernel.
+// Rows up to which the forward streams the weights, by rows or strips.
 constexpr int kFfnRowsMax = 64;
+
+// More rows still take strips where their blocks of 64 rows x 32 features are at
+// most one round: a tile's workgroup is then alone with the whole of K (bf16, 256
+// rows x 4096 -> 2 x 1504: 30 us by strips, 45 by tiles; 192 x 1000 -> 2400: 12
+// and 18; 512 x 1000 -> 800: 12 and 18).  Beyond a round tiles win (256 x 1000 ->
+// 2400: 21 and 19; 128 x 4096 -> 11008: 96 and 66).
+inline bool ffn_takes_strips(const RowsArgs& a) {
+    return a.xvec && a.wvec && ceil_div(a.R, 64) * ceil_div(a.N, 32) <= 256;
+}
 
 int check_ffn(int R, int H, int I, int act, int dtype) {
     if (!known_dtype(dtype)) return SGMV_ERR_BAD_DTYPE;
@@ -27,7 +36,7 @@ int run_rows(const RowsArgs& a, hipStream_t st) {
 
 template <typename DT>
 int run_forward(const RowsArgs& a, hipStream_t st) {
-    if (a.R <= kFfnRowsMax) {
+    if (a.R <= kFfnRowsMax || (DT::kBytes == 2 && ffn_takes_strips(a))) {
         if (a.R <= 4) return run_rows<DT, 4, 1, 2>(a, st);
         if (a.R <= 16) return run_rows<DT, 16, 1, 2>(a, st);
         if constexpr (DT::kBytes == 2) {

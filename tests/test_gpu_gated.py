@@ -81,6 +81,18 @@ def test_forward(R, H, I, dt):
         check(h, *gated_forward(g, u, eg, eu, "silu", x.dtype), f"gated_ffn {R}x{H}->{I} {dt}")
 
 
+# Rows and features enough for tiles in the 16-bit types too: ragged tiles of rows
+# and features, K remainders, K below one step.
+@pytest.mark.parametrize("dt", ["f16", "bf16", "f32"])
+@pytest.mark.parametrize("R,H,I", [(520, 72, 1000), (1000, 520, 520), (130, 24, 4400), (2000, 8, 300),
+                                   (700, 200, 904)])
+def test_forward_by_tiles(R, H, I, dt):
+    x, Wg, Wu, ag, au, _ = _inputs(R, H, I, dt, True, seed=9)
+    h = sg.gated_ffn(x, Wg, Wu, gate_add=ag, up_add=au)
+    g, eg, u, eu = _pre(x, Wg, Wu, ag, au)
+    check(h, *gated_forward(g, u, eg, eu, "silu", x.dtype), f"gated_ffn {R}x{H}->{I} {dt}")
+
+
 @pytest.mark.parametrize("act", ACTS)
 @pytest.mark.parametrize("R", [3, 90])
 def test_activations(act, R):
