@@ -102,6 +102,20 @@ __device__ __forceinline__ void meta_values(uint32_t m, float& s, float& zb) {
     zb = f[1];
 }
 
+// A piece of codes less their zero point, from the piece of codes biased by 16
+// and zb = 16 + z: whole numbers of up to 8 bits, exact in bf16.  float32 results
+// take them so; biased codes with 16 + z taken out of the sum are fewer
+// instructions, but their sums are several times the result's size, and its
+// rounding with them (5 rows x 1000: error 5e-7 that way, 1e-7 this way).
+__device__ __forceinline__ uint4 codes_less_zero(const uint4& biased, float zb) {
+    auto one = [zb](uint32_t d) {
+        const uint32_t lo = __float_as_uint(__uint_as_float(d << 16) - zb);
+        const uint32_t hi = __float_as_uint(__uint_as_float(d & 0xFFFF0000u) - zb);
+        return (lo >> 16) | (hi & 0xFFFF0000u);
+    };
+    return make_uint4(one(biased.x), one(biased.y), one(biased.z), one(biased.w));
+}
+
 // n dwords at p in one load (p aligned to 4 n bytes).
 template <int N>
 __device__ __forceinline__ void load_dwords(const void* p, uint32_t* out) {
@@ -282,8 +296,9 @@ __global__ __launch_bounds__(kRowsThreads) void rows_kernel(RowsArgs a) {
             }
         }
         if constexpr (Src::kQ4) {
-            // Sum of x over each flush, in every column: the codes enter biased
-            // by 16, which is taken out with the zero point.
+            // 16-bit types: the codes enter biased by 16, which is taken out with
+            // the zero point by the sum of x over each flush, in every column.
+            constexpr bool kBiased = DT::kBytes == 2;
 #pragma unroll
             for (int f = 0; f < kFlushes; ++f) {
                 acc4_t sx[MT];
@@ -291,10 +306,8 @@ __global__ __launch_bounds__(kRowsThreads) void rows_kernel(RowsArgs a) {
                 for (int i = 0; i < MT; ++i) {
                     sx[i] = acc4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                    for (int s = 0; s < FL; ++s)
-#pragma unroll
-                        for (int p = 0; p < XP; ++p)
-                            sx[i] = PieceOps<CT>::mma(xv[f * FL + s][i][p], ones_piece<CT>(), sx[i]);
+                    for (int s = 0; s < (kBiased ? FL : 0); ++s)
+                        sx[i] = PieceOps<CT>::mma(xv[f * FL + s][i][0], ones_piece<CT>(), sx[i]);
                 }
 #pragma unroll
                 for (int q = 0; q < NM; ++q)
@@ -311,7 +324,10 @@ __global__ __launch_bounds__(kRowsThreads) void rows_kernel(RowsArgs a) {
                         }
                         uint4 wp[FL];
 #pragma unroll
-                        for (int s = 0; s < FL; ++s) wp[s] = codes_biased<CT>(wd[f * FL + s]);
+                        for (int s = 0; s < FL; ++s) {
+                            wp[s] = codes_biased<CT>(wd[f * FL + s]);
+                            if constexpr (!kBiased) wp[s] = codes_less_zero(wp[s], zb);
+                        }
 #pragma unroll
                         for (int i = 0; i < MT; ++i) {
                             acc4_t t = acc4_t{0.f, 0.f, 0.f, 0.f};
@@ -322,7 +338,7 @@ __global__ __launch_bounds__(kRowsThreads) void rows_kernel(RowsArgs a) {
                                     t = PieceOps<CT>::mma(xv[f * FL + s][i][p], wp[s], t);
 #pragma unroll
                             for (int e = 0; e < 4; ++e)
-                                acc[q][i][j][e] += sc * (t[e] - zb * sx[i][e]);
+                                acc[q][i][j][e] += sc * (kBiased ? t[e] - zb * sx[i][e] : t[e]);
                         }
                         // One n-tile's products at a time: interleaved freely, their
                         // partial sums spill.
