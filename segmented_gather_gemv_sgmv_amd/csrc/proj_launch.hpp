@@ -80,7 +80,8 @@ inline TilePlan plan_tiles(long long M, long long N, int batches, bool gated, bo
     offer(kWideTiles, none, all, 0.);
     offer(kMidTiles, none, all, 0.);
     // 4096 x 4096 -> 2 x 11008 is 1376 tiles, 5.4 rounds: 728 us as six rounds,
-    // 717 as five and one of 128 x 256 tiles; its weights' gradients 650 and 631.  The second launch is priced at 4 us.
+    // 717 as five and one of 128 x 256 tiles; its weights' gradients 650 and 631.
+    // The second launch is priced at 4 us.
     const long long tm = ceil_div(M, 256), tn = ceil_div(N, bn);
     const long long rounds = tm * tn * batches / 256;
     if (rounds > 0) {

@@ -5,10 +5,12 @@
 // (of one matrix, or of both of the gated block) and 16 * MT rows, and its
 // eight waves split K in blocks of four operand pieces, so every weight is
 // read once per 16 * MT rows, straight from memory into the MFMA operand
-// registers, PD blocks ahead of its use; the eight float32 partial tiles are
-// added in a fixed order through LDS.  Rows ride in the MFMA's 16 columns: a
-// single row costs the same matrix-core time as 16, which is far below the
-// weights' stream time.
+// registers, PD blocks ahead of its use (one fp16 row, 4096 -> 4096 in 4 bits,
+// 8.7 MB: 4.7 us, against 3.1 for a plain stream of those bytes; one bf16 row
+// through the gated block of 4096 -> 11008, 180 MB: 33 us against 28); the eight
+// float32 partial tiles are added in a fixed order through LDS.  Rows ride in
+// the MFMA's 16 columns: a single row costs the same matrix-core time as 16,
+// which is far below the weights' stream time.
 //
 // x is the first MFMA operand, so a lane's sums all belong to one output
 // feature, lane % 16, and a 4-bit weight's scale is one value per lane.
@@ -265,8 +267,8 @@ __global__ __launch_bounds__(kRowsThreads) void rows_kernel(RowsArgs a) {
 #pragma unroll
             for (int s = 0; s < kXLoads; ++s) {
                 if constexpr (XR == 16) {
-                    b.x[i][s] = load_piece<DT>(xrow[i], k0 + (s / XL) * Src::kStepK + XL * PK * lg + PK * (s % XL),
-                                               a.K, a.xvec);
+                    b.x[i][s] = load_piece<DT>(
+                        xrow[i], k0 + (s / XL) * Src::kStepK + XL * PK * lg + PK * (s % XL), a.K, a.xvec);
                 } else {
                     b.x[i][s] = load_piece<DT>(xrow[i], k0 + lr / 4 * Src::kStepK + PK * lg, a.K, a.xvec);
                 }
