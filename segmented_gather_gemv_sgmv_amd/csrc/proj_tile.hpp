@@ -9,14 +9,16 @@
 // its buffer's range).  Operands that no 16-byte load fits go through registers
 // instead (kDma false), several times slower.
 //
-// Bound: the MFMA and LDS rates together.  A step of a 256 x 256 tile is 64 MFMAs
-// per SIMD, 0.57 us at the 1.8 GHz the chip holds under this load; its LDS reads
-// (12 KB per wave) and the loads' writes keep the LDS busy for about as long.
-// Measured, bf16: 0.85 us a step where the tiles are one round (4096 x 4096 from
-// 2 x 10240: 1.25 PFLOP/s), 0.95 us over several rounds of the forward
-// (4096 x 4096 -> 2 x 10240: 611 us, 1.12 PFLOP/s).  The same loop with the
-// barrier at the end of a step took 680 us: the next step's operands then arrive
-// with no products left to hide them.  Two waves per SIMD is what the sums (128
+// Bound: the matrix cores at the clock the chip holds under them.  A step of a
+// 256 x 256 tile is 64 MFMAs per SIMD, 0.57 us at the 1.8 GHz measured under this
+// load (2.4 GHz without; products of random values alone, out of registers, reach
+// 1.75 to 2.0 PFLOP/s).  Measured, bf16: 0.78 us a step where the tiles are one
+// round (dx of 4096 x 4096 from 2 x 10240: 1.35 PFLOP/s), 0.92 us over several
+// rounds of the forward (4096 x 4096 -> 2 x 10240: 585 us, 1.17 PFLOP/s), matrix
+// cores busy 59 to 61 % of the cycles, LDS reads 22 %, no bank conflicts; loads
+// that all hit L2 change nothing.  The same loop with the barrier at the end of a
+// step is 14 % slower: the next step's operands then arrive with no products left
+// to hide them.  Two waves per SIMD is what the sums (128
 // registers a lane) leave room for; four waves of 128 x 128 spill.
 //
 // An operand lies in memory either along K (x, W as used by the forward) or
@@ -535,29 +537,32 @@ __global__ __launch_bounds__(SH::NT) void tile_kernel(TileArgs g) {
                 store_codes(s_b0, ca, 0);
                 store_codes(s_b1, ca, 1);
             }
-            // Step c multiplies stage c % 4.  Its B operands and first A operand are in
-            // registers when it begins (they were read in step c - 1); the other A
-            // operands are read at its start, behind the first products.  In its
-            // middle, with half of its products issued, comes the step's one
+            // Step c multiplies stage c % 4.  Its B operands and the first half of its A
+            // operands (of 4-bit B, whose codes need the registers, one) are in registers when it begins (they were read in step c - 1);
+            // the other A operands are read at its start, behind the first products.
+            // In its middle, with half of its products issued, comes the step's one
             // barrier: this wave's own loads of step c + 1 have landed (only what was
-            // issued after them may be in flight) and so has every other wave's;
-            // and every wave is past its reads of stage (c - 1) % 4, which takes step
-            // c + 3.  The next step's first operands are then read behind the second
-            // half of the products, so that the matrix cores have work on both
-            // sides of the barrier.
+            // issued after them may be in flight) and so has every other wave's; and
+            // every wave is past its reads of stage (c - 1) % 4, which takes step c + 3.
+            // The next step's operands are then read behind the second half of the
+            // products, each A operand into the registers of one that the first half
+            // has used, so that the matrix cores have work on both sides of the
+            // barrier.  Waves in their second half go first (not with 4-bit B, where it
+            // is no faster): their products are what the barrier of the next step
+            // waits for (dx of 4096 x 4096 from 2 x 10240:
+            // 250 us, 256 without, 263 with one A operand read ahead instead of half).
             constexpr int kAfter = kLoads + (kPrefetch ? 1 : 0);
             constexpr int kLanded = (kAfter & 15) | ((kAfter >> 4) << 14) | (BL == kCodes ? 0x0070 : 0x0F70);
-            uint4 a0[2], b[2][TN];  // by parity of the step
+            constexpr int kEarly = BL == kCodes ? 1 : TM / 2;
+            uint4 a[TM], b[2][TN];  // b by parity of the step
             auto step = [&](const uint8_t* sa, const uint8_t* next_a, const uint8_t* next_b,
                             uint8_t* ahead_a, uint8_t* ahead_b, uint8_t* codes_b, int c, auto index,
                             const Codes(&cur)[kUnits], const Codes(&nxt)[kUnits]) {
                 constexpr int s = decltype(index)::value;  // c % 4
                 constexpr int X = s & 1, Y = X ^ 1;
                 fence();
-                uint4 a[TM];
-                a[0] = a0[X];
 #pragma unroll
-                for (int i = 1; i < TM; ++i) a[i] = rd_a(sa, i);
+                for (int i = kEarly; i < TM; ++i) a[i] = rd_a(sa, i);
                 fence();
 #pragma unroll
                 for (int i = 0; i < TM / 2; ++i)
@@ -569,7 +574,9 @@ __global__ __launch_bounds__(SH::NT) void tile_kernel(TileArgs g) {
                 fence();
 #pragma unroll
                 for (int j = 0; j < TN; ++j) b[Y][j] = rd_b(next_b, j);
-                a0[Y] = rd_a(next_a, 0);
+#pragma unroll
+                for (int i = 0; i < kEarly; ++i) a[i] = rd_a(next_a, i);
+                if constexpr (BL != kCodes) __builtin_amdgcn_s_setprio(1);
                 fence();
 #pragma unroll
                 for (int i = TM / 2; i < TM; ++i) {
@@ -582,6 +589,7 @@ __global__ __launch_bounds__(SH::NT) void tile_kernel(TileArgs g) {
                         fence();
                     }
                 }
+                if constexpr (BL != kCodes) __builtin_amdgcn_s_setprio(0);
                 if constexpr (kPrefetch && s % 2 == 0) prefetch(c + kAhead);
                 if constexpr (BL == kCodes) {  // step c + 2, read after the next barrier
                     if (s < 2) store_codes(codes_b, cur, s + 2);
@@ -602,7 +610,8 @@ __global__ __launch_bounds__(SH::NT) void tile_kernel(TileArgs g) {
             fence();
 #pragma unroll
             for (int j = 0; j < TN; ++j) b[0][j] = rd_b(s_b0, j);
-            a0[0] = rd_a(s_a0, 0);
+#pragma unroll
+            for (int i = 0; i < kEarly; ++i) a[i] = rd_a(s_a0, i);
             for (int c = 0; c < nsteps; c += kTurn) {
                 four(c, ca, cb);
                 if constexpr (kTurn == 8) four(c + 4, cb, ca);
