@@ -623,19 +623,28 @@ __global__ __launch_bounds__(SH::NT) void tile_kernel(TileArgs g) {
     // ---- epilogue -------------------------------------------------------------
     T* out = (T*)g.out[kSegs == 2 ? 0 : z];
     constexpr int TNO = kGated ? TN / 2 : TN;
+    const int nw = n0 + wc * (16 * TNO) + 4 * lg;  // this lane's first columns
+    float bias[kGated ? 1 : TNO][4] = {};
+    if constexpr (!kGated) {
+        if (g.add[0]) {
 #pragma unroll
-    for (int j = 0; j < TNO; ++j) {
-        const int n = n0 + wc * (16 * TNO) + 16 * j + 4 * lg;
-        if (n >= N) continue;
-        const int left = N - n;
-        float bias[4] = {0.f, 0.f, 0.f, 0.f};
-        if constexpr (!kGated) {
-            if (g.add[0]) load4f<DT>((const T*)g.add[0] + n, left, g.yvec, bias);
+            for (int j = 0; j < TNO; ++j)
+                if (nw + 16 * j < N)
+                    load4f<DT>((const T*)g.add[0] + nw + 16 * j, N - nw - 16 * j, g.yvec, bias[j]);
         }
+    }
+    // Row by row: a store instruction writes 32 bytes of each of 16 rows, and the
+    // stores that complete its lines come next.  Column by column, L2 passed
+    // lines on half written (both 10240 x 4096 weights' gradients: 397 MB written
+    // for 168; of 11008 rows, 620 us against 578).
 #pragma unroll
-        for (int i = 0; i < TM; ++i) {
-            const int m = m0 + wr0 + 16 * i + lr;
-            if (m >= M) continue;
+    for (int i = 0; i < TM; ++i) {
+        const int m = m0 + wr0 + 16 * i + lr;
+        if (m >= M) continue;
+#pragma unroll
+        for (int j = 0; j < TNO; ++j) {
+            const int n = nw + 16 * j, left = N - n;
+            if (n >= N) continue;
             const long long at = (long long)m * N + n;
             float o[4];
             if constexpr (kGated) {
@@ -656,7 +665,7 @@ __global__ __launch_bounds__(SH::NT) void tile_kernel(TileArgs g) {
                 for (int c = 0; c < 4; ++c) o[c] = act_value(g.act, v[0][c]) * v[1][c];
             } else {
 #pragma unroll
-                for (int c = 0; c < 4; ++c) o[c] = acc[i][j][c] + bias[c];
+                for (int c = 0; c < 4; ++c) o[c] = acc[i][j][c] + bias[j][c];
             }
             if (kSegs == 2 && g.partial)
                 store4f<F32>(g.partial + z * g.partial_stride + at, left, N % 4 == 0, o);
