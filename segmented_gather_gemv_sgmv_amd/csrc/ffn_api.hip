@@ -6,8 +6,16 @@ namespace {
 
 using namespace sgmv;
 
-// Rows up to which the forward streams the weights, by rows or strips.
+// Rows up to which a 16-bit forward streams the weights, by rows or strips.
 constexpr int kFfnRowsMax = 64;
+
+// float32: up to 32 rows, and more while the workgroups of 32 rows x 16 features are
+// about one round; tiles then leave more CUs without work (64 rows x 3968 -> 2 x 1504:
+// 40 us by rows, 77 by tiles; 64 x 1000 -> 2400: 22 and 25; beyond, 64 x 2048 ->
+// 2 x 5504: 64 and 44).
+inline bool ffn_f32_takes_rows(const RowsArgs& a) {
+    return a.R <= 32 || ceil_div(a.R, 32) * ceil_div(a.N, 16) <= 320;
+}
 
 // More rows still take strips where their blocks of 64 rows x 32 features are at
 // most one round: a tile's workgroup is then alone with the whole of K (bf16, 256
@@ -36,7 +44,7 @@ int run_rows(const RowsArgs& a, hipStream_t st) {
 
 template <typename DT>
 int run_forward(const RowsArgs& a, hipStream_t st) {
-    if (a.R <= kFfnRowsMax || (DT::kBytes == 2 && ffn_takes_strips(a))) {
+    if (DT::kBytes == 2 ? a.R <= kFfnRowsMax || ffn_takes_strips(a) : ffn_f32_takes_rows(a)) {
         if (a.R <= 4) return run_rows<DT, 4, 1, 2>(a, st);
         if (a.R <= 16) return run_rows<DT, 16, 1, 2>(a, st);
         if constexpr (DT::kBytes == 2) {

@@ -13,6 +13,10 @@ namespace sgmv {
 using BigTile = TileShape<256, 256, 2, 4>;
 using WideTile = TileShape<128, 256, 2, 4>;
 using MidTile = TileShape<128, 128, 2, 2>;
+// float32, whose products take eight times as long per byte: small tiles cost no
+// more loads than there is time for, and leave fewer CUs without work.
+using SmallTile = TileShape<64, 64, 2, 2>;
+using TallTile = TileShape<128, 64, 2, 2>;
 
 inline long long ceil_div(long long a, long long b) { return (a + b - 1) / b; }
 
@@ -42,7 +46,7 @@ int launch_tiles(TileArgs a, TileRange r, hipStream_t st) {
 // CUs (bf16, measured on whole rounds of products along K and across K): a round
 // of 256 x 256 tiles takes 109 to 122, one of 128 x 256 tiles 62 to 79, two
 // 128 x 128 tiles on each CU 67 to 83 and one on each 42 to 52.
-enum TileKind { kBigTiles, kWideTiles, kMidTiles };
+enum TileKind { kBigTiles, kWideTiles, kMidTiles, kSmallTiles, kTallTiles };
 constexpr double kBigTileUs = 118.;
 constexpr double kBigGatedCodesUs = 150.;  // gated 4-bit tiles: their registers spill
 
@@ -99,17 +103,43 @@ inline TilePlan plan_tiles(long long M, long long N, int batches, bool gated, bo
     return best;
 }
 
+// float32: the time of a step of 16 K, in microseconds, for the tiles a CU gets at
+// most; several share it, so a round more costs little more than its products.
+// Forward, 512 rows x 4096 -> 2 x 11008: 743 us by 128 x 64 tiles, 801 by 64 x 64;
+// 333 x 2048 -> 2 x 5504: 198 and 182; 200 x 3968 -> 2 x 1504: 142 and 82 (by 128 x
+// 128 tiles 800, 261 and 268).
+inline double f32_step_us(TileKind kind, long long tiles) {
+    const double each = (double)ceil_div(tiles, 256);
+    if (kind == kTallTiles) return 0.1 + 0.475 * each;
+    return each <= 1. ? 0.32 : 0.285 * each - 0.05;
+}
+inline long long f32_tiles(TileKind kind, long long M, long long N, bool gated) {
+    return ceil_div(M, kind == kTallTiles ? 128 : 64) * ceil_div(N, gated ? 32 : 64);
+}
+inline TileKind f32_kind(long long M, long long N, int batches, bool gated) {
+    const double tall = f32_step_us(kTallTiles, f32_tiles(kTallTiles, M, N, gated) * batches);
+    const double small = f32_step_us(kSmallTiles, f32_tiles(kSmallTiles, M, N, gated) * batches);
+    return tall < small ? kTallTiles : kSmallTiles;
+}
+
 // The register path (operands no 16-byte load fits) always takes the small tiles.
 template <typename DT, int AL, int BL, int kSegs, bool kGated, int kFlushes = 1>
 int launch_kind(TileKind kind, const TileArgs& a, const TileRange& r, bool direct, hipStream_t st) {
-    if (!direct) return launch_tiles<DT, MidTile, AL, BL, kSegs, kGated, false, kFlushes>(a, r, st);
-    if (kind == kBigTiles)
-        return launch_tiles<DT, BigTile, AL, BL, kSegs, kGated, true, kFlushes>(a, r, st);
-    if constexpr (BL != kCodes) {
-        if (kind == kWideTiles)
-            return launch_tiles<DT, WideTile, AL, BL, kSegs, kGated, true, kFlushes>(a, r, st);
+    if constexpr (DT::kBytes == 4) {
+        if (!direct) return launch_tiles<DT, SmallTile, AL, BL, kSegs, kGated, false, kFlushes>(a, r, st);
+        if (kind == kTallTiles)
+            return launch_tiles<DT, TallTile, AL, BL, kSegs, kGated, true, kFlushes>(a, r, st);
+        return launch_tiles<DT, SmallTile, AL, BL, kSegs, kGated, true, kFlushes>(a, r, st);
+    } else {
+        if (!direct) return launch_tiles<DT, MidTile, AL, BL, kSegs, kGated, false, kFlushes>(a, r, st);
+        if (kind == kBigTiles)
+            return launch_tiles<DT, BigTile, AL, BL, kSegs, kGated, true, kFlushes>(a, r, st);
+        if constexpr (BL != kCodes) {
+            if (kind == kWideTiles)
+                return launch_tiles<DT, WideTile, AL, BL, kSegs, kGated, true, kFlushes>(a, r, st);
+        }
+        return launch_tiles<DT, MidTile, AL, BL, kSegs, kGated, true, kFlushes>(a, r, st);
     }
-    return launch_tiles<DT, MidTile, AL, BL, kSegs, kGated, true, kFlushes>(a, r, st);
 }
 
 // Plans and launches a whole product.
@@ -117,20 +147,25 @@ template <typename DT, int AL, int BL, int kSegs, bool kGated, int kFlushes = 1>
 int launch_tiles_any(const TileArgs& a, bool direct, hipStream_t st) {
     const TileRange all{0, a.M, 0, a.N};
     if (!direct) return launch_kind<DT, AL, BL, kSegs, kGated, kFlushes>(kMidTiles, a, all, false, st);
-    const TilePlan p = plan_tiles(a.M, a.N, a.batches, kGated, BL == kCodes);
-    if (p.big.m_end > 0) {
-        const int rc = launch_kind<DT, AL, BL, kSegs, kGated, kFlushes>(kBigTiles, a, p.big, true, st);
-        if (rc != SGMV_OK) return rc;
+    if constexpr (DT::kBytes == 4) {
+        return launch_kind<DT, AL, BL, kSegs, kGated>(f32_kind(a.M, a.N, a.batches, kGated), a, all,
+                                                      true, st);
+    } else {
+        const TilePlan p = plan_tiles(a.M, a.N, a.batches, kGated, BL == kCodes);
+        if (p.big.m_end > 0) {
+            const int rc = launch_kind<DT, AL, BL, kSegs, kGated, kFlushes>(kBigTiles, a, p.big, true, st);
+            if (rc != SGMV_OK) return rc;
+        }
+        return launch_kind<DT, AL, BL, kSegs, kGated, kFlushes>(p.kind, a, p.rest, true, st);
     }
-    return launch_kind<DT, AL, BL, kSegs, kGated, kFlushes>(p.kind, a, p.rest, true, st);
 }
 
 // How the sum of two products over K is taken: by one workgroup per tile, or
 // (ranges > 1) in ranges of K, each by a workgroup of its own that leaves its
 // float32 sums, joined by a second kernel.  Outputs of a few tiles are worth it:
 // their long K would run on a few CUs (1237 rows x 1000 from 2 x 2744, f16:
-// 64 us in one range, 32 in three; 512 x 2048 from 2 x 5504: bf16 105 and 38 in
-// eight, f32 723 and 198 in eight).
+// 64 us in one range, 32 in three; 512 x 2048 from 2 x 5504, bf16: 105 and 38 in
+// eight).
 struct SumPlan {
     TileKind kind;
     int ranges, range_steps;
@@ -142,22 +177,22 @@ constexpr long long kMaxSumBytes = 64ll << 20;
 inline SumPlan plan_sum(long long M, long long N, long long K, int dtype) {
     const bool f32 = dtype == SGMV_F32;
     const long long steps = ceil_div(2 * ceil_div(K, f32 ? 16 : 32), 4) * 4;
-    // Microseconds per step: 128 steps of 32 K are 4096; float32 steps (of 16 K)
-    // multiply three terms on each side.
-    const double per = (f32 ? 4. : 1.) / 128.;
+    // Microseconds per step of 32 (float32: 16) K; 128 of 32 are 4096.
+    auto step_us = [&](TileKind kind, int ranges) {
+        if (f32) return f32_step_us(kind, f32_tiles(kind, M, N, false) * ranges);
+        return tiles_us(kind, ceil_div(M, 128) * ceil_div(N, kind == kMidTiles ? 128 : 256) * ranges) / 128.;
+    };
     const long long stride = ceil_div(M * N, 64) * 64;
-    SumPlan best{kBigTiles, 1, (int)steps, stride};
-    double best_us = plan_tiles(M, N, 1, false, false).us * steps * per;
+    SumPlan best{f32 ? f32_kind(M, N, 1, false) : kBigTiles, 1, (int)steps, stride};
+    double best_us = steps * (f32 ? step_us(best.kind, 1) : plan_tiles(M, N, 1, false, false).us / 128.);
     if (stride > kMaxSumBytes / 8) return best;
-    const long long wide = ceil_div(M, 128) * ceil_div(N, 256);
-    const long long mid = ceil_div(M, 128) * ceil_div(N, 128);
     for (int ranges = 2; ranges <= 64; ++ranges) {
         const long long each = ceil_div(steps, 4ll * ranges) * 4;
         if (each < 16 || ranges * stride * 4 > kMaxSumBytes) break;
         if (ceil_div(steps, each) != ranges) continue;
         const double join = 5. + ranges * stride * 8 / 4e6;  // written and read at 4 TB/s
-        for (const TileKind kind : {kWideTiles, kMidTiles}) {
-            const double us = join + each * per * tiles_us(kind, ranges * (kind == kWideTiles ? wide : mid));
+        for (const TileKind kind : {f32 ? kTallTiles : kWideTiles, f32 ? kSmallTiles : kMidTiles}) {
+            const double us = join + each * step_us(kind, ranges);
             if (us < best_us) {
                 best_us = us;
                 best = SumPlan{kind, ranges, (int)each, stride};
