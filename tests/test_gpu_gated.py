@@ -269,6 +269,23 @@ def test_repeats_and_graph_replay():
                    for a, b in zip(res, sg.gated_ffn_backward(dh, x, Wg, Wu, g, u)))
 
 
+def test_gradients_on_another_stream():
+    """dx in ranges, whose workspace is then that stream's, behind other work there."""
+    x, Wg, Wu, _, _, dh = _inputs(200, 256, 4096, "f16", False, seed=10)
+    g, u = dh * 0.5, dh * 0.25
+    want = sg.gated_ffn_backward(dh, x, Wg, Wu, g, u)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        a = torch.randn(2048, 2048, device=DEV)
+        for _ in range(5):
+            a = a @ a * 1e-3
+        late = dh.clone() + a[0, 0] * 0
+        got = sg.gated_ffn_backward(torch.where(late == late, late, dh), x, Wg, Wu, g, u)
+    s.synchronize()
+    assert all(torch.equal(p, q) for p, q in zip(got, want))
+
+
 def test_refusals():
     x, Wg, Wu, ag, _, dh = _inputs(4, 40, 48, "f16", True)
     with pytest.raises(ValueError, match="act"):

@@ -84,6 +84,26 @@ def test_wide_tiles(dt):
     _linear(3300, 200, 4096, 64, dt, zeros=True, bias=True)
 
 
+# A little more than a round of 256 x 256 tiles: the rest of the rows or of the
+# columns takes smaller ones.
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("R,K,N,G", [(4352, 72, 4400, 32), (2300, 136, 7500, 64), (4100, 40, 4200, 128)])
+def test_rest_tiles(R, K, N, G, dt):
+    _linear(R, K, N, G, dt, zeros=True, bias=True, seed=12)
+
+
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("R,K,N,G", [(4200, 72, 2200, 64), (2300, 40, 4000, 128)])
+def test_gated_rest_tiles(R, K, N, G, dt):
+    gen = torch.Generator().manual_seed(13)
+    dtype = DTYPES[dt]
+    wg, wu = (make_q4(gen, N, K, G, dtype, z, DEV) for z in (True, False))
+    x = _x(gen, R, K, dtype)
+    (g, dg), (u, du) = (q4_product(x, w, K, G, True) for w in (wg, wu))
+    h = sg.q4_gated_ffn(x, *(sg.q4_pack(*w, group_size=G, in_features=K) for w in (wg, wu)))
+    check(h, *gated_forward(g, u, dg, du, "silu", dtype), f"gated rest {R}x{K}->{N} G={G} {dt}")
+
+
 @pytest.mark.parametrize("dt", ["f16", "bf16", "f32"])
 @pytest.mark.parametrize("act", ["silu", "gelu", "gelu_tanh", "relu", "sigmoid"])
 @pytest.mark.parametrize("R,K,N,G", [(1, 256, 64, 128), (7, 136, 43, 32), (40, 520, 96, 64),
