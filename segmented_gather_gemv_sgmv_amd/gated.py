@@ -133,7 +133,10 @@ def gated_ffn(x, Wg, Wu, act: str = "silu", gate_add=None, up_add=None, out=None
     once.  x [R, in], Wg and Wu [hidden, in] (torch's linear layout), addends
     [R, hidden] or None; ``act`` is silu, gelu, gelu_tanh, relu or sigmoid.
     Under autograd the pre-activations are kept in x's dtype for the backward
-    pass; ``out`` (optional) receives h and is only for calls without it."""
+    pass; ``out`` (optional) receives h and is only for calls without it.  A
+    backward pass may be captured into a graph once no graph that eager calls
+    recorded on the same leaves is alive (the engine would wait for their
+    stream inside the capture)."""
     torch = _torch()
     inputs = (x, Wg, Wu, gate_add, up_add)
     if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in inputs):

@@ -269,6 +269,37 @@ def test_repeats_and_graph_replay():
                    for a, b in zip(res, sg.gated_ffn_backward(dh, x, Wg, Wu, g, u)))
 
 
+def test_captured_training_pass():
+    """Forward and backward through autograd in one graph: replays against eager passes.  No
+    eager graph of the captured leaves is alive at the capture."""
+    x, Wg, Wu, ag, au, dh = _inputs(120, 136, 2056, "bf16", True, seed=11)
+    leaves = [t.requires_grad_() for t in (x, Wg, Wu, ag, au)]
+    eager = [t.detach().clone().requires_grad_() for t in leaves]
+
+    def step(v):
+        h = sg.gated_ffn(v[0], v[1], v[2], "gelu", v[3], v[4])
+        return [h.detach()] + list(torch.autograd.grad(h, v, dh))
+
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        step(leaves)
+    torch.cuda.current_stream().wait_stream(s)
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        got = step(leaves)
+    gen = torch.Generator().manual_seed(12)
+    for _ in range(3):
+        with torch.no_grad():
+            for t, e in zip(leaves, eager):
+                t.copy_((torch.randn(t.shape, generator=gen) * 0.1).to(t.dtype))
+                e.copy_(t)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(p, q) for p, q in zip(got, step(eager)))
+
+
 def test_gradients_on_another_stream():
     """dx in ranges, whose workspace is then that stream's, behind other work there."""
     x, Wg, Wu, _, _, dh = _inputs(200, 256, 4096, "f16", False, seed=10)
