@@ -538,19 +538,19 @@ __global__ __launch_bounds__(SH::NT) void tile_kernel(TileArgs g) {
                 store_codes(s_b1, ca, 1);
             }
             // Step c multiplies stage c % 4.  Its B operands and the first half of its A
-            // operands (of 4-bit B, whose codes need the registers, one) are in registers when it begins (they were read in step c - 1);
-            // the other A operands are read at its start, behind the first products.
-            // In its middle, with half of its products issued, comes the step's one
-            // barrier: this wave's own loads of step c + 1 have landed (only what was
-            // issued after them may be in flight) and so has every other wave's; and
-            // every wave is past its reads of stage (c - 1) % 4, which takes step c + 3.
-            // The next step's operands are then read behind the second half of the
-            // products, each A operand into the registers of one that the first half
-            // has used, so that the matrix cores have work on both sides of the
-            // barrier.  Waves in their second half go first (not with 4-bit B, where it
-            // is no faster): their products are what the barrier of the next step
-            // waits for (dx of 4096 x 4096 from 2 x 10240:
-            // 250 us, 256 without, 263 with one A operand read ahead instead of half).
+            // operands (of 4-bit B, whose codes need the registers, one) are in registers
+            // when it begins (they were read in step c - 1); the other A operands are read
+            // at its start, behind the first products. In its middle, with half of its
+            // products issued, comes the step's one barrier: this wave's own loads of step c
+            // + 1 have landed (only what was issued after them may be in flight) and so has
+            // every other wave's; and every wave is past its reads of stage (c - 1) % 4,
+            // which takes step c + 3. The next step's operands are then read behind the
+            // second half of the products, each A operand into the registers of one that the
+            // first half has used, so that the matrix cores have work on both sides of the
+            // barrier.  Waves in their second half go first (not with 4-bit B, where it is
+            // no faster): their products are what the barrier of the next step waits for (dx
+            // of 4096 x 4096 from 2 x 10240: 250 us, 256 without, 263 with one A operand
+            // read ahead instead of half).
             constexpr int kAfter = kLoads + (kPrefetch ? 1 : 0);
             constexpr int kLanded = (kAfter & 15) | ((kAfter >> 4) << 14) | (BL == kCodes ? 0x0070 : 0x0F70);
             constexpr int kEarly = BL == kCodes ? 1 : TM / 2;
