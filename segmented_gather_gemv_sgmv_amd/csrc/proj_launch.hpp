@@ -65,7 +65,8 @@ struct TilePlan {
     double us;
 };
 
-// 4-bit weights have no 128 x 256 tiles: unpacking them for 128 rows costs what
+// 128 x 256 tiles: 2048 rows x 4096 from 2 x 11008, f16, 365 us, without them 470.
+// 4-bit weights have none: unpacking them for 128 rows costs what
 // the larger tile saves (512 x 5120 -> 13824: 104 us against 99 by 128 x 128 tiles).
 inline TilePlan plan_tiles(long long M, long long N, int batches, bool gated, bool codes) {
     const double big_us = gated && codes ? kBigGatedCodesUs : kBigTileUs;
@@ -83,8 +84,8 @@ inline TilePlan plan_tiles(long long M, long long N, int batches, bool gated, bo
     };
     offer(kWideTiles, none, all, 0.);
     offer(kMidTiles, none, all, 0.);
-    // 4096 x 4096 -> 2 x 11008 is 1376 tiles, 5.4 rounds: 728 us as six rounds,
-    // 717 as five and one of 128 x 256 tiles; its weights' gradients 650 and 631.
+    // 4096 x 4096 -> 2 x 11008 is 1376 tiles, 5.4 rounds: 690 us as six rounds,
+    // 676 as five and one of 128 x 256 tiles; its weights' gradients 625 and 606.
     // The second launch is priced at 4 us.
     const long long tm = ceil_div(M, 256), tn = ceil_div(N, bn);
     const long long rounds = tm * tn * batches / 256;

@@ -13,8 +13,8 @@ namespace sgmv {
 // they take per 4096 of K.  Strips run at a steady rate, 240 us for 4096 x 4096
 // outputs (350 with a scale per 32 K); for tiles see above, gated 256 x 256 tiles
 // taking 150 us a round.  Measured, 4096 x 4096 weights, bf16: 1024 rows 48 us by
-// strips, 52 by tiles; 1531 rows 78 and 73; 5120 -> 13824: 512 rows 134 and 95,
-// 2048 rows 506 and 300.  Calls of up to kQ4ExactRows rows never round.
+// strips, 52 by tiles; 1531 rows 78 and 72; 5120 -> 13824: 512 rows 134 and 96,
+// 2048 rows 506 and 288.  Calls of up to kQ4ExactRows rows never round.
 constexpr int kQ4ExactRows = 256;
 
 inline bool q4_takes_tiles(int R, int N, int flushes, bool gated) {
