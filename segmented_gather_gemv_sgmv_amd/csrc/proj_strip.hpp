@@ -15,6 +15,8 @@
 // each block of rows (64 rows 22.9 us, 256 rows 72).
 #pragma once
 
+#include <type_traits>
+
 #include "proj_rows.hpp"
 
 namespace sgmv {
@@ -188,13 +190,16 @@ __global__ __launch_bounds__(kRowsThreads) void strip_kernel(RowsArgs a) {
     // Block `it`: x has landed for this wave (only what was issued after it may be
     // outstanding: S - 1 weight blocks and S - 2 x blocks) and, after the barrier,
     // for every wave, each past block it - 1; then the stage that held that block
-    // takes block it + S - 1.
+    // takes block it + S - 1.  That count is of the loop's loads: the steps after the
+    // loop load weights that nobody uses, which the compiler drops, so they wait for
+    // every load instead (the second of three would else read a block in flight).
     constexpr int kAfter = (S - 1) * kWLoads + (S - 2) * kXLoads;
     static_assert(kAfter < 64, "the wait count fits vmcnt");
-    constexpr int kWait = (kAfter & 15) | ((kAfter >> 4) << 14) | 0x0070;
-    auto step = [&](uint8_t* st, uint8_t* ahead, Block& b, int it) {
+    using InLoop = std::integral_constant<int, (kAfter & 15) | ((kAfter >> 4) << 14) | 0x0070>;
+    using AllLoads = std::integral_constant<int, 0x0070>;
+    auto step = [&](auto wait, uint8_t* st, uint8_t* ahead, Block& b, int it) {
         fence();
-        __builtin_amdgcn_s_waitcnt(kWait);
+        __builtin_amdgcn_s_waitcnt(decltype(wait)::value);
         __builtin_amdgcn_s_barrier();
         fence();
         issue_x(ahead, it + S - 1);
@@ -224,17 +229,21 @@ __global__ __launch_bounds__(kRowsThreads) void strip_kernel(RowsArgs a) {
     }
     int it = 0;
     for (; it + S <= nit; it += S) {
-        step(s_x0, S == 2 ? s_x1 : S == 3 ? s_x2 : s_x3, blk[0], it);
-        step(s_x1, s_x0, blk[1], it + 1);
-        if constexpr (S > 2) step(s_x2, s_x1, blk[2], it + 2);
-        if constexpr (S > 3) step(s_x3, s_x2, blk[S - 1], it + 3);
+        step(InLoop{}, s_x0, S == 2 ? s_x1 : S == 3 ? s_x2 : s_x3, blk[0], it);
+        step(InLoop{}, s_x1, s_x0, blk[1], it + 1);
+        if constexpr (S > 2) step(InLoop{}, s_x2, s_x1, blk[2], it + 2);
+        if constexpr (S > 3) step(InLoop{}, s_x3, s_x2, blk[S - 1], it + 3);
     }
-    if (it < nit) step(s_x0, S == 2 ? s_x1 : S == 3 ? s_x2 : s_x3, blk[0], it);
-    if (S > 2 && it + 1 < nit) step(s_x1, s_x0, blk[1], it + 1);
+    if (it < nit) step(AllLoads{}, s_x0, S == 2 ? s_x1 : S == 3 ? s_x2 : s_x3, blk[0], it);
+    if (S > 2 && it + 1 < nit) step(AllLoads{}, s_x1, s_x0, blk[1], it + 1);
     if constexpr (S > 3) {
-        if (it + 2 < nit) step(s_x2, s_x1, blk[2], it + 2);
+        if (it + 2 < nit) step(AllLoads{}, s_x2, s_x1, blk[2], it + 2);
     }
-    __syncthreads();  // the last reads, and the loads past the last block, are done
+    // Every wave's last reads are done, and no load past the last block is left in
+    // flight to the stage that the partial sums take.
+    fence();
+    __builtin_amdgcn_s_waitcnt(AllLoads::value);
+    __syncthreads();
 
     // ---- add the groups' partial tiles, finish, store -------------------------
     float* part = reinterpret_cast<float*>(s_x0);
