@@ -134,20 +134,23 @@ enum { kActSilu = 0, kActGelu = 1, kActGeluTanh = 2, kActRelu = 3, kActSigmoid =
 
 __device__ __forceinline__ float sigmoid_f(float g) { return 1.f / (1.f + __expf(-g)); }
 
-// tanh by the exponential, 1 - 2 / (e^(2 z) + 1): absolute error a few
-// 2^-24, which is what 1 + tanh needs; both limits are exact.
-__device__ __forceinline__ float tanh_f(float z) { return 1.f - 2.f / (__expf(2.f * z) + 1.f); }
-
 constexpr float kInvSqrt2 = 0.70710678118654752f;
 constexpr float kInvSqrt2Pi = 0.39894228040143268f;
 constexpr float kSqrt2OverPi = 0.79788456080286536f;
 constexpr float kGeluCubic = 0.044715f;
 
+// (1 + tanh z) / 2 is the sigmoid of 2 z, z = sqrt(2 / pi) (g + c g^3).  Taken so, the
+// left tail keeps its relative accuracy; from 1 + tanh z nothing is left of it at
+// g = -5, where the value is -2.3e-7.
+__device__ __forceinline__ float gelu_tanh_arg(float g) {
+    return 2.f * kSqrt2OverPi * (g + kGeluCubic * g * g * g);
+}
+
 __device__ __forceinline__ float act_value(int act, float g) {
     switch (act) {
         case kActSilu: return g * sigmoid_f(g);
         case kActGelu: return g * 0.5f * erfcf(-g * kInvSqrt2);
-        case kActGeluTanh: return 0.5f * g * (1.f + tanh_f(kSqrt2OverPi * (g + kGeluCubic * g * g * g)));
+        case kActGeluTanh: return g * sigmoid_f(gelu_tanh_arg(g));
         case kActRelu: return g < 0.f ? 0.f : g;  // a NaN stays one
         default: return sigmoid_f(g);
     }
@@ -168,10 +171,9 @@ __device__ __forceinline__ void act_value_grad(int act, float g, float& a, float
             return;
         }
         case kActGeluTanh: {
-            const float t = tanh_f(kSqrt2OverPi * (g + kGeluCubic * g * g * g));
-            a = 0.5f * g * (1.f + t);
-            d = 0.5f * (1.f + t) +
-                0.5f * g * (1.f - t * t) * kSqrt2OverPi * (1.f + 3.f * kGeluCubic * g * g);
+            const float z2 = gelu_tanh_arg(g), s = sigmoid_f(z2);
+            a = g * s;
+            d = s + 2.f * g * s * sigmoid_f(-z2) * kSqrt2OverPi * (1.f + 3.f * kGeluCubic * g * g);
             return;
         }
         case kActRelu:
