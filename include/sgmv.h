@@ -419,7 +419,9 @@ int q4_linear(void* y, const void* x, const sgmv_q4_weight* w, const void* bias,
  *     dx = dg Wg + du Wu,  dWg = dg^T x,  dWu = du^T x
  * with dg and du rounded to dtype between the steps.  dx, or dWg and dWu,
  * may be NULL and are then not computed; dg and du are needed.  With
- * num_rows == 0 the weights' gradients are zero.  act' of relu at 0 is 0.
+ * num_rows == 0 the weights' gradients are zero.  act' of relu at 0 is 0.  At
+ * infinities the activations and act' are their limits: a g of minus infinity gives
+ * h = 0 and no gradient.
  * Features beyond 2^20 return SGMV_ERR_UNSUPPORTED.
  * workspace: for dx, at least gated_ffn_backward_workspace_bytes(...) bytes,
  * 16-byte aligned, with the conventions of "Workspace" above: dx of few rows is

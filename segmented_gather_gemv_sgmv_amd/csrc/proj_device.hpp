@@ -146,11 +146,19 @@ __device__ __forceinline__ float gelu_tanh_arg(float g) {
     return 2.f * kSqrt2OverPi * (g + kGeluCubic * g * g * g);
 }
 
+// From |g| = 128 on, silu and both gelus are g or 0 and their slopes 1 or 0 in float32.
+// Their formulas are evaluated no further out, where a cube or a square overflows
+// and infinity times zero would be NaN: a unit masked by the type's lowest value or
+// by minus infinity gives 0 and has no gradient.  A NaN passes.
+constexpr float kActFar = 128.f;
+__device__ __forceinline__ float not_below(float g) { return g < -kActFar ? -kActFar : g; }
+__device__ __forceinline__ float not_above(float g) { return g > kActFar ? kActFar : g; }
+
 __device__ __forceinline__ float act_value(int act, float g) {
     switch (act) {
-        case kActSilu: return g * sigmoid_f(g);
-        case kActGelu: return g * 0.5f * erfcf(-g * kInvSqrt2);
-        case kActGeluTanh: return g * sigmoid_f(gelu_tanh_arg(g));
+        case kActSilu: g = not_below(g); return g * sigmoid_f(g);
+        case kActGelu: g = not_below(g); return g * 0.5f * erfcf(-g * kInvSqrt2);
+        case kActGeluTanh: g = not_below(g); return g * sigmoid_f(gelu_tanh_arg(g));
         case kActRelu: return g < 0.f ? 0.f : g;  // a NaN stays one
         default: return sigmoid_f(g);
     }
@@ -159,21 +167,24 @@ __device__ __forceinline__ float act_value(int act, float g) {
 __device__ __forceinline__ void act_value_grad(int act, float g, float& a, float& d) {
     switch (act) {
         case kActSilu: {
-            const float s = sigmoid_f(g);
+            g = not_below(g);
+            const float n = not_above(g), s = sigmoid_f(n);
             a = g * s;
-            d = s * (1.f + g * (1.f - s));
+            d = s * (1.f + n * (1.f - s));
             return;
         }
         case kActGelu: {
-            const float c = 0.5f * erfcf(-g * kInvSqrt2);
+            g = not_below(g);
+            const float n = not_above(g), c = 0.5f * erfcf(-n * kInvSqrt2);
             a = g * c;
-            d = c + g * __expf(-0.5f * g * g) * kInvSqrt2Pi;
+            d = c + n * __expf(-0.5f * n * n) * kInvSqrt2Pi;
             return;
         }
         case kActGeluTanh: {
-            const float z2 = gelu_tanh_arg(g), s = sigmoid_f(z2);
+            g = not_below(g);
+            const float n = not_above(g), z2 = gelu_tanh_arg(n), s = sigmoid_f(z2);
             a = g * s;
-            d = s + 2.f * g * s * sigmoid_f(-z2) * kSqrt2OverPi * (1.f + 3.f * kGeluCubic * g * g);
+            d = s + 2.f * n * s * sigmoid_f(-z2) * kSqrt2OverPi * (1.f + 3.f * kGeluCubic * n * n);
             return;
         }
         case kActRelu:
