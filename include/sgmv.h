@@ -412,8 +412,9 @@ int q4_linear(void* y, const void* x, const sgmv_q4_weight* w, const void* bias,
  * q4_gated_ffn takes 4-bit weights of one group size, gated_ffn plain ones
  * [out_features, in_features].
  *
- * gated_ffn also stores g and u, rounded to dtype, into g_saved and u_saved
- * [num_rows, out_features] when these are not NULL; gated_ffn_backward takes
+ * gated_ffn also stores g and u, rounded to dtype (finite values past its
+ * largest as that), into g_saved and u_saved [num_rows, out_features] when these
+ * are not NULL; gated_ffn_backward takes
  * them with dh = dL/dh and computes
  *     dg = dh * u * act'(g),  du = dh * act(g)   (also the addends' gradients)
  *     dx = dg Wg + du Wu,  dWg = dg^T x,  dWu = du^T x

@@ -126,6 +126,19 @@ __device__ __forceinline__ void store4f(typename DT::storage* p, int n, bool vec
         if (i < n) p[i] = DT::from_float(f[i]);
 }
 
+// A pre-activation as it is kept for the backward pass: what a 16-bit type cannot hold is
+// kept as its largest finite value (an infinity as it is).  Rounded to infinity it
+// would meet the zeros of dh and of act' there, as NaN.
+template <typename DT>
+__device__ __forceinline__ float kept(float v) {
+    if constexpr (DT::kBytes == 4) {
+        return v;
+    } else {
+        constexpr float kMost = std::is_same<DT, F16>::value ? 65504.f : 0x1.FEp127f;
+        return __builtin_isfinite(v) ? __builtin_amdgcn_fmed3f(v, -kMost, kMost) : v;
+    }
+}
+
 // ---------------------------------------------------------------------------
 // Activations a(g) of the gated block and their derivatives.  `act` is
 // uniform over the launch (SGMV_ACT_* of sgmv.h).

@@ -170,7 +170,7 @@ __device__ __forceinline__ void finish_rows(const RowsArgs& a, const acc4_t (&v)
             for (int q = 0; q < 2; ++q) {
                 p[q] = v[q][c];
                 if (a.add[q]) p[q] += DT::load1((const T*)a.add[q] + at);
-                if (a.save[q]) ((T*)a.save[q])[at] = DT::from_float(p[q]);
+                if (a.save[q]) ((T*)a.save[q])[at] = DT::from_float(kept<DT>(p[q]));
             }
             o = act_value(a.act, p[0]) * p[1];
         } else {

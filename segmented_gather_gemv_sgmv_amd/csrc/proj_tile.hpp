@@ -659,7 +659,12 @@ __global__ __launch_bounds__(SH::NT) void tile_kernel(TileArgs g) {
 #pragma unroll
                         for (int c = 0; c < 4; ++c) v[q][c] += b[c];
                     }
-                    if (g.save[q]) store4f<DT>((T*)g.save[q] + at, left, g.yvec, v[q]);
+                    if (g.save[q]) {
+                        float k[4];
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) k[c] = kept<DT>(v[q][c]);
+                        store4f<DT>((T*)g.save[q] + at, left, g.yvec, k);
+                    }
                 }
 #pragma unroll
                 for (int c = 0; c < 4; ++c) o[c] = act_value(g.act, v[0][c]) * v[1][c];

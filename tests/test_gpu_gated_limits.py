@@ -97,3 +97,21 @@ def test_limits_of_the_derivative(act):
     nan = torch.full((1, 8), math.nan, device=DEV)
     h, dg, du = _of_addends(nan, torch.ones_like(nan), act, torch.ones_like(nan))
     assert bool(torch.isnan(h).all()) and bool(torch.isnan(du).all())
+
+
+@pytest.mark.parametrize("R", [2, 30, 300])
+def test_pre_activations_past_half_precision(R):
+    """g and u of 70000: kept as the largest finite value, so no gradient is
+    infinity times zero.  Where the loss does not depend on h, all are zero."""
+    x = torch.ones(R, 64, dtype=torch.float16, device=DEV)
+    W = torch.full((80, 64), 156.25, dtype=torch.float16, device=DEV)  # x W^T = 10000
+    add = torch.full((R, 80), 60000.0, dtype=torch.float16, device=DEV)
+    leaves = [x.requires_grad_(), add.clone().requires_grad_(), add.clone().requires_grad_()]
+    for act, sign in (("silu", 1), ("sigmoid", 1), ("relu", -1)):
+        h = sg.gated_ffn(leaves[0], sign * W, W, act, sign * leaves[1], leaves[2])
+        grads = torch.autograd.grad(h, leaves, torch.zeros_like(h))
+        assert not any(bool(g.any()) for g in grads), act  # a NaN counts as set
+    g = torch.tensor([[70000.0]], device=DEV)  # in float32 nothing is lost
+    one = torch.ones_like(g)
+    h = sg.gated_ffn(one, g, one, "relu")
+    assert float(h) == 70000.0
