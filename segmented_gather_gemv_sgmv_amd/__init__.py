@@ -191,6 +191,28 @@ def _need(t, name, device, dtype=None, ndim=None):
         raise ValueError(f"{name} must have {ndim} dimensions, got {t.dim()}")
 
 
+_forward_ad = None
+
+
+def _no_tangents(what, *tensors):
+    """Refuses tensors with forward-mode tangents, which ``what`` would drop."""
+    global _forward_ad
+    if _forward_ad is None:
+        import torch.autograd.forward_ad as _forward_ad
+    if getattr(_forward_ad, "_current_level", 0) < 0:  # no level is open: no tangents
+        return
+    if any(t is not None and _forward_ad.unpack_dual(t).tangent is not None for t in tensors):
+        raise RuntimeError(f"{what} has no forward-mode derivative")
+
+
+def _no_gradients(what, *tensors):
+    """Refuses tensors whose gradients or tangents ``what`` would drop."""
+    if _torch().is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors):
+        raise RuntimeError(f"{what} has no gradients: call it under torch.no_grad() or on "
+                           "detached tensors")
+    _no_tangents(what, *tensors)
+
+
 def _segments(seg_indptr, adapter_ids, device):
     torch = _torch()
     _need(seg_indptr, "seg_indptr", device, torch.int32, 1)

@@ -6,13 +6,15 @@
     lora_apply(y, x, A_stack, B_stack, seg, ids, scale)    # ... and the adapters, as ever
 
 W[n, k] = scales[n, k // group_size] * (code[n, k] - zeros[n, k // group_size]),
-zero points 8 where none are given (layouts in include/sgmv.h).
+zero points 8 where none are given (layouts in include/sgmv.h).  These calls
+have no gradients and refuse tensors that would need one; gated_ffn, with plain
+weights, has them.
 """
 from __future__ import annotations
 
 import ctypes
 
-from . import _check, _need, _stream_ptr, _torch, dtype_code, lib
+from . import _check, _need, _no_gradients, _stream_ptr, _torch, dtype_code, lib
 from .gated import _act_code, _addends, _output
 
 
@@ -86,7 +88,9 @@ def _check_weight(w, x, name):
 
 def q4_linear(x, w, bias=None, out=None):
     """y = x W^T (+ bias), float32 sums, rounded once.  x [R, in], ``w`` from
-    q4_pack, bias [out] or None; ``out`` (optional) receives y [R, out]."""
+    q4_pack, bias [out] or None; ``out`` (optional) receives y [R, out].  No
+    gradients (see above)."""
+    _no_gradients("q4_linear", x, bias, out)
     dev = x.device
     _need(x, "x", dev, None, 2)
     _check_weight(w, x, "w")
@@ -106,7 +110,9 @@ def q4_gated_ffn(x, w_gate, w_up, act: str = "silu", gate_add=None, up_add=None,
     """h = act(x Wg^T + gate_add) * (x Wu^T + up_add) in one kernel, rounded
     once.  x [R, in]; the weights from q4_pack, of one shape and group size;
     the addends [R, out] (or None) are what the rows' adapters contribute
-    before the activation; ``out`` (optional) receives h [R, out]."""
+    before the activation; ``out`` (optional) receives h [R, out].  No gradients
+    (see above)."""
+    _no_gradients("q4_gated_ffn", x, gate_add, up_add, out)
     dev = x.device
     _need(x, "x", dev, None, 2)
     _check_weight(w_gate, x, "w_gate")

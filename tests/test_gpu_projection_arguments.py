@@ -1,0 +1,34 @@
+"""What the projections' calls refuse, on GPU tensors: gradients that
+they would drop."""
+import pytest
+import torch
+
+import segmented_gather_gemv_sgmv_amd as sg
+from proj_helpers import make_q4
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+
+
+@pytest.fixture(scope="module")
+def q4():
+    gen = torch.Generator().manual_seed(1)
+    w = sg.q4_pack(*make_q4(gen, 64, 64, 32, torch.float16, True, DEV), group_size=32)
+    x = torch.randn(9, 64, generator=gen).half().to(DEV)
+    return x, w
+
+
+def test_q4_refuses_to_drop_gradients(q4):
+    x, w = q4
+    leaf, add = x.clone().requires_grad_(), x.clone()
+    bias = x[0].clone()
+    for call in (lambda: sg.q4_linear(leaf, w), lambda: sg.q4_linear(x, w, bias.clone().requires_grad_()),
+                 lambda: sg.q4_gated_ffn(leaf, w, w),
+                 lambda: sg.q4_gated_ffn(x, w, w, gate_add=add.clone().requires_grad_()),
+                 lambda: sg.q4_gated_ffn(x, w, w, up_add=add.clone().requires_grad_()),
+                 lambda: sg.q4_linear(x, w, out=x.clone().requires_grad_())):
+        with pytest.raises(RuntimeError, match="gradient"):
+            call()
+    with torch.no_grad():
+        y = sg.q4_linear(leaf, w)
+    assert torch.equal(y, sg.q4_linear(leaf.detach(), w)) and not y.requires_grad
