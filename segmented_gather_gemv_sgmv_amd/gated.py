@@ -2,15 +2,15 @@
 
     h = gated_ffn(x, Wg, Wu, act="silu")       # act(x Wg^T + gate_add) * (x Wu^T + up_add)
 
-Differentiable in x, both weights and both addends; gated_ffn_backward is
-the gradient step by itself.  The addends are what the rows' adapters
+Differentiable (once, in reverse mode) in x, both weights and both addends;
+gated_ffn_backward is the gradient step by itself.  The addends are what the rows' adapters
 contribute before the activation (lora_apply_multi on zeros), so that a batch
 of many adapters is served, and adapters over a frozen base are trained,
 through the same kernel.
 """
 from __future__ import annotations
 
-from . import _check, _need, _stream_ptr, _torch, dtype_code, lib
+from . import _check, _need, _no_tangents, _stream_ptr, _torch, dtype_code, lib
 
 ACTIVATIONS = {"silu": 0, "gelu": 1, "gelu_tanh": 2, "relu": 3, "sigmoid": 4}
 
@@ -139,6 +139,7 @@ def gated_ffn(x, Wg, Wu, act: str = "silu", gate_add=None, up_add=None, out=None
     stream inside the capture)."""
     torch = _torch()
     inputs = (x, Wg, Wu, gate_add, up_add)
+    _no_tangents("gated_ffn", *inputs)
     if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in inputs):
         if out is not None:
             raise ValueError("out cannot be given where gradients are recorded")

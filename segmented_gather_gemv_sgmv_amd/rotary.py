@@ -6,14 +6,14 @@
 
 q [R, q heads, D] and k [R, k heads, D] may be views of a fused projection's
 output (any row and head strides); the first ``rotary_dim`` elements of a
-head turn, the rest is copied.  Differentiable in q and k.
+head turn, the rest is copied.  Differentiable (in reverse mode) in q and k.
 """
 from __future__ import annotations
 
 import ctypes
 import math
 
-from . import _check, _need, _stream_ptr, _torch, dtype_code, lib
+from . import _check, _need, _no_tangents, _stream_ptr, _torch, dtype_code, lib
 
 LAYOUTS = {"half": 0, "interleaved": 1}
 
@@ -211,6 +211,7 @@ def rope(q, k, positions, plan: RopePlan, out=None, inverse: bool = False):
     which is what the gradients take."""
     if not isinstance(plan, RopePlan):
         raise TypeError("plan must be a RopePlan (see rope_plan)")
+    _no_tangents("rope", q, k)
     if out is None:
         return _turn(q, k, positions, plan, inverse)
     if _torch().is_grad_enabled() and any(t is not None and t.requires_grad for t in (q, k)):

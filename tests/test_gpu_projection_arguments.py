@@ -1,7 +1,8 @@
-"""What the projections' calls refuse, on GPU tensors: gradients that
-they would drop."""
+"""What the projections' calls refuse, on GPU tensors: gradients and tangents
+that they would drop."""
 import pytest
 import torch
+import torch.autograd.forward_ad as fwd
 
 import segmented_gather_gemv_sgmv_amd as sg
 from proj_helpers import make_q4
@@ -32,3 +33,21 @@ def test_q4_refuses_to_drop_gradients(q4):
     with torch.no_grad():
         y = sg.q4_linear(leaf, w)
     assert torch.equal(y, sg.q4_linear(leaf.detach(), w)) and not y.requires_grad
+
+
+def test_tangents_are_refused(q4):
+    x, w = q4
+    W = torch.randn(64, 64, device=DEV).half()
+    q = x.view(9, 1, 64)
+    plan, pos = sg.rope_plan(64, device=DEV), torch.arange(9, device=DEV)
+    with fwd.dual_level():
+        dual = fwd.make_dual(x, torch.ones_like(x))
+        dq = fwd.make_dual(q, torch.ones_like(q))
+        for call in (lambda: sg.q4_linear(dual, w), lambda: sg.q4_gated_ffn(x, w, w, up_add=dual),
+                     lambda: sg.gated_ffn(dual, W, W), lambda: sg.gated_ffn(x, W, W, gate_add=dual),
+                     lambda: sg.rope(dq, None, pos, plan), lambda: sg.rope(q, dq, pos, plan),
+                     lambda: sg.rope(dq, None, pos, plan, out=(torch.empty_like(q), None))):
+            with pytest.raises(RuntimeError, match="forward-mode"):
+                call()
+        sg.q4_linear(x, w), sg.gated_ffn(x, W, W), sg.rope(q, None, pos, plan)  # no tangent: fine
+    sg.gated_ffn(x, W, W)
