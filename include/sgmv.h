@@ -363,7 +363,8 @@ int sgmv_group_rows(const int32_t* row_ids, int32_t num_rows, int32_t num_adapte
  * The projections around the adapters: a base model with 4-bit weights, the
  * gated feed-forward block, and rotary positions.  These calls follow the
  * conventions above (device pointers, row-major arrays of one dtype, float32
- * sums, enqueue-only) and need no workspace.
+ * sums, enqueue-only) and need no workspace.  Outputs must not overlap inputs,
+ * except that h may be gate_add or up_add itself and rope works in place.
  */
 
 /*

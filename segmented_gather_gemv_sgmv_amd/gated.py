@@ -21,12 +21,21 @@ def _act_code(act) -> int:
     return ACTIVATIONS[act]
 
 
-def _output(out, shape, like, name="out"):
+def _output(out, shape, like, addends=(), **inputs):
+    """``out`` after its checks, or a new tensor.  A workgroup may write its part of
+    ``out`` while others still read the inputs, so it must lie apart from them; an
+    addend may be ``out`` itself, each element being read where it is written."""
     if out is None:
         return like.new_empty(shape)
-    _need(out, name, like.device, like.dtype, len(shape))
+    _need(out, "out", like.device, like.dtype, len(shape))
     if tuple(out.shape) != tuple(shape):
-        raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(out.shape)}")
+        raise ValueError(f"out must be {tuple(shape)}, got {tuple(out.shape)}")
+    lo = out.data_ptr()
+    hi = lo + out.numel() * out.element_size()
+    others = [*inputs.items()] + [("an addend", a) for a in addends if a is not None and a.data_ptr() != lo]
+    for name, t in others:
+        if t is not None and lo < t.data_ptr() + t.numel() * t.element_size() and t.data_ptr() < hi:
+            raise ValueError(f"out must not overlap {name}")
     return out
 
 
@@ -56,7 +65,7 @@ def _forward(x, Wg, Wu, act, gate_add, up_add, out, save):
     R, H, I = _check_weights(x, Wg, Wu)
     code = _act_code(act)
     ga, ua = _addends(gate_add, up_add, (R, I), x)
-    out = _output(out, (R, I), x)
+    out = _output(out, (R, I), x, (gate_add, up_add), x=x, Wg=Wg, Wu=Wu)
     g = u = None
     if save:
         g, u = x.new_empty((R, I)), x.new_empty((R, I))
@@ -133,10 +142,11 @@ def gated_ffn(x, Wg, Wu, act: str = "silu", gate_add=None, up_add=None, out=None
     once.  x [R, in], Wg and Wu [hidden, in] (torch's linear layout), addends
     [R, hidden] or None; ``act`` is silu, gelu, gelu_tanh, relu or sigmoid.
     Under autograd the pre-activations are kept in x's dtype for the backward
-    pass; ``out`` (optional) receives h and is only for calls without it.  A
-    backward pass may be captured into a graph once no graph that eager calls
-    recorded on the same leaves is alive (the engine would wait for their
-    stream inside the capture)."""
+    pass; ``out`` (optional) receives h, is only for calls without it, and must not
+    overlap the inputs (it may be one of the addends itself).  A backward pass
+    may be captured into a graph once no graph that eager calls recorded on the
+    same leaves is alive (the engine would wait for their stream inside the
+    capture)."""
     torch = _torch()
     inputs = (x, Wg, Wu, gate_add, up_add)
     _no_tangents("gated_ffn", *inputs)

@@ -88,8 +88,8 @@ def _check_weight(w, x, name):
 
 def q4_linear(x, w, bias=None, out=None):
     """y = x W^T (+ bias), float32 sums, rounded once.  x [R, in], ``w`` from
-    q4_pack, bias [out] or None; ``out`` (optional) receives y [R, out].  No
-    gradients (see above)."""
+    q4_pack, bias [out] or None; ``out`` (optional) receives y [R, out] and must not
+    overlap the inputs.  No gradients (see above)."""
     _no_gradients("q4_linear", x, bias, out)
     dev = x.device
     _need(x, "x", dev, None, 2)
@@ -99,7 +99,7 @@ def q4_linear(x, w, bias=None, out=None):
         _need(bias, "bias", dev, x.dtype, 1)
         if bias.shape[0] != N:
             raise ValueError(f"bias must be [{N}], got {tuple(bias.shape)}")
-    out = _output(out, (R, N), x)
+    out = _output(out, (R, N), x, x=x, w=w.tiles, w_scales=w.meta, bias=bias)
     _check(lib().q4_linear(out.data_ptr(), x.data_ptr(), w._ptr,
                            None if bias is None else bias.data_ptr(), R, N, w.in_features,
                            w.group_size, dtype_code(x.dtype), _stream_ptr(dev)), "q4_linear")
@@ -110,8 +110,8 @@ def q4_gated_ffn(x, w_gate, w_up, act: str = "silu", gate_add=None, up_add=None,
     """h = act(x Wg^T + gate_add) * (x Wu^T + up_add) in one kernel, rounded
     once.  x [R, in]; the weights from q4_pack, of one shape and group size;
     the addends [R, out] (or None) are what the rows' adapters contribute
-    before the activation; ``out`` (optional) receives h [R, out].  No gradients
-    (see above)."""
+    before the activation; ``out`` (optional) receives h [R, out] and must not overlap
+    the inputs (it may be one of the addends itself).  No gradients (see above)."""
     _no_gradients("q4_gated_ffn", x, gate_add, up_add, out)
     dev = x.device
     _need(x, "x", dev, None, 2)
@@ -122,7 +122,7 @@ def q4_gated_ffn(x, w_gate, w_up, act: str = "silu", gate_add=None, up_add=None,
     R, N = x.shape[0], w_gate.out_features
     code = _act_code(act)
     ga, ua = _addends(gate_add, up_add, (R, N), x)
-    out = _output(out, (R, N), x)
+    out = _output(out, (R, N), x, (gate_add, up_add), x=x, w_gate=w_gate.tiles, w_up=w_up.tiles)
     _check(lib().q4_gated_ffn(out.data_ptr(), x.data_ptr(), w_gate._ptr, w_up._ptr, ga, ua, R, N,
                               w_gate.in_features, w_gate.group_size, code, dtype_code(x.dtype),
                               _stream_ptr(dev)), "q4_gated_ffn")

@@ -1,5 +1,5 @@
 """What the projections' calls refuse, on GPU tensors: gradients and tangents
-that they would drop."""
+they would drop, and outputs that overlap their inputs."""
 import pytest
 import torch
 import torch.autograd.forward_ad as fwd
@@ -51,3 +51,29 @@ def test_tangents_are_refused(q4):
                 call()
         sg.q4_linear(x, w), sg.gated_ffn(x, W, W), sg.rope(q, None, pos, plan)  # no tangent: fine
     sg.gated_ffn(x, W, W)
+
+
+def test_outputs_apart_from_inputs(q4):
+    x, w = q4
+    W = torch.randn(64, 64, device=DEV).half()
+    flat = torch.zeros(3 * 9 * 64, dtype=torch.float16, device=DEV)
+    rows = lambda at: flat[at:at + 9 * 64].view(9, 64)
+    for out, a in ((rows(0), rows(0)), (rows(64), rows(0)), (rows(0), rows(64))):
+        for call in (lambda: sg.q4_linear(a, w, out=out), lambda: sg.q4_gated_ffn(a, w, w, out=out),
+                     lambda: sg.gated_ffn(a, W, W, out=out)):
+            with pytest.raises(ValueError, match="overlap"):
+                call()
+    for call in (lambda: sg.q4_linear(x, w, bias=flat[64:128], out=rows(0)),
+                 lambda: sg.gated_ffn(x, W, W, out=W[:9]), lambda: sg.gated_ffn(x, W, W.clone(), out=W[5:14]),
+                 lambda: sg.q4_gated_ffn(x, w, w, up_add=rows(64), out=rows(0)),
+                 lambda: sg.gated_ffn(x, W, W, gate_add=rows(0), out=rows(64))):
+        with pytest.raises(ValueError, match="overlap"):
+            call()
+    # an addend may be the output itself: each element is read where it is written
+    add = torch.randn(9, 64, device=DEV).half()
+    want = sg.gated_ffn(x, W, W, gate_add=add)
+    wantq = sg.q4_gated_ffn(x, w, w, up_add=add)
+    a, b = add.clone(), add.clone()
+    assert torch.equal(sg.gated_ffn(x, W, W, gate_add=a, out=a), want)
+    assert torch.equal(sg.q4_gated_ffn(x, w, w, up_add=b, out=b), wantq)
+    sg.q4_linear(rows(0), w, out=rows(9 * 64))  # side by side is apart

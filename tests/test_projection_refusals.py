@@ -35,3 +35,22 @@ def test_tangents_are_refused():
                 call()
         with pytest.raises(ValueError, match="must be on"):
             sg.gated_ffn(x, x, x)  # no tangent: past that check
+
+
+def test_outputs_apart_from_inputs(monkeypatch):
+    """The check itself, on CPU tensors (the GPU's calls make it too)."""
+    from segmented_gather_gemv_sgmv_amd import gated
+    monkeypatch.setattr(gated, "_need", lambda *a: None)
+    flat = torch.zeros(64)
+    at = lambda i: flat[i:i + 16].view(4, 4)
+    for i in (0, 1, 15):
+        for a, b in ((0, i), (i, 0)):
+            with pytest.raises(ValueError, match="overlap x"):
+                gated._output(at(a), (4, 4), flat, x=at(b))
+    out = at(16)
+    assert gated._output(out, (4, 4), flat, (out, None), x=at(0), w=at(32), bias=None) is out
+    for i in (15, 17):
+        with pytest.raises(ValueError, match="overlap an addend"):
+            gated._output(out, (4, 4), flat, (None, at(i)), x=at(32))
+    none = flat[:0].view(0, 4)
+    assert gated._output(none, (0, 4), flat, x=at(0)) is none
