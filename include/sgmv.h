@@ -363,8 +363,9 @@ int sgmv_group_rows(const int32_t* row_ids, int32_t num_rows, int32_t num_adapte
  * The projections around the adapters: a base model with 4-bit weights, the
  * gated feed-forward block, and rotary positions.  These calls follow the
  * conventions above (device pointers, row-major arrays of one dtype, float32
- * sums, enqueue-only) and need no workspace.  Outputs must not overlap inputs,
- * except that h may be gate_add or up_add itself and rope works in place.
+ * sums, enqueue-only); only gated_ffn_backward takes a workspace.  Outputs must
+ * not overlap inputs, except that h may be gate_add or up_add itself and rope
+ * works in place.
  */
 
 /*
@@ -425,9 +426,11 @@ int q4_linear(void* y, const void* x, const sgmv_q4_weight* w, const void* bias,
  * infinities the activations and act' are their limits: a g of minus infinity gives
  * h = 0 and no gradient.
  * Features beyond 2^20 return SGMV_ERR_UNSUPPORTED.
- * workspace: for dx, at least gated_ffn_backward_workspace_bytes(...) bytes,
- * 16-byte aligned, with the conventions of "Workspace" above: dx of few rows is
- * summed in ranges of out_features, whose float32 sums stand there.
+ * workspace: for dx, at least gated_ffn_backward_workspace_bytes(...) bytes (0 for
+ * many sizes: it may then be NULL), 16-byte aligned: dx of few rows is summed in
+ * ranges of out_features, whose float32 sums stand there.  It may hold anything
+ * before the call and does after it, from its first byte on: a buffer of the calls
+ * above, whose counters have to be zero, must not be given here.
  */
 typedef enum {
     SGMV_ACT_SILU = 0,
