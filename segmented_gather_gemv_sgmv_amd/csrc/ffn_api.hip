@@ -6,26 +6,6 @@ namespace {
 
 using namespace sgmv;
 
-// Rows up to which a 16-bit forward streams the weights, by rows or strips.
-constexpr int kFfnRowsMax = 64;
-
-// float32: up to 32 rows, and more while the workgroups of 32 rows x 16 features are
-// about one round; tiles then leave more CUs without work (64 rows x 3968 -> 2 x 1504:
-// 40 us by rows, 77 by tiles; 64 x 1000 -> 2400: 22 and 25; beyond, 64 x 2048 ->
-// 2 x 5504: 64 and 44).
-inline bool ffn_f32_takes_rows(const RowsArgs& a) {
-    return a.R <= 32 || ceil_div(a.R, 32) * ceil_div(a.N, 16) <= 320;
-}
-
-// More rows still take strips where their blocks of 64 rows x 32 features are at
-// most one round: a tile's workgroup is then alone with the whole of K (bf16, 256
-// rows x 4096 -> 2 x 1504: 30 us by strips, 45 by tiles; 192 x 1000 -> 2400: 12
-// and 18; 512 x 1000 -> 800: 12 and 18).  Beyond a round tiles win (256 x 1000 ->
-// 2400: 21 and 19; 128 x 4096 -> 11008: 96 and 66).
-inline bool ffn_takes_strips(const RowsArgs& a) {
-    return a.xvec && a.wvec && ceil_div(a.R, 64) * ceil_div(a.N, 32) <= 256;
-}
-
 int check_ffn(int R, int H, int I, int act, int dtype) {
     if (!known_dtype(dtype)) return SGMV_ERR_BAD_DTYPE;
     if (R < 0 || H < 1 || I < 1 || !known_act(act)) return SGMV_ERR_BAD_SHAPE;
@@ -44,23 +24,19 @@ int run_rows(const RowsArgs& a, hipStream_t st) {
 
 template <typename DT>
 int run_forward(const RowsArgs& a, hipStream_t st) {
-    if (DT::kBytes == 2 ? a.R <= kFfnRowsMax || ffn_takes_strips(a) : ffn_f32_takes_rows(a)) {
-        if (a.R <= 4) return run_rows<DT, 4, 1, 2>(a, st);
-        if (a.R <= 16) return run_rows<DT, 16, 1, 2>(a, st);
-        if constexpr (DT::kBytes == 2) {
-            // From 17 rows on x goes through LDS; more features per workgroup
-            // while that still fills the chip.
-            if (a.xvec && a.wvec) {
-                using Src = PlainSrc<DT>;
-                const bool wide = ceil_div(a.N, 64) >= 128;
-                if (a.R <= 32)
-                    return wide ? launch_strip<DT, Src, 2, 1, 2, 4, 2, 1, true>(a, st)
-                                : launch_strip<DT, Src, 2, 1, 4, 2, 2, 1, true>(a, st);
-                return wide ? launch_strip<DT, Src, 4, 1, 2, 4, 2, 1, true>(a, st)
-                            : launch_strip<DT, Src, 4, 1, 4, 2, 2, 1, true>(a, st);
-            }
-        }
-        return run_rows<DT, 16, 2, 1>(a, st);
+    const FfnPath path = ffn_path(a.R, a.N, DT::kBytes, a.xvec && a.wvec);
+    if (path == kFfnRows4) return run_rows<DT, 4, 1, 2>(a, st);
+    if (path == kFfnRows16) return run_rows<DT, 16, 1, 2>(a, st);
+    if (path == kFfnRows32) return run_rows<DT, 16, 2, 1>(a, st);
+    if constexpr (DT::kBytes == 2) {
+        using Src = PlainSrc<DT>;
+        const bool wide = ffn_wide_strips(a.N);
+        if (path == kFfnStrips32)
+            return wide ? launch_strip<DT, Src, 2, 1, 2, 4, 2, 1, true>(a, st)
+                        : launch_strip<DT, Src, 2, 1, 4, 2, 2, 1, true>(a, st);
+        if (path == kFfnStrips64)
+            return wide ? launch_strip<DT, Src, 4, 1, 2, 4, 2, 1, true>(a, st)
+                        : launch_strip<DT, Src, 4, 1, 4, 2, 2, 1, true>(a, st);
     }
     TileArgs t{};
     t.a[0] = a.x;

@@ -8,22 +8,6 @@
 
 namespace sgmv {
 
-// Whether a 16-bit call of R rows takes tiles (scaled weights, each rounded
-// once) instead of strips (exact codes, scales on float32 sums): by the times
-// they take per 4096 of K.  Strips run at a steady rate, 240 us for 4096 x 4096
-// outputs (350 with a scale per 32 K); for tiles see above, gated 256 x 256 tiles
-// taking 150 us a round.  Measured, 4096 x 4096 weights, bf16: 1024 rows 48 us by
-// strips, 52 by tiles; 1531 rows 78 and 72; 5120 -> 13824: 512 rows 134 and 96,
-// 2048 rows 506 and 288.  Calls of up to kQ4ExactRows rows never round.
-constexpr int kQ4ExactRows = 256;
-
-inline bool q4_takes_tiles(int R, int N, int flushes, bool gated) {
-    const int per = gated ? 2 : 1;  // matrices
-    const double outputs = (double)ceil_div(R, 32) * 32 * N * per / (4096. * 4096.);
-    const double us = plan_tiles(R, N, 1, gated, true).us;
-    return us < outputs * (flushes == 4 ? 350. : 240.);
-}
-
 // FL: 4, 2 or 1 steps of 32 K per scale (1, 2 or 4 flushes per tile of 128 K).
 template <typename DT, int XR, int MT, int PD, int FL, bool kGated>
 int launch_q4_rows(const RowsArgs& a, hipStream_t st) {
@@ -35,29 +19,22 @@ int launch_q4_rows(const RowsArgs& a, hipStream_t st) {
 }
 
 template <typename DT, int FL, bool kGated>
-int run_q4_rows(const RowsArgs& a, hipStream_t st) {
-    if constexpr (DT::kBytes == 2) {
-        if (a.xvec) {
-            // x loads for at most four rows; as many workgroups as n-tiles, so a
-            // single matrix takes it only while these do not fill the chip several
-            // times over (one row, 5120 -> 13824: 12.6 us against 11.2 by strips;
-            // 4096 -> 11008: 7.8 against 8.5; gated 12.8 against 13.6).
-            if (a.R <= 4 && (kGated || ceil_div(a.N, 16) < 768))
-                return launch_q4_rows<DT, 4, 1, kGated ? 1 : FL == 1 ? 3 : 4, FL, kGated>(a, st);
-            return run_strip<DT, Q4Src<DT>, FL, kGated>(a, st);
-        }
-        return a.R <= 16 ? launch_q4_rows<DT, 16, 1, 2, FL, kGated>(a, st)
-                         : launch_q4_rows<DT, 16, 2, 1, FL, kGated>(a, st);
-    } else {
-        return a.R <= 16 ? launch_q4_rows<DT, 16, 1, 1, FL, kGated>(a, st)
-                         : launch_q4_rows<DT, 16, 2, 1, FL, kGated>(a, st);
+int run_q4_few(const RowsArgs& a, Q4Path path, hipStream_t st) {
+    constexpr bool k16 = DT::kBytes == 2;
+    if constexpr (k16) {
+        if (path == kQ4Rows4)
+            return launch_q4_rows<DT, 4, 1, kGated ? 1 : FL == 1 ? 3 : 4, FL, kGated>(a, st);
+        if (path == kQ4Strips) return run_strip<DT, Q4Src<DT>, FL, kGated>(a, st);
     }
+    return path == kQ4Rows16 ? launch_q4_rows<DT, 16, 1, k16 ? 2 : 1, FL, kGated>(a, st)
+                             : launch_q4_rows<DT, 16, 2, 1, FL, kGated>(a, st);
 }
 
 template <typename DT, bool kGated>
 int run_q4(const RowsArgs& a, int flushes, hipStream_t st) {
+    const Q4Path path = q4_path(a.R, a.N, flushes, kGated, DT::kBytes, a.xvec != 0);
     if constexpr (DT::kBytes == 2) {
-        if (a.R > kQ4ExactRows && (!a.xvec || q4_takes_tiles(a.R, a.N, flushes, kGated))) {
+        if (path == kQ4Tiles) {
             TileArgs t{};
             t.a[0] = a.x;
             t.lda = a.K;
@@ -82,11 +59,10 @@ int run_q4(const RowsArgs& a, int flushes, hipStream_t st) {
             return launch_tiles_any<DT, kAlongK, kCodes, 1, kGated, 4>(t, direct, st);
         }
     }
-    if (flushes == 1) return run_q4_rows<DT, 4, kGated>(a, st);
-    if (flushes == 2) return run_q4_rows<DT, 2, kGated>(a, st);
-    return run_q4_rows<DT, 1, kGated>(a, st);
+    if (flushes == 1) return run_q4_few<DT, 4, kGated>(a, path, st);
+    if (flushes == 2) return run_q4_few<DT, 2, kGated>(a, path, st);
+    return run_q4_few<DT, 1, kGated>(a, path, st);
 }
-
 
 extern template int run_q4<F32, false>(const RowsArgs&, int, hipStream_t);
 extern template int run_q4<F32, true>(const RowsArgs&, int, hipStream_t);

@@ -17,12 +17,10 @@
 
 #include <type_traits>
 
+#include "proj_plan.hpp"
 #include "sgmv_device.hpp"
 
 namespace sgmv {
-
-constexpr int kRopeThreads = 256;
-constexpr int kRopeMaxDim = 1024;  // of a head
 
 struct RopeArgs {
     void* out[2];

@@ -1,23 +1,20 @@
 // rope_api.hip -- C ABI of the rotary positions (declared in include/sgmv.h):
 // argument checks and the choice of kernel and grid.
 #include "sgmv_host.hpp"
+#include "proj_plan.hpp"
 #include "rope.hpp"
-
-#include <algorithm>
 
 namespace {
 
 using namespace sgmv;
 
-constexpr int kUnitsMost = 4;  // units per thread
-
 template <typename DT, bool kVec>
 void launch_rope(const RopeArgs& a, hipStream_t st) {
     const dim3 grid((unsigned)((long long)a.rows * a.groups)), block(kRopeThreads);
-    const int each = (a.heads_per_group * a.units + kRopeThreads - 1) / kRopeThreads;
+    const int each = rope_units_per_thread(a.heads_per_group, a.units);
     if (each <= 1) launch(&rope_kernel<DT, kVec, 1>, grid, block, st, a);
-    else if (each <= 2) launch(&rope_kernel<DT, kVec, 2>, grid, block, st, a);
-    else launch(&rope_kernel<DT, kVec, kUnitsMost>, grid, block, st, a);
+    else if (each == 2) launch(&rope_kernel<DT, kVec, 2>, grid, block, st, a);
+    else launch(&rope_kernel<DT, kVec, kRopeUnitsMost>, grid, block, st, a);
 }
 
 template <typename DT>
@@ -73,20 +70,11 @@ extern "C" int rope(void* q_out, void* k_out, const void* q, const void* k,
         vec = vec && aligned16(a.in[w]) && aligned16(a.out[w]);
         for (int s = 0; s < 4; ++s) vec = vec && strides[4 * w + s] % V == 0;
     }
-    const int v = vec ? V : 1;
-    a.units = (interleaved ? (vec ? rotary_dim / V : rotary_dim / 2) : rotary_dim / 2 / v) +
-              (head_dim - rotary_dim) / v;
+    const RopeGrid g = rope_grid(num_rows, heads, head_dim, rotary_dim, interleaved != 0, vec ? V : 1);
+    a.units = g.units;
     a.units_magic = (uint32_t)(((1ull << 32) + a.units - 1) / a.units);
-    // One workgroup per row once the rows fill the chip (4 per CU); with fewer
-    // rows, and where a thread would hold more than kUnitsMost units, the heads are
-    // split too, down to one pass of the workgroup.
-    static_assert(kRopeMaxDim <= kRopeThreads * kUnitsMost, "a head fits a workgroup");
-    const long long per_pass = std::max(1, kRopeThreads / a.units);
-    const long long want = (1024ll + num_rows - 1) / num_rows;
-    long long hpg = std::max(per_pass, (heads + want - 1) / want);
-    hpg = std::min({hpg, heads, (long long)(kRopeThreads * kUnitsMost / a.units)});
-    a.heads_per_group = (int)hpg;
-    a.groups = (int)((heads + hpg - 1) / hpg);
+    a.heads_per_group = g.heads_per_group;
+    a.groups = g.groups;
     if ((long long)num_rows * a.groups > 0x7FFFFFFFll) return SGMV_ERR_UNSUPPORTED;
     const hipStream_t st = (hipStream_t)stream;
     if (dtype == SGMV_F32) launch_rope<F32>(a, vec, st);
