@@ -396,11 +396,12 @@ int q4_pack(void* tiles, void* meta, const uint8_t* codes, const void* scales,
 
 /*
  * y = round(x W^T + bias): x [num_rows, in_features], y [num_rows,
- * out_features] (overwritten), bias [out_features] or NULL.  Up to 256 rows
- * (any number in float32) the codes enter the products exactly and the
- * scales multiply float32 sums per group; beyond that fp16 and bf16 calls may
- * round each scaled weight once to dtype first.  An infinity in x gives a
- * non-finite row (NaN where the products alone would give an infinity).
+ * out_features] (overwritten), bias [out_features] or NULL.  For any number of rows
+ * the codes, less their zero points, enter the products exactly and the scales
+ * multiply float32 sums per group; y's rounding is the only one to fewer bits, so a
+ * row's result depends on the rows beside it by the order of float32 sums alone.
+ * An infinity in x gives a non-finite row (NaN where the products alone would give
+ * an infinity).
  */
 int q4_linear(void* y, const void* x, const sgmv_q4_weight* w, const void* bias, int32_t num_rows,
               int32_t out_features, int32_t in_features, int32_t group_size, int32_t dtype,

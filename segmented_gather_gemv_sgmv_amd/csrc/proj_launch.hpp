@@ -12,6 +12,7 @@ namespace sgmv {
 using BigTile = TileShape<256, 256, 2, 4>;
 using WideTile = TileShape<128, 256, 2, 4>;
 using MidTile = TileShape<128, 128, 2, 2>;
+using DeepTile = TileShape<256, 128, 4, 2>;
 // float32, whose products take eight times as long per byte: small tiles cost no
 // more loads than there is time for, and leave fewer CUs without work.
 using SmallTile = TileShape<64, 64, 2, 2>;
@@ -44,9 +45,12 @@ int launch_kind(TileKind kind, const TileArgs& a, const TileRange& r, bool direc
         return launch_tiles<DT, SmallTile, AL, BL, kSegs, kGated, true, kFlushes>(a, r, st);
     } else {
         if (!direct) return launch_tiles<DT, MidTile, AL, BL, kSegs, kGated, false, kFlushes>(a, r, st);
-        if (kind == kBigTiles)
-            return launch_tiles<DT, BigTile, AL, BL, kSegs, kGated, true, kFlushes>(a, r, st);
-        if constexpr (BL != kCodes) {
+        if constexpr (BL == kCodes) {
+            if (kind == kDeepTiles)
+                return launch_tiles<DT, DeepTile, AL, BL, kSegs, kGated, true, kFlushes>(a, r, st);
+        } else {
+            if (kind == kBigTiles)
+                return launch_tiles<DT, BigTile, AL, BL, kSegs, kGated, true, kFlushes>(a, r, st);
             if (kind == kWideTiles)
                 return launch_tiles<DT, WideTile, AL, BL, kSegs, kGated, true, kFlushes>(a, r, st);
         }
@@ -63,9 +67,9 @@ int launch_tiles_any(const TileArgs& a, bool direct, hipStream_t st) {
         return launch_kind<DT, AL, BL, kSegs, kGated>(f32_kind(a.M, a.N, a.batches, kGated), a, all,
                                                       true, st);
     } else {
-        const TilePlan p = plan_tiles(a.M, a.N, a.batches, kGated, BL == kCodes);
+        const TilePlan p = plan_tiles(a.M, a.N, a.batches, kGated, BL == kCodes ? kFlushes : 0);
         if (p.big.m_end > 0) {
-            const int rc = launch_kind<DT, AL, BL, kSegs, kGated, kFlushes>(kBigTiles, a, p.big, true, st);
+            const int rc = launch_kind<DT, AL, BL, kSegs, kGated, kFlushes>(p.big_kind, a, p.big, true, st);
             if (rc != SGMV_OK) return rc;
         }
         return launch_kind<DT, AL, BL, kSegs, kGated, kFlushes>(p.kind, a, p.rest, true, st);

@@ -23,52 +23,69 @@ struct TileRange {
 };
 
 // ---- tiles of many rows ------------------------------------------------------
+// Tiles of rows x features: big 256 x 256, wide 128 x 256, mid 128 x 128; of float32
+// small 64 x 64 and tall 128 x 64; of 4-bit weights deep 256 x 128 and mid.
+enum TileKind { kBigTiles, kWideTiles, kMidTiles, kSmallTiles, kTallTiles, kDeepTiles };
+
 // Time of `tiles` tiles per 4096 of K, in microseconds, as rounds over the 256
 // CUs (bf16, measured on whole rounds of products along K and across K): a round
 // of 256 x 256 tiles takes 109 to 122, one of 128 x 256 tiles 62 to 79, two
 // 128 x 128 tiles on each CU 67 to 83 and one on each 42 to 52.
-enum TileKind { kBigTiles, kWideTiles, kMidTiles, kSmallTiles, kTallTiles };
-constexpr double kBigTileUs = 118.;
-constexpr double kBigGatedCodesUs = 150.;  // gated 4-bit tiles: their registers spill
-
-inline double tiles_us(TileKind kind, long long tiles, double big_us = kBigTileUs) {
-    if (kind == kBigTiles) return big_us * ceil_div(tiles, 256);
+inline double tiles_us(TileKind kind, long long tiles) {
+    if (kind == kBigTiles) return 118. * ceil_div(tiles, 256);
     if (kind == kWideTiles) return 64. * ceil_div(tiles, 256);
     const long long rest = tiles % 512;
     return 78. * (tiles / 512) + (rest == 0 ? 0. : rest <= 256 ? 45. : 78.);
 }
 
-// A plan: the kind of tile for the whole output, or 256 x 256 tiles for the first
-// rows or columns, as many as fill whole rounds, and `kind` for the rest.
+// The same of 4-bit weights' tiles, with 1, 2 or 4 scales per 128 K: a round of 256 x 128
+// tiles 74 to 79, 82 to 86, 96 to 107; two 128 x 128 tiles on each CU 72 to 90, 84 to 97,
+// 96 to 120, one on each 55 to 66, 65 to 73, 82 to 89.
+inline double code_tiles_us(TileKind kind, long long tiles, int flushes) {
+    if (kind == kDeepTiles)
+        return (flushes == 4 ? 100. : flushes == 2 ? 84. : 76.) * ceil_div(tiles, 256);
+    const double one = flushes == 4 ? 86. : flushes == 2 ? 68. : 61.;
+    const double two = flushes == 4 ? 107. : flushes == 2 ? 90. : 82.;
+    const long long rest = tiles % 512;
+    return two * (tiles / 512) + (rest == 0 ? 0. : rest <= 256 ? one : two);
+}
+
+// A plan: the kind of tile for the whole output, or the largest tiles for the first rows
+// or columns, as many as fill whole rounds, and `kind` for the rest.
 struct TilePlan {
-    TileKind kind;
+    TileKind kind, big_kind;
     TileRange big, rest;  // big: empty unless split
     double us;
 };
 
+// code_flushes: scales per 128 K of 4-bit weights, 0 of plain ones.
 // 128 x 256 tiles: 2048 rows x 4096 from 2 x 11008, f16, 365 us, without them 470.
-// 4-bit weights have none: unpacking them for 128 rows costs what
-// the larger tile saves (512 x 5120 -> 13824: 104 us against 99 by 128 x 128 tiles).
-inline TilePlan plan_tiles(long long M, long long N, int batches, bool gated, bool codes) {
-    const double big_us = gated && codes ? kBigGatedCodesUs : kBigTileUs;
-    const long long bn = gated ? 128 : 256;  // columns per 256 of a tile
-    auto count = [&](TileKind kind, const TileRange& r) {
-        return ceil_div(r.m_end - r.m_first, kind == kBigTiles ? 256 : 128) *
-               ceil_div(r.n_end - r.n_first, kind == kMidTiles ? bn / 2 : bn) * batches;
+// 256 x 128 tiles of 4-bit weights: 1531 x 4096 -> 4096, bf16, 79 us, without them 91;
+// 512 x 5120 -> 13824, 88 and 102.
+inline TilePlan plan_tiles(long long M, long long N, int batches, bool gated, int code_flushes = 0) {
+    const bool codes = code_flushes > 0;
+    const TileKind large = codes ? kDeepTiles : kBigTiles;
+    auto columns = [&](TileKind kind) {  // of each matrix
+        return (kind == kBigTiles || kind == kWideTiles ? 256ll : 128ll) / (gated ? 2 : 1);
+    };
+    auto time = [&](TileKind kind, const TileRange& r) {
+        const long long n = ceil_div(r.m_end - r.m_first, kind == large ? 256 : 128) *
+                            ceil_div(r.n_end - r.n_first, columns(kind)) * batches;
+        return codes ? code_tiles_us(kind, n, code_flushes) : tiles_us(kind, n);
     };
     const TileRange all{0, M, 0, N}, none{0, 0, 0, 0};
-    TilePlan best{kBigTiles, none, all, tiles_us(kBigTiles, count(kBigTiles, all), big_us)};
+    TilePlan best{large, large, none, all, time(large, all)};
     auto offer = [&](TileKind kind, const TileRange& big, const TileRange& rest, double us) {
         if (codes && kind == kWideTiles) return;
-        us += tiles_us(kind, count(kind, rest));
-        if (us < best.us) best = TilePlan{kind, big, rest, us};
+        us += time(kind, rest);
+        if (us < best.us) best = TilePlan{kind, large, big, rest, us};
     };
     offer(kWideTiles, none, all, 0.);
     offer(kMidTiles, none, all, 0.);
     // 4096 x 4096 -> 2 x 11008 is 1376 tiles, 5.4 rounds: 690 us as six rounds,
     // 676 as five and one of 128 x 256 tiles; its weights' gradients 625 and 606.
     // The second launch is priced at 4 us.
-    const long long tm = ceil_div(M, 256), tn = ceil_div(N, bn);
+    const long long bn = columns(large), tm = ceil_div(M, 256), tn = ceil_div(N, bn);
     const long long rounds = tm * tn * batches / 256;
     if (rounds > 0) {
         const long long rows = 256 * rounds / (tn * batches), cols = 256 * rounds / (tm * batches);
@@ -77,7 +94,7 @@ inline TilePlan plan_tiles(long long M, long long N, int batches, bool gated, bo
             if (by_rows) big.m_end = rest.m_first = std::min(rows * 256, M);
             else big.n_end = rest.n_first = std::min(cols * bn, N);
             if (big.m_end == 0 || big.n_end == 0 || rest.m_first == M || rest.n_first == N) continue;
-            const double us = 4. + tiles_us(kBigTiles, count(kBigTiles, big), big_us);
+            const double us = 4. + time(large, big);
             offer(kWideTiles, big, rest, us);
             offer(kMidTiles, big, rest, us);
         }
@@ -128,7 +145,7 @@ inline SumPlan plan_sum(long long M, long long N, long long K, int dtype) {
     };
     const long long stride = ceil_div(M * N, 64) * 64;
     SumPlan best{f32 ? f32_kind(M, N, 1, false) : kBigTiles, 1, (int)steps, stride};
-    double best_us = steps * (f32 ? step_us(best.kind, 1) : plan_tiles(M, N, 1, false, false).us / 128.);
+    double best_us = steps * (f32 ? step_us(best.kind, 1) : plan_tiles(M, N, 1, false).us / 128.);
     if (stride > kMaxSumBytes / 8) return best;
     for (int ranges = 2; ranges <= 64; ++ranges) {
         const long long each = ceil_div(steps, 4ll * ranges) * 4;
@@ -147,41 +164,6 @@ inline SumPlan plan_sum(long long M, long long N, long long K, int dtype) {
 }
 
 // ---- 4-bit projections -------------------------------------------------------
-// Whether a 16-bit call of R rows takes tiles (scaled weights, each rounded
-// once) instead of strips (exact codes, scales on float32 sums): by the times
-// they take per 4096 of K.  Strips run at a steady rate, 240 us for 4096 x 4096
-// outputs (350 with a scale per 32 K); for tiles see above, gated 256 x 256 tiles
-// taking 150 us a round.  Measured, 4096 x 4096 weights, bf16: 1024 rows 48 us by
-// strips, 52 by tiles; 1531 rows 78 and 72; 5120 -> 13824: 512 rows 134 and 96,
-// 2048 rows 506 and 288.  Calls of up to kQ4ExactRows rows never round.
-constexpr int kQ4ExactRows = 256;
-
-inline bool q4_takes_tiles(long long R, long long N, int flushes, bool gated) {
-    const int per = gated ? 2 : 1;  // matrices
-    const double outputs = (double)ceil_div(R, 32) * 32 * N * per / (4096. * 4096.);
-    const double us = plan_tiles(R, N, 1, gated, true).us;
-    return us < outputs * (flushes == 4 ? 350. : 240.);
-}
-
-// Whether a 16-bit call of at most four rows with 16-byte pieces takes the rows kernel:
-// x loads for at most four rows; as many workgroups as n-tiles, so a
-// single matrix takes it only while these do not fill the chip several
-// times over (one row, 5120 -> 13824: 12.6 us against 11.2 by strips;
-// 4096 -> 11008: 7.8 against 8.5; gated 12.8 against 13.6).
-inline bool q4_takes_rows(long long R, long long N, bool gated) {
-    return R <= 4 && (gated || ceil_div(N, 16) < 768);
-}
-
-// The kernel of a 4-bit call (bytes: of an element; vec: x takes 16-byte loads).
-enum Q4Path { kQ4Rows4, kQ4Rows16, kQ4Rows32, kQ4Strips, kQ4Tiles };
-
-inline Q4Path q4_path(long long R, long long N, int flushes, bool gated, int bytes, bool vec) {
-    if (bytes == 4) return R <= 16 ? kQ4Rows16 : kQ4Rows32;
-    if (R > kQ4ExactRows && (!vec || q4_takes_tiles(R, N, flushes, gated))) return kQ4Tiles;
-    if (!vec) return R <= 16 ? kQ4Rows16 : kQ4Rows32;
-    return q4_takes_rows(R, N, gated) ? kQ4Rows4 : kQ4Strips;
-}
-
 // The largest block of rows and features that still gives about two of three
 // CUs a workgroup.  Larger blocks read x and unpack weights less often; below
 // that many workgroups the idle CUs cost more (5120 -> 13824, 4-bit, bf16, 64
@@ -215,6 +197,54 @@ inline StripBlock q4_strip_block(long long R, long long N, int flushes, bool gat
     }
     if (fills(16, 64)) return kStrip16x64;
     return fills(16, 32) ? kStrip16x32 : kStrip16x16;
+}
+
+// Whether a 16-bit call takes tiles instead of strips: by the times they take per 4096 of
+// K, with 1, 2 or 4 scales per 128 K.  Both run in rounds of the 256 CUs: strips' blocks
+// one to a CU, 53, 58 or 76 us for 64 rows x 256 features and less in proportion; tiles
+// see above.  4096 features of 4096, bf16, by strips and 128 x 128 tiles: 1024 rows 52 and
+// 65 us, 1531 rows 89 and 83, 2048 rows 98 and 90; 5120 -> 13824: 256 rows 67 and 79, 300
+// rows 110 and 101, 512 rows 130 and 113; gated 333 x 2048 -> 5632: 54 and 48, with 32
+// K per scale 41 and 61.
+inline bool q4_takes_tiles(long long R, long long N, int flushes, bool gated) {
+    const long long per = gated ? 2 : 1;  // matrices
+    static const struct { int rows, features; } kBlocks[] = {
+        {64, 256}, {64, 128}, {64, 64}, {32, 128}, {32, 64}, {32, 32}, {16, 64}, {16, 32}, {16, 16}};
+    const StripBlock block = q4_strip_block(R, N, flushes, gated);
+    const bool by_pairs = block == kStrip64xMost || block == kStrip64xHalf || block == kStrip32xHalf;
+    const long long rows = kBlocks[block].rows;
+    const long long features = kBlocks[block].features / (by_pairs ? per : 1);
+    const double strip = (flushes == 4 ? 76. : flushes == 2 ? 58. : 53.) * (rows * features * per) / (64 * 256);
+    return plan_tiles(R, N, 1, gated, flushes).us < strip * ceil_div(ceil_div(R, rows) * ceil_div(N, features), 256);
+}
+
+// Whether a 16-bit call of at most four rows takes the rows kernel instead of strips:
+// its x loads suit so few rows, but it has a workgroup per 16 features and matrix, so
+// for one matrix only while these do not fill the chip several times over.  bf16, rows
+// kernel and strips: one row of 4096, 688 workgroups 6.8 and 8.0 us, 768 6.9 and 8.5,
+// 864 8.4 and 8.3, 1024 8.9 and 8.5; four rows 768 7.6 and 8.4, 864 9.3 and 8.5; one row
+// of 8192, 768 12.4 and 14.4, 864 15.8 and 14.9; of 1024 within 0.3 of each other up to
+// 768.  Gated, one row of 4096, 688: 12.8 and 13.6.
+inline bool q4_takes_rows(long long R, long long N, bool gated) {
+    return R <= 4 && (gated || ceil_div(N, 16) <= 768);
+}
+
+// Whether a 16-bit call of x that no 16-byte load fits takes the tiles' register path
+// instead of the rows kernel's workgroups of 32 rows x 16 features.  fp16, rows and
+// tiles: 504 workgroups of 1001 K 23 and 54 us, 1008 42 and 54, 2048 of 4097 K 251 and
+// 217.
+inline bool q4_slow_takes_tiles(long long R, long long N) {
+    return R > 16 && ceil_div(R, 32) * ceil_div(N, 16) > 1500;
+}
+
+// The kernel of a 4-bit call (bytes: of an element; vec: x takes 16-byte loads).
+enum Q4Path { kQ4Rows4, kQ4Rows16, kQ4Rows32, kQ4Strips, kQ4Tiles };
+
+inline Q4Path q4_path(long long R, long long N, int flushes, bool gated, int bytes, bool vec) {
+    if (bytes == 4 || (!vec && !q4_slow_takes_tiles(R, N))) return R <= 16 ? kQ4Rows16 : kQ4Rows32;
+    if (!vec) return kQ4Tiles;
+    if (q4_takes_rows(R, N, gated)) return kQ4Rows4;
+    return q4_takes_tiles(R, N, flushes, gated) ? kQ4Tiles : kQ4Strips;
 }
 
 // ---- gated block of plain weights --------------------------------------------

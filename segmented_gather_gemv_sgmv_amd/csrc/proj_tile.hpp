@@ -130,41 +130,36 @@ struct StageReader {
     }
 };
 
-// Scaled weights of one lane's eight codes, each rounded once to the 16-bit
-// type: s (q - z).  The rows kernel keeps the scales out of the products and
-// rounds nothing here, but a tile of many rows would pay for that with a
-// multiply-add per accumulator and group; one rounding of a weight is what a
-// 16-bit copy of the same weight would carry, and its share of the result's
-// error is below that of the result's own rounding.
+// A lane's eight codes less their zero point, whole numbers of five bits: exact.
 template <typename DT>
-__device__ __forceinline__ uint4 scaled_codes(uint32_t w, uint32_t meta) {
+__device__ __forceinline__ uint4 plain_codes(uint32_t w, float zb) {
     const uint4 b = codes_biased<DT>(w);
     if constexpr (std::is_same<DT, F16>::value) {
         typedef _Float16 h2_t __attribute__((ext_vector_type(2)));
-        const h2_t m = __builtin_bit_cast(h2_t, meta);
-        const h2_t ss = {m.x, m.x}, zz = {m.y, m.y};
-        auto one = [&](uint32_t v) {  // (16 + q) - (16 + z) is exact
-            return __builtin_bit_cast(uint32_t, (__builtin_bit_cast(h2_t, v) - zz) * ss);
+        const h2_t zz = {(_Float16)zb, (_Float16)zb};
+        auto one = [&](uint32_t v) {
+            return __builtin_bit_cast(uint32_t, __builtin_bit_cast(h2_t, v) - zz);
         };
         return make_uint4(one(b.x), one(b.y), one(b.z), one(b.w));
     } else {
-        float s, zb;
-        meta_values<BF16>(meta, s, zb);
-        const float c = -s * zb;  // exact: 8 by 8 significant bits
-        auto one = [&](uint32_t v) {  // v: two bf16 values 16 + q
-            return pack2_rne<BF16>(__builtin_fmaf(__uint_as_float(v << 16), s, c),
-                                   __builtin_fmaf(__uint_as_float(v & 0xFFFF0000u), s, c));
-        };
-        return make_uint4(one(b.x), one(b.y), one(b.z), one(b.w));
+        return codes_less_zero(b, zb);
     }
 }
 
 // kFlushes: scale pairs per feature and tile of 128 K (kCodes), else 1.
 //
-// 4-bit B: threads unpack a block's codes into the stages, scaled (5120 -> 13824,
-// bf16: 2048 rows 292 us, 990 TFLOP/s; 512 rows 99 us).
+// 4-bit B: threads unpack a block's codes into the stages, exactly (less their zero
+// points), and the products of the steps that share a scale are summed apart; the
+// first products of the next such group find that sum done, and scale it into the
+// result's.  So nothing is rounded but float32 sums, as in the calls of few rows.  Two
+// sums per output leave a wave 64 x 64 outputs, whose operands' LDS reads take as long
+// as its products; a scale costs a multiply-add per output (5120 -> 13824, bf16, a
+// scale per 128 K: 512 rows 85 us, 2048 rows 333 us, 870 TFLOP/s; per 32 K 125 and 462).
+// Scaled weights rounded to the type before the products would fit 256 x 256 tiles, 269
+// us for the 2048 rows, and put results off by 2.1e-3 of their size (root mean square,
+// bf16) where their own rounding is 1.65e-3.
 template <typename DT, typename SH, int AL, int BL, int kSegs, bool kGated, bool kDma, int kFlushes>
-__global__ __launch_bounds__(SH::NT) void tile_kernel(TileArgs g) {
+__global__ __launch_bounds__(SH::NT, BL == kCodes ? 2 : 1) void tile_kernel(TileArgs g) {
     using T = typename DT::storage;
     using Ops = PieceOps<DT>;
     constexpr int BM = SH::BM, BN = SH::BN, TM = SH::TM, TN = SH::TN, NT = SH::NT, NW = SH::NW;
@@ -180,6 +175,10 @@ __global__ __launch_bounds__(SH::NT) void tile_kernel(TileArgs g) {
     __shared__ __attribute__((aligned(16))) uint8_t s_a2[BM * 64], s_b2[BN * 64];
     __shared__ __attribute__((aligned(16))) uint8_t s_a3[BM * 64], s_b3[BN * 64];
 
+    // 4-bit: scales of the stage rows of B, by the first step of their group in a turn
+    // of the loop (groups of steps that share a scale: kGroup steps).
+    constexpr int kGroup = 4 / kFlushes;
+    __shared__ __attribute__((aligned(16))) float s_scale[BL == kCodes ? 8 : 1][BL == kCodes ? BN : 4];
     __shared__ uint8_t s_unread[NW == 8 && kDma ? 256 * NW : 1];  // where prefetches land
 
     const int tid = threadIdx.x, lane = tid & (kWave - 1);
@@ -217,10 +216,10 @@ __global__ __launch_bounds__(SH::NT) void tile_kernel(TileArgs g) {
         return n0 + blk * (8 * TN) + (which ? in - 8 * TN : in);
     };
 
-    // 4-bit weights: unit u of this thread (one packed dword of a step) is
-    // lane (unit & 63) of n-tile unit / 64 of the stage.
-    constexpr int kUnits = BL == kCodes ? BN * 4 / NT : 1;
-    static_assert(BL != kCodes || kUnits * NT == BN * 4, "whole units per thread");
+    // 4-bit weights: unit u of a wave is n-tile wid + u NW of the stage's, a lane holding
+    // one packed dword per step.
+    constexpr int kUnits = BL == kCodes ? BN / 16 / NW : 1;
+    static_assert(BL != kCodes || kUnits * NW * 16 == BN, "whole units per wave");
     struct Codes {
         uint4 w;
         uint32_t meta[kFlushes];
@@ -230,27 +229,30 @@ __global__ __launch_bounds__(SH::NT) void tile_kernel(TileArgs g) {
             kb = min(kb, g.kblocks - 1);
 #pragma unroll
             for (int u = 0; u < kUnits; ++u) {
-                const int unit = tid + u * NT, l = unit & 63;
                 int which = 0;
-                const int row = kGated ? gated_row((unit >> 6) * 16, which) : n0 + (unit >> 6) * 16;
-                const long long nt = min(row >> 4, ((N + 15) >> 4) - 1);
+                const int first = (wid + u * NW) * 16;
+                const int row = kGated ? gated_row(first, which) : n0 + first;
+                const long long tile = (long long)min(row >> 4, ((N + 15) >> 4) - 1) * g.kblocks + kb;
                 const ProjWeight& q = g.q[which];
-                c[u].w = load16((const uint4*)q.w + (nt * g.kblocks + kb) * 64 + l);
-                load_dwords<kFlushes>(
-                    (const uint32_t*)q.meta + ((nt * g.kblocks + kb) * 16 + (l & 15)) * kFlushes,
-                    c[u].meta);
+                c[u].w = load16((const uint4*)q.w + tile * 64 + lane);
+                load_dwords<kFlushes>((const uint32_t*)q.meta + tile * 16 * kFlushes + lr * kFlushes,
+                                      c[u].meta);
             }
         }
     };
-    auto store_codes = [&](uint8_t* sb, const Codes(&c)[kUnits], int s) {
+    auto store_codes = [&](uint8_t* sb, const Codes(&c)[kUnits], int s, int slot) {
         if constexpr (BL == kCodes) {
 #pragma unroll
             for (int u = 0; u < kUnits; ++u) {
-                const int unit = tid + u * NT, l = unit & 63;
-                const int row = (unit >> 6) * 16 + (l & 15);
+                const int first = (wid + u * NW) * 16;
                 const uint32_t w = s == 0 ? c[u].w.x : s == 1 ? c[u].w.y : s == 2 ? c[u].w.z : c[u].w.w;
-                store16(sb + row * 64 + (along_piece(row, l >> 4) << 4),
-                        scaled_codes<DT>(w, c[u].meta[s * kFlushes / 4]));
+                float sc, zb;
+                meta_values<DT>(c[u].meta[s * kFlushes / 4], sc, zb);
+                const int unit = tid + u * NT, l = unit & 63, row = (unit >> 6) * 16 + (l & 15);
+                store16(sb + row * 64 + (along_piece(row, l >> 4) << 4), plain_codes<DT>(w, zb));
+                // By all four lanes that hold it: a branch here would make the compiler wait
+                // for every load.
+                if (s % kGroup == 0) s_scale[slot][first + lr] = sc;
             }
         }
     };
@@ -263,15 +265,91 @@ __global__ __launch_bounds__(SH::NT) void tile_kernel(TileArgs g) {
 
     const StageReader<DT, AL, BM> rd_a(wr0, lr, lg);
     const StageReader<DT, BL, BN> rd_b(wc0, lr, lg);
+    auto fence = [] {
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    // 4-bit: sums of the group in hand, and the scales of this lane's features (those of
+    // its sums' four elements) for the group whose sums are done.
+    constexpr int TMC = BL == kCodes ? TM : 1, TNC = BL == kCodes ? TN : 1;
+    acc4_t part[TMC][TNC];
+    auto scales = [&](int slot, int j) {
+        return *reinterpret_cast<const acc4_t*>(&s_scale[slot][wc0 + 16 * j + 4 * lg]);
+    };
+    auto add_part = [&](int i, int j, const acc4_t& scale) {
+        if constexpr (BL == kCodes) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[i][j][e] += scale[e] * part[i][j][e];
+            // Here and not later: left until the result is used, a turn's sums spill.
+            asm volatile("" : "+v"(acc[i][j]));
+        }
+    };
+    // 4-bit: products of rows [i0, i1) of a step.  The first step of a group scales the
+    // sums of the group before it, whose scales are in slot `done`, into the result's.
+    auto code_products = [&](auto i0, auto i1, const uint4(&a)[TM], const uint4(&b)[TN], auto done) {
+        constexpr int I0 = decltype(i0)::value, I1 = decltype(i1)::value, D = decltype(done)::value;
+        if constexpr (BL == kCodes && D >= 0) {
+            constexpr int kHeld = kFlushes == 4 || (kFlushes == 2 && NW == 8) ? 1 : TN;  // as registers allow
+            acc4_t sc[TN];
+#pragma unroll
+            for (int j = 0; j < kHeld; ++j) sc[j] = scales(D, j);
+#pragma unroll
+            for (int j = 0; j < TN; ++j) {
+#pragma unroll
+                for (int i = I0; i < I1; ++i) {
+                    add_part(i, j, sc[j]);
+                    part[i][j] = Ops::mma(b[j], a[i], acc4_t{0.f, 0.f, 0.f, 0.f});
+                }
+                if (j + kHeld < TN) {
+                    fence();
+                    sc[j + kHeld] = scales(D, j + kHeld);
+                }
+            }
+        } else if constexpr (BL == kCodes) {
+#pragma unroll
+            for (int j = 0; j < TN; ++j)
+#pragma unroll
+                for (int i = I0; i < I1; ++i) part[i][j] = Ops::mma(b[j], a[i], part[i][j]);
+        }
+    };
+    using Row0 = std::integral_constant<int, 0>;
+    using RowMid = std::integral_constant<int, TM / 2>;
+    using RowEnd = std::integral_constant<int, TM>;
+    using NoneDone = std::integral_constant<int, -1>;
+    auto finish_parts = [&](int slot) {
+        if constexpr (BL == kCodes) {
+#pragma unroll
+            for (int j = 0; j < TN; ++j) {
+                const acc4_t sc = scales(slot, j);
+#pragma unroll
+                for (int i = 0; i < TM; ++i) add_part(i, j, sc);
+            }
+        }
+    };
+    if constexpr (BL == kCodes) {
+        // The first group finds zeros: sums, and the scales of the slot before it.
+#pragma unroll
+        for (int i = 0; i < TM; ++i)
+#pragma unroll
+            for (int j = 0; j < TN; ++j) part[i][j] = acc4_t{0.f, 0.f, 0.f, 0.f};
+        for (int r = tid; r < BN; r += NT) s_scale[8 - kGroup][r] = 0.f;
+    }
     auto compute = [&](const uint8_t* sa, const uint8_t* sb) {
         uint4 b[TN];
 #pragma unroll
         for (int j = 0; j < TN; ++j) b[j] = rd_b(sb, j);
+        if constexpr (BL == kCodes) {
+            uint4 a[TM];
 #pragma unroll
-        for (int i = 0; i < TM; ++i) {
-            const uint4 a = rd_a(sa, i);
+            for (int i = 0; i < TM; ++i) a[i] = rd_a(sa, i);
+            code_products(Row0{}, RowEnd{}, a, b, NoneDone{});
+        } else {
 #pragma unroll
-            for (int j = 0; j < TN; ++j) acc[i][j] = Ops::mma(b[j], a, acc[i][j]);
+            for (int i = 0; i < TM; ++i) {
+                const uint4 a = rd_a(sa, i);
+#pragma unroll
+                for (int j = 0; j < TN; ++j) acc[i][j] = Ops::mma(b[j], a, acc[i][j]);
+            }
         }
     };
 
@@ -330,17 +408,31 @@ __global__ __launch_bounds__(SH::NT) void tile_kernel(TileArgs g) {
             for (int u = 0; u < kA; ++u) store16(sa + (tid + u * NT) * 16, ra[s][u]);
 #pragma unroll
             for (int u = 0; u < kB; ++u) store16(sb + (tid + u * NT) * 16, rb[s][u]);
-            if constexpr (BL == kCodes) store_codes(sb, cc, s);
+            if constexpr (BL == kCodes) store_codes(sb, cc, s, s);
         };
         put(s_a0, s_b0, 0);
         put(s_a1, s_b1, 1);
         put(s_a2, s_b2, 2);
         put(s_a3, s_b3, 3);
         __syncthreads();
-        compute(s_a0, s_b0);
-        if (kc + KE < K) compute(s_a1, s_b1);
-        if (kc + 2 * KE < K) compute(s_a2, s_b2);
-        if (kc + 3 * KE < K) compute(s_a3, s_b3);
+        // A group's sums are done, and scaled, with its last step; steps past K add zeros.
+        auto one = [&](const uint8_t* sa, const uint8_t* sb, auto index) {
+            constexpr int s = decltype(index)::value;
+            if constexpr (BL == kCodes) {
+                if constexpr (s % kGroup == 0) {
+#pragma unroll
+                    for (int i = 0; i < TM; ++i)
+#pragma unroll
+                        for (int j = 0; j < TN; ++j) part[i][j] = acc4_t{0.f, 0.f, 0.f, 0.f};
+                }
+            }
+            if (kc + s * KE < K) compute(sa, sb);
+            if constexpr ((s + 1) % kGroup == 0) finish_parts(s + 1 - kGroup);
+        };
+        one(s_a0, s_b0, std::integral_constant<int, 0>{});
+        one(s_a1, s_b1, std::integral_constant<int, 1>{});
+        one(s_a2, s_b2, std::integral_constant<int, 2>{});
+        one(s_a3, s_b3, std::integral_constant<int, 3>{});
     };
     if constexpr (!kDma) {
         const int seg_turns = (K + 4 * KE - 1) / (4 * KE);
@@ -521,21 +613,21 @@ __global__ __launch_bounds__(SH::NT) void tile_kernel(TileArgs g) {
 #pragma unroll
                 for (int u = 0; u < kLoads; ++u) issue1(sa, sb, step, u);
             };
-            // Packed codes of two K blocks: a block's four steps unpack it while the
-            // next one loads.
+            // Packed codes of two K blocks, the one being unpacked and the one being loaded.
             Codes ca[kUnits], cb[kUnits];
-            auto fence = [] {
-                asm volatile("" ::: "memory");
-                __builtin_amdgcn_sched_barrier(0);
-            };
-            if constexpr (BL == kCodes) load_codes(0, ca);
+            // 4-bit: their first two blocks.
+            if constexpr (BL == kCodes) {
+                load_codes(0, ca);
+                load_codes(1, cb);
+                fence();
+            }
             issue(s_a0, s_b0, 0);
             issue(s_a1, s_b1, 1);
             issue(s_a2, s_b2, 2);
             if constexpr (kPrefetch) prefetch(kAhead - 2);
             if constexpr (BL == kCodes) {
-                store_codes(s_b0, ca, 0);
-                store_codes(s_b1, ca, 1);
+                store_codes(s_b0, ca, 0, 0);
+                store_codes(s_b1, ca, 1, 1);
             }
             // Step c multiplies stage c % 4.  Its B operands and the first half of its A
             // operands (of 4-bit B, whose codes need the registers, one) are in registers
@@ -552,24 +644,39 @@ __global__ __launch_bounds__(SH::NT) void tile_kernel(TileArgs g) {
             // of 4096 x 4096 from 2 x 10240: 250 us, 256 without, 263 with one A operand
             // read ahead instead of half).
             constexpr int kAfter = kLoads + (kPrefetch ? 1 : 0);
-            constexpr int kLanded = (kAfter & 15) | ((kAfter >> 4) << 14) | (BL == kCodes ? 0x0070 : 0x0F70);
+            // 4-bit: the next block's codes but one are asked for at the start of the third step
+            // of four, which leaves them in flight as long as the loads into the stages; until
+            // the fourth step's barrier they are among what was issued after.
+            constexpr int kCodeLoads = BL == kCodes ? 2 * kUnits : 0;
+            static_assert(kAfter + kCodeLoads < 64, "the wait count fits vmcnt");
             constexpr int kEarly = BL == kCodes ? 1 : TM / 2;
             uint4 a[TM], b[2][TN];  // b by parity of the step
             auto step = [&](const uint8_t* sa, const uint8_t* next_a, const uint8_t* next_b,
                             uint8_t* ahead_a, uint8_t* ahead_b, uint8_t* codes_b, int c, auto index,
-                            const Codes(&cur)[kUnits], const Codes(&nxt)[kUnits]) {
-                constexpr int s = decltype(index)::value;  // c % 4
+                            Codes(&cur)[kUnits], const Codes(&nxt)[kUnits]) {
+                constexpr int in_turn = decltype(index)::value;  // c % kTurn
+                constexpr int s = in_turn % 4;
                 constexpr int X = s & 1, Y = X ^ 1;
+                // 4-bit: where the scales of the group that ends with the step before are.
+                using Done = std::integral_constant<int, s % kGroup == 0 ? (in_turn + 8 - kGroup) % 8 : -1>;
+                fence();
+                if constexpr (BL == kCodes && s == 2) load_codes(c / 4 + 2, cur);
                 fence();
 #pragma unroll
                 for (int i = kEarly; i < TM; ++i) a[i] = rd_a(sa, i);
                 fence();
+                if constexpr (BL == kCodes) {
+                    code_products(Row0{}, RowMid{}, a, b[X], Done{});
+                } else {
 #pragma unroll
-                for (int i = 0; i < TM / 2; ++i)
+                    for (int i = 0; i < TM / 2; ++i)
 #pragma unroll
-                    for (int j = 0; j < TN; ++j) acc[i][j] = Ops::mma(b[X][j], a[i], acc[i][j]);
+                        for (int j = 0; j < TN; ++j) acc[i][j] = Ops::mma(b[X][j], a[i], acc[i][j]);
+                }
                 fence();
-                __builtin_amdgcn_s_waitcnt(kLanded);
+                constexpr int kFlying = kAfter + (s >= 2 ? kCodeLoads : 0);
+                __builtin_amdgcn_s_waitcnt((kFlying & 15) | ((kFlying >> 4) << 14) |
+                                           (BL == kCodes ? 0x0070 : 0x0F70));
                 __builtin_amdgcn_s_barrier();
                 fence();
 #pragma unroll
@@ -578,31 +685,38 @@ __global__ __launch_bounds__(SH::NT) void tile_kernel(TileArgs g) {
                 for (int i = 0; i < kEarly; ++i) a[i] = rd_a(next_a, i);
                 if constexpr (BL != kCodes) __builtin_amdgcn_s_setprio(1);
                 fence();
+                if constexpr (BL == kCodes) {
+                    code_products(RowMid{}, RowEnd{}, a, b[X], Done{});
+                    fence();
+                    issue(ahead_a, ahead_b, c + 3);
+                    fence();
+                } else {
 #pragma unroll
-                for (int i = TM / 2; i < TM; ++i) {
+                    for (int i = TM / 2; i < TM; ++i) {
 #pragma unroll
-                    for (int j = 0; j < TN; ++j) acc[i][j] = Ops::mma(b[X][j], a[i], acc[i][j]);
+                        for (int j = 0; j < TN; ++j) acc[i][j] = Ops::mma(b[X][j], a[i], acc[i][j]);
 #pragma unroll
-                    for (int u = 2 * kLoads * (i - TM / 2) / TM; u < 2 * kLoads * (i + 1 - TM / 2) / TM; ++u) {
-                        fence();
-                        issue1(ahead_a, ahead_b, c + 3, u);
-                        fence();
+                        for (int u = 2 * kLoads * (i - TM / 2) / TM; u < 2 * kLoads * (i + 1 - TM / 2) / TM; ++u) {
+                            fence();
+                            issue1(ahead_a, ahead_b, c + 3, u);
+                            fence();
+                        }
                     }
                 }
                 if constexpr (BL != kCodes) __builtin_amdgcn_s_setprio(0);
                 if constexpr (kPrefetch && s % 2 == 0) prefetch(c + kAhead);
                 if constexpr (BL == kCodes) {  // step c + 2, read after the next barrier
-                    if (s < 2) store_codes(codes_b, cur, s + 2);
-                    else store_codes(codes_b, nxt, s - 2);
+                    if (s < 2) store_codes(codes_b, cur, s + 2, in_turn + 2);
+                    else store_codes(codes_b, nxt, s - 2, (in_turn + 2) % 8);
                 }
                 fence();
             };
-            auto four = [&](int c, Codes(&cur)[kUnits], Codes(&nxt)[kUnits]) {
-                load_codes(c / 4 + 1, nxt);
-                step(s_a0, s_a1, s_b1, s_a3, s_b3, s_b2, c, std::integral_constant<int, 0>{}, cur, nxt);
-                step(s_a1, s_a2, s_b2, s_a0, s_b0, s_b3, c + 1, std::integral_constant<int, 1>{}, cur, nxt);
-                step(s_a2, s_a3, s_b3, s_a1, s_b1, s_b0, c + 2, std::integral_constant<int, 2>{}, cur, nxt);
-                step(s_a3, s_a0, s_b0, s_a2, s_b2, s_b1, c + 3, std::integral_constant<int, 3>{}, cur, nxt);
+            auto four = [&](int c, auto first, Codes(&cur)[kUnits], Codes(&nxt)[kUnits]) {
+                constexpr int h = decltype(first)::value;  // c % kTurn
+                step(s_a0, s_a1, s_b1, s_a3, s_b3, s_b2, c, std::integral_constant<int, h>{}, cur, nxt);
+                step(s_a1, s_a2, s_b2, s_a0, s_b0, s_b3, c + 1, std::integral_constant<int, h + 1>{}, cur, nxt);
+                step(s_a2, s_a3, s_b3, s_a1, s_b1, s_b0, c + 2, std::integral_constant<int, h + 2>{}, cur, nxt);
+                step(s_a3, s_a0, s_b0, s_a2, s_b2, s_b1, c + 3, std::integral_constant<int, h + 3>{}, cur, nxt);
             };
             fence();
             __builtin_amdgcn_s_waitcnt(kWaitSteps);  // step 0 has landed
@@ -613,10 +727,11 @@ __global__ __launch_bounds__(SH::NT) void tile_kernel(TileArgs g) {
 #pragma unroll
             for (int i = 0; i < kEarly; ++i) a[i] = rd_a(s_a0, i);
             for (int c = 0; c < nsteps; c += kTurn) {
-                four(c, ca, cb);
-                if constexpr (kTurn == 8) four(c + 4, cb, ca);
+                four(c, std::integral_constant<int, 0>{}, ca, cb);
+                if constexpr (kTurn == 8) four(c + 4, std::integral_constant<int, 4>{}, cb, ca);
             }
             __builtin_amdgcn_s_waitcnt(0x0070);  // no load is left in flight to the stages
+            finish_parts(8 - kGroup);
         }
     }
 

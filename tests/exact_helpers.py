@@ -6,8 +6,7 @@ whole i, so a weight less its zero point times x is a multiple of 2^-12.  Every
 partial sum of the sizes used here stays below 2^10 and so within 24 bits, in any
 order, biased codes (whole numbers below 2^17) included.  The scaled weight
 itself has up to 12 significant bits, more than fp16 (11) and bf16 (8) hold: a
-kernel that rounds it first does not give these results.  (plain_scales: powers
-of two, so that it may.)
+kernel that rounds it first does not give these results.
 
 Gated block: everything is a whole number, g and u of at most 8 bits.
 """
@@ -20,11 +19,9 @@ from proj_helpers import half_step, make_q4, tiny
 F32 = 2.0 ** -24
 
 
-def exact_q4(gen, N, K, G, dtype, zeros, device, plain_scales=False):
+def exact_q4(gen, N, K, G, dtype, zeros, device):
     codes, scales, z = make_q4(gen, N, K, G, dtype, zeros, "cpu")
-    i = torch.randint(0, 128, scales.shape, generator=gen)
-    scales = 2.0 ** -(5 + i % 2) if plain_scales else (1 + i / 128) * 2.0 ** -5
-    scales = scales.to(dtype)
+    scales = ((1 + torch.randint(0, 128, scales.shape, generator=gen) / 128) * 2.0 ** -5).to(dtype)
     return tuple(None if t is None else t.to(device) for t in (codes, scales, z))
 
 

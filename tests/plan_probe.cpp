@@ -15,10 +15,10 @@ int probe_ffn_path(long long R, long long N, int bytes, int vec) { return ffn_pa
 int probe_ffn_wide(long long N) { return ffn_wide_strips(N); }
 
 // Kinds of tile of a 16-bit product: of the first whole rounds (-1: not split off)
-// and of the rest, or of all.
-void probe_tiles(long long M, long long N, int batches, int gated, int codes, int* kinds) {
-    const TilePlan p = plan_tiles(M, N, batches, gated, codes);
-    kinds[0] = p.big.m_end > 0 ? (int)kBigTiles : -1;
+// and of the rest, or of all.  flushes: of 4-bit weights, else 0.
+void probe_tiles(long long M, long long N, int batches, int gated, int flushes, int* kinds) {
+    const TilePlan p = plan_tiles(M, N, batches, gated, flushes);
+    kinds[0] = p.big.m_end > 0 ? (int)p.big_kind : -1;
     kinds[1] = p.kind;
 }
 int probe_f32_tiles(long long M, long long N, int batches, int gated) {

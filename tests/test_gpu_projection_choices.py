@@ -15,10 +15,10 @@ pytestmark = pytest.mark.gpu
 DEV = "cuda:0"
 
 
-def _q4(R, K, N, G, dt, plain_scales):
+def _q4(R, K, N, G, dt):
     gen = torch.Generator().manual_seed(R + K + N)
     dtype = DTYPES[dt]
-    wg, wu = (exact_q4(gen, N, K, G, dtype, z, DEV, plain_scales) for z in (True, False))
+    wg, wu = (exact_q4(gen, N, K, G, dtype, z, DEV) for z in (True, False))
     x = exact_x(gen, R, K, dtype, DEV)
     add = torch.randint(-4, 5, (N,), generator=gen).to(dtype).to(DEV)
     pg, pu = (sg.q4_pack(*w, group_size=G, in_features=K) for w in (wg, wu))
@@ -36,21 +36,21 @@ def _q4(R, K, N, G, dt, plain_scales):
 @pytest.mark.parametrize("G", [32, 64, 128])
 @pytest.mark.parametrize("R,N", Q4_FEW)
 def test_q4_few_rows(R, N, G, dt):
-    _q4(R, Q4_FEW_K, N, G, dt, False)
+    _q4(R, Q4_FEW_K, N, G, dt)
 
 
 @pytest.mark.parametrize("dt", ["f16", "bf16"])
 @pytest.mark.parametrize("G", [32, 64, 128])
 @pytest.mark.parametrize("R,K,N", Q4_TILES)
 def test_q4_tiles(R, K, N, G, dt):
-    _q4(R, K, N, G, dt, True)
+    _q4(R, K, N, G, dt)
 
 
 @pytest.mark.parametrize("dt", ["f16", "bf16"])
 @pytest.mark.parametrize("G", [32, 64, 128])
 @pytest.mark.parametrize("R,K,N", Q4_SLOW)
 def test_q4_register_path(R, K, N, G, dt):
-    _q4(R, K, N, G, dt, True)
+    _q4(R, K, N, G, dt)
 
 
 def _block(R, H, I, dt):
@@ -65,6 +65,19 @@ def _block(R, H, I, dt):
     with torch.no_grad():
         check_exact(sg.gated_ffn(x, Wg, Wu, "relu"), exact_gated(x, Wg, Wu, None, None, dh)[0],
                     f"h without addends of {R}x{H}->{I} {dt}")
+
+
+# A row's result does not depend on the rows beside it, whichever kernels they take: on
+# these inputs, bit for bit.
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+def test_q4_rows_are_the_same_in_any_batch(dt):
+    gen = torch.Generator().manual_seed(3)
+    dtype = DTYPES[dt]
+    w = sg.q4_pack(*exact_q4(gen, 9000, 1000, 64, dtype, True, DEV), group_size=64)
+    x = exact_x(gen, 700, 1000, dtype, DEV)
+    y = sg.q4_linear(x, w)
+    for rows in (1, 4, 30, 100, 256, 257, 300):
+        assert torch.equal(sg.q4_linear(x[:rows], w), y[:rows]), rows
 
 
 @pytest.mark.parametrize("dt", ["f16", "bf16"])

@@ -11,7 +11,7 @@ from choice_shapes import FFN16, FFN16_SLOW, FFN32, Q4_FEW, Q4_SLOW, Q4_TILES, R
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
-TILES_PATH, STRIPS_PATH = 4, 3  # of Q4Path
+STRIPS_PATH, TILES_PATH = 3, 4  # of Q4Path
 FFN_TILES = 5                   # of FfnPath
 FLUSHES = (1, 2, 4)
 
@@ -30,9 +30,9 @@ class Rules:
     def __init__(self, dll):
         self.dll = dll
 
-    def _tiles(self, M, N, batches, gated, codes):
+    def _tiles(self, M, N, batches, gated, flushes=0):
         out = (ctypes.c_int * 2)()
-        self.dll.probe_tiles(ctypes.c_longlong(M), ctypes.c_longlong(N), batches, gated, codes, out)
+        self.dll.probe_tiles(ctypes.c_longlong(M), ctypes.c_longlong(N), batches, gated, flushes, out)
         return tuple(out)
 
     def q4(self, R, N, flushes, gated, nbytes=2, vec=1):
@@ -43,7 +43,7 @@ class Rules:
         if path == STRIPS_PATH:
             detail = self.dll.probe_q4_strip(ll(R), ll(N), flushes, gated)
         elif path == TILES_PATH:
-            detail = self._tiles(R, N, 1, gated, 1) if vec else "registers"
+            detail = self._tiles(R, N, 1, gated, flushes) if vec else "registers"
         return (nbytes, vec, gated, flushes, path, detail)
 
     def block(self, R, H, I, nbytes=2, vec=1):
@@ -60,8 +60,8 @@ class Rules:
             f32 = lambda M, N, b, g: self.dll.probe_f32_tiles(ll(M), ll(N), b, g)
             fwd, dx, dw = f32(R, I, 1, 1), kind, f32(I, H, 2, 0)
         else:
-            fwd, dw = self._tiles(R, I, 1, 1, 0), self._tiles(I, H, 2, 0, 0)
-            dx = kind if split else self._tiles(R, H, 1, 0, 0)
+            fwd, dw = self._tiles(R, I, 1, 1), self._tiles(I, H, 2, 0)
+            dx = kind if split else self._tiles(R, H, 1, 0)
         if path != FFN_TILES:
             fwd = self.dll.probe_ffn_wide(ll(I)) if path in (3, 4) else None
         return {key + ("forward", path, fwd), key + ("dx", split, dx), key + ("dW", dw)}
@@ -87,6 +87,10 @@ def test_every_q4_kernel_is_tested(rules):
         tested |= {rules.q4(R, N, flushes, gated) for R, K, N in Q4_TILES}
         tested |= {rules.q4(R, N, flushes, gated, 2, 0) for R, K, N in Q4_SLOW}
         assert taken <= tested, sorted(taken - tested, key=str)
+        # each kind of tile with several turns of the loop over K, too
+        for kind in {k[5] for k in taken if k[4] == TILES_PATH and k[1]}:
+            turns = [K for R, K, N in Q4_TILES if rules.q4(R, N, flushes, gated)[4:] == (TILES_PATH, kind)]
+            assert max(turns) > 512, (gated, flushes, kind, turns)
     assert all(K % 8 == 0 for _, K, _ in Q4_TILES) and all(K % 8 for _, K, _ in Q4_SLOW)
 
 
