@@ -422,7 +422,10 @@ int q4_linear(void* y, const void* x, const sgmv_q4_weight* w, const void* bias,
  *     dg = dh * u * act'(g),  du = dh * act(g)   (also the addends' gradients)
  *     dx = dg Wg + du Wu,  dWg = dg^T x,  dWu = du^T x
  * with dg and du rounded to dtype between the steps.  dx, or dWg and dWu,
- * may be NULL and are then not computed; dg and du are needed.  With
+ * may be NULL and are then not computed; dg and du are needed.  Options, OR-ed into
+ * dtype:
+ *   SGMV_ONE_WEIGHT      one of dWg and dWu alone may be NULL.
+ * With
  * num_rows == 0 the weights' gradients are zero.  act' of relu at 0 is 0.  At
  * infinities the activations and act' are their limits: a g of minus infinity gives
  * h = 0 and no gradient.
@@ -440,6 +443,8 @@ typedef enum {
     SGMV_ACT_RELU = 3,
     SGMV_ACT_SIGMOID = 4
 } sgmv_act_t;
+
+#define SGMV_ONE_WEIGHT 0x200
 
 int q4_gated_ffn(void* h, const void* x, const sgmv_q4_weight* gate, const sgmv_q4_weight* up,
                  const void* gate_add, const void* up_add, int32_t num_rows, int32_t out_features,

@@ -14,6 +14,13 @@ int check_ffn(int R, int H, int I, int act, int dtype) {
     return SGMV_OK;
 }
 
+// Takes an option's bit out of dtype.
+bool take_option(int32_t& dtype, int option) {
+    const bool has = dtype >= 0 && (dtype & option) != 0;
+    if (has) dtype &= ~option;
+    return has;
+}
+
 template <typename DT, int XR, int MT, int PD>
 int run_rows(const RowsArgs& a, hipStream_t st) {
     launch(&rows_kernel<DT, PlainSrc<DT>, XR, MT, 1, PD, 1, true>,
@@ -120,21 +127,21 @@ int run_backward(const GradArgs& b, hipStream_t st) {
         }
         if (rc != SGMV_OK) return rc;
     }
-    if (b.dWg) {
-        // dWg = dg^T x and dWu = du^T x: K = rows, both operands across K.
+    if (b.dWg || b.dWu) {
+        // dWg = dg^T x and dWu = du^T x, or one of them: K = rows, both operands across K.
         TileArgs t{};
-        t.a[0] = b.dg;
+        t.a[0] = b.dWg ? b.dg : b.du;
         t.a[1] = b.du;
         t.lda = b.I;
         t.b[0] = b.x;
         t.b[1] = b.x;
         t.ldb = b.H;
-        t.out[0] = b.dWg;
+        t.out[0] = b.dWg ? b.dWg : b.dWu;
         t.out[1] = b.dWu;
         t.M = b.I;
         t.N = b.H;
         t.K = b.R;
-        t.batches = 2;
+        t.batches = b.dWg && b.dWu ? 2 : 1;
         t.avec = gvec;
         t.bvec = hvec && aligned16(b.x);
         t.yvec = b.H % 4 == 0 && aligned16(b.dWg) && aligned16(b.dWu);
@@ -179,6 +186,7 @@ int gated_ffn(void* h, void* g_saved, void* u_saved, const void* x, const void* 
 
 size_t gated_ffn_backward_workspace_bytes(int32_t num_rows, int32_t in_features,
                                           int32_t out_features, int32_t dtype) {
+    take_option(dtype, SGMV_ONE_WEIGHT);
     if (check_ffn(num_rows, in_features, out_features, SGMV_ACT_SILU, dtype) != SGMV_OK || num_rows == 0)
         return 0;
     const SumPlan p = plan_sum(num_rows, in_features, out_features, dtype);
@@ -189,10 +197,12 @@ int gated_ffn_backward(void* dx, void* dWg, void* dWu, void* dg, void* du, const
                        const void* x, const void* Wg, const void* Wu, const void* g, const void* u,
                        int32_t num_rows, int32_t in_features, int32_t out_features, int32_t act,
                        int32_t dtype, void* workspace, size_t workspace_bytes, void* stream) {
+    const bool one_weight = take_option(dtype, SGMV_ONE_WEIGHT);
     const int rc = check_ffn(num_rows, in_features, out_features, act, dtype);
     if (rc != SGMV_OK) return rc;
-    if ((dWg == nullptr) != (dWu == nullptr)) return SGMV_ERR_NULL_PTR;
-    if (num_rows > 0 && (!dg || !du || !dh || !g || !u || (dx && (!Wg || !Wu)) || (dWg && !x)))
+    if (!one_weight && (dWg == nullptr) != (dWu == nullptr)) return SGMV_ERR_NULL_PTR;
+    if (num_rows > 0 &&
+        (!dg || !du || !dh || !g || !u || (dx && (!Wg || !Wu)) || ((dWg || dWu) && !x)))
         return SGMV_ERR_NULL_PTR;
     const size_t need =
         dx ? gated_ffn_backward_workspace_bytes(num_rows, in_features, out_features, dtype) : 0;

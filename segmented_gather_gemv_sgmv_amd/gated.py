@@ -12,6 +12,8 @@ from __future__ import annotations
 
 from . import _check, _need, _no_tangents, _stream_ptr, _torch, dtype_code, lib
 
+ONE_WEIGHT = 0x200  # an option of sgmv.h, OR-ed into the dtype's code
+
 ACTIVATIONS = {"silu": 0, "gelu": 1, "gelu_tanh": 2, "relu": 3, "sigmoid": 4}
 
 
@@ -80,25 +82,29 @@ def gated_ffn_backward(dh, x, Wg, Wu, g, u, act: str = "silu", need_dx=True, nee
     """Gradients of gated_ffn from dh = dL/dh and the saved g and u (its
     pre-activations, addends included): returns ``(dx, dWg, dWu, dg, du)``,
     dx or the weights' gradients None where not needed; dg and du are also
-    the addends' gradients."""
+    the addends' gradients.  ``need_dw`` may be a pair, for Wg and Wu."""
     R, H, I = _check_weights(x, Wg, Wu)
-    code = _act_code(act)
+    code, dtype = _act_code(act), dtype_code(x.dtype)
     for t, name in ((dh, "dh"), (g, "g"), (u, "u")):
         _need(t, name, x.device, x.dtype, 2)
         if tuple(t.shape) != (R, I):
             raise ValueError(f"{name} must be {(R, I)}, got {tuple(t.shape)}")
+    need_g, need_u = need_dw if isinstance(need_dw, (tuple, list)) else (need_dw, need_dw)
     dg, du = x.new_empty((R, I)), x.new_empty((R, I))
     dx = x.new_empty((R, H)) if need_dx else None
-    dWg, dWu = (x.new_empty((I, H)), x.new_empty((I, H))) if need_dw else (None, None)
+    dWg = x.new_empty((I, H)) if need_g else None
+    dWu = x.new_empty((I, H)) if need_u else None
     ptr = lambda t: None if t is None else t.data_ptr()
     ws, ws_bytes = None, 0
     if need_dx:
-        ws_bytes = lib().gated_ffn_backward_workspace_bytes(R, H, I, dtype_code(x.dtype))
+        ws_bytes = lib().gated_ffn_backward_workspace_bytes(R, H, I, dtype)
         if ws_bytes:
             ws = x.new_empty(ws_bytes, dtype=_torch().uint8)
+    if bool(need_g) != bool(need_u):
+        dtype |= ONE_WEIGHT
     _check(lib().gated_ffn_backward(ptr(dx), ptr(dWg), ptr(dWu), dg.data_ptr(), du.data_ptr(),
                                     dh.data_ptr(), x.data_ptr(), Wg.data_ptr(), Wu.data_ptr(),
-                                    g.data_ptr(), u.data_ptr(), R, H, I, code, dtype_code(x.dtype),
+                                    g.data_ptr(), u.data_ptr(), R, H, I, code, dtype,
                                     ptr(ws), ws_bytes, _stream_ptr(x.device)),
            "gated_ffn_backward")
     return dx, dWg, dWu, dg, du
@@ -128,10 +134,8 @@ def _autograd_function():
                 x, Wg, Wu, g, u = ctx.saved_tensors
                 want = ctx.needs_input_grad
                 dx, dWg, dWu, dg, du = gated_ffn_backward(
-                    dh.contiguous(), x, Wg, Wu, g, u, ctx.act, need_dx=want[0],
-                    need_dw=want[1] or want[2])
-                return (dx, dWg if want[1] else None, dWu if want[2] else None,
-                        dg if want[3] else None, du if want[4] else None, None)
+                    dh.contiguous(), x, Wg, Wu, g, u, ctx.act, need_dx=want[0], need_dw=want[1:3])
+                return dx, dWg, dWu, dg if want[3] else None, du if want[4] else None, None
 
         _function = GatedFFN
     return _function
