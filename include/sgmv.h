@@ -423,16 +423,23 @@ int q4_linear(void* y, const void* x, const sgmv_q4_weight* w, const void* bias,
  *     dx = dg Wg + du Wu,  dWg = dg^T x,  dWu = du^T x
  * with dg and du rounded to dtype between the steps.  dx, or dWg and dWu,
  * may be NULL and are then not computed; dg and du are needed.  Options, OR-ed into
- * dtype:
+ * dtype (of the workspace query too):
+ *   SGMV_FULL_GRADIENTS  g_saved, u_saved, g and u are float32, and dg and du go
+ *                        through the products in two parts of dtype each (rounded
+ *                        once where they are stored), so that no gradient is off by
+ *                        more than float32 sums and its own rounding; the backward
+ *                        products take twice as long.  Without it gradients carry
+ *                        the roundings of g, u, dg and du.
  *   SGMV_ONE_WEIGHT      one of dWg and dWu alone may be NULL.
  * With
  * num_rows == 0 the weights' gradients are zero.  act' of relu at 0 is 0.  At
  * infinities the activations and act' are their limits: a g of minus infinity gives
  * h = 0 and no gradient.
  * Features beyond 2^20 return SGMV_ERR_UNSUPPORTED.
- * workspace: for dx, at least gated_ffn_backward_workspace_bytes(...) bytes (0 for
- * many sizes: it may then be NULL), 16-byte aligned: dx of few rows is summed in
- * ranges of out_features, whose float32 sums stand there.  It may hold anything
+ * workspace: for dx, and with SGMV_FULL_GRADIENTS always, at least
+ * gated_ffn_backward_workspace_bytes(...) bytes (0 for many sizes: it may then be
+ * NULL), 16-byte aligned: dx of few rows is summed in ranges of out_features, whose
+ * float32 sums stand there, and second parts of dg and du.  It may hold anything
  * before the call and does after it, from its first byte on: a buffer of the calls
  * above, whose counters have to be zero, must not be given here.
  */
@@ -444,6 +451,7 @@ typedef enum {
     SGMV_ACT_SIGMOID = 4
 } sgmv_act_t;
 
+#define SGMV_FULL_GRADIENTS 0x100
 #define SGMV_ONE_WEIGHT 0x200
 
 int q4_gated_ffn(void* h, const void* x, const sgmv_q4_weight* gate, const sgmv_q4_weight* up,

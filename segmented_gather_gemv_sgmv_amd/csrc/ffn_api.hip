@@ -56,6 +56,7 @@ int run_forward(const RowsArgs& a, hipStream_t st) {
         t.add[q] = a.add[q];
         t.save[q] = a.save[q];
     }
+    t.save_f32 = a.save_f32;
     t.M = a.R;
     t.N = a.N;
     t.K = a.K;
@@ -68,25 +69,56 @@ int run_forward(const RowsArgs& a, hipStream_t st) {
     return launch_tiles_any<DT, kAlongK, kAlongK, 1, true>(t, a.xvec && a.wvec, st);
 }
 
+// Where a backward pass keeps what: floats of dx's sums, then (full gradients) the
+// second parts of dg and du.
+struct GradPlan {
+    SumPlan sum;
+    int parts;             // of dg and du: 1 or 2
+    size_t lo_at, lo_each; // bytes
+    size_t bytes;
+};
+
+GradPlan plan_gradients(long long R, long long H, long long I, int dtype, bool full, bool dx) {
+    GradPlan p{plan_sum(R, H, I, dtype), full && dtype != SGMV_F32 ? 2 : 1, 0, 0, 0};
+    // A second part's products are sums of their own, joined with the first's.
+    if (dx && (p.sum.ranges > 1 || p.parts == 2))
+        p.lo_at = (size_t)p.parts * p.sum.ranges * p.sum.stride * sizeof(float);
+    p.bytes = p.lo_at;
+    if (p.parts == 2) {
+        p.lo_each = (size_t)ceil_div(R * I * elem_size(dtype), 256) * 256;
+        p.bytes += 2 * p.lo_each;
+    }
+    return p;
+}
+
 struct GradArgs {
     void *dx, *dWg, *dWu, *dg, *du;
     const void *dh, *x, *Wg, *Wu, *g, *u;
     int R, H, I, act;
-    float* workspace;  // of dx's sums, when they are taken in ranges
-    SumPlan sum;
+    char* workspace;
+    GradPlan plan;
 };
 
 template <typename DT>
 int run_backward(const GradArgs& b, hipStream_t st) {
     using T = typename DT::storage;
     constexpr int PK = PieceOps<DT>::kPK;
+    const int parts = b.plan.parts;
+    void* const lo[2] = {parts == 2 ? b.workspace + b.plan.lo_at : nullptr,
+                         parts == 2 ? b.workspace + b.plan.lo_at + b.plan.lo_each : nullptr};
     if (b.R > 0) {
         const long long n = (long long)b.R * b.I;
         const int vec = aligned16(b.dg) && aligned16(b.du) && aligned16(b.dh) && aligned16(b.g) &&
                         aligned16(b.u);
         const long long blocks = std::min<long long>(ceil_div(n, 256 * DT::kVec), 4096);
-        launch(&gated_grad_kernel<DT>, dim3((unsigned)blocks), dim3(256), st, (T*)b.dg, (T*)b.du,
-               (const T*)b.dh, (const T*)b.g, (const T*)b.u, n, b.act, vec);
+        auto run = [&](auto kernel) {
+            launch(kernel, dim3((unsigned)blocks), dim3(256), st, (T*)b.dg, (T*)b.du, (T*)lo[0],
+                   (T*)lo[1], (const T*)b.dh, b.g, b.u, n, b.act, vec);
+        };
+        if constexpr (DT::kBytes == 2) {
+            if (parts == 2) run(&gated_grad_kernel<DT, true>);
+        }
+        if (parts == 1) run(&gated_grad_kernel<DT, false>);
         int rc = launch_status();
         if (rc != SGMV_OK) return rc;
     }
@@ -94,9 +126,8 @@ int run_backward(const GradArgs& b, hipStream_t st) {
     const bool gvec = ivec && aligned16(b.dg) && aligned16(b.du);
     if (b.dx && b.R > 0) {
         // dx = dg Wg + du Wu: two segments of K = I, the weights across K.
+        const SumPlan& sum = b.plan.sum;
         TileArgs t{};
-        t.a[0] = b.dg;
-        t.a[1] = b.du;
         t.lda = b.I;
         t.b[0] = b.Wg;
         t.b[1] = b.Wu;
@@ -105,47 +136,66 @@ int run_backward(const GradArgs& b, hipStream_t st) {
         t.M = b.R;
         t.N = b.H;
         t.K = b.I;
-        t.batches = b.sum.ranges;
-        t.range_steps = b.sum.range_steps;
+        t.batches = sum.ranges;
+        t.range_steps = sum.range_steps;
         t.avec = gvec;
         t.bvec = hvec && aligned16(b.Wg) && aligned16(b.Wu);
         t.yvec = b.H % 4 == 0 && aligned16(b.dx);
         const bool direct = t.avec && t.bvec;
-        int rc;
-        if (b.sum.ranges == 1) {
-            rc = launch_tiles_any<DT, kAlongK, kAcrossK, 2, false>(t, direct, st);
-        } else {
-            t.partial = b.workspace;
-            t.partial_stride = b.sum.stride;
-            rc = launch_kind<DT, kAlongK, kAcrossK, 2, false>(
-                b.sum.kind, t, TileRange{0, t.M, 0, t.N}, direct, st);
+        const bool joined = sum.ranges > 1 || parts == 2;
+        for (int p = 0; p < parts; ++p) {
+            t.a[0] = p == 0 ? b.dg : lo[0];
+            t.a[1] = p == 0 ? b.du : lo[1];
+            if (joined) {
+                t.partial = (float*)b.workspace + (long long)p * sum.ranges * sum.stride;
+                t.partial_stride = sum.stride;
+            }
+            const int rc = sum.ranges == 1
+                ? launch_tiles_any<DT, kAlongK, kAcrossK, 2, false>(t, direct, st)
+                : launch_kind<DT, kAlongK, kAcrossK, 2, false>(
+                      sum.kind, t, TileRange{0, t.M, 0, t.N}, direct, st);
             if (rc != SGMV_OK) return rc;
+        }
+        if (joined) {
             const long long n = (long long)b.R * b.H;
             launch(&join_kernel<DT>, dim3((unsigned)ceil_div(n, 1024)), dim3(256), st, (T*)b.dx,
-                   (const float*)b.workspace, b.sum.ranges, b.sum.stride, n, (int)aligned16(b.dx));
-            rc = launch_status();
+                   (const float*)b.workspace, parts * sum.ranges, sum.stride, n, (int)aligned16(b.dx));
+            const int rc = launch_status();
+            if (rc != SGMV_OK) return rc;
         }
-        if (rc != SGMV_OK) return rc;
     }
-    if (b.dWg || b.dWu) {
-        // dWg = dg^T x and dWu = du^T x, or one of them: K = rows, both operands across K.
-        TileArgs t{};
+    // dWg = dg^T x and dWu = du^T x: K = rows, both operands across K; second parts are
+    // a second segment of K.
+    TileArgs t{};
+    t.lda = b.I;
+    t.b[0] = t.b[1] = b.x;
+    t.ldb = b.H;
+    t.M = b.I;
+    t.N = b.H;
+    t.K = b.R;
+    t.avec = gvec;
+    t.bvec = hvec && aligned16(b.x);
+    t.yvec = b.H % 4 == 0 && aligned16(b.dWg) && aligned16(b.dWu);
+    const bool direct = t.avec && t.bvec;
+    if (parts == 1) {
         t.a[0] = b.dWg ? b.dg : b.du;
         t.a[1] = b.du;
-        t.lda = b.I;
-        t.b[0] = b.x;
-        t.b[1] = b.x;
-        t.ldb = b.H;
         t.out[0] = b.dWg ? b.dWg : b.dWu;
         t.out[1] = b.dWu;
-        t.M = b.I;
-        t.N = b.H;
-        t.K = b.R;
-        t.batches = b.dWg && b.dWu ? 2 : 1;
-        t.avec = gvec;
-        t.bvec = hvec && aligned16(b.x);
-        t.yvec = b.H % 4 == 0 && aligned16(b.dWg) && aligned16(b.dWu);
-        return launch_tiles_any<DT, kAcrossK, kAcrossK, 1, false>(t, t.avec && t.bvec, st);
+        t.batches = (b.dWg ? 1 : 0) + (b.dWu ? 1 : 0);
+        return t.batches > 0 ? launch_tiles_any<DT, kAcrossK, kAcrossK, 1, false>(t, direct, st) : SGMV_OK;
+    }
+    if constexpr (DT::kBytes == 2) {
+        t.batches = 1;
+        t.range_steps = 1 << 30;  // one range: all steps
+        for (int q = 0; q < 2; ++q) {
+            t.out[0] = q == 0 ? b.dWg : b.dWu;
+            if (!t.out[0]) continue;
+            t.a[0] = q == 0 ? b.dg : b.du;
+            t.a[1] = lo[q];
+            const int rc = launch_tiles_any<DT, kAcrossK, kAcrossK, 2, false>(t, direct, st);
+            if (rc != SGMV_OK) return rc;
+        }
     }
     return SGMV_OK;
 }
@@ -157,6 +207,8 @@ extern "C" {
 int gated_ffn(void* h, void* g_saved, void* u_saved, const void* x, const void* Wg, const void* Wu,
               const void* gate_add, const void* up_add, int32_t num_rows, int32_t in_features,
               int32_t out_features, int32_t act, int32_t dtype, void* stream) {
+    const bool full = take_option(dtype, SGMV_FULL_GRADIENTS);
+    take_option(dtype, SGMV_ONE_WEIGHT);
     const int rc = check_ffn(num_rows, in_features, out_features, act, dtype);
     if (rc != SGMV_OK) return rc;
     if (num_rows == 0) return SGMV_OK;
@@ -171,6 +223,7 @@ int gated_ffn(void* h, void* g_saved, void* u_saved, const void* x, const void* 
     a.add[1] = up_add;
     a.save[0] = g_saved;
     a.save[1] = u_saved;
+    a.save_f32 = full;
     a.R = num_rows;
     a.N = out_features;
     a.K = in_features;
@@ -186,17 +239,18 @@ int gated_ffn(void* h, void* g_saved, void* u_saved, const void* x, const void* 
 
 size_t gated_ffn_backward_workspace_bytes(int32_t num_rows, int32_t in_features,
                                           int32_t out_features, int32_t dtype) {
+    const bool full = take_option(dtype, SGMV_FULL_GRADIENTS);
     take_option(dtype, SGMV_ONE_WEIGHT);
     if (check_ffn(num_rows, in_features, out_features, SGMV_ACT_SILU, dtype) != SGMV_OK || num_rows == 0)
         return 0;
-    const SumPlan p = plan_sum(num_rows, in_features, out_features, dtype);
-    return p.ranges == 1 ? 0 : (size_t)(p.ranges * p.stride) * sizeof(float);
+    return plan_gradients(num_rows, in_features, out_features, dtype, full, true).bytes;
 }
 
 int gated_ffn_backward(void* dx, void* dWg, void* dWu, void* dg, void* du, const void* dh,
                        const void* x, const void* Wg, const void* Wu, const void* g, const void* u,
                        int32_t num_rows, int32_t in_features, int32_t out_features, int32_t act,
                        int32_t dtype, void* workspace, size_t workspace_bytes, void* stream) {
+    const bool full = take_option(dtype, SGMV_FULL_GRADIENTS);
     const bool one_weight = take_option(dtype, SGMV_ONE_WEIGHT);
     const int rc = check_ffn(num_rows, in_features, out_features, act, dtype);
     if (rc != SGMV_OK) return rc;
@@ -204,13 +258,12 @@ int gated_ffn_backward(void* dx, void* dWg, void* dWu, void* dg, void* du, const
     if (num_rows > 0 &&
         (!dg || !du || !dh || !g || !u || (dx && (!Wg || !Wu)) || ((dWg || dWu) && !x)))
         return SGMV_ERR_NULL_PTR;
-    const size_t need =
-        dx ? gated_ffn_backward_workspace_bytes(num_rows, in_features, out_features, dtype) : 0;
-    if (need > 0 && (!workspace || workspace_bytes < need || !aligned16(workspace)))
+    GradPlan plan = plan_gradients(num_rows, in_features, out_features, dtype, full, dx != nullptr);
+    if (num_rows == 0) plan.bytes = 0, plan.parts = 1;
+    if (plan.bytes > 0 && (!workspace || workspace_bytes < plan.bytes || !aligned16(workspace)))
         return SGMV_ERR_WORKSPACE;
     const GradArgs b{dx, dWg, dWu, dg, du, dh, x, Wg, Wu, g, u, num_rows, in_features, out_features,
-                     act, (float*)workspace,
-                     plan_sum(num_rows, in_features, out_features, dtype)};
+                     act, (char*)workspace, plan};
     const hipStream_t st = (hipStream_t)stream;
     if (dtype == SGMV_F32) return run_backward<F32>(b, st);
     if (dtype == SGMV_F16) return run_backward<F16>(b, st);

@@ -41,6 +41,7 @@ struct RowsArgs {
     const void* add[2];   // gated: addends before the activation [R, N] or NULL;
                           // else add[0] = bias [N] or NULL
     void* save[2];        // gated: where g and u are kept [R, N], or NULL
+    int save_f32;         // they are kept in float32
     int R, N, K;
     int kblocks;          // blocks of four pieces of K
     int act;
@@ -170,7 +171,10 @@ __device__ __forceinline__ void finish_rows(const RowsArgs& a, const acc4_t (&v)
             for (int q = 0; q < 2; ++q) {
                 p[q] = v[q][c];
                 if (a.add[q]) p[q] += DT::load1((const T*)a.add[q] + at);
-                if (a.save[q]) ((T*)a.save[q])[at] = DT::from_float(kept<DT>(p[q]));
+                if (a.save[q]) {
+                    if (a.save_f32) ((float*)a.save[q])[at] = p[q];
+                    else ((T*)a.save[q])[at] = DT::from_float(kept<DT>(p[q]));
+                }
             }
             o = act_value(a.act, p[0]) * p[1];
         } else {

@@ -52,6 +52,7 @@ struct TileArgs {
     void* out[2];         // [M, N]
     const void* add[2];   // gated: addends [M, N]; else add[0] = bias [N]; or NULL
     void* save[2];        // gated: g and u [M, N], or NULL
+    int save_f32;         // these in float32
     int M, N, K;          // gated: N columns of each matrix
     int batches;          // kSegs == 2: ranges of K, each summed by workgroups of its own
     int range_steps;      // kSegs == 2, direct loads: steps per range, a multiple of 4
@@ -774,7 +775,9 @@ __global__ __launch_bounds__(SH::NT, BL == kCodes ? 2 : 1) void tile_kernel(Tile
 #pragma unroll
                         for (int c = 0; c < 4; ++c) v[q][c] += b[c];
                     }
-                    if (g.save[q]) {
+                    if (g.save[q] && g.save_f32) {
+                        store4f<F32>((float*)g.save[q] + at, left, g.yvec, v[q]);
+                    } else if (g.save[q]) {
                         float k[4];
 #pragma unroll
                         for (int c = 0; c < 4; ++c) k[c] = kept<DT>(v[q][c]);
@@ -801,31 +804,41 @@ __global__ __launch_bounds__(SH::NT, BL == kCodes ? 2 : 1) void tile_kernel(Tile
 // Bound: HBM; 4096 x 11008 bf16, 451 MB: 87 us, 5.2 TB/s.
 // g and u come, and dg and du go on to the matrix products, in the activations'
 // type: a training step's bf16 gradients are then off by 0.0031 of their size (root
-// mean square) where float32 in between leaves their own rounding, 0.0017.  float32 g
-// and u would move 360 MB more at these sizes, and products of float32 dg and du
-// would take two passes of the matrix cores.
+// mean square) where float32 in between leaves their own rounding, 0.0017.  kFull, for
+// callers who ask for that: g and u come in float32, and what dg and du lose by their
+// rounding goes to the products too, as second parts (lo), 16 and 22 bits in all.  4096 x
+// 11008 bf16 moves 811 MB then, and the products take twice as long.
 // ---------------------------------------------------------------------------
-template <typename DT>
+template <typename DT, bool kFull>
 __global__ __launch_bounds__(256) void gated_grad_kernel(
     typename DT::storage* __restrict__ dg, typename DT::storage* __restrict__ du,
-    const typename DT::storage* __restrict__ dh, const typename DT::storage* __restrict__ gs,
-    const typename DT::storage* __restrict__ us, long long n, int act, int vec) {
+    typename DT::storage* __restrict__ dg_lo, typename DT::storage* __restrict__ du_lo,
+    const typename DT::storage* __restrict__ dh, const void* __restrict__ gs,
+    const void* __restrict__ us, long long n, int act, int vec) {
+    using KT = std::conditional_t<kFull, F32, DT>;  // of g and u
+    using K = typename KT::storage;
     constexpr int V = DT::kVec;
+    const K* const gk = (const K*)gs;
+    const K* const uk = (const K*)us;
+    auto unpack = [](const K* p, float* f) {
+#pragma unroll
+        for (int i = 0; i < V; i += KT::kVec) KT::unpack(load16(p + i), f + i);
+    };
     const long long stride = (long long)gridDim.x * 256 * V;
     for (long long i = ((long long)blockIdx.x * 256 + threadIdx.x) * V; i < n; i += stride) {
         float h[V], a[V], b[V];
         const bool whole = vec && i + V <= n;
         if (whole) {
             DT::unpack(load16(dh + i), h);
-            DT::unpack(load16(gs + i), a);
-            DT::unpack(load16(us + i), b);
+            unpack(gk + i, a);
+            unpack(uk + i, b);
         } else {
 #pragma unroll
             for (int e = 0; e < V; ++e) {
                 const bool in = i + e < n;
                 h[e] = in ? DT::load1(dh + i + e) : 0.f;
-                a[e] = in ? DT::load1(gs + i + e) : 0.f;
-                b[e] = in ? DT::load1(us + i + e) : 0.f;
+                a[e] = in ? KT::load1(gk + i + e) : 0.f;
+                b[e] = in ? KT::load1(uk + i + e) : 0.f;
             }
         }
 #pragma unroll
@@ -835,17 +848,34 @@ __global__ __launch_bounds__(256) void gated_grad_kernel(
             a[e] = h[e] * b[e] * d;
             b[e] = h[e] * v;
         }
-        if (whole) {
-            store16(dg + i, DT::pack(a));
-            store16(du + i, DT::pack(b));
-        } else {
+        auto put = [&](typename DT::storage* hi, typename DT::storage* lo, const float* f) {
+            if (whole) {
+                store16(hi + i, DT::pack(f));
+            } else {
 #pragma unroll
-            for (int e = 0; e < V; ++e)
-                if (i + e < n) {
-                    dg[i + e] = DT::from_float(a[e]);
-                    du[i + e] = DT::from_float(b[e]);
+                for (int e = 0; e < V; ++e)
+                    if (i + e < n) hi[i + e] = DT::from_float(f[e]);
+            }
+            if constexpr (kFull) {
+                float r[V];
+#pragma unroll
+                for (int e = 0; e < V; ++e) {
+                    const typename DT::storage one = DT::from_float(f[e]);
+                    const float rounded = DT::load1(&one);
+                    // Past the type's range (and for NaN) the first part says it all.
+                    r[e] = __builtin_isfinite(rounded) ? f[e] - rounded : 0.f;
                 }
-        }
+                if (whole) {
+                    store16(lo + i, DT::pack(r));
+                } else {
+#pragma unroll
+                    for (int e = 0; e < V; ++e)
+                        if (i + e < n) lo[i + e] = DT::from_float(r[e]);
+                }
+            }
+        };
+        put(dg, dg_lo, a);
+        put(du, du_lo, b);
     }
 }
 

@@ -12,7 +12,7 @@ from __future__ import annotations
 
 from . import _check, _need, _no_tangents, _stream_ptr, _torch, dtype_code, lib
 
-ONE_WEIGHT = 0x200  # an option of sgmv.h, OR-ed into the dtype's code
+FULL_GRADIENTS, ONE_WEIGHT = 0x100, 0x200  # options of sgmv.h, OR-ed into the dtype's code
 
 ACTIVATIONS = {"silu": 0, "gelu": 1, "gelu_tanh": 2, "relu": 3, "sigmoid": 4}
 
@@ -63,17 +63,21 @@ def _check_weights(x, Wg, Wu):
     return x.shape[0], x.shape[1], Wg.shape[0]
 
 
-def _forward(x, Wg, Wu, act, gate_add, up_add, out, save):
+def _forward(x, Wg, Wu, act, gate_add, up_add, out, kept):
+    """(h, g, u); ``kept`` is the type g and u are stored in, None if they are not."""
     R, H, I = _check_weights(x, Wg, Wu)
     code = _act_code(act)
     ga, ua = _addends(gate_add, up_add, (R, I), x)
     out = _output(out, (R, I), x, (gate_add, up_add), x=x, Wg=Wg, Wu=Wu)
     g = u = None
-    if save:
-        g, u = x.new_empty((R, I)), x.new_empty((R, I))
-    _check(lib().gated_ffn(out.data_ptr(), g.data_ptr() if save else None,
-                           u.data_ptr() if save else None, x.data_ptr(), Wg.data_ptr(),
-                           Wu.data_ptr(), ga, ua, R, H, I, code, dtype_code(x.dtype),
+    dtype = dtype_code(x.dtype)
+    if kept is not None:
+        g, u = x.new_empty((R, I), dtype=kept), x.new_empty((R, I), dtype=kept)
+        if kept != x.dtype:
+            dtype |= FULL_GRADIENTS
+    _check(lib().gated_ffn(out.data_ptr(), None if g is None else g.data_ptr(),
+                           None if u is None else u.data_ptr(), x.data_ptr(), Wg.data_ptr(),
+                           Wu.data_ptr(), ga, ua, R, H, I, code, dtype,
                            _stream_ptr(x.device)), "gated_ffn")
     return out, g, u
 
@@ -82,11 +86,18 @@ def gated_ffn_backward(dh, x, Wg, Wu, g, u, act: str = "silu", need_dx=True, nee
     """Gradients of gated_ffn from dh = dL/dh and the saved g and u (its
     pre-activations, addends included): returns ``(dx, dWg, dWu, dg, du)``,
     dx or the weights' gradients None where not needed; dg and du are also
-    the addends' gradients.  ``need_dw`` may be a pair, for Wg and Wu."""
+    the addends' gradients.  ``need_dw`` may be a pair, for Wg and Wu.
+
+    g and u in x's dtype: dg and du are rounded to it too before the products.
+    g and u in float32 (x in 16 bits): nothing is rounded but the gradients
+    returned, and the products take twice as long."""
+    torch = _torch()
     R, H, I = _check_weights(x, Wg, Wu)
     code, dtype = _act_code(act), dtype_code(x.dtype)
-    for t, name in ((dh, "dh"), (g, "g"), (u, "u")):
-        _need(t, name, x.device, x.dtype, 2)
+    full = g.dtype != x.dtype and g.dtype == torch.float32
+    for t, name, kind in ((dh, "dh", x.dtype), (g, "g", g.dtype if full else x.dtype),
+                          (u, "u", g.dtype if full else x.dtype)):
+        _need(t, name, x.device, kind, 2)
         if tuple(t.shape) != (R, I):
             raise ValueError(f"{name} must be {(R, I)}, got {tuple(t.shape)}")
     need_g, need_u = need_dw if isinstance(need_dw, (tuple, list)) else (need_dw, need_dw)
@@ -94,12 +105,14 @@ def gated_ffn_backward(dh, x, Wg, Wu, g, u, act: str = "silu", need_dx=True, nee
     dx = x.new_empty((R, H)) if need_dx else None
     dWg = x.new_empty((I, H)) if need_g else None
     dWu = x.new_empty((I, H)) if need_u else None
+    if full:
+        dtype |= FULL_GRADIENTS
     ptr = lambda t: None if t is None else t.data_ptr()
     ws, ws_bytes = None, 0
-    if need_dx:
+    if need_dx or full:
         ws_bytes = lib().gated_ffn_backward_workspace_bytes(R, H, I, dtype)
         if ws_bytes:
-            ws = x.new_empty(ws_bytes, dtype=_torch().uint8)
+            ws = x.new_empty(ws_bytes, dtype=torch.uint8)
     if bool(need_g) != bool(need_u):
         dtype |= ONE_WEIGHT
     _check(lib().gated_ffn_backward(ptr(dx), ptr(dWg), ptr(dWu), dg.data_ptr(), du.data_ptr(),
@@ -121,8 +134,9 @@ def _autograd_function():
 
         class GatedFFN(torch.autograd.Function):
             @staticmethod
-            def forward(ctx, x, Wg, Wu, gate_add, up_add, act):
-                h, g, u = _forward(x, Wg, Wu, act, gate_add, up_add, None, True)
+            def forward(ctx, x, Wg, Wu, gate_add, up_add, act, full):
+                h, g, u = _forward(x, Wg, Wu, act, gate_add, up_add, None,
+                                   torch.float32 if full else x.dtype)
                 ctx.save_for_backward(x, Wg, Wu, g, u)
                 ctx.act = act
                 return h
@@ -135,27 +149,31 @@ def _autograd_function():
                 want = ctx.needs_input_grad
                 dx, dWg, dWu, dg, du = gated_ffn_backward(
                     dh.contiguous(), x, Wg, Wu, g, u, ctx.act, need_dx=want[0], need_dw=want[1:3])
-                return dx, dWg, dWu, dg if want[3] else None, du if want[4] else None, None
+                return (dx, dWg, dWu, dg if want[3] else None, du if want[4] else None, None, None)
 
         _function = GatedFFN
     return _function
 
 
-def gated_ffn(x, Wg, Wu, act: str = "silu", gate_add=None, up_add=None, out=None):
+def gated_ffn(x, Wg, Wu, act: str = "silu", gate_add=None, up_add=None, out=None,
+              full_gradients: bool = False):
     """h = act(x Wg^T + gate_add) * (x Wu^T + up_add), float32 sums, rounded
     once.  x [R, in], Wg and Wu [hidden, in] (torch's linear layout), addends
     [R, hidden] or None; ``act`` is silu, gelu, gelu_tanh, relu or sigmoid.
     Under autograd the pre-activations are kept in x's dtype for the backward
-    pass; ``out`` (optional) receives h, is only for calls without it, and must not
-    overlap the inputs (it may be one of the addends itself).  A backward pass
-    may be captured into a graph once no graph that eager calls recorded on the
-    same leaves is alive (the engine would wait for their stream inside the
-    capture)."""
+    pass, whose dg and du are rounded to it too before the products;
+    ``full_gradients`` keeps them in float32 and carries dg and du in two parts,
+    so that 16-bit gradients are off by their own rounding alone, for twice the
+    time in the backward products.  ``out`` (optional) receives h, is only for
+    calls without it, and must not overlap the inputs (it may be one of the
+    addends itself).  A backward pass may be captured into a graph once no graph
+    that eager calls recorded on the same leaves is alive (the engine would wait
+    for their stream inside the capture)."""
     torch = _torch()
     inputs = (x, Wg, Wu, gate_add, up_add)
     _no_tangents("gated_ffn", *inputs)
     if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in inputs):
         if out is not None:
             raise ValueError("out cannot be given where gradients are recorded")
-        return _autograd_function().apply(x, Wg, Wu, gate_add, up_add, act)
-    return _forward(x, Wg, Wu, act, gate_add, up_add, out, False)[0]
+        return _autograd_function().apply(x, Wg, Wu, gate_add, up_add, act, full_gradients)
+    return _forward(x, Wg, Wu, act, gate_add, up_add, out, None)[0]

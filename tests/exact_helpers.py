@@ -62,13 +62,14 @@ def exact_block(gen, R, H, I, dtype, device):
     return t(R, H), W(), W(), t(R, I) * 3, t(R, I) * 2, t(R, I)
 
 
-def exact_gated(x, Wg, Wu, ag, au, dh):
+def exact_gated(x, Wg, Wu, ag, au, dh, most=256):
     """h of relu and the five gradients, before their one rounding."""
     x, Wg, Wu, dh = (t.detach().double() for t in (x, Wg, Wu, dh))
     g, u = x @ Wg.t(), x @ Wu.t()
     if ag is not None:
         g, u = g + ag.detach().double(), u + au.detach().double()
-    assert float(g.abs().max()) <= 256 and float(u.abs().max()) <= 256  # kept in bf16 as they are
+    # 256: g and u are kept in bf16 as they are
+    assert float(g.abs().max()) <= most and float(u.abs().max()) <= most
     a = g.clamp(min=0)
     dg, du = dh * u * (g > 0), dh * a
     return [a * u, dg @ Wg + du @ Wu, dg.t() @ x, du.t() @ x, dg, du]

@@ -10,20 +10,22 @@ pytestmark = pytest.mark.gpu
 DEV = "cuda:0"
 
 
+@pytest.mark.parametrize("full", [False, True])
 @pytest.mark.parametrize("dt", ["f16", "bf16", "f32"])
 @pytest.mark.parametrize("R,H,I", [(40, 72, 104), (300, 264, 1000), (140, 131, 201), (0, 64, 48)])
-def test_one_weight(R, H, I, dt):
+def test_one_weight(R, H, I, dt, full):
     gen = torch.Generator().manual_seed(R + I)
     x, Wg, Wu, ag, au, dh = exact_block(gen, R, H, I, DTYPES[dt], DEV)
     want = exact_gated(x, Wg, Wu, ag, au, dh) if R else [None, None] + [Wg.double() * 0] * 2
     g, u = (x.double() @ W.double().t() + a.double() for W, a in ((Wg, ag), (Wu, au)))
+    kept = torch.float32 if full else x.dtype
     for need, at in (((True, False), 1), ((False, True), 2)):
-        got = sg.gated_ffn_backward(dh, x, Wg, Wu, g.to(x.dtype), u.to(x.dtype), "relu", need_dx=False, need_dw=need)
+        got = sg.gated_ffn_backward(dh, x, Wg, Wu, g.to(kept), u.to(kept), "relu", need_dx=False, need_dw=need)
         assert got[0] is None and got[3 - at] is None
         check_exact(got[at], want[at + 1], f"need_dw={need}")
         leaf = (Wg if at == 1 else Wu).clone().requires_grad_()
         W = [leaf, Wu] if at == 1 else [Wg, leaf]
-        h = sg.gated_ffn(x, *W, "relu", ag, au)
+        h = sg.gated_ffn(x, *W, "relu", ag, au, full_gradients=full)
         grad, = torch.autograd.grad(h, [leaf], dh)
         check_exact(grad, want[at + 1], "autograd")
 
