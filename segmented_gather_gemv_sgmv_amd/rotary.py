@@ -177,7 +177,13 @@ def _autograd_function():
             def forward(ctx, q, k, positions, plan, inverse):
                 ctx.save_for_backward(positions)
                 ctx.plan, ctx.inverse = plan, inverse
-                return _run(q, k, positions, plan, None, inverse)
+                q2, k2 = _run(q, k, positions, plan, None, inverse)
+                # What needs no gradient must not ask for one after the turn.
+                if k2 is not None and not k.requires_grad:
+                    ctx.mark_non_differentiable(k2)
+                elif q2 is not None and not q.requires_grad:
+                    ctx.mark_non_differentiable(q2)
+                return q2, k2
 
             @staticmethod
             def backward(ctx, dq, dk):
