@@ -13,9 +13,10 @@
 // 256 x 256 tile is 64 MFMAs per SIMD, 0.57 us at the 1.8 GHz measured under this
 // load (2.4 GHz without; products of random values alone, out of registers, reach
 // 1.75 to 2.0 PFLOP/s).  Measured, bf16: 0.78 us a step where the tiles are one
-// round (dx of 4096 x 4096 from 2 x 10240: 1.35 PFLOP/s), 0.92 us over several
-// rounds of the forward (4096 x 4096 -> 2 x 10240: 585 us, 1.17 PFLOP/s), matrix
-// cores busy 59 to 61 % of the cycles, LDS reads 22 %, no bank conflicts; loads
+// round (dx of 4096 x 4096 from 2 x 10240: 510 to 555 us by the card, 1.24 to 1.35
+// PFLOP/s), 0.92 us over several rounds of the forward (4096 x 4096 -> 2 x 10240: 585
+// us, 1.17 PFLOP/s), matrix cores busy 59 to 67 % of the cycles, LDS reads 22 %, no
+// bank conflicts; loads
 // that all hit L2 change nothing.  The same loop with the barrier at the end of a
 // step is 14 % slower: the next step's operands then arrive with no products left
 // to hide them.  Two waves per SIMD is what the sums (128
@@ -642,8 +643,8 @@ __global__ __launch_bounds__(SH::NT, BL == kCodes ? 2 : 1) void tile_kernel(Tile
             // first half has used, so that the matrix cores have work on both sides of the
             // barrier.  Waves in their second half go first (not with 4-bit B, where it is
             // no faster): their products are what the barrier of the next step waits for (dx
-            // of 4096 x 4096 from 2 x 10240: 250 us, 256 without, 263 with one A operand
-            // read ahead instead of half).
+            // of 4096 x 4096 from 2 x 10240, bf16, the three in turn on one card: 549 to 559
+            // us, 578 without, and 550 with one A operand read ahead instead of half).
             constexpr int kAfter = kLoads + (kPrefetch ? 1 : 0);
             // 4-bit: the next block's codes but one are asked for at the start of the third step
             // of four, which leaves them in flight as long as the loads into the stages; until
