@@ -72,17 +72,17 @@ int run_forward(const RowsArgs& a, hipStream_t st) {
 // Where a backward pass keeps what: floats of dx's sums, then (full gradients) the
 // second parts of dg and du.
 struct GradPlan {
-    SumPlan sum;
-    int parts;             // of dg and du: 1 or 2
-    size_t lo_at, lo_each; // bytes
+    SumPlan sum;            // dx: of dg Wg, du Wu and, with second parts, theirs
+    int parts;              // of dg and du: 1 or 2
+    size_t lo_at, lo_each;  // bytes
     size_t bytes;
 };
 
 GradPlan plan_gradients(long long R, long long H, long long I, int dtype, bool full, bool dx) {
-    GradPlan p{plan_sum(R, H, I, dtype), full && dtype != SGMV_F32 ? 2 : 1, 0, 0, 0};
-    // A second part's products are sums of their own, joined with the first's.
-    if (dx && (p.sum.ranges > 1 || p.parts == 2))
-        p.lo_at = (size_t)p.parts * p.sum.ranges * p.sum.stride * sizeof(float);
+    GradPlan p{};
+    p.parts = full && dtype != SGMV_F32 ? 2 : 1;
+    p.sum = plan_sum(R, H, I, 2 * p.parts, dtype);
+    if (dx && p.sum.ranges > 1) p.lo_at = (size_t)p.sum.ranges * p.sum.stride * sizeof(float);
     p.bytes = p.lo_at;
     if (p.parts == 2) {
         p.lo_each = (size_t)ceil_div(R * I * elem_size(dtype), 256) * 256;
@@ -125,77 +125,76 @@ int run_backward(const GradArgs& b, hipStream_t st) {
     const bool hvec = b.H % PK == 0, ivec = b.I % PK == 0;
     const bool gvec = ivec && aligned16(b.dg) && aligned16(b.du);
     if (b.dx && b.R > 0) {
-        // dx = dg Wg + du Wu: two segments of K = I, the weights across K.
+        // dx = dg Wg + du Wu: segments of K = I, the weights across K.
         const SumPlan& sum = b.plan.sum;
         TileArgs t{};
+        const void* const a[4] = {b.dg, b.du, lo[0], lo[1]};
+        for (int s = 0; s < 2 * parts; ++s) {
+            t.a[s] = a[s];
+            t.b[s] = s % 2 == 0 ? b.Wg : b.Wu;
+        }
         t.lda = b.I;
-        t.b[0] = b.Wg;
-        t.b[1] = b.Wu;
         t.ldb = b.H;
         t.out[0] = b.dx;
         t.M = b.R;
         t.N = b.H;
         t.K = b.I;
         t.batches = sum.ranges;
+        t.in_ranges = 1;
         t.range_steps = sum.range_steps;
         t.avec = gvec;
         t.bvec = hvec && aligned16(b.Wg) && aligned16(b.Wu);
         t.yvec = b.H % 4 == 0 && aligned16(b.dx);
-        const bool direct = t.avec && t.bvec;
-        const bool joined = sum.ranges > 1 || parts == 2;
-        for (int p = 0; p < parts; ++p) {
-            t.a[0] = p == 0 ? b.dg : lo[0];
-            t.a[1] = p == 0 ? b.du : lo[1];
-            if (joined) {
-                t.partial = (float*)b.workspace + (long long)p * sum.ranges * sum.stride;
-                t.partial_stride = sum.stride;
-            }
-            const int rc = sum.ranges == 1
-                ? launch_tiles_any<DT, kAlongK, kAcrossK, 2, false>(t, direct, st)
-                : launch_kind<DT, kAlongK, kAcrossK, 2, false>(
-                      sum.kind, t, TileRange{0, t.M, 0, t.N}, direct, st);
-            if (rc != SGMV_OK) return rc;
+        if (sum.ranges > 1) {
+            t.partial = (float*)b.workspace;
+            t.partial_stride = sum.stride;
         }
-        if (joined) {
+        const bool direct = t.avec && t.bvec;
+        auto run = [&](auto segments) {
+            constexpr int kSegs = decltype(segments)::value;
+            return sum.ranges == 1
+                ? launch_tiles_any<DT, kAlongK, kAcrossK, kSegs, false>(t, direct, st)
+                : launch_kind<DT, kAlongK, kAcrossK, kSegs, false>(
+                      sum.kind, t, TileRange{0, t.M, 0, t.N}, direct, st);
+        };
+        int rc = SGMV_OK;
+        if (parts == 1) rc = run(std::integral_constant<int, 2>{});
+        else if constexpr (DT::kBytes == 2) rc = run(std::integral_constant<int, 4>{});
+        if (rc != SGMV_OK) return rc;
+        if (sum.ranges > 1) {
             const long long n = (long long)b.R * b.H;
             launch(&join_kernel<DT>, dim3((unsigned)ceil_div(n, 1024)), dim3(256), st, (T*)b.dx,
-                   (const float*)b.workspace, parts * sum.ranges, sum.stride, n, (int)aligned16(b.dx));
-            const int rc = launch_status();
+                   (const float*)b.workspace, sum.ranges, sum.stride, n, (int)aligned16(b.dx));
+            rc = launch_status();
             if (rc != SGMV_OK) return rc;
         }
     }
-    // dWg = dg^T x and dWu = du^T x: K = rows, both operands across K; second parts are
-    // a second segment of K.
-    TileArgs t{};
-    t.lda = b.I;
-    t.b[0] = t.b[1] = b.x;
-    t.ldb = b.H;
-    t.M = b.I;
-    t.N = b.H;
-    t.K = b.R;
-    t.avec = gvec;
-    t.bvec = hvec && aligned16(b.x);
-    t.yvec = b.H % 4 == 0 && aligned16(b.dWg) && aligned16(b.dWu);
-    const bool direct = t.avec && t.bvec;
-    if (parts == 1) {
-        t.a[0] = b.dWg ? b.dg : b.du;
-        t.a[1] = b.du;
-        t.out[0] = b.dWg ? b.dWg : b.dWu;
-        t.out[1] = b.dWu;
-        t.batches = (b.dWg ? 1 : 0) + (b.dWu ? 1 : 0);
-        return t.batches > 0 ? launch_tiles_any<DT, kAcrossK, kAcrossK, 1, false>(t, direct, st) : SGMV_OK;
-    }
-    if constexpr (DT::kBytes == 2) {
-        t.batches = 1;
-        t.range_steps = 1 << 30;  // one range: all steps
+    if (b.dWg || b.dWu) {
+        // dWg = dg^T x and dWu = du^T x, or one of them: K = rows, both operands across
+        // K; second parts are a second segment of K.
+        TileArgs t{};
         for (int q = 0; q < 2; ++q) {
-            t.out[0] = q == 0 ? b.dWg : b.dWu;
-            if (!t.out[0]) continue;
-            t.a[0] = q == 0 ? b.dg : b.du;
-            t.a[1] = lo[q];
-            const int rc = launch_tiles_any<DT, kAcrossK, kAcrossK, 2, false>(t, direct, st);
-            if (rc != SGMV_OK) return rc;
+            void* const out = q == 0 ? b.dWg : b.dWu;
+            if (!out) continue;
+            t.out[t.batches] = out;
+            for (int p = 0; p < parts; ++p) {
+                t.a[parts * t.batches + p] = p == 1 ? lo[q] : q == 0 ? b.dg : b.du;
+                t.b[parts * t.batches + p] = b.x;
+            }
+            ++t.batches;
         }
+        t.lda = b.I;
+        t.ldb = b.H;
+        t.M = b.I;
+        t.N = b.H;
+        t.K = b.R;
+        t.avec = gvec;
+        t.bvec = hvec && aligned16(b.x);
+        t.yvec = b.H % 4 == 0 && aligned16(b.dWg) && aligned16(b.dWu);
+        const bool direct = t.avec && t.bvec;
+        if (parts == 1) return launch_tiles_any<DT, kAcrossK, kAcrossK, 1, false>(t, direct, st);
+        if constexpr (DT::kBytes == 2)
+            return launch_tiles_any<DT, kAcrossK, kAcrossK, 2, false>(t, direct, st);
     }
     return SGMV_OK;
 }

@@ -121,7 +121,7 @@ inline TileKind f32_kind(long long M, long long N, int batches, bool gated) {
     return tall < small ? kTallTiles : kSmallTiles;
 }
 
-// How the sum of two products over K is taken: by one workgroup per tile, or
+// How the sum of `segments` products over K each is taken: by one workgroup per tile, or
 // (ranges > 1) in ranges of K, each by a workgroup of its own that leaves its
 // float32 sums, joined by a second kernel.  Outputs of a few tiles are worth it:
 // their long K would run on a few CUs (1237 rows x 1000 from 2 x 2744, f16:
@@ -135,9 +135,9 @@ struct SumPlan {
 
 constexpr long long kMaxSumBytes = 64ll << 20;
 
-inline SumPlan plan_sum(long long M, long long N, long long K, int dtype) {
+inline SumPlan plan_sum(long long M, long long N, long long K, int segments, int dtype) {
     const bool f32 = dtype == SGMV_F32;
-    const long long steps = ceil_div(2 * ceil_div(K, f32 ? 16 : 32), 4) * 4;
+    const long long steps = ceil_div(segments * ceil_div(K, f32 ? 16 : 32), 4) * 4;
     // Microseconds per step of 32 (float32: 16) K; 128 of 32 are 4096.
     auto step_us = [&](TileKind kind, int ranges) {
         if (f32) return f32_step_us(kind, f32_tiles(kind, M, N, false) * ranges);

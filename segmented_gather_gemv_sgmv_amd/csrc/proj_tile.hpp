@@ -44,10 +44,10 @@ struct TileShape {
 };
 
 struct TileArgs {
-    // One product C = A B^T over K, or (kSegs == 2) the sum of two of the
-    // same shapes; `batches` == 2: two products a[z], b[z] -> out[z].
-    const void* a[2];
-    const void* b[2];
+    // One product C = A B^T over K, or the sum of kSegs of the same shapes; `batches`
+    // == 2: two such, of a and b from [kSegs z] on -> out[z].
+    const void* a[4];
+    const void* b[4];
     long long lda, ldb;   // elements between rows (kAlongK) or K (kAcrossK)
     ProjWeight q[2];      // kCodes
     void* out[2];         // [M, N]
@@ -55,9 +55,10 @@ struct TileArgs {
     void* save[2];        // gated: g and u [M, N], or NULL
     int save_f32;         // these in float32
     int M, N, K;          // gated: N columns of each matrix
-    int batches;          // kSegs == 2: ranges of K, each summed by workgroups of its own
-    int range_steps;      // kSegs == 2, direct loads: steps per range, a multiple of 4
-    float* partial;       // kSegs == 2: sums of the ranges, [batches][partial_stride]; or NULL
+    int batches;
+    int in_ranges;        // kSegs > 1: the batches are ranges of K of one product
+    int range_steps;      // in_ranges, direct loads: steps per range, a multiple of 4
+    float* partial;       // in_ranges: their sums, [batches][partial_stride]; or NULL
     long long partial_stride;
     int m_first, n_first;            // row and column (of each matrix) of the first tile
     int tiles_m, tiles_n, tiles;     // of this launch
@@ -373,8 +374,9 @@ __global__ __launch_bounds__(SH::NT, BL == kCodes ? 2 : 1) void tile_kernel(Tile
             return load_piece<DT>(p + (long long)(kc + kr) * ld, r0 + piece * PK, rows, vec);
         }
     };
+    const int pair0 = kSegs > 1 && g.in_ranges ? 0 : kSegs * z;  // this product's first a and b
     auto slow_steps = [&](int seg, int kc) {
-        const int which = kSegs == 2 ? seg : z;
+        const int which = pair0 + seg;
         constexpr int kA = BM * 4 / NT, kB = BL == kCodes ? 0 : BN * 4 / NT;
         static_assert(kA * NT == BM * 4 && (BL == kCodes || kB * NT == BN * 4), "whole slots per thread");
         constexpr int kBn = kB > 0 ? kB : 1;
@@ -439,13 +441,13 @@ __global__ __launch_bounds__(SH::NT, BL == kCodes ? 2 : 1) void tile_kernel(Tile
     if constexpr (!kDma) {
         const int seg_turns = (K + 4 * KE - 1) / (4 * KE);
         int turn = 0, end = kSegs * seg_turns;
-        if constexpr (kSegs == 2) {
+        if (kSegs > 1 && g.in_ranges) {
             const int each = (end + g.batches - 1) / g.batches;  // turns per range
             turn = z * each;
             end = min(end, turn + each);
         }
         for (; turn < end; ++turn) {
-            const int seg = kSegs == 2 && turn >= seg_turns;
+            const int seg = kSegs > 1 ? turn / seg_turns : 0;
             slow_steps(seg, (turn - seg * seg_turns) * 4 * KE);
         }
     }
@@ -457,7 +459,7 @@ __global__ __launch_bounds__(SH::NT, BL == kCodes ? 2 : 1) void tile_kernel(Tile
         const int seg_steps = (K + KE - 1) / KE;
         int nsteps = (kSegs * seg_steps + kTurn - 1) / kTurn * kTurn;
         int step0 = 0;  // first step of this workgroup's range
-        if constexpr (kSegs == 2) {
+        if (kSegs > 1 && g.in_ranges) {
             step0 = z * g.range_steps;
             nsteps = min(nsteps - step0, g.range_steps);
         }
@@ -470,7 +472,7 @@ __global__ __launch_bounds__(SH::NT, BL == kCodes ? 2 : 1) void tile_kernel(Tile
             static_assert(2 * kLoads < 64, "the wait count fits vmcnt");
             constexpr int kWaitSteps = (2 * kLoads & 15) | ((2 * kLoads >> 4) << 14) | 0x0070;
             using lds_t = __attribute__((address_space(3))) void;
-            const int which = kSegs == 2 ? 0 : z;
+            const int which = pair0;
             // Lane's byte offset in load `load` of an operand from its tile's first row
             // (along K) or first column (across K), and its first K within a step; past
             // the end of the rows (columns) it reads the last.
@@ -520,8 +522,31 @@ __global__ __launch_bounds__(SH::NT, BL == kCodes ? 2 : 1) void tile_kernel(Tile
             }
             const long long stride_a = AL == kAlongK ? 64 : KE * g.lda * B;  // bytes per step
             const long long stride_b = BL == kAcrossK ? KE * g.ldb * B : 64;
-            const long long jump_a = kSegs == 2 ? (const char*)g.a[1] - (const char*)g.a[0] : 0;
-            const long long jump_b = kSegs == 2 ? (const char*)g.b[1] - (const char*)g.b[0] : 0;
+            // From the first segment's operands to the others'.
+            struct Jumps {
+                long long to[kSegs];
+            };
+            Jumps jump_a, jump_b;
+#pragma unroll
+            for (int s = 0; s < kSegs; ++s) {
+                jump_a.to[s] = (const char*)g.a[which + s] - (const char*)g.a[which];
+                jump_b.to[s] = (const char*)g.b[which + s] - (const char*)g.b[which];
+            }
+            // A step within its segment, and that segment (past the last step, the last).
+            auto segment = [&](int& step) {
+                int seg = 0;
+#pragma unroll
+                for (int s = 1; s < kSegs; ++s) seg += step >= s * seg_steps;
+                step -= seg * seg_steps;
+                return seg;
+            };
+            auto jump = [](const Jumps& j, int seg) {
+                long long at = 0;
+#pragma unroll
+                for (int s = 1; s < kSegs; ++s)
+                    if (seg >= s) at = j.to[s];
+                return at;
+            };
             // Buffer loads: the step's address is the (scalar) base, a lane adds its
             // 32-bit offset, and a lane past the end of K takes an offset past the
             // buffer's range, for which the load returns zeros.
@@ -541,21 +566,16 @@ __global__ __launch_bounds__(SH::NT, BL == kCodes ? 2 : 1) void tile_kernel(Tile
             };
             // Load u of a step (A's, then B's).
             auto issue1 = [&](uint8_t* sa, uint8_t* sb, int step, int u) {
-                long long ja = 0, jb = 0;
                 step += step0;
-                if (kSegs == 2 && step >= seg_steps) {
-                    step -= seg_steps;
-                    ja = jump_a;
-                    jb = jump_b;
-                }
+                const int seg = segment(step);
                 const int k_left = K - step * KE;  // not positive past the last step
                 if (u < kLA) {
                     const int o = ka[u < kLA ? u : 0] < k_left ? (int)off_a[u < kLA ? u : 0] : -16;
-                    load_lds(base_a + (ja + step * stride_a), o, sa + (wid + u * NW) * 1024);
+                    load_lds(base_a + (jump(jump_a, seg) + step * stride_a), o, sa + (wid + u * NW) * 1024);
                 } else {
                     const int v = u >= kLA ? u - kLA : 0;
                     const int o = kb[v] < k_left ? (int)off_b[v] : -16;
-                    load_lds(base_b[v] + (jb + step * stride_b), o, sb + (wid + v * NW) * 1024);
+                    load_lds(base_b[v] + (jump(jump_b, seg) + step * stride_b), o, sb + (wid + v * NW) * 1024);
                 }
             };
             // L2 prefetch, kAhead steps before a step is loaded, of 128-byte lines that
@@ -567,7 +587,8 @@ __global__ __launch_bounds__(SH::NT, BL == kCodes ? 2 : 1) void tile_kernel(Tile
             constexpr int kAhead = 6;
             constexpr bool kPrefetch = NW == 8;
             const char* pf_base = base_a;
-            long long pf_stride = stride_a, pf_jump = jump_a;
+            long long pf_stride = stride_a;
+            Jumps pf_jump = jump_a;
             int pf_off = -16, pf_k = 0;
             if constexpr (kPrefetch) {
                 // Line `id` of an operand's tile of COLS rows (columns), two steps being
@@ -602,12 +623,8 @@ __global__ __launch_bounds__(SH::NT, BL == kCodes ? 2 : 1) void tile_kernel(Tile
                 }
             }
             auto prefetch = [&](int step) {
-                long long at = 0;
                 step += step0;
-                if (kSegs == 2 && step >= seg_steps) {
-                    step -= seg_steps;
-                    at = pf_jump;
-                }
+                const long long at = jump(pf_jump, segment(step));
                 const int o = pf_k < K - step * KE ? pf_off : -16;
                 load_lds4(pf_base + (at + step * pf_stride), o, s_unread + 256 * wid);
             };
@@ -738,7 +755,7 @@ __global__ __launch_bounds__(SH::NT, BL == kCodes ? 2 : 1) void tile_kernel(Tile
     }
 
     // ---- epilogue -------------------------------------------------------------
-    T* out = (T*)g.out[kSegs == 2 ? 0 : z];
+    T* out = (T*)g.out[kSegs > 1 && g.in_ranges ? 0 : z];
     constexpr int TNO = kGated ? TN / 2 : TN;
     const int nw = n0 + wc * (16 * TNO) + 4 * lg;  // this lane's first columns
     float bias[kGated ? 1 : TNO][4] = {};
@@ -791,7 +808,7 @@ __global__ __launch_bounds__(SH::NT, BL == kCodes ? 2 : 1) void tile_kernel(Tile
 #pragma unroll
                 for (int c = 0; c < 4; ++c) o[c] = acc[i][j][c] + bias[j][c];
             }
-            if (kSegs == 2 && g.partial)
+            if (kSegs > 1 && g.partial)
                 store4f<F32>(g.partial + z * g.partial_stride + at, left, N % 4 == 0, o);
             else
                 store4f<DT>(out + at, left, g.yvec, o);
@@ -803,12 +820,12 @@ __global__ __launch_bounds__(SH::NT, BL == kCodes ? 2 : 1) void tile_kernel(Tile
 // dg = dh u a'(g), du = dh a(g), element by element (three reads, two
 // writes).  n is the element count; `vec`: every array is 16-byte aligned.
 // Bound: HBM; 4096 x 11008 bf16, 451 MB: 87 us, 5.2 TB/s.
-// g and u come, and dg and du go on to the matrix products, in the activations'
-// type: a training step's bf16 gradients are then off by 0.0031 of their size (root
-// mean square) where float32 in between leaves their own rounding, 0.0017.  kFull, for
-// callers who ask for that: g and u come in float32, and what dg and du lose by their
-// rounding goes to the products too, as second parts (lo), 16 and 22 bits in all.  4096 x
-// 11008 bf16 moves 811 MB then, and the products take twice as long.
+// kFull: g and u come in float32, and what dg and du lose by their rounding goes on to
+// the matrix products too, as second parts (lo), 16 and 22 bits in all: gradients are
+// off by their own rounding, 0.0017 of their size (bf16, root mean square over a
+// training step's).  4096 x 11008 bf16 moves 811 MB then, 180 us, and the products take
+// twice as long.  Without it, where the caller chooses that, g, u, dg and du are held in
+// the activations' type: 0.0031.
 // ---------------------------------------------------------------------------
 template <typename DT, bool kFull>
 __global__ __launch_bounds__(256) void gated_grad_kernel(

@@ -25,8 +25,8 @@ int probe_f32_tiles(long long M, long long N, int batches, int gated) {
     return f32_kind(M, N, batches, gated);
 }
 // dx's sums: the kind of tile, and how many ranges of K.
-int probe_sum(long long M, long long N, long long K, int dtype, int* ranges) {
-    const SumPlan p = plan_sum(M, N, K, dtype);
+int probe_sum(long long M, long long N, long long K, int segments, int dtype, int* ranges) {
+    const SumPlan p = plan_sum(M, N, K, segments, dtype);
     *ranges = p.ranges;
     return p.kind;
 }

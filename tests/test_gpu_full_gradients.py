@@ -21,6 +21,16 @@ def _gradients64(x, Wg, Wu, ag, au, dh, act):
     return [a * u, dg @ Wg + du @ Wu, dg.t() @ x, du.t() @ x, dg, du]
 
 
+def test_the_default_is_full():
+    gen = torch.Generator().manual_seed(4)
+    x, Wg, Wu, ag, au, dh = exact_block(gen, 90, 72, 104, torch.bfloat16, DEV)
+    leaves = [t.requires_grad_() for t in (x, Wg, Wu, ag * 171, au * 171)]
+    got = torch.autograd.grad(sg.gated_ffn(x, Wg, Wu, "relu", *leaves[3:]), leaves, dh)
+    for a, b in zip(got, _run(leaves, dh, "relu", True)[1:]):
+        assert torch.equal(a, b)
+    assert not torch.equal(got[0], _run(leaves, dh, "relu", False)[1])
+
+
 def _run(leaves, dh, act, full):
     h = sg.gated_ffn(*leaves[:3], act, *leaves[3:], full_gradients=full)
     return [h.detach(), *torch.autograd.grad(h, leaves, dh)]
@@ -47,10 +57,11 @@ def test_error_is_the_results_own_rounding(R, H, I, act, dt):
 
 # Whole numbers that need more than 8 bits in g, u, dg and du: held in bf16 they
 # would not give these results.
+@pytest.mark.parametrize("dt", ["bf16", "f16"])  # fp16 holds them: the same kernels' sums
 @pytest.mark.parametrize("R,H,I", FFN16 + FFN16_SLOW)
-def test_exact_where_16_bits_are_not_enough(R, H, I):
+def test_exact_where_16_bits_are_not_enough(R, H, I, dt):
     gen = torch.Generator().manual_seed(R + H + I)
-    x, Wg, Wu, ag, au, dh = exact_block(gen, R, H, I, torch.bfloat16, DEV)
+    x, Wg, Wu, ag, au, dh = exact_block(gen, R, H, I, DTYPES[dt], DEV)
     ag, au = ag * 171, au * 171  # up to 513: 10 bits with g's own
     leaves = [t.requires_grad_() for t in (x, Wg, Wu, ag, au)]
     got = _run(leaves, dh, "relu", True)

@@ -46,14 +46,15 @@ class Rules:
             detail = self._tiles(R, N, 1, gated, flushes) if vec else "registers"
         return (nbytes, vec, gated, flushes, path, detail)
 
-    def block(self, R, H, I, nbytes=2, vec=1):
+    def block(self, R, H, I, nbytes=2, vec=1, full=0):
         """The kernels of the gated block: forward, dx, the weights' gradients."""
         ll = ctypes.c_longlong
         path = self.dll.probe_ffn_path(ll(R), ll(I), nbytes, vec)
         ranges = ctypes.c_int()
-        kind = self.dll.probe_sum(ll(R), ll(H), ll(I), 0 if nbytes == 4 else 1, ctypes.byref(ranges))
+        kind = self.dll.probe_sum(ll(R), ll(H), ll(I), 4 if full else 2, 0 if nbytes == 4 else 1,
+                                  ctypes.byref(ranges))
         split = ranges.value > 1
-        key = (nbytes, vec)
+        key = (nbytes, vec, full)
         if not vec:
             fwd = dx = dw = "registers"
         elif nbytes == 4:
@@ -97,9 +98,10 @@ def test_every_q4_kernel_is_tested(rules):
 def test_every_gated_kernel_is_tested(rules):
     taken, tested = set(), set()
     for R, H, I in itertools.product(ROWS, SIZES, SIZES):
-        for how in ((2, 1), (2, 0), (4, 1)):
+        for how in ((2, 1), (2, 1, 1), (2, 0), (2, 0, 1), (4, 1)):
             taken |= rules.block(R, H, I, *how)
-    for shapes, how in ((FFN16, (2, 1)), (FFN16_SLOW, (2, 0)), (FFN32, (4, 1))):
+    for shapes, how in ((FFN16, (2, 1)), (FFN16, (2, 1, 1)), (FFN16_SLOW, (2, 0)), (FFN16_SLOW, (2, 0, 1)),
+                        (FFN32, (4, 1))):
         for s in shapes:
             tested |= rules.block(*s, *how)
     assert taken <= tested, sorted(taken - tested, key=str)
