@@ -207,9 +207,11 @@ def _no_tangents(what, *tensors):
 
 def _no_gradients(what, *tensors):
     """Refuses tensors whose gradients or tangents ``what`` would drop."""
-    if _torch().is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors):
-        raise RuntimeError(f"{what} has no gradients: call it under torch.no_grad() or on "
-                           "detached tensors")
+    if _torch().is_grad_enabled():
+        for t in tensors:
+            if t is not None and t.requires_grad:
+                raise RuntimeError(f"{what} has no gradients: call it under torch.no_grad() or "
+                                   "on detached tensors")
     _no_tangents(what, *tensors)
 
 
