@@ -487,6 +487,127 @@ int rope(void* q_out, void* k_out, const void* q, const void* k, const void* pos
          int32_t q_heads, int32_t k_heads, int32_t head_dim, int32_t rotary_dim,
          const int64_t* strides, int32_t interleaved, int32_t inverse, int32_t dtype, void* stream);
 
+/*
+ * Norms of queries and keys for each head, with the rotation in the same
+ * pass: a head x [head_dim] becomes Rot(x / sqrt(mean(x^2) + eps) * weight),
+ * Rot as in rope (times magnitude, elements from rotary_dim on not turned),
+ * rounded once.  weights [head_dim] of dtype, or NULL for ones.  strides as for
+ * rope; the outputs may be the inputs themselves.  eps is not negative.
+ *
+ * qk_norm_rope_backward takes the outputs' gradients dq_out, dk_out and writes
+ * dq, dk [num_rows, heads, head_dim] and the weights' gradients [head_dim]
+ * (any of the four may be NULL and is then not computed; heads of zero leave a
+ * side out, and its weight's gradient is zero).  strides: HOST array of
+ * twelve, for q {in row, in head, gradient row, gradient head, dq row, dq
+ * head} and then for k.  Sums are float32 in an order that depends on the sizes
+ * alone.  workspace: qk_norm_rope_backward_workspace_bytes(...), 16-byte aligned, needed
+ * where a weight's gradient is; it may hold anything.  With num_rows == 0
+ * the weights' gradients are zero.
+ */
+int qk_norm_rope(void* q_out, void* k_out, const void* q, const void* k, const void* q_weight,
+                 const void* k_weight, const void* positions, int32_t position_bytes,
+                 const double* inv_freq, float magnitude, float eps, int32_t num_rows,
+                 int32_t q_heads, int32_t k_heads, int32_t head_dim, int32_t rotary_dim,
+                 const int64_t* strides, int32_t interleaved, int32_t dtype, void* stream);
+size_t qk_norm_rope_backward_workspace_bytes(int32_t num_rows, int32_t head_dim, int32_t rotary_dim);
+int qk_norm_rope_backward(void* dq, void* dk, void* dq_weight, void* dk_weight, const void* dq_out,
+                          const void* dk_out, const void* q, const void* k, const void* q_weight,
+                          const void* k_weight, const void* positions, int32_t position_bytes,
+                          const double* inv_freq, float magnitude, float eps, int32_t num_rows,
+                          int32_t q_heads, int32_t k_heads, int32_t head_dim, int32_t rotary_dim,
+                          const int64_t* strides, int32_t interleaved, int32_t dtype,
+                          void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * A paged cache of K and V in 8 or 4 bits.  Token slots are numbered page by
+ * page: slot = page * page_size + place in it.  Values are code * 2^e:
+ *   SGMV_KV_FP8  e4m3 codes, one exponent per token and head (of K, of V);
+ *   SGMV_KV_FP4  e2m1 codes, one exponent per 32 elements of a token's head.
+ * e is the least exponent with |x| <= M 2^e over its group (M = 448 or 6), held to
+ * what the type of the written rows represents exactly (float16: values of
+ * 2^-24 to 57344 or 49152; else about 1e-38 to 3e38 or 2.5e38; larger ones saturate);
+ * code is x 2^-e rounded to nearest even.  A group that holds a NaN or an
+ * infinity reads as NaN.
+ *
+ * The caller owns the four device arrays (16-byte aligned; kv_codes_bytes for k and for v,
+ * kv_scales_bytes for each scales array) and zeroes them once before use; their
+ * layout is the library's own.  page_size is a multiple of 16, head_dim at most 256.
+ *
+ * kv_write quantizes row i of k and v [num_rows, kv_heads, head_dim] into
+ * slots[i] (int32 or int64: slot_bytes 4 or 8); rows whose slot lies outside the
+ * cache (-1 for padding) are skipped.  Slots of one call must differ: one named twice
+ * holds parts of either row.  kv_read is the reverse, exact in the dtype that was written
+ * (and in any wider one); rows without a slot read as zeros.  strides: HOST array of four element
+ * strides, k {row, head}, v {row, head}; the last dimension is dense.
+ */
+typedef enum { SGMV_KV_FP8 = 0, SGMV_KV_FP4 = 1 } sgmv_kv_kind;
+
+typedef struct {
+    void* k;
+    void* v;
+    void* k_scales;
+    void* v_scales;
+    int32_t num_pages, page_size, kv_heads, head_dim;
+    int32_t kind; /* sgmv_kv_kind */
+} sgmv_kv_cache;
+
+size_t kv_codes_bytes(int32_t num_pages, int32_t page_size, int32_t kv_heads, int32_t head_dim,
+                      int32_t kind);
+size_t kv_scales_bytes(int32_t num_pages, int32_t page_size, int32_t kv_heads, int32_t head_dim,
+                       int32_t kind);
+int kv_write(const sgmv_kv_cache* cache, const void* k, const void* v, const void* slots,
+             int32_t slot_bytes, int32_t num_rows, const int64_t* strides, int32_t dtype,
+             void* stream);
+int kv_read(void* k, void* v, const sgmv_kv_cache* cache, const void* slots, int32_t slot_bytes,
+            int32_t num_rows, const int64_t* strides, int32_t dtype, void* stream);
+
+/*
+ * Attention of a batch over such a cache.  num_seqs sequences have tokens of
+ * their own in the cache; runs of consecutive sequences may share a prefix, which is
+ * read once for all of them.  Rows of sequence s, row_indptr[s] up to
+ * row_indptr[s + 1], are the last of its own tokens: row i of n sees the whole of its
+ * run's prefix and the first lengths[s] - n + i + 1 of its own tokens,
+ *     o = softmax(scale q K^T) V,   lse = log(sum of exp(scale q k)),
+ * with float32 sums and maxima, rounded once.  q_heads / kv_heads consecutive heads of q share a
+ * K / V head.  A row that sees no key gets zeros and an lse of minus infinity.  Rows of no
+ * sequence are left as they are.  A visible NaN gives a row of NaN.
+ *
+ * Tables, int32 device arrays: lengths [num_seqs], tokens in the cache (a step's new
+ * ones among them, written before); row_indptr [num_seqs + 1], or NULL for one row each (row s
+ * of sequence s); pages [num_seqs, pages_per_seq], the pages of a sequence's own tokens;
+ * prefix_lengths [num_prefixes], prefix_pages [num_prefixes, pages_per_prefix]; prefix_indptr
+ * [num_prefixes + 1], the first sequence of every run and the end (NULL with one prefix:
+ * all sequences; sequences outside every run have no prefix).  They are
+ * read on the device and not validated on the host: lengths are held to what the page tables have
+ * room for, row and run bounds to the arrays, and tokens on a page outside the cache
+ * are not seen; what a malformed table (one whose bounds decrease) computes is otherwise unspecified.
+ *
+ * prefix_plan cuts the work (prefix_plan_bytes, 16-byte aligned) from the lengths and
+ * row tables: once per step, for all layers' prefix_attention calls with caches of the
+ * same sizes; the page tables are read by these calls themselves.  The cache's
+ * arrays are not read by prefix_plan.  prefix_attention needs a workspace
+ * (prefix_attention_workspace_bytes, 16-byte aligned, any contents; calls that may run
+ * at the same time must not share one).  scale is positive.  strides: HOST array of
+ * element strides q {row, head}, o {row, head}; lse [num_rows, q_heads] or NULL.  o must not
+ * overlap q.  Where lse is NULL nothing else changes.
+ */
+size_t prefix_plan_bytes(const sgmv_kv_cache* cache, int32_t num_rows, int32_t num_seqs,
+                         int32_t num_prefixes, int32_t q_heads, int32_t dtype);
+int prefix_plan(void* plan, size_t plan_bytes, const sgmv_kv_cache* cache, const int32_t* lengths,
+                const int32_t* row_indptr, int32_t pages_per_seq, const int32_t* prefix_lengths,
+                const int32_t* prefix_indptr, int32_t pages_per_prefix, int32_t num_rows,
+                int32_t num_seqs, int32_t num_prefixes, int32_t q_heads, int32_t dtype,
+                void* stream);
+size_t prefix_attention_workspace_bytes(const sgmv_kv_cache* cache, int32_t num_rows,
+                                        int32_t num_seqs, int32_t num_prefixes, int32_t q_heads,
+                                        int32_t dtype);
+int prefix_attention(void* o, float* lse, const void* q, const sgmv_kv_cache* cache,
+                     const void* plan, const int32_t* pages, int32_t pages_per_seq,
+                     const int32_t* prefix_pages, int32_t pages_per_prefix, int32_t num_rows,
+                     int32_t num_seqs, int32_t num_prefixes, int32_t q_heads, float scale,
+                     const int64_t* strides, int32_t dtype, void* workspace,
+                     size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -88,6 +88,22 @@ ABI = [
     ("gated_ffn_backward_workspace_bytes", _sz, [_i32, _i32, _i32, _i32]),
     ("rope", ctypes.c_int, [_vp, _vp, _vp, _vp, _vp, _i32, _vp, _f32, _i32, _i32, _i32, _i32, _i32,
                             _vp, _i32, _i32, _i32, _vp]),
+    ("qk_norm_rope", ctypes.c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i32, _vp, _f32, _f32, _i32,
+                                    _i32, _i32, _i32, _i32, _vp, _i32, _i32, _vp]),
+    ("qk_norm_rope_backward_workspace_bytes", _sz, [_i32, _i32, _i32]),
+    ("qk_norm_rope_backward", ctypes.c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
+                                             _i32, _vp, _f32, _f32, _i32, _i32, _i32, _i32, _i32,
+                                             _vp, _i32, _i32, _vp, _sz, _vp]),
+    ("kv_codes_bytes", _sz, [_i32, _i32, _i32, _i32, _i32]),
+    ("kv_scales_bytes", _sz, [_i32, _i32, _i32, _i32, _i32]),
+    ("kv_write", ctypes.c_int, [_vp, _vp, _vp, _vp, _i32, _i32, _vp, _i32, _vp]),
+    ("kv_read", ctypes.c_int, [_vp, _vp, _vp, _vp, _i32, _i32, _vp, _i32, _vp]),
+    ("prefix_plan_bytes", _sz, [_vp, _i32, _i32, _i32, _i32, _i32]),
+    ("prefix_plan", ctypes.c_int, [_vp, _sz, _vp, _vp, _vp, _i32, _vp, _vp, _i32, _i32, _i32, _i32,
+                                   _i32, _i32, _vp]),
+    ("prefix_attention_workspace_bytes", _sz, [_vp, _i32, _i32, _i32, _i32, _i32]),
+    ("prefix_attention", ctypes.c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _i32, _vp, _i32, _i32, _i32,
+                                        _i32, _i32, _f32, _vp, _i32, _vp, _sz, _vp]),
 ]
 
 
@@ -573,9 +589,16 @@ from .gated import gated_ffn, gated_ffn_backward  # noqa: E402
 from .q4 import Q4Weight, q4_gated_ffn, q4_linear, q4_pack  # noqa: E402
 from .rotary import RopePlan, rope, rope_frequencies, rope_plan  # noqa: E402
 
+# Queries and keys on their way into attention, the cache, and attention over it.
+from .norm import qk_norm_rope, qk_norm_rope_backward  # noqa: E402
+from .kv import KVCache, kv_cache, kv_read, kv_write  # noqa: E402
+from .attention import PrefixPlan, prefix_attention, prefix_plan  # noqa: E402
+
 __all__ = [
     "gated_ffn", "gated_ffn_backward", "q4_pack", "q4_linear", "q4_gated_ffn", "Q4Weight",
     "rope", "rope_plan", "rope_frequencies", "RopePlan",
+    "qk_norm_rope", "qk_norm_rope_backward", "kv_cache", "kv_write", "kv_read", "KVCache",
+    "prefix_plan", "prefix_attention", "PrefixPlan",
     "lora_linear", "lora_linear_workspace_bytes",
     "build_segments", "group_rows", "lora_apply_multi", "lora_apply_multi_workspace_bytes",
     "load_adapter",

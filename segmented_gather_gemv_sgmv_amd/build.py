@@ -18,7 +18,9 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIBRARY = os.path.join(PKG, "libsgmv.so")
 SOURCES = [os.path.join(CSRC, f) for f in ("sgmv_api.hip", "q4_api.hip", "q4_f32.hip", "q4_f16.hip",
-                                           "q4_bf16.hip", "ffn_api.hip", "rope_api.hip")]
+                                           "q4_bf16.hip", "ffn_api.hip", "rope_api.hip",
+                                           "norm_rope_api.hip", "kv_api.hip", "attn_api.hip",
+                                           "attn_f32.hip", "attn_f16.hip", "attn_bf16.hip")]
 OBJECTS = os.path.join(PKG, "_build")
 ARCH = "gfx950"
 

@@ -1,0 +1,52 @@
+// norm_plan.hpp -- how the normed rotation's kernels are cut (host code without HIP, shared
+// with the kernels for its constants).
+#pragma once
+
+#include <algorithm>
+
+namespace sgmv {
+
+constexpr int kNormThreads = 256;
+constexpr int kNormMaxDim = 1024;    // of a head
+constexpr int kNormAngles = 512;     // of a workgroup's rows: rows x rot / 2
+constexpr int kNormGradBlocks = 1024;  // workgroups of the gradients, at most
+
+struct NormShape {
+    int units, lanes, per_lane;  // units of a head, lanes that hold it, units of a lane (1, 2, 4 or 16)
+};
+
+// v: elements of a unit's piece (16 bytes, or 1 where those do not fit).
+inline NormShape norm_shape(int head_dim, int rotary_dim, bool interleaved, int v) {
+    NormShape s;
+    s.units = (interleaved ? (v > 1 ? rotary_dim / v : rotary_dim / 2) : rotary_dim / 2 / v) +
+              (head_dim - rotary_dim) / v;
+    s.lanes = 1;
+    while (s.lanes < s.units && s.lanes < 64) s.lanes *= 2;
+    const int each = (s.units + s.lanes - 1) / s.lanes;
+    s.per_lane = each <= 1 ? 1 : each <= 2 ? 2 : each <= 4 ? 4 : 16;
+    return s;
+}
+
+// Rows a workgroup takes at once: as many as give its threads an angle each and whole
+// passes over heads, but no more than leave the chip without work (4 workgroups per CU).
+inline int norm_rows_per_block(long long rows, int rotary_dim) {
+    const long long most = std::min(8, kNormAngles / (rotary_dim / 2));
+    return (int)std::max(1ll, std::min(most, rows / 1024));
+}
+
+// Workgroups of the gradients: each takes the same number of blocks of rows, give or take one.
+inline int norm_grad_workgroups(long long rows, int rows_per_block) {
+    const long long blocks = (rows + rows_per_block - 1) / rows_per_block;
+    const long long turns = (blocks + kNormGradBlocks - 1) / kNormGradBlocks;
+    return turns ? (int)((blocks + turns - 1) / turns) : 0;
+}
+
+// Heads of a workgroup in the forward pass: all of them once the blocks of rows fill the
+// chip, else split down to one pass.
+inline int norm_heads_per_group(long long blocks, long long heads, int lanes) {
+    const long long pass = std::max(1, kNormThreads / lanes);
+    const long long want = (1024 + blocks - 1) / blocks;
+    return (int)std::min(heads, std::max(pass, (heads + want - 1) / want));
+}
+
+}  // namespace sgmv
