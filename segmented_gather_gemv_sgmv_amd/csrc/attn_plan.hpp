@@ -22,7 +22,7 @@ constexpr int kPlanThreads = 1024;
 
 struct Stack {
     int row0, rows, len;
-    int tile, mtiles, steps;  // rows of a tile, tiles per K / V head, steps of a chunk's waves
+    int tile, mtiles, blocks;  // rows of a tile, tiles per K / V head, steps of 64 keys
 };
 
 __device__ __forceinline__ int plan_row(const PlanArgs& a, int s) {
@@ -55,10 +55,7 @@ __device__ __forceinline__ Stack plan_stack(const PlanArgs& a, int i) {
     k.tile = 16;
     while (k.tile < M && k.tile < wide) k.tile *= 2;
     k.mtiles = (M + k.tile - 1) / k.tile;
-    const int waves_m = max(k.tile / (16 * a.tiles), 1);  // waves side by side over rows
-    const int per_step = kAttnWaves / waves_m;            // steps of 64 keys at once
-    const int blocks = (k.len + kAttnKeys - 1) / kAttnKeys;
-    k.steps = (blocks + per_step - 1) / per_step;
+    k.blocks = (k.len + kAttnKeys - 1) / kAttnKeys;
     return k;
 }
 
@@ -93,16 +90,16 @@ __device__ __forceinline__ long long block_scan64(long long v, long long* s, lon
 __global__ __launch_bounds__(kPlanThreads) void attn_plan_kernel(PlanArgs a) {
     __shared__ long long s_sum[kPlanThreads / 64];
     const int n = a.prefixes + a.seqs, tid = threadIdx.x, lane = tid & 63;
-    // Steps in all, and from them the steps of a chunk.
+    // Steps of 64 keys in all, and from them those of a chunk.
     long long work = 0;
     for (int i = tid; i < n; i += kPlanThreads) {
         const Stack k = plan_stack(a, i);
-        work += (long long)a.kv_heads * k.mtiles * k.steps;
+        work += (long long)a.kv_heads * k.mtiles * k.blocks;
     }
     work = block_sum64(work, s_sum);
     const int chunk = (int)min(max((long long)kAttnLeast, (work + kAttnTarget - 1) / kAttnTarget), 0x3FFFFFFFll);
     auto items_of = [&](const Stack& k) {
-        return (long long)a.kv_heads * k.mtiles * ((k.steps + chunk - 1) / chunk);
+        return (long long)a.kv_heads * k.mtiles * ((k.blocks + chunk - 1) / chunk);
     };
     // Row tables whose sequences overlap could ask for more than there is: no work then.
     long long items = 0, slots = 0;
@@ -134,7 +131,7 @@ __global__ __launch_bounds__(kPlanThreads) void attn_plan_kernel(PlanArgs a) {
             r[1] = k.rows;
             r[2] = k.len;
             r[3] = (int)(item_base + i1 - mine);
-            r[4] = mine ? (k.steps + chunk - 1) / chunk : 0;
+            r[4] = mine ? (k.blocks + chunk - 1) / chunk : 0;
             r[5] = k.mtiles;
             r[6] = k.tile;
             r[7] = (int)(slot_base + s1 - mine * k.tile);
@@ -157,8 +154,6 @@ __global__ __launch_bounds__(kPlanThreads) void attn_plan_kernel(PlanArgs a) {
         const Stack k = plan_stack(a, i);
         const int* r = a.plan + a.at.stacks + (long long)i * kStackInts;
         const int item0 = r[3], chunks = r[4], slot0 = r[7];
-        const int waves_m = max(k.tile / (16 * a.tiles), 1), per_step = kAttnWaves / waves_m;
-        const int blocks = (k.len + kAttnKeys - 1) / kAttnKeys;
         for (int j = lane; j < a.kv_heads * k.mtiles * chunks; j += 64) {
             const int t = j / chunks, part = j - t * chunks;  // (head, tile), chunk
             const int head = t / k.mtiles, mt = t - head * k.mtiles;
@@ -166,8 +161,8 @@ __global__ __launch_bounds__(kPlanThreads) void attn_plan_kernel(PlanArgs a) {
             e[0] = i;
             e[1] = head;
             e[2] = mt * k.tile;
-            e[3] = part * chunk * per_step;
-            e[4] = min((part + 1) * chunk * per_step, blocks);
+            e[3] = part * chunk;
+            e[4] = min((part + 1) * chunk, k.blocks);
             e[5] = slot0 + j * k.tile;
             e[6] = k.tile;
             e[7] = 0;

@@ -122,76 +122,112 @@ __device__ __forceinline__ float column_sum(float v) {
     return __uint_as_float(s[0]) + __uint_as_float(s[1]);
 }
 
-__device__ __forceinline__ uint32_t pack_f16(float a, float b) { return F16::pack2(a, b); }
+// Two floats to float16, nearest-even, in one instruction.
+__device__ __forceinline__ uint32_t pack_f16(float a, float b) {
+    typedef float f2_t __attribute__((ext_vector_type(2)));
+    typedef _Float16 h2_t __attribute__((ext_vector_type(2)));
+    return bits2(__builtin_convertvector((f2_t){a, b}, h2_t));
+}
 
 // ---------------------------------------------------------------------------
-// An item.
+// The rows of a wave: R tiles of 16 rows, one row a lane column.
 // ---------------------------------------------------------------------------
 constexpr float kAttnSlack = 4.f;   // p may reach 2^4 before the maximum is moved
 constexpr int kAttnHeadroom = 11;   // 2^(4 + 11) stays below float16's largest value
 
-template <typename QT, int BITS, int P, int RMAX>
-struct Attn {
+template <typename QT, int BITS, int P>
+struct AttnTypes {
     static constexpr int kSteps = P / 32;                 // products over d of S
     static constexpr int kDTiles = P / 16;                // tiles of O over d
-    static constexpr int kRow = P * BITS / 8;             // bytes of a token's codes
-    static constexpr int kPiece = kRow / 4;               // of a lane's
-    static constexpr int kLines = BITS == 8 ? P / 16 : P / 32;  // 16-byte lines of V a lane reads
+    static constexpr int kRow = P * BITS / 8;             // bytes of a token's codes; lines of V
+    static constexpr int kPiece = kRow / 4;               // bytes of a token's codes that a lane takes
+    static constexpr int kLines = kRow / 16;              // 16-byte lines of V a lane takes
+    static constexpr int kLineTiles = 8 / BITS;           // tiles of O that a line feeds
     static constexpr int kGroups = BITS == 8 ? 1 : P / 32;
     static constexpr int kKGroups = BITS == 8 || P == 64 || P == 128 ? 1 : 2;  // that a lane's piece of K meets
     static constexpr int kQTerms = QT::kBytes == 4 ? 3 : 1;
     static constexpr int kPTerms = std::is_same<QT, BF16>::value ? 1 : 2;
     using KT = std::conditional_t<std::is_same<QT, F16>::value, F16, BF16>;  // operands of S
+};
 
-    // Waves of one group over rows hold their sums here, one after the other.
-    static constexpr int kLdsFloats = kAttnWaves / 2 * kDTiles * RMAX * 256;
+// An item as its workgroup sees it.
+struct Item {
+    int head, m0, row0, M, len, blk0, blk1, slot, tile;
+    bool own;
+    int hidden;         // own: tokens before the first row
+    const int* table;   // pages
+};
 
-    template <int R>
-    static __device__ __forceinline__ void run(const AttnArgs& a, const int* e, float* s_o, float2* s_ml) {
-        const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
-        const int lr = lane & 15, lg = lane >> 4;
-        const int stack = e[0], head = e[1], m0 = e[2], blk0 = e[3], tile = e[6];
-        const int* rec = a.plan + a.at.stacks + (long long)stack * kStackInts;
-        const int row0 = rec[0], M = rec[1] * a.rep, len = rec[2];
-        const bool own = stack >= a.prefixes;
-        const int* table = own ? a.own_pages + (long long)(stack - a.prefixes) * a.own_width
-                               : a.prefix_pages + (long long)stack * a.prefix_width;
-        const int waves_m = tile / (16 * R);
-        const int waves_k = kAttnWaves / waves_m;
-        const int wm = wave % waves_m, wk = wave / waves_m;
-        const int mw = m0 + wm * 16 * R;  // first row of the wave
-        // Keys that a row sees; rows of an own stack are the last of its tokens.
-        const int hidden = own ? len - rec[1] : len;
-        int lim[R];
-        int most = 0;  // of the wave's rows
+__device__ __forceinline__ Item attn_item(const AttnArgs& a, const int* e) {
+    Item t;
+    const int stack = e[0];
+    const int* rec = a.plan + a.at.stacks + (long long)stack * kStackInts;
+    t.head = e[1];
+    t.m0 = e[2];
+    t.blk0 = e[3];
+    t.blk1 = e[4];
+    t.slot = e[5];
+    t.tile = e[6];
+    t.row0 = rec[0];
+    t.M = rec[1] * a.rep;
+    t.len = rec[2];
+    t.own = stack >= a.prefixes;
+    t.hidden = t.len - rec[1];
+    t.table = t.own ? a.own_pages + (long long)(stack - a.prefixes) * a.own_width
+                    : a.prefix_pages + (long long)stack * a.prefix_width;
+    return t;
+}
+
+// Where 16-token block `b` of the item's keys lies (block 0 of the cache where there is none), if it
+// is there: blocks counted over pages and heads.
+__device__ __forceinline__ long long attn_place(const AttnArgs& a, const Item& it, int b, bool& ok) {
+    const int index = a.blocks_per_page == 1 ? b : (int)__umulhi((uint32_t)b, a.page_magic);
+    ok = b * kKvBlock < it.len;
+    const int page = ok ? it.table[index] : 0;
+    ok = ok && (unsigned)page < (unsigned)a.num_pages;
+    const int in = ok ? b - index * a.blocks_per_page : 0;
+    return ((long long)(ok ? page : 0) * a.kv_heads + it.head) * a.blocks_per_page + in;
+}
+
+template <typename QT, int BITS, int P, int R>
+struct AttnRows : AttnTypes<QT, BITS, P> {
+    using A = AttnTypes<QT, BITS, P>;
+    using KT = typename A::KT;
+    uint4 qf[R][A::kQTerms][A::kSteps];
+    acc4_t o[R][A::kDTiles], s[R][4];
+    float mref[R], l[R];
+    int lim[R];   // keys that the lane's row sees
+    int eref;     // biased exponent that p 2^e is relative to
+    int m_first;  // first row of the wave
+    int blk_end;  // blocks that any of its rows sees
+
+    // q: lane (lr, lg) holds d = lg P / 4 + 8 s + 0..7 of row lr of each tile.
+    __device__ __forceinline__ void init(const AttnArgs& a, const Item& it, int first, int lr, int lg) {
+        m_first = first;
+        const int last = min(first + 16 * R, it.M) - 1;
+        const int most = last < first ? 0 : it.own ? it.hidden + last / a.rep + 1 : it.len;
+        blk_end = min(it.blk1, (most + kAttnKeys - 1) / kAttnKeys);
+        eref = 20;
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-            const int m = mw + 16 * r + lr;
-            lim[r] = m >= M ? len : own ? hidden + m / a.rep + 1 : len;
-        }
-        {
-            const int last = min(mw + 16 * R, M) - 1;
-            most = last < mw ? 0 : own ? hidden + last / a.rep + 1 : len;
-        }
-        const int blk1 = min(e[4], (most + kAttnKeys - 1) / kAttnKeys);
-
-        // q: lane (lr, lg) holds d = lg P / 4 + 8 s + 0..7 of row lr of each tile.
-        uint4 qf[R][kQTerms][kSteps];
-#pragma unroll
-        for (int r = 0; r < R; ++r) {
-            const int m = mw + 16 * r + lr;
-            const bool ok = m < M;
+            const int m = first + 16 * r + lr;
+            const bool ok = m < it.M;
             const int i = ok ? m / a.rep : 0;
-            const int h = head * a.rep + (ok ? m - i * a.rep : 0);
-            const typename QT::storage* p =
-                (const typename QT::storage*)a.q + (long long)(row0 + i) * a.q_row + (long long)h * a.q_head;
+            const int h = it.head * a.rep + (ok ? m - i * a.rep : 0);
+            lim[r] = ok && it.own ? it.hidden + i + 1 : it.len;
+            mref[r] = -__builtin_inff();
+            l[r] = 0.f;
 #pragma unroll
-            for (int s = 0; s < kSteps; ++s) {
-                const int d = lg * (P / 4) + 8 * s;
+            for (int t = 0; t < A::kDTiles; ++t) o[r][t] = acc4_t{0.f, 0.f, 0.f, 0.f};
+            const typename QT::storage* p =
+                (const typename QT::storage*)a.q + (long long)(it.row0 + i) * a.q_row + (long long)h * a.q_head;
+#pragma unroll
+            for (int x = 0; x < A::kSteps; ++x) {
+                const int d = lg * (P / 4) + 8 * x;
                 float f[8];
                 if (ok && a.vec && d + 8 <= a.D) {
                     if constexpr (QT::kBytes == 2) {
-                        qf[r][0][s] = load16(p + d);
+                        qf[r][0][x] = load16(p + d);
                         continue;
                     } else {
                         QT::unpack(load16(p + d), f);
@@ -199,335 +235,473 @@ struct Attn {
                     }
                 } else {
 #pragma unroll
-                    for (int x = 0; x < 8; ++x) f[x] = ok && d + x < a.D ? QT::load1(p + d + x) : 0.f;
+                    for (int y = 0; y < 8; ++y) f[y] = ok && d + y < a.D ? QT::load1(p + d + y) : 0.f;
                 }
 #pragma unroll
-                for (int t = 0; t < kQTerms; ++t) {
-                    qf[r][t][s] = make_uint4(pack2_rne<KT>(f[0], f[1]), pack2_rne<KT>(f[2], f[3]),
+                for (int t = 0; t < A::kQTerms; ++t) {
+                    qf[r][t][x] = make_uint4(pack2_rne<KT>(f[0], f[1]), pack2_rne<KT>(f[2], f[3]),
                                              pack2_rne<KT>(f[4], f[5]), pack2_rne<KT>(f[6], f[7]));
-                    if (t + 1 < kQTerms) {
+                    if (t + 1 < A::kQTerms) {
                         float g[8];
-                        KT::unpack(qf[r][t][s], g);
+                        KT::unpack(qf[r][t][x], g);
 #pragma unroll
-                        for (int x = 0; x < 8; ++x) f[x] -= g[x];
+                        for (int y = 0; y < 8; ++y) f[y] -= g[y];
                     }
                 }
             }
         }
+    }
 
-        acc4_t o[R][kDTiles];
-        float mref[R], l[R];
+    // S tile t += K Q^T of the d of step x.
+    __device__ __forceinline__ void score(int t, int x, const uint4& kf) {
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+            for (int y = 0; y < A::kQTerms; ++y)
+                s[r][t] = PieceOps<KT>::mma(kf, qf[r][y][x], x == 0 && y == 0 ? acc4_t{0.f, 0.f, 0.f, 0.f} : s[r][t]);
+    }
+
+    // Scores of keys [first, first + 16) of the lane to p, running maxima and sums; `there`: how many
+    // of these keys the cache holds.  Returns whether every row sees all of them.
+    __device__ __forceinline__ bool soften(const AttnArgs& a, int first, int there) {
+        bool whole = there >= 16;
+#pragma unroll
+        for (int r = 0; r < R; ++r) whole = whole && lim[r] - first >= 16;
+        const bool all = __all(whole);
+        if (!all) {
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                const int rem = min(lim[r] - first, there);
+#pragma unroll
+                for (int t = 0; t < 16; ++t)
+                    if (t >= rem) s[r][t / 4][t % 4] = -__builtin_inff();
+            }
+        }
+        // Maxima are moved only where p would pass 2^4.
+        float mx[R];
+        bool move = false;
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-            mref[r] = -__builtin_inff();
-            l[r] = 0.f;
+            float v = s[r][0][0];
 #pragma unroll
-            for (int t = 0; t < kDTiles; ++t) o[r][t] = acc4_t{0.f, 0.f, 0.f, 0.f};
+            for (int t = 1; t < 16; ++t) v = fmaxf(v, s[r][t / 4][t % 4]);
+            mx[r] = column_max(v) * a.c;
+            move = move || mx[r] > mref[r] + kAttnSlack;
         }
-        int eref = 20;  // biased exponent that p 2^e is relative to
-
-        // Where 16-token block `b` of the stack lies (page 0 where there is none), if it is there.
-        auto place = [&](int b, bool& ok) {
-            const int pi = (int)__umulhi((uint32_t)b, a.page_magic);
-            const int page_index = a.blocks_per_page == 1 ? b : pi;
-            ok = b * kKvBlock < len;
-            const int page = ok ? table[page_index] : 0;
-            ok = ok && (unsigned)page < (unsigned)a.num_pages;
-            const int in = ok ? b - page_index * a.blocks_per_page : 0;
-            return ((long long)(ok ? page : 0) * a.kv_heads + head) * a.blocks_per_page + in;
-        };
-        uint32_t kw[4][kPiece / 4], ks[kKGroups][4];
-        uint32_t vw[kLines][4], vs[kGroups][4];
-        bool v_ok = false;
-        const int g0 = BITS == 8 ? 0 : (lg * (P / 4)) >> 5;
-        auto load_k = [&](int blk) {
-            bool ok;
-            const long long b = place(blk * 4 + (lr >> 2), ok);
+        if (__any(move)) {
 #pragma unroll
-            for (int t = 0; t < 4; ++t)
-                load_words<kPiece>(a.k + (b * 16 + t * 4 + (lr & 3)) * kRow + lg * kPiece, kw[t]);
+            for (int r = 0; r < R; ++r) {
+                const float m = fmaxf(mref[r], mx[r]);
+                const float f = m == mref[r] ? 1.f : __builtin_amdgcn_exp2f(mref[r] - m);
+                mref[r] = m;
+                l[r] *= f;
 #pragma unroll
-            for (int g = 0; g < kKGroups; ++g)
-                load_words<16>(a.k_scales + (b * kGroups + min(g0 + g, kGroups - 1)) * 16, ks[g]);
-        };
-        auto load_v = [&](int blk) {
-            const long long b = place(blk * 4 + lg, v_ok);
-#pragma unroll
-            for (int i = 0; i < kLines; ++i) load_words<16>(a.v + (b * kRow + i * 16 + lr) * 16, vw[i]);
-#pragma unroll
-            for (int g = 0; g < kGroups; ++g) load_words<16>(a.v_scales + (b * kGroups + g) * 16, vs[g]);
-        };
-
-        int blk = blk0 + wk;
-        if (blk < blk1) {
-            load_k(blk);
-            load_v(blk);
+                for (int t = 0; t < A::kDTiles; ++t) o[r][t] *= f;
+            }
         }
-        for (; blk < blk1; blk += waves_k) {
-            // Scores.
-            acc4_t s[R][4];
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const float m = mref[r] == -__builtin_inff() ? 0.f : mref[r];
+#pragma unroll
+            for (int t = 0; t < 16; ++t) {
+                const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(s[r][t / 4][t % 4], a.c, -m));
+                s[r][t / 4][t % 4] = p;
+                l[r] += p;
+            }
+        }
+        return all;
+    }
+
+    // The largest scale of the block's tokens (of those that are there) becomes the reference
+    // exponent if it is larger; a NaN's is left out.
+    __device__ __forceinline__ void raise(uint32_t (*vs)[4], bool all, int there) {
+        typedef unsigned short u16x2_t __attribute__((ext_vector_type(2)));
+        if (!all) {
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
-                float sc[kKGroups];
+                const int n = min(max(there - 4 * t, 0), 4);
+                const uint32_t mask = n == 4 ? ~0u : (1u << (8 * n)) - 1u;
 #pragma unroll
-                for (int g = 0; g < kKGroups; ++g) sc[g] = __uint_as_float(((ks[g][t] >> (8 * (lr & 3))) & 255u) << 23);
-#pragma unroll
-                for (int r = 0; r < R; ++r) s[r][t] = acc4_t{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                for (int d = 0; d < kSteps; ++d) {
-                    float scale = sc[0];
-                    if constexpr (kKGroups == 2)
-                        if (((lg * (P / 4) + 8 * d) >> 5) != g0) scale = sc[1];
-                    const uint4 kf = code_piece<KT, BITS>(kw[t] + d * (BITS / 4), scale);
-#pragma unroll
-                    for (int r = 0; r < R; ++r)
-#pragma unroll
-                        for (int x = 0; x < kQTerms; ++x) s[r][t] = PieceOps<KT>::mma(kf, qf[r][x][d], s[r][t]);
-                }
+                for (int g = 0; g < A::kGroups; ++g) vs[g][t] &= mask;
             }
-            const bool more = blk + waves_k < blk1;
-            if (more) load_k(blk + waves_k);
-
-            // Keys past a row's limit, or on a page that is not there.
-            int rem[R];
-            bool whole = true;
+        }
+        u16x2_t even = {0, 0}, odd = {0, 0};
 #pragma unroll
-            for (int r = 0; r < R; ++r) {
-                rem[r] = v_ok ? lim[r] - (blk * kAttnKeys + lg * 16) : 0;
-                whole = whole && rem[r] >= 16;
+        for (int g = 0; g < A::kGroups; ++g)
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                even = __builtin_elementwise_max(even, __builtin_bit_cast(u16x2_t, vs[g][t] & 0x00FF00FFu));
+                odd = __builtin_elementwise_max(odd, __builtin_bit_cast(u16x2_t, (vs[g][t] >> 8) & 0x00FF00FFu));
             }
-            const bool all = __all(whole);
-            const int there = v_ok ? len - (blk * kAttnKeys + lg * 16) : 0;  // tokens of the lane's block
-            if (!all) {
-#pragma unroll
-                for (int r = 0; r < R; ++r)
-#pragma unroll
-                    for (int t = 0; t < 4; ++t)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            if (t * 4 + i >= rem[r]) s[r][t][i] = -__builtin_inff();
-            }
-            // Running maxima, moved only where p would pass 2^4.
-            float mx[R];
-            bool move = false;
-#pragma unroll
-            for (int r = 0; r < R; ++r) {
-                float v = -__builtin_inff();
-#pragma unroll
+        even = __builtin_elementwise_max(even, odd);
+        int top = largest_of_column(max((int)even.x, (int)even.y));
+        if (__builtin_expect(top == kKvNaN, 0)) {
+            int t2 = 0;
+            for (int g = 0; g < A::kGroups; ++g)
                 for (int t = 0; t < 4; ++t)
+                    for (int y = 0; y < 4; ++y) {
+                        const int b = (int)((vs[g][t] >> (8 * y)) & 255u);
+                        if (b != kKvNaN) t2 = max(t2, b);
+                    }
+            top = largest_of_column(t2);
+        }
+        if (top > eref) {
+            const float f = __builtin_ldexpf(1.f, max(eref - top, -126));
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) v = fmaxf(v, s[r][t][i]);
-                mx[r] = column_max(v) * a.c;
-                move = move || mx[r] > mref[r] + kAttnSlack;
+            for (int r = 0; r < R; ++r)
+#pragma unroll
+                for (int t = 0; t < A::kDTiles; ++t) o[r][t] *= f;
+            eref = top;
+        }
+    }
+    // Uniform over the wave (lanes of a group of 16 hold the same).
+    static __device__ __forceinline__ int largest_of_column(int v) {
+        auto x = __builtin_amdgcn_permlane16_swap((unsigned)v, (unsigned)v, false, false);
+        v = max((int)x[0], (int)x[1]);
+        x = __builtin_amdgcn_permlane32_swap((unsigned)v, (unsigned)v, false, false);
+        return __builtin_amdgcn_readfirstlane(max((int)x[0], (int)x[1]));
+    }
+
+    // O^T += V^T (p 2^e)^T; vline(i, u, out) gives the operands of line i, half u of its tokens.
+    template <typename Line>
+    __device__ __forceinline__ void accumulate(uint32_t (*vs)[4], bool all, int first, int there, Line vline) {
+        raise(vs, all, there);
+        // with a scale 2^(b - 127), p is multiplied by 2^(b - eref + headroom)
+        const float unit = __builtin_ldexpf(1.f, kAttnHeadroom + 127 - eref);
+#pragma unroll
+        for (int g = 0; g < A::kGroups; ++g) {
+            float f[16];
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                f[4 * t] = __uint_as_float((vs[g][t] << 23) & 0x7F800000u) * unit;
+                f[4 * t + 1] = __uint_as_float((vs[g][t] << 15) & 0x7F800000u) * unit;
+                f[4 * t + 2] = __uint_as_float((vs[g][t] << 7) & 0x7F800000u) * unit;
+                f[4 * t + 3] = __uint_as_float((vs[g][t] >> 1) & 0x7F800000u) * unit;
             }
-            if (__any(move)) {
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                uint4 pf[R][A::kPTerms];
 #pragma unroll
                 for (int r = 0; r < R; ++r) {
-                    const float m = fmaxf(mref[r], mx[r]);
-                    const float f = m == mref[r] ? 1.f : __builtin_amdgcn_exp2f(mref[r] - m);
-                    mref[r] = m;
-                    l[r] *= f;
+                    float w[8];
 #pragma unroll
-                    for (int t = 0; t < kDTiles; ++t) o[r][t] *= f;
-                }
-            }
+                    for (int x = 0; x < 8; ++x) w[x] = s[r][2 * u + x / 4][x % 4] * f[8 * u + x];
+                    if (!all) {  // what lies behind a row's last key may be NaN
+                        const int rem = min(lim[r] - first, there) - 8 * u;
 #pragma unroll
-            for (int r = 0; r < R; ++r) {
-                const float m = mref[r] == -__builtin_inff() ? 0.f : mref[r];
-#pragma unroll
-                for (int t = 0; t < 4; ++t)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(s[r][t][i], a.c, -m));
-                        s[r][t][i] = p;
-                        l[r] += p;
+                        for (int x = 0; x < 8; ++x)
+                            if (x >= rem) w[x] = 0.f;
                     }
-            }
-            // V's scales; the largest exponent of tokens that are there (a NaN's is left out).
-            auto factors = [&](int g, float* f) {
 #pragma unroll
-                for (int t = 0; t < 4; ++t) {
-                    f[4 * t] = __uint_as_float((vs[g][t] << 23) & 0x7F800000u);
-                    f[4 * t + 1] = __uint_as_float((vs[g][t] << 15) & 0x7F800000u);
-                    f[4 * t + 2] = __uint_as_float((vs[g][t] << 7) & 0x7F800000u);
-                    f[4 * t + 3] = __uint_as_float((vs[g][t] >> 1) & 0x7F800000u);
-                }
-                if (!all) {
+                    for (int x = 0; x < A::kPTerms; ++x) {
+                        pf[r][x] = make_uint4(pack_f16(w[0], w[1]), pack_f16(w[2], w[3]), pack_f16(w[4], w[5]),
+                                              pack_f16(w[6], w[7]));
+                        if (x + 1 < A::kPTerms) {
+                            float h[8];
+                            F16::unpack(pf[r][x], h);
 #pragma unroll
-                    for (int t = 0; t < 16; ++t) f[t] = t < there ? f[t] : 0.f;
-                }
-            };
-            float top = 0.f;
-#pragma unroll
-            for (int g = 0; g < kGroups; ++g) {
-                float f[16];
-                factors(g, f);
-#pragma unroll
-                for (int t = 0; t < 16; ++t) top = fmaxf(top, f[t]);
-            }
-            top = column_max(top);
-            if (__builtin_expect(__any(top == __builtin_inff()), 0)) {
-                top = 0.f;
-#pragma unroll
-                for (int g = 0; g < kGroups; ++g) {
-                    float f[16];
-                    factors(g, f);
-#pragma unroll
-                    for (int t = 0; t < 16; ++t) top = fmaxf(top, f[t] == __builtin_inff() ? 0.f : f[t]);
-                }
-                top = column_max(top);
-            }
-            const int etop = __builtin_amdgcn_readfirstlane((int)(__float_as_uint(top) >> 23));
-            if (etop > eref) {
-                const float f = __builtin_ldexpf(1.f, max(eref - etop, -126));
-#pragma unroll
-                for (int r = 0; r < R; ++r)
-#pragma unroll
-                    for (int t = 0; t < kDTiles; ++t) o[r][t] *= f;
-                eref = etop;
-            }
-            // 2^(headroom + 127 - eref): with a scale 2^(b - 127), p is multiplied by 2^(b - eref + headroom)
-            const float unit = __builtin_ldexpf(1.f, kAttnHeadroom + 127 - eref);
-
-            // O^T += V^T (p 2^e)^T: half u of a line's tokens at a time.
-#pragma unroll
-            for (int g = 0; g < kGroups; ++g) {
-                float f[16];
-                factors(g, f);
-#pragma unroll
-                for (int t = 0; t < 16; ++t) f[t] *= unit;
-#pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    uint4 pf[R][kPTerms];
-#pragma unroll
-                    for (int r = 0; r < R; ++r) {
-                        float w[8];
-#pragma unroll
-                        for (int x = 0; x < 8; ++x) {
-                            w[x] = s[r][2 * u + x / 4][x % 4] * f[8 * u + x];
-                            if (!all && 8 * u + x >= rem[r]) w[x] = 0.f;  // what lies there may be NaN
+                            for (int y = 0; y < 8; ++y) w[y] -= h[y];
                         }
+                    }
+                }
 #pragma unroll
-                        for (int x = 0; x < kPTerms; ++x) {
-                            pf[r][x] = make_uint4(pack_f16(w[0], w[1]), pack_f16(w[2], w[3]), pack_f16(w[4], w[5]),
-                                                  pack_f16(w[6], w[7]));
-                            if (x + 1 < kPTerms) {
-                                float h[8];
-                                F16::unpack(pf[r][x], h);
+                for (int i = BITS == 8 ? 0 : g; i < (BITS == 8 ? A::kLines : g + 1); ++i) {
+                    uint4 vf[A::kLineTiles];
+                    vline(i, u, vf);
 #pragma unroll
-                                for (int y = 0; y < 8; ++y) w[y] -= h[y];
+                    for (int y = 0; y < A::kLineTiles; ++y)
+#pragma unroll
+                        for (int r = 0; r < R; ++r)
+#pragma unroll
+                            for (int x = 0; x < A::kPTerms; ++x) {
+                                acc4_t& c = o[r][i * A::kLineTiles + y];
+                                c = PieceOps<F16>::mma(vf[y], pf[r][x], c);
                             }
-                        }
-                    }
-                    if constexpr (BITS == 8) {
-#pragma unroll
-                        for (int t = 0; t < kDTiles; ++t) {
-                            const uint4 vf = code_piece<F16, 8>(vw[t] + 2 * u, 1.f);
-#pragma unroll
-                            for (int r = 0; r < R; ++r)
-#pragma unroll
-                                for (int x = 0; x < kPTerms; ++x) o[r][t] = PieceOps<F16>::mma(vf, pf[r][x], o[r][t]);
-                        }
-                    } else {
-                        // A byte holds a token's codes of tiles 2 g (low) and 2 g + 1.
-                        uint32_t c[8];
-#pragma unroll
-                        for (int y = 0; y < 2; ++y) {
-                            c[4 * y] = code_pair<F16, 4, 0>(vw[g][2 * u + y], 1.f);
-                            c[4 * y + 1] = code_pair<F16, 4, 1>(vw[g][2 * u + y], 1.f);
-                            c[4 * y + 2] = code_pair<F16, 4, 2>(vw[g][2 * u + y], 1.f);
-                            c[4 * y + 3] = code_pair<F16, 4, 3>(vw[g][2 * u + y], 1.f);
-                        }
-#pragma unroll
-                        for (int y = 0; y < 2; ++y) {
-                            const uint32_t sel = y ? 0x07060302u : 0x05040100u;
-                            const uint4 vf = make_uint4(
-                                __builtin_amdgcn_perm(c[1], c[0], sel), __builtin_amdgcn_perm(c[3], c[2], sel),
-                                __builtin_amdgcn_perm(c[5], c[4], sel), __builtin_amdgcn_perm(c[7], c[6], sel));
-#pragma unroll
-                            for (int r = 0; r < R; ++r)
-#pragma unroll
-                                for (int x = 0; x < kPTerms; ++x)
-                                    o[r][2 * g + y] = PieceOps<F16>::mma(vf, pf[r][x], o[r][2 * g + y]);
-                        }
-                    }
                 }
             }
-            if (more) load_v(blk + waves_k);
         }
+    }
 
-        // The waves over the keys of the same rows: their maxima, then their sums pairwise.
-#pragma unroll
-        for (int r = 0; r < R; ++r) l[r] = column_sum(l[r]);
-        const float back = __builtin_ldexpf(1.f, eref - 127 - kAttnHeadroom);
-        if (lg == 0)
-#pragma unroll
-            for (int r = 0; r < R; ++r) s_ml[(wave * R + r) * 16 + lr] = make_float2(mref[r], l[r]);
-        __syncthreads();
-        float m_all[R], l_all[R];
+    // The wave's rows to their slots: O scaled to its true exponent by `f`, maxima and sums.
+    __device__ __forceinline__ void write(const AttnArgs& a, const Item& it, int lr, int lg) const {
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-            float m = -__builtin_inff();
-            for (int k = 0; k < waves_k; ++k) m = fmaxf(m, s_ml[((k * waves_m + wm) * R + r) * 16 + lr].x);
-            float t = 0.f;
-            for (int k = 0; k < waves_k; ++k) {
-                const float2 x = s_ml[((k * waves_m + wm) * R + r) * 16 + lr];
-                t += x.x == m ? x.y : x.y * __builtin_amdgcn_exp2f(x.x - m);
-            }
-            m_all[r] = m;
-            l_all[r] = t;
-            const float f = (mref[r] == m ? 1.f : __builtin_amdgcn_exp2f(mref[r] - m)) * back;
+            const int m = m_first + 16 * r + lr;
+            if (m >= it.M) continue;
+            const long long slot = (long long)it.slot + m - it.m0;
+            float* out = a.part_o + slot * P + lg * 4;
 #pragma unroll
-            for (int d = 0; d < kDTiles; ++d) o[r][d] *= f;
+            for (int d = 0; d < A::kDTiles; ++d) *reinterpret_cast<acc4_t*>(out + 16 * d) = o[r][d];
+            if (lg == 0) a.part_ml[slot] = make_float2(mref[r], l[r]);
         }
-        for (int half = waves_k / 2; half > 0; half /= 2) {
-            float* at = s_o + (size_t)(wm * (waves_k / 2) + (wk >= half ? wk - half : wk)) * (kDTiles * R * 256);
-            if (wk >= half && wk < 2 * half) {
-#pragma unroll
-                for (int r = 0; r < R; ++r)
-#pragma unroll
-                    for (int d = 0; d < kDTiles; ++d)
-                        *reinterpret_cast<acc4_t*>(at + ((r * kDTiles + d) * 64 + lane) * 4) = o[r][d];
-            }
-            __syncthreads();
-            if (wk < half) {
-#pragma unroll
-                for (int r = 0; r < R; ++r)
-#pragma unroll
-                    for (int d = 0; d < kDTiles; ++d)
-                        o[r][d] += *reinterpret_cast<const acc4_t*>(at + ((r * kDTiles + d) * 64 + lane) * 4);
-            }
-            __syncthreads();
-        }
-        if (wk == 0) {
-#pragma unroll
-            for (int r = 0; r < R; ++r) {
-                const int m = mw + 16 * r + lr;
-                if (m >= M) continue;
-                const long long slot = (long long)e[5] + m - m0;
-                float* out = a.part_o + slot * P + lg * 4;
-#pragma unroll
-                for (int d = 0; d < kDTiles; ++d) *reinterpret_cast<acc4_t*>(out + 16 * d) = o[r][d];
-                if (lg == 0) a.part_ml[slot] = make_float2(m_all[r], l_all[r]);
-            }
-        }
+    }
+    __device__ __forceinline__ float true_exponent() const {
+        return __builtin_ldexpf(1.f, eref - 127 - kAttnHeadroom);
     }
 };
 
-template <typename QT, int BITS, int P, int RMAX>
-__global__ __launch_bounds__(kAttnThreads, 1) void attn_kernel(AttnArgs a) {
-    using A = Attn<QT, BITS, P, RMAX>;
-    __shared__ __align__(16) float s_o[A::kLdsFloats];
-    __shared__ float2 s_ml[kAttnWaves * RMAX * 16];
-    if ((int)blockIdx.x >= a.plan[0]) return;
-    const int* e = a.plan + a.at.items + (long long)blockIdx.x * kItemInts;
-    if constexpr (RMAX == 2) {
-        if (e[6] == 16) {
-            A::template run<1>(a, e, s_o, s_ml);
-            return;
+// Operands of a line of V from its codes: half u of its 16 tokens.
+template <int BITS>
+__device__ __forceinline__ void line_operands(const uint32_t* w, int u, uint4* vf) {
+    if constexpr (BITS == 8) {
+        vf[0] = code_piece<F16, 8>(w + 2 * u, 1.f);
+    } else {
+        // A byte holds a token's codes of two tiles: low halves the first's.
+        uint32_t c[8];
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+            c[4 * y] = code_pair<F16, 4, 0>(w[2 * u + y], 1.f);
+            c[4 * y + 1] = code_pair<F16, 4, 1>(w[2 * u + y], 1.f);
+            c[4 * y + 2] = code_pair<F16, 4, 2>(w[2 * u + y], 1.f);
+            c[4 * y + 3] = code_pair<F16, 4, 3>(w[2 * u + y], 1.f);
+        }
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+            const uint32_t sel = y ? 0x07060302u : 0x05040100u;
+            vf[y] = make_uint4(__builtin_amdgcn_perm(c[1], c[0], sel), __builtin_amdgcn_perm(c[3], c[2], sel),
+                               __builtin_amdgcn_perm(c[5], c[4], sel), __builtin_amdgcn_perm(c[7], c[6], sel));
         }
     }
-    A::template run<RMAX>(a, e, s_o, s_ml);
+}
+
+// ---------------------------------------------------------------------------
+// Items of up to 32 rows: codes go from memory to operand registers, every wave has keys of its own
+// (of 32 rows two waves share them), and the waves' results are joined through LDS.
+// ---------------------------------------------------------------------------
+template <typename QT, int BITS, int P>
+__device__ __forceinline__ void attn_direct(const AttnArgs& a, const Item& it, unsigned char* lds) {
+    using A = AttnTypes<QT, BITS, P>;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+    const int lr = lane & 15, lg = lane >> 4;
+    const int waves_m = it.tile / 16, waves_k = kAttnWaves / waves_m;
+    const int wm = wave % waves_m, wk = wave / waves_m;
+    AttnRows<QT, BITS, P, 1> rows;
+    rows.init(a, it, it.m0 + wm * 16, lr, lg);
+
+    uint32_t kw[4][A::kPiece / 4], ks[A::kKGroups][4], vw[A::kLines][4], vs[A::kGroups][4];
+    bool v_ok = false;
+    const int g0 = BITS == 8 ? 0 : (lg * (P / 4)) >> 5;
+    auto load_k = [&](int blk) {
+        bool ok;
+        const long long b = attn_place(a, it, blk * 4 + (lr >> 2), ok);
+        const uint8_t* p = a.k + (b * 16 + (lr & 3)) * A::kRow + lg * A::kPiece;
+#pragma unroll
+        for (int t = 0; t < 4; ++t) load_words<A::kPiece>(p + t * 4 * A::kRow, kw[t]);
+#pragma unroll
+        for (int g = 0; g < A::kKGroups; ++g)
+            load_words<16>(a.k_scales + (b * A::kGroups + min(g0 + g, A::kGroups - 1)) * 16, ks[g]);
+    };
+    auto load_v = [&](int blk) {
+        const long long b = attn_place(a, it, blk * 4 + lg, v_ok);
+        const uint8_t* p = a.v + (b * A::kRow + lr) * 16;
+#pragma unroll
+        for (int i = 0; i < A::kLines; ++i) load_words<16>(p + i * 256, vw[i]);
+#pragma unroll
+        for (int g = 0; g < A::kGroups; ++g) load_words<16>(a.v_scales + (b * A::kGroups + g) * 16, vs[g]);
+    };
+
+    int blk = it.blk0 + wk;
+    const int end = rows.blk_end;
+    if (blk < end) {
+        load_k(blk);
+        load_v(blk);
+    }
+    for (; blk < end; blk += waves_k) {
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            float sc[A::kKGroups];
+#pragma unroll
+            for (int g = 0; g < A::kKGroups; ++g)
+                sc[g] = __uint_as_float(((ks[g][t] >> (8 * (lr & 3))) & 255u) << 23);
+#pragma unroll
+            for (int x = 0; x < A::kSteps; ++x) {
+                float scale = sc[0];
+                if constexpr (A::kKGroups == 2)
+                    if (((lg * (P / 4) + 8 * x) >> 5) != g0) scale = sc[1];
+                rows.score(t, x, code_piece<typename A::KT, BITS>(kw[t] + x * (BITS / 4), scale));
+            }
+        }
+        const bool more = blk + waves_k < end;
+        if (more) load_k(blk + waves_k);  // behind the rest of this step
+        const int first = blk * kAttnKeys + lg * 16;
+        const int there = v_ok ? it.len - first : 0;
+        const bool all = rows.soften(a, first, there);
+        rows.accumulate(vs, all, first, there,
+                        [&](int i, int u, uint4* vf) { line_operands<BITS>(vw[i], u, vf); });
+        if (more) load_v(blk + waves_k);
+    }
+
+    // The waves over the keys of the same rows: their maxima, then their sums pairwise.
+    float* s_o = (float*)lds;
+    float2* s_ml = (float2*)(lds + kAttnWaves / 2 * A::kDTiles * 1024);
+    rows.l[0] = column_sum(rows.l[0]);
+    if (lg == 0) s_ml[wave * 16 + lr] = make_float2(rows.mref[0], rows.l[0]);
+    __syncthreads();
+    float m = -__builtin_inff();
+    for (int k = 0; k < waves_k; ++k) m = fmaxf(m, s_ml[(k * waves_m + wm) * 16 + lr].x);
+    float l = 0.f;
+    for (int k = 0; k < waves_k; ++k) {
+        const float2 x = s_ml[(k * waves_m + wm) * 16 + lr];
+        l += x.x == m ? x.y : x.y * __builtin_amdgcn_exp2f(x.x - m);
+    }
+    const float f = (rows.mref[0] == m ? 1.f : __builtin_amdgcn_exp2f(rows.mref[0] - m)) * rows.true_exponent();
+#pragma unroll
+    for (int d = 0; d < A::kDTiles; ++d) rows.o[0][d] *= f;
+    rows.mref[0] = m;
+    rows.l[0] = l;
+    for (int half = waves_k / 2; half > 0; half /= 2) {
+        float* at = s_o + (wm * (waves_k / 2) + (wk >= half ? wk - half : wk)) * (A::kDTiles * 256);
+        if (wk >= half && wk < 2 * half) {
+#pragma unroll
+            for (int d = 0; d < A::kDTiles; ++d) *reinterpret_cast<acc4_t*>(at + (d * 64 + lane) * 4) = rows.o[0][d];
+        }
+        __syncthreads();
+        if (wk < half) {
+#pragma unroll
+            for (int d = 0; d < A::kDTiles; ++d)
+                rows.o[0][d] += *reinterpret_cast<const acc4_t*>(at + (d * 64 + lane) * 4);
+        }
+        __syncthreads();
+    }
+    if (wk == 0) rows.write(a, it, lr, lg);
+}
+
+// ---------------------------------------------------------------------------
+// Items of 64 or 128 rows: the four waves share the keys.  Each converts a quarter of a step's codes
+// into LDS, in the order in which lanes read them as operands (piece after piece of 16
+// bytes a lane: no bank is met twice), one step ahead of the products.
+// ---------------------------------------------------------------------------
+template <typename QT, int BITS, int P, int R>
+__device__ __forceinline__ void attn_shared(const AttnArgs& a, const Item& it, unsigned char* lds) {
+    using A = AttnTypes<QT, BITS, P>;
+    constexpr int kMine = (A::kLines + kAttnWaves - 1) / kAttnWaves;  // lines of V that a wave converts
+    constexpr int kKPieces = 4 * A::kSteps, kVPieces = A::kDTiles * 2, kStage = (kKPieces + kVPieces) * 64;
+    static_assert(kAttnWaves == 4, "a wave converts one tile of K");
+    uint4* stage = (uint4*)lds;  // two of kStage pieces
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+    const int lr = lane & 15, lg = lane >> 4;
+    AttnRows<QT, BITS, P, R> rows;
+    rows.init(a, it, it.m0 + wave * 16 * R, lr, lg);
+    int end = 0;  // of the workgroup's rows
+    {
+        const int last = min(it.m0 + it.tile, it.M) - 1;
+        const int most = it.own ? it.hidden + last / a.rep + 1 : it.len;
+        end = min(it.blk1, (most + kAttnKeys - 1) / kAttnKeys);
+    }
+
+    uint32_t kw[A::kPiece / 4], vw[kMine][4], vs_next[A::kGroups][4], vs[A::kGroups][4];
+    uint32_t ks[A::kKGroups];
+    bool ok_next = false, ok = false;
+    const int g0 = BITS == 8 ? 0 : (lg * (P / 4)) >> 5;
+    auto load = [&](int blk) {
+        bool there;
+        const long long bk = attn_place(a, it, blk * 4 + (lr >> 2), there);
+        const int token = wave * 4 + (lr & 3);
+        load_words<A::kPiece>(a.k + (bk * 16 + token) * A::kRow + lg * A::kPiece, kw);
+#pragma unroll
+        for (int g = 0; g < A::kKGroups; ++g)
+            ks[g] = a.k_scales[(bk * A::kGroups + min(g0 + g, A::kGroups - 1)) * 16 + token];
+        const long long bv = attn_place(a, it, blk * 4 + lg, ok_next);
+#pragma unroll
+        for (int i = 0; i < kMine; ++i)
+            if (A::kLines % kAttnWaves == 0 || i * kAttnWaves + wave < A::kLines)
+                load_words<16>(a.v + (bv * A::kRow + (i * kAttnWaves + wave) * 16 + lr) * 16, vw[i]);
+#pragma unroll
+        for (int g = 0; g < A::kGroups; ++g) load_words<16>(a.v_scales + (bv * A::kGroups + g) * 16, vs_next[g]);
+    };
+    auto convert = [&](uint4* to) {
+#pragma unroll
+        for (int x = 0; x < A::kSteps; ++x) {
+            uint32_t b = ks[0];
+            if constexpr (A::kKGroups == 2)
+                if (((lg * (P / 4) + 8 * x) >> 5) != g0) b = ks[1];
+            to[(wave * A::kSteps + x) * 64 + lane] =
+                code_piece<typename A::KT, BITS>(kw + x * (BITS / 4), __uint_as_float(b << 23));
+        }
+#pragma unroll
+        for (int i = 0; i < kMine; ++i) {
+            if (A::kLines % kAttnWaves != 0 && i * kAttnWaves + wave >= A::kLines) continue;
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                uint4 vf[A::kLineTiles];
+                line_operands<BITS>(vw[i], u, vf);
+#pragma unroll
+                for (int y = 0; y < A::kLineTiles; ++y)
+                    to[(kKPieces + ((i * kAttnWaves + wave) * A::kLineTiles + y) * 2 + u) * 64 + lane] = vf[y];
+            }
+        }
+    };
+
+    int blk = it.blk0;
+    if (blk < end) {
+        load(blk);
+        convert(stage);
+#pragma unroll
+        for (int g = 0; g < A::kGroups; ++g)
+#pragma unroll
+            for (int t = 0; t < 4; ++t) vs[g][t] = vs_next[g][t];
+        ok = ok_next;
+        if (blk + 1 < end) load(blk + 1);
+    }
+    for (int n = 0; blk < end; ++blk, n ^= 1) {
+        // The stage of this step is written, and the other one read, by all waves.  Only LDS is waited for.
+        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+        __builtin_amdgcn_s_barrier();
+        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+        const uint4* from = stage + n * kStage + lane;
+        const bool mine = blk < rows.blk_end;
+        if (mine) {
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+#pragma unroll
+                for (int x = 0; x < A::kSteps; ++x) rows.score(t, x, from[(t * A::kSteps + x) * 64]);
+        }
+        const bool more = blk + 1 < end;
+        uint32_t vs_then[A::kGroups][4];
+        const bool ok_then = ok_next;
+        if (more) {
+            convert(stage + (n ^ 1) * kStage);
+#pragma unroll
+            for (int g = 0; g < A::kGroups; ++g)
+#pragma unroll
+                for (int t = 0; t < 4; ++t) vs_then[g][t] = vs_next[g][t];
+            if (blk + 2 < end) load(blk + 2);
+        }
+        if (mine) {
+            const int first = blk * kAttnKeys + lg * 16;
+            const int there = ok ? it.len - first : 0;
+            const bool all = rows.soften(a, first, there);
+            rows.accumulate(vs, all, first, there, [&](int i, int u, uint4* vf) {
+#pragma unroll
+                for (int y = 0; y < A::kLineTiles; ++y) vf[y] = from[(kKPieces + (i * A::kLineTiles + y) * 2 + u) * 64];
+            });
+        }
+#pragma unroll
+        for (int g = 0; g < A::kGroups; ++g)
+#pragma unroll
+            for (int t = 0; t < 4; ++t) vs[g][t] = vs_then[g][t];
+        ok = ok_then;
+    }
+    const float back = rows.true_exponent();
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        rows.l[r] = column_sum(rows.l[r]);
+#pragma unroll
+        for (int d = 0; d < A::kDTiles; ++d) rows.o[r][d] *= back;
+    }
+    rows.write(a, it, lr, lg);
+}
+
+template <typename QT, int BITS, int P, int RMAX>
+__global__ __launch_bounds__(kAttnThreads, P <= 128 ? 2 : 1) void attn_kernel(AttnArgs a) {
+    // attn_direct: sums of half the waves, maxima; attn_shared: two stages.
+    constexpr int kDirect = kAttnWaves / 2 * P / 16 * 1024 + kAttnWaves * 16 * 8, kShared = 2 * P * 64 * 2 * 2;
+    __shared__ __align__(16) unsigned char lds[kDirect > kShared ? kDirect : kShared];
+    if ((int)blockIdx.x >= a.plan[0]) return;
+    const Item it = attn_item(a, a.plan + a.at.items + (long long)blockIdx.x * kItemInts);
+    if (it.tile <= 32) attn_direct<QT, BITS, P>(a, it, lds);
+    else if (RMAX == 1 || it.tile == 64) attn_shared<QT, BITS, P, 1>(a, it, lds);
+    else attn_shared<QT, BITS, P, RMAX>(a, it, lds);
 }
 
 // A row's items into its output: LANES lanes, 4 elements each.

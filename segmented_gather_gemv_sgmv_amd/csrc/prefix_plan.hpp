@@ -19,8 +19,8 @@ namespace sgmv {
 constexpr int kAttnWaves = 4;            // of an item's workgroup
 constexpr int kAttnThreads = 64 * kAttnWaves;
 constexpr int kAttnKeys = 64;            // keys of a wave's step
-constexpr int kAttnTarget = 1024;        // items to aim at
-constexpr int kAttnLeast = 2;            // steps of an item, at least
+constexpr int kAttnTarget = 768;        // items to aim at
+constexpr int kAttnLeast = 4;            // steps of an item, at least
 constexpr int kPlanHeader = 16;          // ints: items, slots, chunk
 constexpr int kStackInts = 8, kItemInts = 8;
 
