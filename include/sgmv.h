@@ -526,8 +526,8 @@ int qk_norm_rope_backward(void* dq, void* dk, void* dq_weight, void* dk_weight, 
  * e is the least exponent with |x| <= M 2^e over its group (M = 448 or 6), held to
  * what the type of the written rows represents exactly (float16: values of
  * 2^-24 to 57344 or 49152; else about 1e-38 to 3e38 or 2.5e38; larger ones saturate);
- * code is x 2^-e rounded to nearest even.  A group that holds a NaN or an
- * infinity reads as NaN.
+ * code is x 2^-e rounded to nearest even.  A token's head that holds a NaN or an
+ * infinity reads as NaN, all of it.
  *
  * The caller owns the four device arrays (16-byte aligned; kv_codes_bytes for k and for v,
  * kv_scales_bytes for each scales array) and zeroes them once before use; their

@@ -161,8 +161,8 @@ __global__ __launch_bounds__(kPlanThreads) void attn_plan_kernel(PlanArgs a) {
             e[0] = i;
             e[1] = head;
             e[2] = mt * k.tile;
-            e[3] = part * chunk;
-            e[4] = min((part + 1) * chunk, k.blocks);
+            e[3] = (int)((long long)k.blocks * part / chunks);  // chunks of a stack alike in length
+            e[4] = (int)((long long)k.blocks * (part + 1) / chunks);
             e[5] = slot0 + j * k.tile;
             e[6] = k.tile;
             e[7] = 0;

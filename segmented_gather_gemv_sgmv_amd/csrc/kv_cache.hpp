@@ -211,11 +211,12 @@ __global__ __launch_bounds__(kKvThreads) void kv_write_kernel(KvArgs a) {
         uint32_t most = 0;  // magnitudes' bits order like the magnitudes; NaN and infinity above all
 #pragma unroll
         for (int k = 0; k < 8; ++k) most = max(most, __float_as_uint(f[k]) & 0x7FFFFFFFu);
-        most = BITS == 8 ? lanes_max<Tile::kLanes>(most) : lanes_max<4>(most);
+        if constexpr (BITS == 4) most = lanes_max<4>(most);
+        const uint32_t head_most = BITS == 4 ? lanes_max<Tile::kLanes>(most) : (most = lanes_max<Tile::kLanes>(most));
         // least e with most <= 1.75 2^8 2^e, or 1.5 2^2 2^e
         constexpr uint32_t kBump = BITS == 8 ? 0x1FFFFF : 0x3FFFFF;
         constexpr float kMost = BITS == 8 ? 448.f : 6.f;
-        const bool finite = most < 0x7F800000u;
+        const bool finite = head_most < 0x7F800000u;  // of all the head
         int e = (int)((most + kBump) >> 23) - 127 - (BITS == 8 ? 8 : 2);
         e = min(max(e, a.lo), a.hi);
         const float scale = __uint_as_float((uint32_t)(e + 127) << 23);

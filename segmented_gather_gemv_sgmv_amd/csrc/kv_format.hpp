@@ -7,8 +7,8 @@
 // converts two codes to two 16-bit operands, scaled, in one instruction.  The exponent is
 // the least one with |x| <= M 2^e over the group (M = 448, 6), held where code and
 // scale stay exact in the cache's type (float16: between 2^-24 and 65504); what lies
-// above the largest exponent's reach saturates.  Scale byte 255 marks a group that held a
-// NaN or an infinity: all of it reads as NaN.
+// above the largest exponent's reach saturates.  Scale byte 255, in all groups of a token's
+// head, marks one that held a NaN or an infinity: all of it reads as NaN.
 //
 // Layout, for attention (prefix_attention.hpp): a head of head_dim elements is padded to
 // P (64, 96, 128, 192 or 256).  Pages are cut into blocks of 16 tokens.

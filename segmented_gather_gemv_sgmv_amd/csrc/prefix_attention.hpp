@@ -20,11 +20,9 @@
 // is transposed, every load is 16 bytes (K: pieces of a token's row).
 //
 // Types: codes of K become operands of q's type, scaled, in one conversion (exact; float32
-// q goes through in three bfloat16 terms, which hold its 24 bits).  V's scale differs by
-// key, so it multiplies p; p 2^e goes into float16 operands (11 bits; two terms, 22 bits, for
-// float16 and float32 outputs), relative to the largest exponent seen, with 2^11 of
-// headroom: what underflows is below 2^-35 of the largest value.  Sums, maxima and outputs
-// are float32.
+// q goes through in three bfloat16 terms, which hold its 24 bits).  V's scale differs by key; how
+// it and p enter the second product is told at the two kinds of items.  Sums, maxima and outputs are
+// float32.
 #pragma once
 
 #include <type_traits>
@@ -121,19 +119,38 @@ __device__ __forceinline__ float column_sum(float v) {
     s = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
     return __uint_as_float(s[0]) + __uint_as_float(s[1]);
 }
+// Largest over a wave: quads swapped, halves of 8 and 16 mirrored, rows swapped.
+__device__ __forceinline__ int wave_max(int v) {
+    v = max(v, __builtin_amdgcn_update_dpp(0, v, 0xB1, 0xf, 0xf, true));
+    v = max(v, __builtin_amdgcn_update_dpp(0, v, 0x4E, 0xf, 0xf, true));
+    v = max(v, __builtin_amdgcn_update_dpp(0, v, 0x141, 0xf, 0xf, true));
+    v = max(v, __builtin_amdgcn_update_dpp(0, v, 0x140, 0xf, 0xf, true));
+    auto s = __builtin_amdgcn_permlane16_swap((unsigned)v, (unsigned)v, false, false);
+    v = max((int)s[0], (int)s[1]);
+    s = __builtin_amdgcn_permlane32_swap((unsigned)v, (unsigned)v, false, false);
+    return __builtin_amdgcn_readfirstlane(max((int)s[0], (int)s[1]));
+}
 
-// Two floats to float16, nearest-even, in one instruction.
-__device__ __forceinline__ uint32_t pack_f16(float a, float b) {
+// Scale byte `i` of a word as the exponent of a float; sign and mantissa hold other bytes' bits,
+// which the conversions of codes do not look at.
+__device__ __forceinline__ float scale_operand(uint32_t w, int i) {
+    return __uint_as_float(__builtin_amdgcn_alignbit(w, w, 9 + 8 * i));
+}
+
+// Two floats to two operands, nearest-even, in one instruction.
+template <typename OT>
+__device__ __forceinline__ uint32_t pack_operands(float a, float b) {
     typedef float f2_t __attribute__((ext_vector_type(2)));
     typedef _Float16 h2_t __attribute__((ext_vector_type(2)));
-    return bits2(__builtin_convertvector((f2_t){a, b}, h2_t));
+    if constexpr (std::is_same<OT, F16>::value) return bits2(__builtin_convertvector((f2_t){a, b}, h2_t));
+    else return pack2_rne<BF16>(a, b);
 }
 
 // ---------------------------------------------------------------------------
-// The rows of a wave: R tiles of 16 rows, one row a lane column.
+// The rows of a wave: R tiles of 16 rows, one row a lane column.  VT: the operands of the second product
+// (see the two kinds of items below).
 // ---------------------------------------------------------------------------
-constexpr float kAttnSlack = 4.f;   // p may reach 2^4 before the maximum is moved
-constexpr int kAttnHeadroom = 11;   // 2^(4 + 11) stays below float16's largest value
+constexpr float kAttnSlack = 4.f;  // p may reach 2^4 before the maximum is moved
 
 template <typename QT, int BITS, int P>
 struct AttnTypes {
@@ -146,7 +163,6 @@ struct AttnTypes {
     static constexpr int kGroups = BITS == 8 ? 1 : P / 32;
     static constexpr int kKGroups = BITS == 8 || P == 64 || P == 128 ? 1 : 2;  // that a lane's piece of K meets
     static constexpr int kQTerms = QT::kBytes == 4 ? 3 : 1;
-    static constexpr int kPTerms = std::is_same<QT, BF16>::value ? 1 : 2;
     using KT = std::conditional_t<std::is_same<QT, F16>::value, F16, BF16>;  // operands of S
 };
 
@@ -189,15 +205,15 @@ __device__ __forceinline__ long long attn_place(const AttnArgs& a, const Item& i
     return ((long long)(ok ? page : 0) * a.kv_heads + it.head) * a.blocks_per_page + in;
 }
 
-template <typename QT, int BITS, int P, int R>
-struct AttnRows : AttnTypes<QT, BITS, P> {
+// HEAD: p is held times 2^HEAD.  TERMS: operands that p is split into, one after the other.
+template <typename QT, int BITS, int P, int R, typename VT, int TERMS, int HEAD>
+struct AttnRows {
     using A = AttnTypes<QT, BITS, P>;
     using KT = typename A::KT;
     uint4 qf[R][A::kQTerms][A::kSteps];
     acc4_t o[R][A::kDTiles], s[R][4];
     float mref[R], l[R];
     int lim[R];   // keys that the lane's row sees
-    int eref;     // biased exponent that p 2^e is relative to
     int m_first;  // first row of the wave
     int blk_end;  // blocks that any of its rows sees
 
@@ -207,7 +223,6 @@ struct AttnRows : AttnTypes<QT, BITS, P> {
         const int last = min(first + 16 * R, it.M) - 1;
         const int most = last < first ? 0 : it.own ? it.hidden + last / a.rep + 1 : it.len;
         blk_end = min(it.blk1, (most + kAttnKeys - 1) / kAttnKeys);
-        eref = 20;
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             const int m = first + 16 * r + lr;
@@ -261,17 +276,23 @@ struct AttnRows : AttnTypes<QT, BITS, P> {
                 s[r][t] = PieceOps<KT>::mma(kf, qf[r][y][x], x == 0 && y == 0 ? acc4_t{0.f, 0.f, 0.f, 0.f} : s[r][t]);
     }
 
-    // Scores of keys [first, first + 16) of the lane to p, running maxima and sums; `there`: how many
-    // of these keys the cache holds.  Returns whether every row sees all of them.
-    __device__ __forceinline__ bool soften(const AttnArgs& a, int first, int there) {
+    // Of the lane's 16 keys from `first` on, `there` are in the cache: whether every row of the wave
+    // sees all of its 16.
+    __device__ __forceinline__ bool all_seen(int first, int there) const {
         bool whole = there >= 16;
 #pragma unroll
         for (int r = 0; r < R; ++r) whole = whole && lim[r] - first >= 16;
-        const bool all = __all(whole);
-        if (!all) {
+        return __all(whole);
+    }
+    __device__ __forceinline__ int seen(int r, int first, int there) const { return min(lim[r] - first, there); }
+
+    // Scores to p; running maxima and sums.
+    template <bool ALL>
+    __device__ __forceinline__ void soften(float c, int first, int there) {
+        if constexpr (!ALL) {
 #pragma unroll
             for (int r = 0; r < R; ++r) {
-                const int rem = min(lim[r] - first, there);
+                const int rem = seen(r, first, there);
 #pragma unroll
                 for (int t = 0; t < 16; ++t)
                     if (t >= rem) s[r][t / 4][t % 4] = -__builtin_inff();
@@ -285,7 +306,7 @@ struct AttnRows : AttnTypes<QT, BITS, P> {
             float v = s[r][0][0];
 #pragma unroll
             for (int t = 1; t < 16; ++t) v = fmaxf(v, s[r][t / 4][t % 4]);
-            mx[r] = column_max(v) * a.c;
+            mx[r] = column_max(v) * c;
             move = move || mx[r] > mref[r] + kAttnSlack;
         }
         if (__any(move)) {
@@ -301,128 +322,37 @@ struct AttnRows : AttnTypes<QT, BITS, P> {
         }
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-            const float m = mref[r] == -__builtin_inff() ? 0.f : mref[r];
+            const float m = (mref[r] == -__builtin_inff() ? 0.f : mref[r]) - HEAD;
 #pragma unroll
             for (int t = 0; t < 16; ++t) {
-                const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(s[r][t / 4][t % 4], a.c, -m));
+                const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(s[r][t / 4][t % 4], c, -m));
                 s[r][t / 4][t % 4] = p;
                 l[r] += p;
             }
         }
-        return all;
     }
 
-    // The largest scale of the block's tokens (of those that are there) becomes the reference
-    // exponent if it is larger; a NaN's is left out.
-    __device__ __forceinline__ void raise(uint32_t (*vs)[4], bool all, int there) {
-        typedef unsigned short u16x2_t __attribute__((ext_vector_type(2)));
-        if (!all) {
+    // w [8] as operands, each part what the parts before left.
+    static __device__ __forceinline__ void split(float* w, uint4* pf) {
 #pragma unroll
-            for (int t = 0; t < 4; ++t) {
-                const int n = min(max(there - 4 * t, 0), 4);
-                const uint32_t mask = n == 4 ? ~0u : (1u << (8 * n)) - 1u;
+        for (int x = 0; x < TERMS; ++x) {
+            pf[x] = make_uint4(pack_operands<VT>(w[0], w[1]), pack_operands<VT>(w[2], w[3]),
+                               pack_operands<VT>(w[4], w[5]), pack_operands<VT>(w[6], w[7]));
+            if (x + 1 < TERMS) {
+                float h[8];
+                VT::unpack(pf[x], h);
 #pragma unroll
-                for (int g = 0; g < A::kGroups; ++g) vs[g][t] &= mask;
-            }
-        }
-        u16x2_t even = {0, 0}, odd = {0, 0};
-#pragma unroll
-        for (int g = 0; g < A::kGroups; ++g)
-#pragma unroll
-            for (int t = 0; t < 4; ++t) {
-                even = __builtin_elementwise_max(even, __builtin_bit_cast(u16x2_t, vs[g][t] & 0x00FF00FFu));
-                odd = __builtin_elementwise_max(odd, __builtin_bit_cast(u16x2_t, (vs[g][t] >> 8) & 0x00FF00FFu));
-            }
-        even = __builtin_elementwise_max(even, odd);
-        int top = largest_of_column(max((int)even.x, (int)even.y));
-        if (__builtin_expect(top == kKvNaN, 0)) {
-            int t2 = 0;
-            for (int g = 0; g < A::kGroups; ++g)
-                for (int t = 0; t < 4; ++t)
-                    for (int y = 0; y < 4; ++y) {
-                        const int b = (int)((vs[g][t] >> (8 * y)) & 255u);
-                        if (b != kKvNaN) t2 = max(t2, b);
-                    }
-            top = largest_of_column(t2);
-        }
-        if (top > eref) {
-            const float f = __builtin_ldexpf(1.f, max(eref - top, -126));
-#pragma unroll
-            for (int r = 0; r < R; ++r)
-#pragma unroll
-                for (int t = 0; t < A::kDTiles; ++t) o[r][t] *= f;
-            eref = top;
-        }
-    }
-    // Uniform over the wave (lanes of a group of 16 hold the same).
-    static __device__ __forceinline__ int largest_of_column(int v) {
-        auto x = __builtin_amdgcn_permlane16_swap((unsigned)v, (unsigned)v, false, false);
-        v = max((int)x[0], (int)x[1]);
-        x = __builtin_amdgcn_permlane32_swap((unsigned)v, (unsigned)v, false, false);
-        return __builtin_amdgcn_readfirstlane(max((int)x[0], (int)x[1]));
-    }
-
-    // O^T += V^T (p 2^e)^T; vline(i, u, out) gives the operands of line i, half u of its tokens.
-    template <typename Line>
-    __device__ __forceinline__ void accumulate(uint32_t (*vs)[4], bool all, int first, int there, Line vline) {
-        raise(vs, all, there);
-        // with a scale 2^(b - 127), p is multiplied by 2^(b - eref + headroom)
-        const float unit = __builtin_ldexpf(1.f, kAttnHeadroom + 127 - eref);
-#pragma unroll
-        for (int g = 0; g < A::kGroups; ++g) {
-            float f[16];
-#pragma unroll
-            for (int t = 0; t < 4; ++t) {
-                f[4 * t] = __uint_as_float((vs[g][t] << 23) & 0x7F800000u) * unit;
-                f[4 * t + 1] = __uint_as_float((vs[g][t] << 15) & 0x7F800000u) * unit;
-                f[4 * t + 2] = __uint_as_float((vs[g][t] << 7) & 0x7F800000u) * unit;
-                f[4 * t + 3] = __uint_as_float((vs[g][t] >> 1) & 0x7F800000u) * unit;
-            }
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                uint4 pf[R][A::kPTerms];
-#pragma unroll
-                for (int r = 0; r < R; ++r) {
-                    float w[8];
-#pragma unroll
-                    for (int x = 0; x < 8; ++x) w[x] = s[r][2 * u + x / 4][x % 4] * f[8 * u + x];
-                    if (!all) {  // what lies behind a row's last key may be NaN
-                        const int rem = min(lim[r] - first, there) - 8 * u;
-#pragma unroll
-                        for (int x = 0; x < 8; ++x)
-                            if (x >= rem) w[x] = 0.f;
-                    }
-#pragma unroll
-                    for (int x = 0; x < A::kPTerms; ++x) {
-                        pf[r][x] = make_uint4(pack_f16(w[0], w[1]), pack_f16(w[2], w[3]), pack_f16(w[4], w[5]),
-                                              pack_f16(w[6], w[7]));
-                        if (x + 1 < A::kPTerms) {
-                            float h[8];
-                            F16::unpack(pf[r][x], h);
-#pragma unroll
-                            for (int y = 0; y < 8; ++y) w[y] -= h[y];
-                        }
-                    }
-                }
-#pragma unroll
-                for (int i = BITS == 8 ? 0 : g; i < (BITS == 8 ? A::kLines : g + 1); ++i) {
-                    uint4 vf[A::kLineTiles];
-                    vline(i, u, vf);
-#pragma unroll
-                    for (int y = 0; y < A::kLineTiles; ++y)
-#pragma unroll
-                        for (int r = 0; r < R; ++r)
-#pragma unroll
-                            for (int x = 0; x < A::kPTerms; ++x) {
-                                acc4_t& c = o[r][i * A::kLineTiles + y];
-                                c = PieceOps<F16>::mma(vf[y], pf[r][x], c);
-                            }
-                }
+                for (int y = 0; y < 8; ++y) w[y] -= h[y];
             }
         }
     }
 
-    // The wave's rows to their slots: O scaled to its true exponent by `f`, maxima and sums.
+    __device__ __forceinline__ void product(int tile, int r, const uint4& vf, const uint4* pf) {
+#pragma unroll
+        for (int x = 0; x < TERMS; ++x) o[r][tile] = PieceOps<VT>::mma(vf, pf[x], o[r][tile]);
+    }
+
+    // The wave's rows to their slots.
     __device__ __forceinline__ void write(const AttnArgs& a, const Item& it, int lr, int lg) const {
 #pragma unroll
         for (int r = 0; r < R; ++r) {
@@ -435,47 +365,45 @@ struct AttnRows : AttnTypes<QT, BITS, P> {
             if (lg == 0) a.part_ml[slot] = make_float2(mref[r], l[r]);
         }
     }
-    __device__ __forceinline__ float true_exponent() const {
-        return __builtin_ldexpf(1.f, eref - 127 - kAttnHeadroom);
-    }
 };
 
-// Operands of a line of V from its codes: half u of its 16 tokens.
-template <int BITS>
-__device__ __forceinline__ void line_operands(const uint32_t* w, int u, uint4* vf) {
-    if constexpr (BITS == 8) {
-        vf[0] = code_piece<F16, 8>(w + 2 * u, 1.f);
-    } else {
-        // A byte holds a token's codes of two tiles: low halves the first's.
-        uint32_t c[8];
+// 4-bit codes of a line, two words (8 tokens): a byte holds a token's codes of two tiles.  Converted with the
+// tokens' scales, then sorted by tile.
+template <typename VT>
+__device__ __forceinline__ void line_operands4(const uint32_t* w, const float* scale, uint4* vf) {
+    uint32_t c[8];
 #pragma unroll
-        for (int y = 0; y < 2; ++y) {
-            c[4 * y] = code_pair<F16, 4, 0>(w[2 * u + y], 1.f);
-            c[4 * y + 1] = code_pair<F16, 4, 1>(w[2 * u + y], 1.f);
-            c[4 * y + 2] = code_pair<F16, 4, 2>(w[2 * u + y], 1.f);
-            c[4 * y + 3] = code_pair<F16, 4, 3>(w[2 * u + y], 1.f);
-        }
+    for (int y = 0; y < 2; ++y) {
+        c[4 * y] = code_pair<VT, 4, 0>(w[y], scale[4 * y]);
+        c[4 * y + 1] = code_pair<VT, 4, 1>(w[y], scale[4 * y + 1]);
+        c[4 * y + 2] = code_pair<VT, 4, 2>(w[y], scale[4 * y + 2]);
+        c[4 * y + 3] = code_pair<VT, 4, 3>(w[y], scale[4 * y + 3]);
+    }
 #pragma unroll
-        for (int y = 0; y < 2; ++y) {
-            const uint32_t sel = y ? 0x07060302u : 0x05040100u;
-            vf[y] = make_uint4(__builtin_amdgcn_perm(c[1], c[0], sel), __builtin_amdgcn_perm(c[3], c[2], sel),
-                               __builtin_amdgcn_perm(c[5], c[4], sel), __builtin_amdgcn_perm(c[7], c[6], sel));
-        }
+    for (int y = 0; y < 2; ++y) {
+        const uint32_t sel = y ? 0x07060302u : 0x05040100u;
+        vf[y] = make_uint4(__builtin_amdgcn_perm(c[1], c[0], sel), __builtin_amdgcn_perm(c[3], c[2], sel),
+                           __builtin_amdgcn_perm(c[5], c[4], sel), __builtin_amdgcn_perm(c[7], c[6], sel));
     }
 }
 
 // ---------------------------------------------------------------------------
 // Items of up to 32 rows: codes go from memory to operand registers, every wave has keys of its own
 // (of 32 rows two waves share them), and the waves' results are joined through LDS.
+//
+// Operands of the second product are bfloat16, whose range takes every scale as it is: 8-bit codes enter
+// as they are and p times the key's scale, in two terms (16 bits; float32 outputs: three); 4-bit
+// codes enter with their scale, p alone.
 // ---------------------------------------------------------------------------
 template <typename QT, int BITS, int P>
 __device__ __forceinline__ void attn_direct(const AttnArgs& a, const Item& it, unsigned char* lds) {
     using A = AttnTypes<QT, BITS, P>;
+    constexpr int kTerms = QT::kBytes == 4 ? 3 : 2;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
     const int lr = lane & 15, lg = lane >> 4;
     const int waves_m = it.tile / 16, waves_k = kAttnWaves / waves_m;
     const int wm = wave % waves_m, wk = wave / waves_m;
-    AttnRows<QT, BITS, P, 1> rows;
+    AttnRows<QT, BITS, P, 1, BF16, kTerms, 0> rows;
     rows.init(a, it, it.m0 + wm * 16, lr, lg);
 
     uint32_t kw[4][A::kPiece / 4], ks[A::kKGroups][4], vw[A::kLines][4], vs[A::kGroups][4];
@@ -499,6 +427,67 @@ __device__ __forceinline__ void attn_direct(const AttnArgs& a, const Item& it, u
 #pragma unroll
         for (int g = 0; g < A::kGroups; ++g) load_words<16>(a.v_scales + (b * A::kGroups + g) * 16, vs[g]);
     };
+    auto finish = [&](auto all, int first, int there) {
+        constexpr bool ALL = decltype(all)::value;
+        rows.template soften<ALL>(a.c, first, there);
+        const int rem = rows.seen(0, first, there);
+        bool poison = false;  // 4-bit: a row sees a NaN
+        if constexpr (BITS == 4 && !ALL) {
+            // Scales of tokens that are not there may be anything, and a NaN's must not meet rows that do
+            // not see it: both become 0, and the rows that do see it are made NaN.
+#pragma unroll
+            for (int t = 0; t < 16; ++t) {
+                const uint32_t bits = 255u << (8 * (t % 4));
+                const bool nan = (vs[0][t / 4] & bits) == bits && t < there;
+                poison = poison || (nan && t < rem);
+#pragma unroll
+                for (int g = 0; g < A::kGroups; ++g)
+                    if (nan || t >= there) vs[g][t / 4] &= ~bits;
+            }
+        }
+        if constexpr (BITS == 8) {
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                float w[8];
+#pragma unroll
+                for (int x = 0; x < 8; ++x) {
+                    const int t = 8 * u + x;
+                    w[x] = rows.s[0][t / 4][t % 4] * __uint_as_float(((vs[0][t / 4] >> (8 * (t % 4))) & 255u) << 23);
+                    if (!ALL && t >= rem) w[x] = 0.f;  // what lies there may be NaN
+                }
+                uint4 pf[kTerms];
+                rows.split(w, pf);
+#pragma unroll
+                for (int i = 0; i < A::kLines; ++i) rows.product(i, 0, code_piece<BF16, 8>(vw[i] + 2 * u, 1.f), pf);
+            }
+        } else {
+            uint4 pf[2][kTerms];
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                float w[8];
+#pragma unroll
+                for (int x = 0; x < 8; ++x) w[x] = rows.s[0][2 * u + x / 4][x % 4];
+                rows.split(w, pf[u]);
+            }
+#pragma unroll
+            for (int g = 0; g < A::kGroups; ++g)
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    float scale[8];
+#pragma unroll
+                    for (int x = 0; x < 8; ++x) scale[x] = scale_operand(vs[g][2 * u + x / 4], x % 4);
+                    uint4 vf[2];
+                    line_operands4<BF16>(vw[g] + 2 * u, scale, vf);
+                    rows.product(2 * g, 0, vf[0], pf[u]);
+                    rows.product(2 * g + 1, 0, vf[1], pf[u]);
+                }
+            if (!ALL && __any(poison)) {
+                const float nan = column_max(poison ? 1.f : 0.f) > 0.f ? __builtin_nanf("") : 0.f;
+#pragma unroll
+                for (int d = 0; d < A::kDTiles; ++d) rows.o[0][d] += nan;
+            }
+        }
+    };
 
     int blk = it.blk0 + wk;
     const int end = rows.blk_end;
@@ -511,8 +500,7 @@ __device__ __forceinline__ void attn_direct(const AttnArgs& a, const Item& it, u
         for (int t = 0; t < 4; ++t) {
             float sc[A::kKGroups];
 #pragma unroll
-            for (int g = 0; g < A::kKGroups; ++g)
-                sc[g] = __uint_as_float(((ks[g][t] >> (8 * (lr & 3))) & 255u) << 23);
+            for (int g = 0; g < A::kKGroups; ++g) sc[g] = scale_operand(ks[g][t], lr & 3);
 #pragma unroll
             for (int x = 0; x < A::kSteps; ++x) {
                 float scale = sc[0];
@@ -525,9 +513,8 @@ __device__ __forceinline__ void attn_direct(const AttnArgs& a, const Item& it, u
         if (more) load_k(blk + waves_k);  // behind the rest of this step
         const int first = blk * kAttnKeys + lg * 16;
         const int there = v_ok ? it.len - first : 0;
-        const bool all = rows.soften(a, first, there);
-        rows.accumulate(vs, all, first, there,
-                        [&](int i, int u, uint4* vf) { line_operands<BITS>(vw[i], u, vf); });
+        if (rows.all_seen(first, there)) finish(std::true_type{}, first, there);
+        else finish(std::false_type{}, first, there);
         if (more) load_v(blk + waves_k);
     }
 
@@ -544,7 +531,7 @@ __device__ __forceinline__ void attn_direct(const AttnArgs& a, const Item& it, u
         const float2 x = s_ml[(k * waves_m + wm) * 16 + lr];
         l += x.x == m ? x.y : x.y * __builtin_amdgcn_exp2f(x.x - m);
     }
-    const float f = (rows.mref[0] == m ? 1.f : __builtin_amdgcn_exp2f(rows.mref[0] - m)) * rows.true_exponent();
+    const float f = rows.mref[0] == m ? 1.f : __builtin_amdgcn_exp2f(rows.mref[0] - m);
 #pragma unroll
     for (int d = 0; d < A::kDTiles; ++d) rows.o[0][d] *= f;
     rows.mref[0] = m;
@@ -570,17 +557,26 @@ __device__ __forceinline__ void attn_direct(const AttnArgs& a, const Item& it, u
 // Items of 64 or 128 rows: the four waves share the keys.  Each converts a quarter of a step's codes
 // into LDS, in the order in which lanes read them as operands (piece after piece of 16
 // bytes a lane: no bank is met twice), one step ahead of the products.
+//
+// Operands of the second product are float16: p in one term (11 bits) for bfloat16 outputs, in two (22) for the
+// others, and V scaled relative to the largest exponent that the item has met, which all waves follow alike;
+// a value below 2^-32 of the largest is lost.  When a larger exponent comes, O is scaled down.
 // ---------------------------------------------------------------------------
+constexpr int kAttnHead = 11;  // p 2^11 reaches 2^15 at most
+
 template <typename QT, int BITS, int P, int R>
 __device__ __forceinline__ void attn_shared(const AttnArgs& a, const Item& it, unsigned char* lds) {
     using A = AttnTypes<QT, BITS, P>;
+    constexpr int kTerms = std::is_same<QT, BF16>::value ? 1 : 2;
     constexpr int kMine = (A::kLines + kAttnWaves - 1) / kAttnWaves;  // lines of V that a wave converts
     constexpr int kKPieces = 4 * A::kSteps, kVPieces = A::kDTiles * 2, kStage = (kKPieces + kVPieces) * 64;
+    constexpr int kUp = BITS == 8 ? 7 : 13;  // largest code 2^kUp stays below 65504
     static_assert(kAttnWaves == 4, "a wave converts one tile of K");
     uint4* stage = (uint4*)lds;  // two of kStage pieces
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+    uint32_t* factors = (uint32_t*)(stage + 2 * kStage) + wave * 64;  // the wave's own
     const int lr = lane & 15, lg = lane >> 4;
-    AttnRows<QT, BITS, P, R> rows;
+    AttnRows<QT, BITS, P, R, F16, kTerms, kAttnHead> rows;
     rows.init(a, it, it.m0 + wave * 16 * R, lr, lg);
     int end = 0;  // of the workgroup's rows
     {
@@ -589,9 +585,9 @@ __device__ __forceinline__ void attn_shared(const AttnArgs& a, const Item& it, u
         end = min(it.blk1, (most + kAttnKeys - 1) / kAttnKeys);
     }
 
-    uint32_t kw[A::kPiece / 4], vw[kMine][4], vs_next[A::kGroups][4], vs[A::kGroups][4];
-    uint32_t ks[A::kKGroups];
-    bool ok_next = false, ok = false;
+    // Codes of the next step; vb: its scale bytes of V, one token a lane.
+    uint32_t kw[A::kPiece / 4], vw[kMine][4], ks[A::kKGroups], vb[A::kGroups];
+    bool ok = false;
     const int g0 = BITS == 8 ? 0 : (lg * (P / 4)) >> 5;
     auto load = [&](int blk) {
         bool there;
@@ -601,15 +597,28 @@ __device__ __forceinline__ void attn_shared(const AttnArgs& a, const Item& it, u
 #pragma unroll
         for (int g = 0; g < A::kKGroups; ++g)
             ks[g] = a.k_scales[(bk * A::kGroups + min(g0 + g, A::kGroups - 1)) * 16 + token];
-        const long long bv = attn_place(a, it, blk * 4 + lg, ok_next);
+        const long long bv = attn_place(a, it, blk * 4 + lg, ok);
 #pragma unroll
         for (int i = 0; i < kMine; ++i)
             if (A::kLines % kAttnWaves == 0 || i * kAttnWaves + wave < A::kLines)
                 load_words<16>(a.v + (bv * A::kRow + (i * kAttnWaves + wave) * 16 + lr) * 16, vw[i]);
 #pragma unroll
-        for (int g = 0; g < A::kGroups; ++g) load_words<16>(a.v_scales + (bv * A::kGroups + g) * 16, vs_next[g]);
+        for (int g = 0; g < A::kGroups; ++g) vb[g] = a.v_scales[(bv * A::kGroups + g) * 16 + lr];
     };
-    auto convert = [&](uint4* to) {
+    // Exponents of the converted steps (biased), whether one of their tokens is a NaN, and whether the
+    // lane's block of 16 tokens is there.
+    int eref = 20, eref_next = 20;
+    bool nan = false, nan_next = false, ok_now = false;
+    auto convert = [&](int blk, uint4* to) {
+        const bool there = ok && blk * kAttnKeys + lane < it.len;
+        nan_next = __any(there && vb[0] == kKvNaN);
+        int top = 0;
+#pragma unroll
+        for (int g = 0; g < A::kGroups; ++g) {
+            if (!there || vb[g] == kKvNaN) vb[g] = 0;
+            top = max(top, (int)vb[g]);
+        }
+        eref_next = max(eref_next, wave_max(top));
 #pragma unroll
         for (int x = 0; x < A::kSteps; ++x) {
             uint32_t b = ks[0];
@@ -620,14 +629,73 @@ __device__ __forceinline__ void attn_shared(const AttnArgs& a, const Item& it, u
         }
 #pragma unroll
         for (int i = 0; i < kMine; ++i) {
-            if (A::kLines % kAttnWaves != 0 && i * kAttnWaves + wave >= A::kLines) continue;
+            const int line = i * kAttnWaves + wave;
+            if (A::kLines % kAttnWaves != 0 && line >= A::kLines) continue;
+            // The tokens' factors 2^(b - eref + kUp), through the wave's own LDS from lane = token to all lanes of
+            // their block.
+            uint32_t b = vb[0];
+            if constexpr (BITS == 4) {
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                uint4 vf[A::kLineTiles];
-                line_operands<BITS>(vw[i], u, vf);
+                for (int g = 1; g < A::kGroups; ++g) b = g == line ? vb[g] : b;
+            }
+            const uint32_t bits = (uint32_t)max((int)b - eref_next + 127 + kUp, 0) << 23;
+            if constexpr (BITS == 8) {
+                if (i == 0) ((uint16_t*)factors)[lane] = F16::from_float(__uint_as_float(bits));
+            } else {
+                factors[lane] = bits;
+            }
+            __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
+            if constexpr (BITS == 8) {
+                typedef _Float16 h2_t __attribute__((ext_vector_type(2)));
 #pragma unroll
-                for (int y = 0; y < A::kLineTiles; ++y)
-                    to[(kKPieces + ((i * kAttnWaves + wave) * A::kLineTiles + y) * 2 + u) * 64 + lane] = vf[y];
+                for (int u = 0; u < 2; ++u) {
+                    const uint4 f = ((const uint4*)factors)[lg * 2 + u];
+                    const uint4 c = code_piece<F16, 8>(vw[i] + 2 * u, 1.f);
+                    auto times = [](uint32_t x, uint32_t y) {
+                        return bits2(__builtin_bit_cast(h2_t, x) * __builtin_bit_cast(h2_t, y));
+                    };
+                    to[(kKPieces + line * 2 + u) * 64 + lane] =
+                        make_uint4(times(c.x, f.x), times(c.y, f.y), times(c.z, f.z), times(c.w, f.w));
+                }
+            } else {
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    float scale[8];
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        const uint4 f = ((const uint4*)factors)[lg * 4 + u * 2 + x];
+                        scale[4 * x] = __uint_as_float(f.x);
+                        scale[4 * x + 1] = __uint_as_float(f.y);
+                        scale[4 * x + 2] = __uint_as_float(f.z);
+                        scale[4 * x + 3] = __uint_as_float(f.w);
+                    }
+                    uint4 vf[2];
+                    line_operands4<F16>(vw[i] + 2 * u, scale, vf);
+#pragma unroll
+                    for (int y = 0; y < 2; ++y) to[(kKPieces + (line * 2 + y) * 2 + u) * 64 + lane] = vf[y];
+                }
+            }
+            __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront", "local");
+        }
+    };
+    auto finish = [&](auto all, int blk, const uint4* from, int first, int there) {
+        constexpr bool ALL = decltype(all)::value;
+        rows.template soften<ALL>(a.c, first, there);
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            uint4 pf[R][kTerms];
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                float w[8];
+#pragma unroll
+                for (int x = 0; x < 8; ++x) w[x] = rows.s[r][2 * u + x / 4][x % 4];
+                rows.split(w, pf[r]);
+            }
+#pragma unroll
+            for (int t = 0; t < A::kDTiles; ++t) {
+                const uint4 vf = from[(kKPieces + t * 2 + u) * 64];
+#pragma unroll
+                for (int r = 0; r < R; ++r) rows.product(t, r, vf, pf[r]);
             }
         }
     };
@@ -635,12 +703,9 @@ __device__ __forceinline__ void attn_shared(const AttnArgs& a, const Item& it, u
     int blk = it.blk0;
     if (blk < end) {
         load(blk);
-        convert(stage);
-#pragma unroll
-        for (int g = 0; g < A::kGroups; ++g)
-#pragma unroll
-            for (int t = 0; t < 4; ++t) vs[g][t] = vs_next[g][t];
-        ok = ok_next;
+        convert(blk, stage);
+        ok_now = ok;
+        nan = nan_next;
         if (blk + 1 < end) load(blk + 1);
     }
     for (int n = 0; blk < end; ++blk, n ^= 1) {
@@ -656,36 +721,50 @@ __device__ __forceinline__ void attn_shared(const AttnArgs& a, const Item& it, u
 #pragma unroll
                 for (int x = 0; x < A::kSteps; ++x) rows.score(t, x, from[(t * A::kSteps + x) * 64]);
         }
-        const bool more = blk + 1 < end;
-        uint32_t vs_then[A::kGroups][4];
-        const bool ok_then = ok_next;
-        if (more) {
-            convert(stage + (n ^ 1) * kStage);
+        if (eref_next > eref) {  // this step's values are relative to a larger exponent
+            const float f = __builtin_ldexpf(1.f, max(eref - eref_next, -126));
 #pragma unroll
-            for (int g = 0; g < A::kGroups; ++g)
+            for (int r = 0; r < R; ++r)
 #pragma unroll
-                for (int t = 0; t < 4; ++t) vs_then[g][t] = vs_next[g][t];
+                for (int t = 0; t < A::kDTiles; ++t) rows.o[r][t] *= f;
+            eref = eref_next;
+        }
+        const bool ok_then = ok;
+        if (blk + 1 < end) {
+            convert(blk + 1, stage + (n ^ 1) * kStage);
             if (blk + 2 < end) load(blk + 2);
         }
         if (mine) {
             const int first = blk * kAttnKeys + lg * 16;
-            const int there = ok ? it.len - first : 0;
-            const bool all = rows.soften(a, first, there);
-            rows.accumulate(vs, all, first, there, [&](int i, int u, uint4* vf) {
+            const int there = ok_now ? it.len - first : 0;
+            if (rows.all_seen(first, there)) finish(std::true_type{}, blk, from, first, there);
+            else finish(std::false_type{}, blk, from, first, there);
+            if (__builtin_expect(nan, 0)) {
+                // A NaN's values went in as zeros: rows that see it are made NaN.
+                bool here;
+                const long long b = attn_place(a, it, blk * 4 + lg, here);
+                uint32_t w[4];
+                load_words<16>(a.v_scales + b * A::kGroups * 16, w);
 #pragma unroll
-                for (int y = 0; y < A::kLineTiles; ++y) vf[y] = from[(kKPieces + (i * A::kLineTiles + y) * 2 + u) * 64];
-            });
+                for (int r = 0; r < R; ++r) {
+                    const int rem = rows.seen(r, first, there);
+                    float bad = 0.f;
+#pragma unroll
+                    for (int t = 0; t < 16; ++t)
+                        if (t < rem && ((w[t / 4] >> (8 * (t % 4))) & 255u) == kKvNaN) bad = 1.f;
+                    const float v = column_max(bad) > 0.f ? __builtin_nanf("") : 0.f;
+#pragma unroll
+                    for (int t = 0; t < A::kDTiles; ++t) rows.o[r][t] += v;
+                }
+            }
         }
-#pragma unroll
-        for (int g = 0; g < A::kGroups; ++g)
-#pragma unroll
-            for (int t = 0; t < 4; ++t) vs[g][t] = vs_then[g][t];
-        ok = ok_then;
+        ok_now = ok_then;
+        nan = nan_next;
     }
-    const float back = rows.true_exponent();
+    const float back = __builtin_ldexpf(1.f, eref - 127 - kUp - kAttnHead);
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-        rows.l[r] = column_sum(rows.l[r]);
+        rows.l[r] = column_sum(rows.l[r]) * (1.f / (1 << kAttnHead));
 #pragma unroll
         for (int d = 0; d < A::kDTiles; ++d) rows.o[r][d] *= back;
     }
@@ -694,8 +773,9 @@ __device__ __forceinline__ void attn_shared(const AttnArgs& a, const Item& it, u
 
 template <typename QT, int BITS, int P, int RMAX>
 __global__ __launch_bounds__(kAttnThreads, P <= 128 ? 2 : 1) void attn_kernel(AttnArgs a) {
-    // attn_direct: sums of half the waves, maxima; attn_shared: two stages.
-    constexpr int kDirect = kAttnWaves / 2 * P / 16 * 1024 + kAttnWaves * 16 * 8, kShared = 2 * P * 64 * 2 * 2;
+    // attn_direct: sums of half the waves, maxima; attn_shared: two stages, factors.
+    constexpr int kDirect = kAttnWaves / 2 * P / 16 * 1024 + kAttnWaves * 16 * 8;
+    constexpr int kShared = 2 * P * 64 * 2 * 2 + kAttnWaves * 64 * 4;
     __shared__ __align__(16) unsigned char lds[kDirect > kShared ? kDirect : kShared];
     if ((int)blockIdx.x >= a.plan[0]) return;
     const Item it = attn_item(a, a.plan + a.at.items + (long long)blockIdx.x * kItemInts);

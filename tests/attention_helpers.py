@@ -34,8 +34,8 @@ def kept(x, kind, dt):
         tie = y.abs() == between[code.clamp(max=between.numel() - 1)]
         code = (code + (tie & (code % 2 == 1)).long()).clamp(max=grid.numel() - 1)
         val = grid[code] * torch.where(y < 0, -1.0, 1.0) * torch.exp2(e)
-        out[..., at: at + part.shape[-1]] = torch.where(torch.isfinite(size), val, torch.nan)
-    return out
+        out[..., at: at + part.shape[-1]] = val
+    return torch.where(torch.isfinite(x).all(-1, keepdim=True), out, torch.nan)
 
 
 # -- norm and rotation -------------------------------------------------------------
