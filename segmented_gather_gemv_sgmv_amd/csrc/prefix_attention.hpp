@@ -286,18 +286,19 @@ struct AttnRows {
     }
     __device__ __forceinline__ int seen(int r, int first, int there) const { return min(lim[r] - first, there); }
 
-    // Scores to p; running maxima and sums.
-    template <bool ALL>
-    __device__ __forceinline__ void soften(float c, int first, int there) {
-        if constexpr (!ALL) {
+    // Keys that a row does not see: their scores.
+    __device__ __forceinline__ void mask(int first, int there) {
 #pragma unroll
-            for (int r = 0; r < R; ++r) {
-                const int rem = seen(r, first, there);
+        for (int r = 0; r < R; ++r) {
+            const int rem = seen(r, first, there);
 #pragma unroll
-                for (int t = 0; t < 16; ++t)
-                    if (t >= rem) s[r][t / 4][t % 4] = -__builtin_inff();
-            }
+            for (int t = 0; t < 16; ++t)
+                if (t >= rem) s[r][t / 4][t % 4] = -__builtin_inff();
         }
+    }
+
+    // Scores to p; running maxima and sums.
+    __device__ __forceinline__ void soften(float c) {
         // Maxima are moved only where p would pass 2^4.
         float mx[R];
         bool move = false;
@@ -427,66 +428,23 @@ __device__ __forceinline__ void attn_direct(const AttnArgs& a, const Item& it, u
 #pragma unroll
         for (int g = 0; g < A::kGroups; ++g) load_words<16>(a.v_scales + (b * A::kGroups + g) * 16, vs[g]);
     };
-    auto finish = [&](auto all, int first, int there) {
-        constexpr bool ALL = decltype(all)::value;
-        rows.template soften<ALL>(a.c, first, there);
+    // A step whose keys are not all seen by all rows.  V's scales of tokens that are not there may be
+    // anything, and a NaN's must not meet rows that do not see it: both become 0, and the rows
+    // that do see it (returned) are to be made NaN.
+    auto partial = [&](int first, int there) {
+        rows.mask(first, there);
         const int rem = rows.seen(0, first, there);
-        bool poison = false;  // 4-bit: a row sees a NaN
-        if constexpr (BITS == 4 && !ALL) {
-            // Scales of tokens that are not there may be anything, and a NaN's must not meet rows that do
-            // not see it: both become 0, and the rows that do see it are made NaN.
+        bool poison = false;
 #pragma unroll
-            for (int t = 0; t < 16; ++t) {
-                const uint32_t bits = 255u << (8 * (t % 4));
-                const bool nan = (vs[0][t / 4] & bits) == bits && t < there;
-                poison = poison || (nan && t < rem);
-#pragma unroll
-                for (int g = 0; g < A::kGroups; ++g)
-                    if (nan || t >= there) vs[g][t / 4] &= ~bits;
-            }
-        }
-        if constexpr (BITS == 8) {
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                float w[8];
-#pragma unroll
-                for (int x = 0; x < 8; ++x) {
-                    const int t = 8 * u + x;
-                    w[x] = rows.s[0][t / 4][t % 4] * __uint_as_float(((vs[0][t / 4] >> (8 * (t % 4))) & 255u) << 23);
-                    if (!ALL && t >= rem) w[x] = 0.f;  // what lies there may be NaN
-                }
-                uint4 pf[kTerms];
-                rows.split(w, pf);
-#pragma unroll
-                for (int i = 0; i < A::kLines; ++i) rows.product(i, 0, code_piece<BF16, 8>(vw[i] + 2 * u, 1.f), pf);
-            }
-        } else {
-            uint4 pf[2][kTerms];
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                float w[8];
-#pragma unroll
-                for (int x = 0; x < 8; ++x) w[x] = rows.s[0][2 * u + x / 4][x % 4];
-                rows.split(w, pf[u]);
-            }
+        for (int t = 0; t < 16; ++t) {
+            const uint32_t bits = 255u << (8 * (t % 4));
+            const bool nan = (vs[0][t / 4] & bits) == bits && t < there;
+            poison = poison || (nan && t < rem);
 #pragma unroll
             for (int g = 0; g < A::kGroups; ++g)
-#pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    float scale[8];
-#pragma unroll
-                    for (int x = 0; x < 8; ++x) scale[x] = scale_operand(vs[g][2 * u + x / 4], x % 4);
-                    uint4 vf[2];
-                    line_operands4<BF16>(vw[g] + 2 * u, scale, vf);
-                    rows.product(2 * g, 0, vf[0], pf[u]);
-                    rows.product(2 * g + 1, 0, vf[1], pf[u]);
-                }
-            if (!ALL && __any(poison)) {
-                const float nan = column_max(poison ? 1.f : 0.f) > 0.f ? __builtin_nanf("") : 0.f;
-#pragma unroll
-                for (int d = 0; d < A::kDTiles; ++d) rows.o[0][d] += nan;
-            }
+                if (nan || t >= there) vs[g][t / 4] &= ~bits;
         }
+        return poison;
     };
 
     int blk = it.blk0 + wk;
@@ -513,8 +471,42 @@ __device__ __forceinline__ void attn_direct(const AttnArgs& a, const Item& it, u
         if (more) load_k(blk + waves_k);  // behind the rest of this step
         const int first = blk * kAttnKeys + lg * 16;
         const int there = v_ok ? it.len - first : 0;
-        if (rows.all_seen(first, there)) finish(std::true_type{}, first, there);
-        else finish(std::false_type{}, first, there);
+        bool poison = false;
+        if (!rows.all_seen(first, there)) poison = partial(first, there);
+        rows.soften(a.c);
+        uint4 pf[2][kTerms];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            float w[8];
+#pragma unroll
+            for (int x = 0; x < 8; ++x) {
+                const int t = 8 * u + x;
+                w[x] = rows.s[0][t / 4][t % 4];
+                if constexpr (BITS == 8) w[x] *= __uint_as_float(((vs[0][t / 4] >> (8 * (t % 4))) & 255u) << 23);
+            }
+            rows.split(w, pf[u]);
+        }
+#pragma unroll
+        for (int i = 0; i < A::kLines; ++i)
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                if constexpr (BITS == 8) {
+                    rows.product(i, 0, code_piece<BF16, 8>(vw[i] + 2 * u, 1.f), pf[u]);
+                } else {
+                    float scale[8];
+#pragma unroll
+                    for (int x = 0; x < 8; ++x) scale[x] = scale_operand(vs[i][2 * u + x / 4], x % 4);
+                    uint4 vf[2];
+                    line_operands4<BF16>(vw[i] + 2 * u, scale, vf);
+                    rows.product(2 * i, 0, vf[0], pf[u]);
+                    rows.product(2 * i + 1, 0, vf[1], pf[u]);
+                }
+            }
+        if (__any(poison)) {
+            const float nan = column_max(poison ? 1.f : 0.f) > 0.f ? __builtin_nanf("") : 0.f;
+#pragma unroll
+            for (int d = 0; d < A::kDTiles; ++d) rows.o[0][d] += nan;
+        }
         if (more) load_v(blk + waves_k);
     }
 
@@ -678,28 +670,6 @@ __device__ __forceinline__ void attn_shared(const AttnArgs& a, const Item& it, u
             __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront", "local");
         }
     };
-    auto finish = [&](auto all, int blk, const uint4* from, int first, int there) {
-        constexpr bool ALL = decltype(all)::value;
-        rows.template soften<ALL>(a.c, first, there);
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            uint4 pf[R][kTerms];
-#pragma unroll
-            for (int r = 0; r < R; ++r) {
-                float w[8];
-#pragma unroll
-                for (int x = 0; x < 8; ++x) w[x] = rows.s[r][2 * u + x / 4][x % 4];
-                rows.split(w, pf[r]);
-            }
-#pragma unroll
-            for (int t = 0; t < A::kDTiles; ++t) {
-                const uint4 vf = from[(kKPieces + t * 2 + u) * 64];
-#pragma unroll
-                for (int r = 0; r < R; ++r) rows.product(t, r, vf, pf[r]);
-            }
-        }
-    };
-
     int blk = it.blk0;
     if (blk < end) {
         load(blk);
@@ -737,8 +707,25 @@ __device__ __forceinline__ void attn_shared(const AttnArgs& a, const Item& it, u
         if (mine) {
             const int first = blk * kAttnKeys + lg * 16;
             const int there = ok_now ? it.len - first : 0;
-            if (rows.all_seen(first, there)) finish(std::true_type{}, blk, from, first, there);
-            else finish(std::false_type{}, blk, from, first, there);
+            if (!rows.all_seen(first, there)) rows.mask(first, there);
+            rows.soften(a.c);
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                uint4 pf[R][kTerms];
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    float w[8];
+#pragma unroll
+                    for (int x = 0; x < 8; ++x) w[x] = rows.s[r][2 * u + x / 4][x % 4];
+                    rows.split(w, pf[r]);
+                }
+#pragma unroll
+                for (int t = 0; t < A::kDTiles; ++t) {
+                    const uint4 vf = from[(kKPieces + t * 2 + u) * 64];
+#pragma unroll
+                    for (int r = 0; r < R; ++r) rows.product(t, r, vf, pf[r]);
+                }
+            }
             if (__builtin_expect(nan, 0)) {
                 // A NaN's values went in as zeros: rows that see it are made NaN.
                 bool here;
