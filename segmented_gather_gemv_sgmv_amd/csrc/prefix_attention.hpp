@@ -194,16 +194,22 @@ __device__ __forceinline__ Item attn_item(const AttnArgs& a, const int* e) {
     return t;
 }
 
-// Where 16-token block `b` of the item's keys lies (block 0 of the cache where there is none), if it
-// is there: blocks counted over pages and heads.
-__device__ __forceinline__ long long attn_place(const AttnArgs& a, const Item& it, int b, bool& ok) {
-    const int index = a.blocks_per_page == 1 ? b : (int)__umulhi((uint32_t)b, a.page_magic);
-    ok = b * kKvBlock < it.len;
-    const int page = ok ? it.table[index] : 0;
-    ok = ok && (unsigned)page < (unsigned)a.num_pages;
-    const int in = ok ? b - index * a.blocks_per_page : 0;
+// The page table's entry for 16-token block `b` of the item's keys (any entry where there is none).  Asked for a
+// step ahead of the loads that need it, in no branch and looked at only then, so that no step waits for it.
+__device__ __forceinline__ int attn_page_index(const AttnArgs& a, int b) {
+    return a.blocks_per_page == 1 ? b : (int)__umulhi((uint32_t)b, a.page_magic);
+}
+__device__ __forceinline__ int attn_page(const AttnArgs& a, const Item& it, int b) {
+    return it.table[attn_page_index(a, min(b, (it.len - 1) / kKvBlock))];  // an item has a token at least
+}
+// Where block `b` lies, counted over pages and heads (block 0 of the cache where there is none), and whether it is there.
+__device__ __forceinline__ long long attn_place(const AttnArgs& a, const Item& it, int b, int page, bool& ok) {
+    ok = b * kKvBlock < it.len && (unsigned)page < (unsigned)a.num_pages;
+    const int in = ok ? b - attn_page_index(a, b) * a.blocks_per_page : 0;
     return ((long long)(ok ? page : 0) * a.kv_heads + it.head) * a.blocks_per_page + in;
 }
+// Keeps loads before it where they are written: without, a loop's loads for its next round are moved into that round.
+__device__ __forceinline__ void loads_stay() { asm volatile("" ::: "memory"); }
 
 // HEAD: p is held times 2^HEAD.  TERMS: operands that p is split into, one after the other.
 template <typename QT, int BITS, int P, int R, typename VT, int TERMS, int HEAD>
@@ -407,12 +413,16 @@ __device__ __forceinline__ void attn_direct(const AttnArgs& a, const Item& it, u
     AttnRows<QT, BITS, P, 1, BF16, kTerms, 0> rows;
     rows.init(a, it, it.m0 + wm * 16, lr, lg);
 
+    int blk = it.blk0 + wk;
+    const int end = rows.blk_end;
     uint32_t kw[4][A::kPiece / 4], ks[A::kKGroups][4], vw[A::kLines][4], vs[A::kGroups][4];
     bool v_ok = false;
     const int g0 = BITS == 8 ? 0 : (lg * (P / 4)) >> 5;
-    auto load_k = [&](int blk) {
+    int page_k = 0, page_v = 0;  // of the next loads
+    auto load_k = [&](int at) {
         bool ok;
-        const long long b = attn_place(a, it, blk * 4 + (lr >> 2), ok);
+        const long long b = attn_place(a, it, at * 4 + (lr >> 2), at < end ? page_k : -1, ok);
+        page_k = attn_page(a, it, (at + waves_k) * 4 + (lr >> 2));
         const uint8_t* p = a.k + (b * 16 + (lr & 3)) * A::kRow + lg * A::kPiece;
 #pragma unroll
         for (int t = 0; t < 4; ++t) load_words<A::kPiece>(p + t * 4 * A::kRow, kw[t]);
@@ -420,8 +430,9 @@ __device__ __forceinline__ void attn_direct(const AttnArgs& a, const Item& it, u
         for (int g = 0; g < A::kKGroups; ++g)
             load_words<16>(a.k_scales + (b * A::kGroups + min(g0 + g, A::kGroups - 1)) * 16, ks[g]);
     };
-    auto load_v = [&](int blk) {
-        const long long b = attn_place(a, it, blk * 4 + lg, v_ok);
+    auto load_v = [&](int at) {
+        const long long b = attn_place(a, it, at * 4 + lg, at < end ? page_v : -1, v_ok);
+        page_v = attn_page(a, it, (at + waves_k) * 4 + lg);
         const uint8_t* p = a.v + (b * A::kRow + lr) * 16;
 #pragma unroll
         for (int i = 0; i < A::kLines; ++i) load_words<16>(p + i * 256, vw[i]);
@@ -447,13 +458,15 @@ __device__ __forceinline__ void attn_direct(const AttnArgs& a, const Item& it, u
         return poison;
     };
 
-    int blk = it.blk0 + wk;
-    const int end = rows.blk_end;
     if (blk < end) {
+        page_k = attn_page(a, it, blk * 4 + (lr >> 2));
+        page_v = attn_page(a, it, blk * 4 + lg);
         load_k(blk);
         load_v(blk);
     }
-    for (; blk < end; blk += waves_k) {
+    while (blk < end) {
+        // The step after this one is asked for behind its scores and behind its products; after the last one the
+        // cache's first block (from L2), since with loads in a branch every step would wait for all of them.
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
             float sc[A::kKGroups];
@@ -467,8 +480,7 @@ __device__ __forceinline__ void attn_direct(const AttnArgs& a, const Item& it, u
                 rows.score(t, x, code_piece<typename A::KT, BITS>(kw[t] + x * (BITS / 4), scale));
             }
         }
-        const bool more = blk + waves_k < end;
-        if (more) load_k(blk + waves_k);  // behind the rest of this step
+        load_k(blk + waves_k);
         const int first = blk * kAttnKeys + lg * 16;
         const int there = v_ok ? it.len - first : 0;
         bool poison = false;
@@ -507,7 +519,9 @@ __device__ __forceinline__ void attn_direct(const AttnArgs& a, const Item& it, u
 #pragma unroll
             for (int d = 0; d < A::kDTiles; ++d) rows.o[0][d] += nan;
         }
-        if (more) load_v(blk + waves_k);
+        load_v(blk + waves_k);
+        loads_stay();
+        blk += waves_k;
     }
 
     // The waves over the keys of the same rows: their maxima, then their sums pairwise.
@@ -581,15 +595,18 @@ __device__ __forceinline__ void attn_shared(const AttnArgs& a, const Item& it, u
     uint32_t kw[A::kPiece / 4], vw[kMine][4], ks[A::kKGroups], vb[A::kGroups];
     bool ok = false;
     const int g0 = BITS == 8 ? 0 : (lg * (P / 4)) >> 5;
+    int page_k = 0, page_v = 0;  // of the next loads
     auto load = [&](int blk) {
         bool there;
-        const long long bk = attn_place(a, it, blk * 4 + (lr >> 2), there);
+        const long long bk = attn_place(a, it, blk * 4 + (lr >> 2), page_k, there);
+        const long long bv = attn_place(a, it, blk * 4 + lg, page_v, ok);
+        page_k = attn_page(a, it, (blk + 1) * 4 + (lr >> 2));
+        page_v = attn_page(a, it, (blk + 1) * 4 + lg);
         const int token = wave * 4 + (lr & 3);
         load_words<A::kPiece>(a.k + (bk * 16 + token) * A::kRow + lg * A::kPiece, kw);
 #pragma unroll
         for (int g = 0; g < A::kKGroups; ++g)
             ks[g] = a.k_scales[(bk * A::kGroups + min(g0 + g, A::kGroups - 1)) * 16 + token];
-        const long long bv = attn_place(a, it, blk * 4 + lg, ok);
 #pragma unroll
         for (int i = 0; i < kMine; ++i)
             if (A::kLines % kAttnWaves == 0 || i * kAttnWaves + wave < A::kLines)
@@ -670,15 +687,18 @@ __device__ __forceinline__ void attn_shared(const AttnArgs& a, const Item& it, u
             __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront", "local");
         }
     };
-    int blk = it.blk0;
+    // The loop is left out, not entered, where there is nothing: a path to it past the first conversion, which
+    // waits for all loads, q's too, would have every step wait for the codes it has just asked for.
+    int blk = it.blk0, n = 0;
     if (blk < end) {
+        page_k = attn_page(a, it, blk * 4 + (lr >> 2));
+        page_v = attn_page(a, it, blk * 4 + lg);
         load(blk);
         convert(blk, stage);
         ok_now = ok;
         nan = nan_next;
         if (blk + 1 < end) load(blk + 1);
-    }
-    for (int n = 0; blk < end; ++blk, n ^= 1) {
+        do {
         // The stage of this step is written, and the other one read, by all waves.  Only LDS is waited for.
         __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
         __builtin_amdgcn_s_barrier();
@@ -729,7 +749,7 @@ __device__ __forceinline__ void attn_shared(const AttnArgs& a, const Item& it, u
             if (__builtin_expect(nan, 0)) {
                 // A NaN's values went in as zeros: rows that see it are made NaN.
                 bool here;
-                const long long b = attn_place(a, it, blk * 4 + lg, here);
+                const long long b = attn_place(a, it, blk * 4 + lg, attn_page(a, it, blk * 4 + lg), here);
                 uint32_t w[4];
                 load_words<16>(a.v_scales + b * A::kGroups * 16, w);
 #pragma unroll
@@ -747,6 +767,8 @@ __device__ __forceinline__ void attn_shared(const AttnArgs& a, const Item& it, u
         }
         ok_now = ok_then;
         nan = nan_next;
+        n ^= 1;
+        } while (++blk < end);
     }
     const float back = __builtin_ldexpf(1.f, eref - 127 - kUp - kAttnHead);
 #pragma unroll
