@@ -208,6 +208,8 @@ __device__ __forceinline__ long long attn_place(const AttnArgs& a, const Item& i
     const int in = ok ? b - attn_page_index(a, b) * a.blocks_per_page : 0;
     return ((long long)(ok ? page : 0) * a.kv_heads + it.head) * a.blocks_per_page + in;
 }
+constexpr int kWaitLoads = 0x0F70;  // s_waitcnt: no load outstanding, LDS and scalars as they are
+
 // Keeps loads before it where they are written: without, a loop's loads for its next round are moved into that round.
 __device__ __forceinline__ void loads_stay() { asm volatile("" ::: "memory"); }
 
@@ -463,6 +465,8 @@ __device__ __forceinline__ void attn_direct(const AttnArgs& a, const Item& it, u
         page_v = attn_page(a, it, blk * 4 + lg);
         load_k(blk);
         load_v(blk);
+        // q is there with them: else the loop's first step, and with it every one, would wait for it anew.
+        __builtin_amdgcn_s_waitcnt(kWaitLoads);
     }
     while (blk < end) {
         // The step after this one is asked for behind its scores and behind its products; after the last one the
@@ -580,7 +584,7 @@ __device__ __forceinline__ void attn_shared(const AttnArgs& a, const Item& it, u
     static_assert(kAttnWaves == 4, "a wave converts one tile of K");
     uint4* stage = (uint4*)lds;  // two of kStage pieces
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
-    uint32_t* factors = (uint32_t*)(stage + 2 * kStage) + wave * 64;  // the wave's own
+    uint32_t* factors = (uint32_t*)(stage + 2 * kStage) + wave * 64 * kMine;  // the wave's own
     const int lr = lane & 15, lg = lane >> 4;
     AttnRows<QT, BITS, P, R, F16, kTerms, kAttnHead> rows;
     rows.init(a, it, it.m0 + wave * 16 * R, lr, lg);
@@ -628,6 +632,19 @@ __device__ __forceinline__ void attn_shared(const AttnArgs& a, const Item& it, u
             top = max(top, (int)vb[g]);
         }
         eref_next = max(eref_next, wave_max(top));
+        // The tokens' factors 2^(b - eref + kUp), through the wave's own LDS from lane = token to all lanes of their
+        // block: written here, read behind K's conversion.
+#pragma unroll
+        for (int i = 0; i < (BITS == 8 ? 1 : kMine); ++i) {
+            uint32_t b = vb[0];
+            if constexpr (BITS == 4) {
+#pragma unroll
+                for (int g = 1; g < A::kGroups; ++g) b = g == i * kAttnWaves + wave ? vb[g] : b;
+            }
+            const uint32_t bits = (uint32_t)max((int)b - eref_next + 127 + kUp, 0) << 23;
+            if constexpr (BITS == 8) ((uint16_t*)factors)[lane] = F16::from_float(__uint_as_float(bits));
+            else factors[i * 64 + lane] = bits;
+        }
 #pragma unroll
         for (int x = 0; x < A::kSteps; ++x) {
             uint32_t b = ks[0];
@@ -636,35 +653,27 @@ __device__ __forceinline__ void attn_shared(const AttnArgs& a, const Item& it, u
             to[(wave * A::kSteps + x) * 64 + lane] =
                 code_piece<typename A::KT, BITS>(kw + x * (BITS / 4), __uint_as_float(b << 23));
         }
+        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
+        uint4 f[BITS == 8 ? 1 : kMine][BITS == 8 ? 2 : 4];
+#pragma unroll
+        for (int i = 0; i < (BITS == 8 ? 1 : kMine); ++i)
+#pragma unroll
+            for (int x = 0; x < (BITS == 8 ? 2 : 4); ++x)
+                f[i][x] = ((const uint4*)factors)[BITS == 8 ? lg * 2 + x : i * 16 + lg * 4 + x];
 #pragma unroll
         for (int i = 0; i < kMine; ++i) {
             const int line = i * kAttnWaves + wave;
             if (A::kLines % kAttnWaves != 0 && line >= A::kLines) continue;
-            // The tokens' factors 2^(b - eref + kUp), through the wave's own LDS from lane = token to all lanes of
-            // their block.
-            uint32_t b = vb[0];
-            if constexpr (BITS == 4) {
-#pragma unroll
-                for (int g = 1; g < A::kGroups; ++g) b = g == line ? vb[g] : b;
-            }
-            const uint32_t bits = (uint32_t)max((int)b - eref_next + 127 + kUp, 0) << 23;
-            if constexpr (BITS == 8) {
-                if (i == 0) ((uint16_t*)factors)[lane] = F16::from_float(__uint_as_float(bits));
-            } else {
-                factors[lane] = bits;
-            }
-            __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
             if constexpr (BITS == 8) {
                 typedef _Float16 h2_t __attribute__((ext_vector_type(2)));
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
-                    const uint4 f = ((const uint4*)factors)[lg * 2 + u];
                     const uint4 c = code_piece<F16, 8>(vw[i] + 2 * u, 1.f);
                     auto times = [](uint32_t x, uint32_t y) {
                         return bits2(__builtin_bit_cast(h2_t, x) * __builtin_bit_cast(h2_t, y));
                     };
                     to[(kKPieces + line * 2 + u) * 64 + lane] =
-                        make_uint4(times(c.x, f.x), times(c.y, f.y), times(c.z, f.z), times(c.w, f.w));
+                        make_uint4(times(c.x, f[0][u].x), times(c.y, f[0][u].y), times(c.z, f[0][u].z), times(c.w, f[0][u].w));
                 }
             } else {
 #pragma unroll
@@ -672,11 +681,11 @@ __device__ __forceinline__ void attn_shared(const AttnArgs& a, const Item& it, u
                     float scale[8];
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
-                        const uint4 f = ((const uint4*)factors)[lg * 4 + u * 2 + x];
-                        scale[4 * x] = __uint_as_float(f.x);
-                        scale[4 * x + 1] = __uint_as_float(f.y);
-                        scale[4 * x + 2] = __uint_as_float(f.z);
-                        scale[4 * x + 3] = __uint_as_float(f.w);
+                        const uint4 w = f[i][u * 2 + x];
+                        scale[4 * x] = __uint_as_float(w.x);
+                        scale[4 * x + 1] = __uint_as_float(w.y);
+                        scale[4 * x + 2] = __uint_as_float(w.z);
+                        scale[4 * x + 3] = __uint_as_float(w.w);
                     }
                     uint4 vf[2];
                     line_operands4<F16>(vw[i] + 2 * u, scale, vf);
@@ -684,8 +693,8 @@ __device__ __forceinline__ void attn_shared(const AttnArgs& a, const Item& it, u
                     for (int y = 0; y < 2; ++y) to[(kKPieces + (line * 2 + y) * 2 + u) * 64 + lane] = vf[y];
                 }
             }
-            __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront", "local");
         }
+        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront", "local");
     };
     // The loop is left out, not entered, where there is nothing: a path to it past the first conversion, which
     // waits for all loads, q's too, would have every step wait for the codes it has just asked for.
@@ -706,10 +715,20 @@ __device__ __forceinline__ void attn_shared(const AttnArgs& a, const Item& it, u
         const uint4* from = stage + n * kStage + lane;
         const bool mine = blk < rows.blk_end;
         if (mine) {
+            uint4 kf[2][A::kSteps];
 #pragma unroll
-            for (int t = 0; t < 4; ++t)
+            for (int x = 0; x < A::kSteps; ++x) kf[0][x] = from[x * 64];
 #pragma unroll
-                for (int x = 0; x < A::kSteps; ++x) rows.score(t, x, from[(t * A::kSteps + x) * 64]);
+            for (int t = 0; t < 4; ++t) {
+                if (t < 3) {
+#pragma unroll
+                    for (int x = 0; x < A::kSteps; ++x) kf[(t + 1) & 1][x] = from[((t + 1) * A::kSteps + x) * 64];
+                }
+                __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                for (int x = 0; x < A::kSteps; ++x) rows.score(t, x, kf[t & 1][x]);
+                __builtin_amdgcn_sched_barrier(0);
+            }
         }
         if (eref_next > eref) {  // this step's values are relative to a larger exponent
             const float f = __builtin_ldexpf(1.f, max(eref - eref_next, -126));
@@ -728,23 +747,37 @@ __device__ __forceinline__ void attn_shared(const AttnArgs& a, const Item& it, u
             const int first = blk * kAttnKeys + lg * 16;
             const int there = ok_now ? it.len - first : 0;
             if (!rows.all_seen(first, there)) rows.mask(first, there);
-            rows.soften(a.c);
+            // V's operands four pieces ahead of their products, the first ones across the exponentials.
+            constexpr int kAhead = 4;
+            uint4 vf[2][kAhead];
+            auto fetch = [&](int i, uint4* to) {  // pieces [i, i + kAhead) in the order of their use: half u, tile
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                uint4 pf[R][kTerms];
+                for (int x = 0; x < kAhead; ++x)
+                    to[x] = from[(kKPieces + (i + x) % A::kDTiles * 2 + (i + x) / A::kDTiles) * 64];
+            };
+            static_assert(A::kDTiles % 2 == 0 && kVPieces % kAhead == 0, "whole groups of pieces");
+            fetch(0, vf[0]);
+            rows.soften(a.c);
+            uint4 pf[2][R][kTerms];
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
 #pragma unroll
                 for (int r = 0; r < R; ++r) {
                     float w[8];
 #pragma unroll
                     for (int x = 0; x < 8; ++x) w[x] = rows.s[r][2 * u + x / 4][x % 4];
-                    rows.split(w, pf[r]);
+                    rows.split(w, pf[u][r]);
                 }
 #pragma unroll
-                for (int t = 0; t < A::kDTiles; ++t) {
-                    const uint4 vf = from[(kKPieces + t * 2 + u) * 64];
+            for (int i = 0; i < kVPieces; i += kAhead) {
+                if (i + kAhead < kVPieces) fetch(i + kAhead, vf[(i / kAhead + 1) & 1]);
+                __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-                    for (int r = 0; r < R; ++r) rows.product(t, r, vf, pf[r]);
-                }
+                for (int x = 0; x < kAhead; ++x)
+#pragma unroll
+                    for (int r = 0; r < R; ++r)
+                        rows.product((i + x) % A::kDTiles, r, vf[(i / kAhead) & 1][x], pf[(i + x) / A::kDTiles][r]);
+                __builtin_amdgcn_sched_barrier(0);
             }
             if (__builtin_expect(nan, 0)) {
                 // A NaN's values went in as zeros: rows that see it are made NaN.
@@ -784,7 +817,7 @@ template <typename QT, int BITS, int P, int RMAX>
 __global__ __launch_bounds__(kAttnThreads, P <= 128 ? 2 : 1) void attn_kernel(AttnArgs a) {
     // attn_direct: sums of half the waves, maxima; attn_shared: two stages, factors.
     constexpr int kDirect = kAttnWaves / 2 * P / 16 * 1024 + kAttnWaves * 16 * 8;
-    constexpr int kShared = 2 * P * 64 * 2 * 2 + kAttnWaves * 64 * 4;
+    constexpr int kShared = 2 * P * 64 * 2 * 2 + (P * BITS / 128 + 3) / 4 * kAttnWaves * 64 * 4;
     __shared__ __align__(16) unsigned char lds[kDirect > kShared ? kDirect : kShared];
     if ((int)blockIdx.x >= a.plan[0]) return;
     const Item it = attn_item(a, a.plan + a.at.items + (long long)blockIdx.x * kItemInts);
