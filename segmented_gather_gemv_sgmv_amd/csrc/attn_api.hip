@@ -104,7 +104,9 @@ extern "C" int prefix_attention(void* o, float* lse, const void* q, const sgmv_k
     Shape s;
     if (const int e = check_shape(cache, num_rows, num_seqs, num_prefixes, q_heads, dtype, &s)) return e;
     if (pages_per_seq < 0 || pages_per_prefix < 0 || !(scale > 0.f) || scale > 3e38f) return SGMV_ERR_BAD_SHAPE;
-    if (!table_fits(cache, pages_per_seq) || !table_fits(cache, pages_per_prefix)) return SGMV_ERR_UNSUPPORTED;
+    if (!table_fits(cache, pages_per_seq) || !table_fits(cache, pages_per_prefix) ||
+        (long long)cache->kv_heads * (cache->page_size / kKvBlock) > 0x7FFFFFFFll)
+        return SGMV_ERR_UNSUPPORTED;
     if (num_rows == 0 || num_seqs == 0) return SGMV_OK;
     if (const int e = kv_check(cache)) return e;
     if (!o || !q || !plan || !strides || (pages_per_seq > 0 && !pages) ||
@@ -127,7 +129,8 @@ extern "C" int prefix_attention(void* o, float* lse, const void* q, const sgmv_k
     a.v_scales = (const uint8_t*)cache->v_scales;
     a.num_pages = cache->num_pages;
     a.blocks_per_page = cache->page_size / kKvBlock;
-    a.page_magic = (uint32_t)(((1ull << 32) + a.blocks_per_page - 1) / a.blocks_per_page);
+    a.page_one = a.blocks_per_page == 1 ? ~0u : 0u;
+    a.page_magic = a.page_one ? 0u : (uint32_t)(((1ull << 32) + a.blocks_per_page - 1) / a.blocks_per_page);
     a.own_pages = pages;
     a.prefix_pages = prefix_pages;
     a.own_width = pages_per_seq;

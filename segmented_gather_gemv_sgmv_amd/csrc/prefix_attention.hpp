@@ -39,7 +39,7 @@ struct AttnArgs {
     long long q_row, q_head, o_row, o_head;  // strides in elements
     const uint8_t *k, *v, *k_scales, *v_scales;
     int num_pages, blocks_per_page;   // of 16 tokens
-    uint32_t page_magic;              // ceil(2^32 / blocks_per_page)
+    uint32_t page_magic, page_one;    // ceil(2^32 / blocks_per_page) and 0; 0 and ~0 for one block a page
     const int *own_pages, *prefix_pages;
     int own_width, prefix_width;
     const int* plan;
@@ -172,6 +172,7 @@ struct Item {
     bool own;
     int hidden;         // own: tokens before the first row
     const int* table;   // pages
+    uint32_t stride, base;  // blocks of a page (of all heads), of the heads before this one
 };
 
 __device__ __forceinline__ Item attn_item(const AttnArgs& a, const int* e) {
@@ -191,22 +192,29 @@ __device__ __forceinline__ Item attn_item(const AttnArgs& a, const int* e) {
     t.hidden = t.len - rec[1];
     t.table = t.own ? a.own_pages + (long long)(stack - a.prefixes) * a.own_width
                     : a.prefix_pages + (long long)stack * a.prefix_width;
+    t.stride = (uint32_t)a.kv_heads * a.blocks_per_page;
+    t.base = (uint32_t)t.head * a.blocks_per_page;
     return t;
 }
 
-// The page table's entry for 16-token block `b` of the item's keys (any entry where there is none).  Asked for a
-// step ahead of the loads that need it, in no branch and looked at only then, so that no step waits for it.
-__device__ __forceinline__ int attn_page_index(const AttnArgs& a, int b) {
-    return a.blocks_per_page == 1 ? b : (int)__umulhi((uint32_t)b, a.page_magic);
+// 16-token block `b` of the item's keys: its page's entry in the table and its place in the page.  Asked for a step
+// ahead of the loads that need it, in no branch and looked at only then, so that no step waits for it.
+struct KeyBlock {
+    int b, in, page;
+};
+__device__ __forceinline__ KeyBlock key_block(const AttnArgs& a, const Item& it, int b) {
+    KeyBlock k;
+    k.b = b;
+    const uint32_t c = (uint32_t)min(b, (it.len - 1) / kKvBlock);  // any entry where there is none; an item has a token
+    const uint32_t index = __umulhi(c, a.page_magic) + (c & a.page_one);
+    k.in = (int)(c - index * (uint32_t)a.blocks_per_page);
+    k.page = it.table[index];
+    return k;
 }
-__device__ __forceinline__ int attn_page(const AttnArgs& a, const Item& it, int b) {
-    return it.table[attn_page_index(a, min(b, (it.len - 1) / kKvBlock))];  // an item has a token at least
-}
-// Where block `b` lies, counted over pages and heads (block 0 of the cache where there is none), and whether it is there.
-__device__ __forceinline__ long long attn_place(const AttnArgs& a, const Item& it, int b, int page, bool& ok) {
-    ok = b * kKvBlock < it.len && (unsigned)page < (unsigned)a.num_pages;
-    const int in = ok ? b - attn_page_index(a, b) * a.blocks_per_page : 0;
-    return ((long long)(ok ? page : 0) * a.kv_heads + it.head) * a.blocks_per_page + in;
+// Where it lies, counted over pages and heads, and whether it is there (else some block of the cache).
+__device__ __forceinline__ uint64_t place_of(const AttnArgs& a, const Item& it, const KeyBlock& k, bool& ok) {
+    ok = k.b * kKvBlock < it.len && (unsigned)k.page < (unsigned)a.num_pages;
+    return (uint64_t)(ok ? (uint32_t)k.page : 0u) * it.stride + (it.base + (uint32_t)k.in);
 }
 constexpr int kWaitLoads = 0x0F70;  // s_waitcnt: no load outstanding, LDS and scalars as they are
 
@@ -420,11 +428,13 @@ __device__ __forceinline__ void attn_direct(const AttnArgs& a, const Item& it, u
     uint32_t kw[4][A::kPiece / 4], ks[A::kKGroups][4], vw[A::kLines][4], vs[A::kGroups][4];
     bool v_ok = false;
     const int g0 = BITS == 8 ? 0 : (lg * (P / 4)) >> 5;
-    int page_k = 0, page_v = 0;  // of the next loads
-    auto load_k = [&](int at) {
+    // Where the next loads go.  Behind the last step they go on, to keys of the next chunk or to block 0 of a page:
+    // with loads in a branch every step would wait for all of them.
+    KeyBlock at_k = key_block(a, it, blk * 4 + (lr >> 2)), at_v = key_block(a, it, blk * 4 + lg);
+    auto load_k = [&] {
         bool ok;
-        const long long b = attn_place(a, it, at * 4 + (lr >> 2), at < end ? page_k : -1, ok);
-        page_k = attn_page(a, it, (at + waves_k) * 4 + (lr >> 2));
+        const uint64_t b = place_of(a, it, at_k, ok);
+        at_k = key_block(a, it, at_k.b + 4 * waves_k);
         const uint8_t* p = a.k + (b * 16 + (lr & 3)) * A::kRow + lg * A::kPiece;
 #pragma unroll
         for (int t = 0; t < 4; ++t) load_words<A::kPiece>(p + t * 4 * A::kRow, kw[t]);
@@ -432,9 +442,9 @@ __device__ __forceinline__ void attn_direct(const AttnArgs& a, const Item& it, u
         for (int g = 0; g < A::kKGroups; ++g)
             load_words<16>(a.k_scales + (b * A::kGroups + min(g0 + g, A::kGroups - 1)) * 16, ks[g]);
     };
-    auto load_v = [&](int at) {
-        const long long b = attn_place(a, it, at * 4 + lg, at < end ? page_v : -1, v_ok);
-        page_v = attn_page(a, it, (at + waves_k) * 4 + lg);
+    auto load_v = [&] {
+        const uint64_t b = place_of(a, it, at_v, v_ok);
+        at_v = key_block(a, it, at_v.b + 4 * waves_k);
         const uint8_t* p = a.v + (b * A::kRow + lr) * 16;
 #pragma unroll
         for (int i = 0; i < A::kLines; ++i) load_words<16>(p + i * 256, vw[i]);
@@ -461,16 +471,13 @@ __device__ __forceinline__ void attn_direct(const AttnArgs& a, const Item& it, u
     };
 
     if (blk < end) {
-        page_k = attn_page(a, it, blk * 4 + (lr >> 2));
-        page_v = attn_page(a, it, blk * 4 + lg);
-        load_k(blk);
-        load_v(blk);
+        load_k();
+        load_v();
         // q is there with them: else the loop's first step, and with it every one, would wait for it anew.
         __builtin_amdgcn_s_waitcnt(kWaitLoads);
     }
     while (blk < end) {
-        // The step after this one is asked for behind its scores and behind its products; after the last one the
-        // cache's first block (from L2), since with loads in a branch every step would wait for all of them.
+        // The step after this one is asked for behind its scores and behind its products.
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
             float sc[A::kKGroups];
@@ -484,7 +491,7 @@ __device__ __forceinline__ void attn_direct(const AttnArgs& a, const Item& it, u
                 rows.score(t, x, code_piece<typename A::KT, BITS>(kw[t] + x * (BITS / 4), scale));
             }
         }
-        load_k(blk + waves_k);
+        load_k();
         const int first = blk * kAttnKeys + lg * 16;
         const int there = v_ok ? it.len - first : 0;
         bool poison = false;
@@ -523,7 +530,7 @@ __device__ __forceinline__ void attn_direct(const AttnArgs& a, const Item& it, u
 #pragma unroll
             for (int d = 0; d < A::kDTiles; ++d) rows.o[0][d] += nan;
         }
-        load_v(blk + waves_k);
+        load_v();
         loads_stay();
         blk += waves_k;
     }
@@ -599,13 +606,14 @@ __device__ __forceinline__ void attn_shared(const AttnArgs& a, const Item& it, u
     uint32_t kw[A::kPiece / 4], vw[kMine][4], ks[A::kKGroups], vb[A::kGroups];
     bool ok = false;
     const int g0 = BITS == 8 ? 0 : (lg * (P / 4)) >> 5;
-    int page_k = 0, page_v = 0;  // of the next loads
-    auto load = [&](int blk) {
+    // Where the next loads go; as in attn_direct they go on behind the last step.
+    KeyBlock at_k = key_block(a, it, it.blk0 * 4 + (lr >> 2)), at_v = key_block(a, it, it.blk0 * 4 + lg);
+    auto load = [&] {
         bool there;
-        const long long bk = attn_place(a, it, blk * 4 + (lr >> 2), page_k, there);
-        const long long bv = attn_place(a, it, blk * 4 + lg, page_v, ok);
-        page_k = attn_page(a, it, (blk + 1) * 4 + (lr >> 2));
-        page_v = attn_page(a, it, (blk + 1) * 4 + lg);
+        const uint64_t bk = place_of(a, it, at_k, there);
+        const uint64_t bv = place_of(a, it, at_v, ok);
+        at_k = key_block(a, it, at_k.b + 4);
+        at_v = key_block(a, it, at_v.b + 4);
         const int token = wave * 4 + (lr & 3);
         load_words<A::kPiece>(a.k + (bk * 16 + token) * A::kRow + lg * A::kPiece, kw);
 #pragma unroll
@@ -697,16 +705,15 @@ __device__ __forceinline__ void attn_shared(const AttnArgs& a, const Item& it, u
         __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront", "local");
     };
     // The loop is left out, not entered, where there is nothing: a path to it past the first conversion, which
-    // waits for all loads, q's too, would have every step wait for the codes it has just asked for.
+    // waits for all loads, q's too, would have every step wait for the codes it has just asked for.  For the same
+    // reason nothing is converted or asked for in a branch.
     int blk = it.blk0, n = 0;
     if (blk < end) {
-        page_k = attn_page(a, it, blk * 4 + (lr >> 2));
-        page_v = attn_page(a, it, blk * 4 + lg);
-        load(blk);
+        load();
         convert(blk, stage);
         ok_now = ok;
         nan = nan_next;
-        if (blk + 1 < end) load(blk + 1);
+        load();
         do {
         // The stage of this step is written, and the other one read, by all waves.  Only LDS is waited for.
         __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
@@ -739,10 +746,8 @@ __device__ __forceinline__ void attn_shared(const AttnArgs& a, const Item& it, u
             eref = eref_next;
         }
         const bool ok_then = ok;
-        if (blk + 1 < end) {
-            convert(blk + 1, stage + (n ^ 1) * kStage);
-            if (blk + 2 < end) load(blk + 2);
-        }
+        convert(blk + 1, stage + (n ^ 1) * kStage);
+        load();
         if (mine) {
             const int first = blk * kAttnKeys + lg * 16;
             const int there = ok_now ? it.len - first : 0;
@@ -782,7 +787,7 @@ __device__ __forceinline__ void attn_shared(const AttnArgs& a, const Item& it, u
             if (__builtin_expect(nan, 0)) {
                 // A NaN's values went in as zeros: rows that see it are made NaN.
                 bool here;
-                const long long b = attn_place(a, it, blk * 4 + lg, attn_page(a, it, blk * 4 + lg), here);
+                const uint64_t b = place_of(a, it, key_block(a, it, blk * 4 + lg), here);
                 uint32_t w[4];
                 load_words<16>(a.v_scales + b * A::kGroups * 16, w);
 #pragma unroll
