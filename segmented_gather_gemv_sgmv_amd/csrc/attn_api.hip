@@ -149,6 +149,8 @@ extern "C" int prefix_attention(void* o, float* lse, const void* q, const sgmv_k
     a.c = scale * 1.4426950408889634f;
     const int V = dtype == SGMV_F32 ? 4 : 8;
     a.vec = aligned16(q) && strides[0] % V == 0 && strides[1] % V == 0;
+    const uintptr_t four = dtype == SGMV_F32 ? 16 : 8;
+    a.o_vec = (uintptr_t)o % four == 0 && strides[2] % 4 == 0 && strides[3] % 4 == 0;
     const hipStream_t st = (hipStream_t)stream;
     const int items = (int)s.sizes.items;
     if (dtype == SGMV_F32) run_attn_f32(a, cache->kind, items, st);

@@ -20,44 +20,23 @@ struct PlanArgs {
 
 constexpr int kPlanThreads = 1024;
 
-struct Stack {
-    int row0, rows, len;
-    int tile, mtiles, blocks;  // rows of a tile, tiles per K / V head, steps of 64 keys
-};
-
 __device__ __forceinline__ int plan_row(const PlanArgs& a, int s) {
     const int r = a.row_indptr ? a.row_indptr[s] : s;
     return min(max(r, 0), a.rows);
 }
-
-__device__ __forceinline__ Stack plan_stack(const PlanArgs& a, int i) {
-    Stack k;
-    int lo, hi;
-    long long len, most;
-    if (i < a.prefixes) {
-        const int s0 = a.prefix_indptr ? a.prefix_indptr[i] : 0;
-        const int s1 = a.prefix_indptr ? a.prefix_indptr[i + 1] : a.seqs;
-        lo = min(max(s0, 0), a.seqs);
-        hi = min(max(s1, lo), a.seqs);
-        len = a.prefix_lengths[i];
-        most = a.prefix_tokens;
-    } else {
-        lo = i - a.prefixes;
-        hi = lo + 1;
-        len = a.lengths[lo];
-        most = a.own_tokens;
-    }
-    k.row0 = plan_row(a, lo);
-    k.rows = max(plan_row(a, hi) - k.row0, 0);
-    k.len = (int)min(max(len, 0ll), most);
-    const int M = k.rows * a.rep;
-    const int wide = 16 * a.tiles * kAttnWaves;
-    k.tile = 16;
-    while (k.tile < M && k.tile < wide) k.tile *= 2;
-    k.mtiles = (M + k.tile - 1) / k.tile;
-    k.blocks = (k.len + kAttnKeys - 1) / kAttnKeys;
-    return k;
+__device__ __forceinline__ int plan_rows(const PlanArgs& a, int lo, int hi) {
+    return max(plan_row(a, hi) - plan_row(a, lo), 0);
 }
+// Sequences [lo, hi) of prefix g.
+__device__ __forceinline__ void plan_run(const PlanArgs& a, int g, int& lo, int& hi) {
+    lo = a.prefix_indptr ? min(max(a.prefix_indptr[g], 0), a.seqs) : 0;
+    hi = a.prefix_indptr ? min(max(a.prefix_indptr[g + 1], lo), a.seqs) : a.seqs;
+}
+__device__ __forceinline__ int plan_length(int len, long long most) {
+    return (int)min((long long)max(len, 0), most);
+}
+__device__ __forceinline__ int plan_blocks(int len) { return (len + kAttnKeys - 1) / kAttnKeys; }
+__device__ __forceinline__ int plan_weight(int tile) { return tile >= 64 ? 2 : 1; }
 
 __device__ __forceinline__ long long block_sum64(long long v, long long* s) {
     for (int m = 1; m < 64; m *= 2) v += __shfl_xor(v, m);
@@ -89,24 +68,79 @@ __device__ __forceinline__ long long block_scan64(long long v, long long* s, lon
 
 __global__ __launch_bounds__(kPlanThreads) void attn_plan_kernel(PlanArgs a) {
     __shared__ long long s_sum[kPlanThreads / 64];
-    const int n = a.prefixes + a.seqs, tid = threadIdx.x, lane = tid & 63;
-    // Steps of 64 keys in all, and from them those of a chunk.
+    const int n = a.prefixes + a.seqs, tid = threadIdx.x, lane = tid & 63, wave = tid / 64;
+    constexpr int kWaves = kPlanThreads / 64;
+    const int wide = 16 * a.tiles * kAttnWaves;
+    int* seq_prefix = a.plan + a.at.seq_prefix;
+    int* apart = a.plan + a.at.apart;  // prefixes that are read apart from their sequences' tokens
+    // Which prefix a sequence has (-1: none); rows of no sequence.
+    for (int s = tid; s < a.seqs; s += kPlanThreads) seq_prefix[s] = -1;
+    for (int g = tid; g < a.prefixes; g += kPlanThreads) apart[g] = 0;
+    const int first = plan_row(a, 0), last = plan_row(a, a.seqs);
+    for (int r = tid; r < a.rows; r += kPlanThreads)
+        if (r < first || r >= last) a.plan[a.at.row_seq + r] = -1;
+    __syncthreads();
+    for (int g = wave; g < a.prefixes; g += kWaves) {
+        int lo, hi;
+        plan_run(a, g, lo, hi);
+        for (int s = lo + lane; s < hi; s += 64) seq_prefix[s] = g;
+    }
+    __syncthreads();
+    for (int s = tid; s < a.seqs; s += kPlanThreads) {
+        const int M = plan_rows(a, s, s + 1) * a.rep, g = seq_prefix[s];
+        if (g >= 0 && M > 0 && M < wide) apart[g] = 1;
+    }
+    __syncthreads();
+    // The stacks and the work in all.
     long long work = 0;
     for (int i = tid; i < n; i += kPlanThreads) {
-        const Stack k = plan_stack(a, i);
-        work += (long long)a.kv_heads * k.mtiles * k.blocks;
+        int row0, rows, len, front = 0, prefix = -1;
+        if (i < a.prefixes) {
+            int lo, hi;
+            plan_run(a, i, lo, hi);
+            row0 = plan_row(a, lo);
+            rows = plan_rows(a, lo, hi);
+            len = plan_length(a.prefix_lengths[i], a.prefix_tokens);
+            if (!apart[i]) rows = 0;  // in front of its sequences' tokens
+        } else {
+            const int s = i - a.prefixes;
+            row0 = plan_row(a, s);
+            rows = plan_rows(a, s, s + 1);
+            len = plan_length(a.lengths[s], a.own_tokens);
+            prefix = seq_prefix[s];
+            if (prefix >= 0 && !apart[prefix])
+                front = plan_length(a.prefix_lengths[prefix], a.prefix_tokens);
+        }
+        const int M = rows * a.rep;
+        int tile = 16;
+        while (tile < M && tile < wide) tile *= 2;
+        const int tiles = (M + tile - 1) / tile, blocks = plan_blocks(front) + plan_blocks(len);
+        int* r = a.plan + a.at.stacks + (long long)i * kStackInts;
+        r[kStackRow0] = row0;
+        r[kStackRows] = rows;
+        r[kStackLen] = len;
+        r[kStackTiles] = tiles;
+        r[kStackTile] = tile;
+        r[kStackBlocks] = blocks;
+        r[kStackFront] = front;
+        r[kStackPrefix] = prefix;
+        work += (long long)a.kv_heads * tiles * blocks * plan_weight(tile);
     }
     work = block_sum64(work, s_sum);
-    const int chunk = (int)min(max((long long)kAttnLeast, (work + kAttnTarget - 1) / kAttnTarget), 0x3FFFFFFFll);
-    auto items_of = [&](const Stack& k) {
-        return (long long)a.kv_heads * k.mtiles * ((k.blocks + chunk - 1) / chunk);
+    const long long chunk = max((long long)kAttnLeast, (work + kAttnTarget - 1) / kAttnTarget);
+    auto record = [&](int i) { return a.plan + a.at.stacks + (long long)i * kStackInts; };
+    auto chunks_of = [&](const int* r) {
+        if (r[kStackRows] == 0 || r[kStackBlocks] == 0) return 0;
+        const long long w = (long long)r[kStackBlocks] * plan_weight(r[kStackTile]);
+        return (int)max(1ll, (10 * w + 3 * chunk) / (10 * chunk));
     };
     // Row tables whose sequences overlap could ask for more than there is: no work then.
     long long items = 0, slots = 0;
     for (int i = tid; i < n; i += kPlanThreads) {
-        const Stack k = plan_stack(a, i);
-        items += items_of(k);
-        slots += items_of(k) * k.tile;
+        const int* r = record(i);
+        const long long mine = (long long)a.kv_heads * r[kStackTiles] * chunks_of(r);
+        items += mine;
+        slots += mine * r[kStackTile];
     }
     items = block_sum64(items, s_sum);
     slots = block_sum64(slots, s_sum);
@@ -115,26 +149,23 @@ __global__ __launch_bounds__(kPlanThreads) void attn_plan_kernel(PlanArgs a) {
     long long item_base = 0, slot_base = 0;
     for (int base = 0; base < n; base += kPlanThreads) {
         const int i = base + tid;
-        Stack k{};
-        long long mine = 0;
-        if (i < n && fits) {
-            k = plan_stack(a, i);
-            mine = items_of(k);
-        }
+        const bool live = i < n;
+        int* r = record(live ? i : 0);
+        const int chunks = live && fits ? chunks_of(r) : 0;
+        const long long mine = live ? (long long)a.kv_heads * r[kStackTiles] * chunks : 0;
+        const long long size = live ? mine * r[kStackTile] : 0;
         long long all_items, all_slots;
         const long long i1 = block_scan64(mine, s_sum, all_items);
-        const long long s1 = block_scan64(mine * k.tile, s_sum, all_slots);
-        if (i < n) {
-            k = plan_stack(a, i);
-            int* r = a.plan + a.at.stacks + (long long)i * kStackInts;
-            r[0] = k.row0;
-            r[1] = k.rows;
-            r[2] = k.len;
-            r[3] = (int)(item_base + i1 - mine);
-            r[4] = mine ? (k.blocks + chunk - 1) / chunk : 0;
-            r[5] = k.mtiles;
-            r[6] = k.tile;
-            r[7] = (int)(slot_base + s1 - mine * k.tile);
+        const long long s1 = block_scan64(size, s_sum, all_slots);
+        if (live) {
+            // One chunk, and no prefix apart: the rows' outputs come from their items.
+            const int g = r[kStackPrefix];
+            const bool alone = i >= a.prefixes && chunks == 1 &&
+                               (g < 0 || !apart[g] || plan_length(a.prefix_lengths[g], a.prefix_tokens) == 0);
+            r[kStackItem0] = (int)(item_base + i1 - mine);
+            r[kStackChunks] = chunks;
+            r[kStackSlot0] = (int)(slot_base + s1 - size);
+            r[kStackDone] = alone;
         }
         item_base += all_items;
         slot_base += all_slots;
@@ -142,38 +173,43 @@ __global__ __launch_bounds__(kPlanThreads) void attn_plan_kernel(PlanArgs a) {
     if (tid == 0) {
         a.plan[0] = fits ? (int)items : 0;
         a.plan[1] = fits ? (int)slots : 0;
-        a.plan[2] = chunk;
+        a.plan[2] = (int)min(chunk, 0x7FFFFFFFll);
     }
-    __syncthreads();  // the stacks' records are read below by other threads of this workgroup
-    // Rows of no sequence.
-    const int first = plan_row(a, 0), last = plan_row(a, a.seqs);
-    for (int r = tid; r < a.rows; r += kPlanThreads)
-        if (r < first || r >= last) a.plan[a.at.row_seq + r] = -1;
-    // Items, one stack a wave; rows and sequences of the stack.
-    for (int i = tid / 64; i < n; i += kPlanThreads / 64) {
-        const Stack k = plan_stack(a, i);
-        const int* r = a.plan + a.at.stacks + (long long)i * kStackInts;
-        const int item0 = r[3], chunks = r[4], slot0 = r[7];
-        for (int j = lane; j < a.kv_heads * k.mtiles * chunks; j += 64) {
-            const int t = j / chunks, part = j - t * chunks;  // (head, tile), chunk
-            const int head = t / k.mtiles, mt = t - head * k.mtiles;
-            int* e = a.plan + a.at.items + (long long)(item0 + j) * kItemInts;
-            e[0] = i;
-            e[1] = head;
-            e[2] = mt * k.tile;
-            e[3] = (int)((long long)k.blocks * part / chunks);  // chunks of a stack alike in length
-            e[4] = (int)((long long)k.blocks * (part + 1) / chunks);
-            e[5] = slot0 + j * k.tile;
-            e[6] = k.tile;
-            e[7] = 0;
+    __syncthreads();
+    // Items, one stack a wave, later tiles (which see more keys) first; rows of the stack.
+    for (int i = wave; i < n; i += kWaves) {
+        const int* r = record(i);
+        const bool own = i >= a.prefixes;
+        const int row0 = r[kStackRow0], rows = r[kStackRows], len = r[kStackLen], chunks = r[kStackChunks];
+        const int tiles = r[kStackTiles], tile = r[kStackTile], front = r[kStackFront];
+        const int M = rows * a.rep, hidden = len - rows;
+        for (int j = lane; j < a.kv_heads * tiles * chunks; j += 64) {
+            const int t = j / chunks, part = j - t * chunks;
+            const int mt = tiles - 1 - t / a.kv_heads, head = t % a.kv_heads;
+            // Steps that the tile's last row sees, shared out over its chunks.
+            const int end = min((mt + 1) * tile, M) - 1;
+            const int seen = own ? min(max(hidden + end / a.rep + 1, 0), len) : len;
+            const int blocks = plan_blocks(front) + plan_blocks(seen);
+            int* e = a.plan + a.at.items + (long long)(r[kStackItem0] + j) * kItemInts;
+            e[kItemTile] = tile;
+            e[kItemHead] = head;
+            e[kItemM0] = mt * tile;
+            e[kItemBlk0] = (int)((long long)blocks * part / chunks);
+            e[kItemBlk1] = (int)((long long)blocks * (part + 1) / chunks);
+            e[kItemSlot] = r[kStackSlot0] + ((head * tiles + mt) * chunks + part) * tile;
+            e[kItemRow0] = row0;
+            e[kItemM] = M;
+            e[kItemLen] = len;
+            e[kItemHidden] = hidden;
+            e[kItemTable] = own ? i - a.prefixes : i;
+            e[kItemOwn] = own;
+            e[kItemFrontLen] = front;
+            e[kItemFrontTable] = r[kStackPrefix];
+            e[kItemFrontBlocks] = plan_blocks(front);
+            e[kItemFinal] = r[kStackDone];
         }
-        if (i >= a.prefixes) {
-            for (int j = lane; j < k.rows; j += 64) a.plan[a.at.row_seq + k.row0 + j] = i - a.prefixes;
-        } else {
-            const int s0 = a.prefix_indptr ? min(max(a.prefix_indptr[i], 0), a.seqs) : 0;
-            const int s1 = a.prefix_indptr ? min(max(a.prefix_indptr[i + 1], s0), a.seqs) : a.seqs;
-            for (int s = s0 + lane; s < s1; s += 64) a.plan[a.at.seq_prefix + s] = i;
-        }
+        if (own)
+            for (int j = lane; j < rows; j += 64) a.plan[a.at.row_seq + row0 + j] = i - a.prefixes;
     }
 }
 

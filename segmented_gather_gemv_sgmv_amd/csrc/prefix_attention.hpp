@@ -48,7 +48,7 @@ struct AttnArgs {
     float2* part_ml;                  // [slot]: maximum (of base 2), sum
     int rows, seqs, prefixes, q_heads, kv_heads, rep, D;
     float c;                          // scale * log2(e)
-    int vec;                          // q takes 16-byte loads
+    int vec, o_vec;                   // q takes 16-byte loads, o stores of 4 elements
 };
 
 // ---------------------------------------------------------------------------
@@ -166,60 +166,74 @@ struct AttnTypes {
     using KT = std::conditional_t<std::is_same<QT, F16>::value, F16, BF16>;  // operands of S
 };
 
-// An item as its workgroup sees it.
-struct Item {
-    int head, m0, row0, M, len, blk0, blk1, slot, tile;
-    bool own;
-    int hidden;         // own: tokens before the first row
+// An item as its workgroup sees it.  Its steps of 64 keys run over the prefix in front, if any, and then over the
+// stack's keys.
+struct Keys {
+    int len;
     const int* table;   // pages
+};
+struct Item {
+    int tile, head, m0, blk0, blk1, slot, row0, M;
+    Keys keys, front;
+    int front_blocks;
+    bool own, final;    // own: the rows are the last of the keys' tokens; final: outputs come from here
+    int hidden;         // own: tokens before the first row
     uint32_t stride, base;  // blocks of a page (of all heads), of the heads before this one
 };
 
 __device__ __forceinline__ Item attn_item(const AttnArgs& a, const int* e) {
     Item t;
-    const int stack = e[0];
-    const int* rec = a.plan + a.at.stacks + (long long)stack * kStackInts;
-    t.head = e[1];
-    t.m0 = e[2];
-    t.blk0 = e[3];
-    t.blk1 = e[4];
-    t.slot = e[5];
-    t.tile = e[6];
-    t.row0 = rec[0];
-    t.M = rec[1] * a.rep;
-    t.len = rec[2];
-    t.own = stack >= a.prefixes;
-    t.hidden = t.len - rec[1];
-    t.table = t.own ? a.own_pages + (long long)(stack - a.prefixes) * a.own_width
-                    : a.prefix_pages + (long long)stack * a.prefix_width;
+    t.tile = e[kItemTile];
+    t.head = e[kItemHead];
+    t.m0 = e[kItemM0];
+    t.blk0 = e[kItemBlk0];
+    t.blk1 = e[kItemBlk1];
+    t.slot = e[kItemSlot];
+    t.row0 = e[kItemRow0];
+    t.M = e[kItemM];
+    t.own = e[kItemOwn] != 0;
+    t.hidden = e[kItemHidden];
+    t.final = e[kItemFinal] != 0;
+    t.keys.len = e[kItemLen];
+    t.keys.table = t.own ? a.own_pages + (long long)e[kItemTable] * a.own_width
+                         : a.prefix_pages + (long long)e[kItemTable] * a.prefix_width;
+    t.front.len = e[kItemFrontLen];
+    t.front.table = a.prefix_pages + (long long)max(e[kItemFrontTable], 0) * a.prefix_width;
+    t.front_blocks = e[kItemFrontBlocks];
     t.stride = (uint32_t)a.kv_heads * a.blocks_per_page;
     t.base = (uint32_t)t.head * a.blocks_per_page;
     return t;
 }
 
-// 16-token block `b` of the item's keys: its page's entry in the table and its place in the page.  Asked for a step
+// 16-token block `b` of some keys: its page's entry in the table and its place in the page.  Asked for a step
 // ahead of the loads that need it, in no branch and looked at only then, so that no step waits for it.
 struct KeyBlock {
-    int b, in, page;
+    int in, page;
+    bool there;
 };
-__device__ __forceinline__ KeyBlock key_block(const AttnArgs& a, const Item& it, int b) {
+__device__ __forceinline__ KeyBlock key_block(const AttnArgs& a, const Keys& keys, int b) {
     KeyBlock k;
-    k.b = b;
-    const uint32_t c = (uint32_t)min(b, (it.len - 1) / kKvBlock);  // any entry where there is none; an item has a token
+    k.there = b * kKvBlock < keys.len;
+    const uint32_t c = (uint32_t)max(min(b, (keys.len - 1) / kKvBlock), 0);  // any entry where there is none
     const uint32_t index = __umulhi(c, a.page_magic) + (c & a.page_one);
     k.in = (int)(c - index * (uint32_t)a.blocks_per_page);
-    k.page = it.table[index];
+    k.page = keys.table[index];
     return k;
 }
 // Where it lies, counted over pages and heads, and whether it is there (else some block of the cache).
 __device__ __forceinline__ uint64_t place_of(const AttnArgs& a, const Item& it, const KeyBlock& k, bool& ok) {
-    ok = k.b * kKvBlock < it.len && (unsigned)k.page < (unsigned)a.num_pages;
+    ok = k.there && (unsigned)k.page < (unsigned)a.num_pages;
     return (uint64_t)(ok ? (uint32_t)k.page : 0u) * it.stride + (it.base + (uint32_t)k.in);
 }
 constexpr int kWaitLoads = 0x0F70;  // s_waitcnt: no load outstanding, LDS and scalars as they are
 
 // Keeps loads before it where they are written: without, a loop's loads for its next round are moved into that round.
 __device__ __forceinline__ void loads_stay() { asm volatile("" ::: "memory"); }
+
+// Natural logarithm of l 2^m, minus infinity for no key.
+__device__ __forceinline__ float log_sum(float m, float l) {
+    return l == 0.f ? -__builtin_inff() : (m + __builtin_log2f(l)) * 0.69314718055994531f;
+}
 
 // HEAD: p is held times 2^HEAD.  TERMS: operands that p is split into, one after the other.
 template <typename QT, int BITS, int P, int R, typename VT, int TERMS, int HEAD>
@@ -229,7 +243,7 @@ struct AttnRows {
     uint4 qf[R][A::kQTerms][A::kSteps];
     acc4_t o[R][A::kDTiles], s[R][4];
     float mref[R], l[R];
-    int lim[R];   // keys that the lane's row sees
+    int lim[R];   // keys that the lane's row sees (behind a prefix in front)
     int m_first;  // first row of the wave
     int blk_end;  // blocks that any of its rows sees
 
@@ -237,15 +251,15 @@ struct AttnRows {
     __device__ __forceinline__ void init(const AttnArgs& a, const Item& it, int first, int lr, int lg) {
         m_first = first;
         const int last = min(first + 16 * R, it.M) - 1;
-        const int most = last < first ? 0 : it.own ? it.hidden + last / a.rep + 1 : it.len;
-        blk_end = min(it.blk1, (most + kAttnKeys - 1) / kAttnKeys);
+        const int most = last < first ? -it.front_blocks * kAttnKeys : it.own ? it.hidden + last / a.rep + 1 : it.keys.len;
+        blk_end = min(it.blk1, it.front_blocks + (most + kAttnKeys - 1) / kAttnKeys);
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             const int m = first + 16 * r + lr;
             const bool ok = m < it.M;
             const int i = ok ? m / a.rep : 0;
             const int h = it.head * a.rep + (ok ? m - i * a.rep : 0);
-            lim[r] = ok && it.own ? it.hidden + i + 1 : it.len;
+            lim[r] = ok && it.own ? it.hidden + i + 1 : it.keys.len;
             mref[r] = -__builtin_inff();
             l[r] = 0.f;
 #pragma unroll
@@ -292,21 +306,23 @@ struct AttnRows {
                 s[r][t] = PieceOps<KT>::mma(kf, qf[r][y][x], x == 0 && y == 0 ? acc4_t{0.f, 0.f, 0.f, 0.f} : s[r][t]);
     }
 
-    // Of the lane's 16 keys from `first` on, `there` are in the cache: whether every row of the wave
-    // sees all of its 16.
-    __device__ __forceinline__ bool all_seen(int first, int there) const {
-        bool whole = there >= 16;
+    // Of the lane's 16 keys from `first` on, `there` are in the cache; rows see all of a prefix in `front` of their own
+    // keys.  How many a row sees, and whether every row of the wave sees all of its 16.
+    __device__ __forceinline__ int seen(int r, int first, int there, bool front) const {
+        return front ? there : min(lim[r] - first, there);
+    }
+    __device__ __forceinline__ bool all_seen(int first, int there, bool front) const {
+        bool whole = true;
 #pragma unroll
-        for (int r = 0; r < R; ++r) whole = whole && lim[r] - first >= 16;
+        for (int r = 0; r < R; ++r) whole = whole && seen(r, first, there, front) >= 16;
         return __all(whole);
     }
-    __device__ __forceinline__ int seen(int r, int first, int there) const { return min(lim[r] - first, there); }
 
     // Keys that a row does not see: their scores.
-    __device__ __forceinline__ void mask(int first, int there) {
+    __device__ __forceinline__ void mask(int first, int there, bool front) {
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-            const int rem = seen(r, first, there);
+            const int rem = seen(r, first, there, front);
 #pragma unroll
             for (int t = 0; t < 16; ++t)
                 if (t >= rem) s[r][t / 4][t % 4] = -__builtin_inff();
@@ -369,12 +385,27 @@ struct AttnRows {
         for (int x = 0; x < TERMS; ++x) o[r][tile] = PieceOps<VT>::mma(vf, pf[x], o[r][tile]);
     }
 
-    // The wave's rows to their slots.
+    // The wave's rows to their slots, or to the outputs.
     __device__ __forceinline__ void write(const AttnArgs& a, const Item& it, int lr, int lg) const {
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             const int m = m_first + 16 * r + lr;
             if (m >= it.M) continue;
+            if (it.final) {
+                const int i = m / a.rep, h = it.head * a.rep + m - i * a.rep;
+                const long long row = it.row0 + i;
+                const float inv = l[r] == 0.f ? 0.f : 1.f / l[r];
+                typename QT::storage* out = (typename QT::storage*)a.o + row * a.o_row + (long long)h * a.o_head + lg * 4;
+#pragma unroll
+                for (int d = 0; d < A::kDTiles; ++d) {
+                    float f[4];
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) f[x] = o[r][d][x] * inv;
+                    store4f<QT>(out + 16 * d, a.D - 16 * d - lg * 4, a.o_vec, f);
+                }
+                if (a.lse && lg == 0) a.lse[row * a.q_heads + h] = log_sum(mref[r], l[r]);
+                continue;
+            }
             const long long slot = (long long)it.slot + m - it.m0;
             float* out = a.part_o + slot * P + lg * 4;
 #pragma unroll
@@ -430,11 +461,12 @@ __device__ __forceinline__ void attn_direct(const AttnArgs& a, const Item& it, u
     const int g0 = BITS == 8 ? 0 : (lg * (P / 4)) >> 5;
     // Where the next loads go.  Behind the last step they go on, to keys of the next chunk or to block 0 of a page:
     // with loads in a branch every step would wait for all of them.
-    KeyBlock at_k = key_block(a, it, blk * 4 + (lr >> 2)), at_v = key_block(a, it, blk * 4 + lg);
+    int next_k = blk * 4 + (lr >> 2), next_v = blk * 4 + lg;
+    KeyBlock at_k = key_block(a, it.keys, next_k), at_v = key_block(a, it.keys, next_v);
     auto load_k = [&] {
         bool ok;
         const uint64_t b = place_of(a, it, at_k, ok);
-        at_k = key_block(a, it, at_k.b + 4 * waves_k);
+        at_k = key_block(a, it.keys, next_k += 4 * waves_k);
         const uint8_t* p = a.k + (b * 16 + (lr & 3)) * A::kRow + lg * A::kPiece;
 #pragma unroll
         for (int t = 0; t < 4; ++t) load_words<A::kPiece>(p + t * 4 * A::kRow, kw[t]);
@@ -444,7 +476,7 @@ __device__ __forceinline__ void attn_direct(const AttnArgs& a, const Item& it, u
     };
     auto load_v = [&] {
         const uint64_t b = place_of(a, it, at_v, v_ok);
-        at_v = key_block(a, it, at_v.b + 4 * waves_k);
+        at_v = key_block(a, it.keys, next_v += 4 * waves_k);
         const uint8_t* p = a.v + (b * A::kRow + lr) * 16;
 #pragma unroll
         for (int i = 0; i < A::kLines; ++i) load_words<16>(p + i * 256, vw[i]);
@@ -455,8 +487,8 @@ __device__ __forceinline__ void attn_direct(const AttnArgs& a, const Item& it, u
     // anything, and a NaN's must not meet rows that do not see it: both become 0, and the rows
     // that do see it (returned) are to be made NaN.
     auto partial = [&](int first, int there) {
-        rows.mask(first, there);
-        const int rem = rows.seen(0, first, there);
+        rows.mask(first, there, false);
+        const int rem = rows.seen(0, first, there, false);
         bool poison = false;
 #pragma unroll
         for (int t = 0; t < 16; ++t) {
@@ -493,9 +525,9 @@ __device__ __forceinline__ void attn_direct(const AttnArgs& a, const Item& it, u
         }
         load_k();
         const int first = blk * kAttnKeys + lg * 16;
-        const int there = v_ok ? it.len - first : 0;
+        const int there = v_ok ? it.keys.len - first : 0;
         bool poison = false;
-        if (!rows.all_seen(first, there)) poison = partial(first, there);
+        if (!rows.all_seen(first, there, false)) poison = partial(first, there);
         rows.soften(a.c);
         uint4 pf[2][kTerms];
 #pragma unroll
@@ -598,8 +630,8 @@ __device__ __forceinline__ void attn_shared(const AttnArgs& a, const Item& it, u
     int end = 0;  // of the workgroup's rows
     {
         const int last = min(it.m0 + it.tile, it.M) - 1;
-        const int most = it.own ? it.hidden + last / a.rep + 1 : it.len;
-        end = min(it.blk1, (most + kAttnKeys - 1) / kAttnKeys);
+        const int most = it.own ? it.hidden + last / a.rep + 1 : it.keys.len;
+        end = min(it.blk1, it.front_blocks + (most + kAttnKeys - 1) / kAttnKeys);
     }
 
     // Codes of the next step; vb: its scale bytes of V, one token a lane.
@@ -607,13 +639,22 @@ __device__ __forceinline__ void attn_shared(const AttnArgs& a, const Item& it, u
     bool ok = false;
     const int g0 = BITS == 8 ? 0 : (lg * (P / 4)) >> 5;
     // Where the next loads go; as in attn_direct they go on behind the last step.
-    KeyBlock at_k = key_block(a, it, it.blk0 * 4 + (lr >> 2)), at_v = key_block(a, it, it.blk0 * 4 + lg);
+    int next = it.blk0;
+    KeyBlock at_k, at_v;
+    auto seek = [&] {
+        const bool front = next < it.front_blocks;
+        const Keys keys = front || it.keys.len == 0 ? it.front : it.keys;
+        const int b = (front ? next : next - it.front_blocks) * 4;
+        at_k = key_block(a, keys, b + (lr >> 2));
+        at_v = key_block(a, keys, b + lg);
+        ++next;
+    };
+    seek();
     auto load = [&] {
         bool there;
         const uint64_t bk = place_of(a, it, at_k, there);
         const uint64_t bv = place_of(a, it, at_v, ok);
-        at_k = key_block(a, it, at_k.b + 4);
-        at_v = key_block(a, it, at_v.b + 4);
+        seek();
         const int token = wave * 4 + (lr & 3);
         load_words<A::kPiece>(a.k + (bk * 16 + token) * A::kRow + lg * A::kPiece, kw);
 #pragma unroll
@@ -630,8 +671,11 @@ __device__ __forceinline__ void attn_shared(const AttnArgs& a, const Item& it, u
     // lane's block of 16 tokens is there.
     int eref = 20, eref_next = 20;
     bool nan = false, nan_next = false, ok_now = false;
+    // Step blk among its keys: the first of them, and how many there are.
+    auto key_of = [&](int blk) { return (blk < it.front_blocks ? blk : blk - it.front_blocks) * kAttnKeys; };
+    auto len_of = [&](int blk) { return blk < it.front_blocks ? it.front.len : it.keys.len; };
     auto convert = [&](int blk, uint4* to) {
-        const bool there = ok && blk * kAttnKeys + lane < it.len;
+        const bool there = ok && key_of(blk) + lane < len_of(blk);
         nan_next = __any(there && vb[0] == kKvNaN);
         int top = 0;
 #pragma unroll
@@ -749,9 +793,10 @@ __device__ __forceinline__ void attn_shared(const AttnArgs& a, const Item& it, u
         convert(blk + 1, stage + (n ^ 1) * kStage);
         load();
         if (mine) {
-            const int first = blk * kAttnKeys + lg * 16;
-            const int there = ok_now ? it.len - first : 0;
-            if (!rows.all_seen(first, there)) rows.mask(first, there);
+            const int first = key_of(blk) + lg * 16;
+            const int there = ok_now ? len_of(blk) - first : 0;
+            const bool front = blk < it.front_blocks;
+            if (!rows.all_seen(first, there, front)) rows.mask(first, there, front);
             // V's operands four pieces ahead of their products, the first ones across the exponentials.
             constexpr int kAhead = 4;
             uint4 vf[2][kAhead];
@@ -787,12 +832,13 @@ __device__ __forceinline__ void attn_shared(const AttnArgs& a, const Item& it, u
             if (__builtin_expect(nan, 0)) {
                 // A NaN's values went in as zeros: rows that see it are made NaN.
                 bool here;
-                const uint64_t b = place_of(a, it, key_block(a, it, blk * 4 + lg), here);
+                const uint64_t b =
+                    place_of(a, it, key_block(a, front ? it.front : it.keys, key_of(blk) / kKvBlock + lg), here);
                 uint32_t w[4];
                 load_words<16>(a.v_scales + b * A::kGroups * 16, w);
 #pragma unroll
                 for (int r = 0; r < R; ++r) {
-                    const int rem = rows.seen(r, first, there);
+                    const int rem = rows.seen(r, first, there, front);
                     float bad = 0.f;
 #pragma unroll
                     for (int t = 0; t < 16; ++t)
@@ -844,57 +890,79 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a) {
     if (seq < 0 || seq >= a.seqs) return;
     // The sequence's stack and its prefix's, looked over since a table may be malformed.
     int first[2], step[2], chunks[2];
+    int prefix = -1;
 #pragma unroll
     for (int w = 0; w < 2; ++w) {
         first[w] = step[w] = chunks[w] = 0;
-        int stack = a.prefixes + seq;
-        if (w == 1) {
-            if (a.prefixes == 0) continue;
-            stack = a.plan[a.at.seq_prefix + seq];
-            if (stack < 0 || stack >= a.prefixes) continue;
-        }
+        const int stack = w == 0 ? a.prefixes + seq : prefix;
+        if (stack < 0 || (w == 1 && stack >= a.prefixes)) continue;
         const int* r = a.plan + a.at.stacks + (long long)stack * kStackInts;
-        if (row < r[0] || row >= r[0] + r[1]) {
+        if (w == 0) {
+            if (r[kStackDone]) return;
+            prefix = r[kStackPrefix];
+        }
+        if (row < r[kStackRow0] || row >= r[kStackRow0] + r[kStackRows]) {
             if (w == 0) return;  // covered by no sequence after all
             continue;
         }
-        const int m = (row - r[0]) * a.rep + h % a.rep, mt = m / r[6];
-        chunks[w] = r[4];
-        step[w] = r[6];
-        first[w] = r[7] + ((h / a.rep) * r[5] + mt) * r[4] * r[6] + (m - mt * r[6]);
+        const int tile = r[kStackTile], m = (row - r[kStackRow0]) * a.rep + h % a.rep, mt = m / tile;
+        chunks[w] = r[kStackChunks];
+        step[w] = tile;
+        first[w] = r[kStackSlot0] + ((h / a.rep) * r[kStackTiles] + mt) * chunks[w] * tile + (m - mt * tile);
     }
     const int n = chunks[0] + chunks[1];
     auto slot = [&](int j) {
-        return j < chunks[0] ? first[0] + j * step[0] : first[1] + (j - chunks[0]) * step[1];
+        return (long long)(j < chunks[0] ? first[0] + j * step[0] : first[1] + (j - chunks[0]) * step[1]);
     };
-    float m = -__builtin_inff();
-    for (int j = lane; j < n; j += kLanes) {
-        const float2 x = a.part_ml[slot(j)];
-        if (x.y != 0.f) m = fmaxf(m, x.x);
-    }
+    // Factors of the items' results, one a lane; where there are more items than lanes, in turns, what was summed
+    // before becoming one more result.
+    float m = -__builtin_inff(), l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    const bool mine = lane * 4 < P;
+    for (int j0 = 0; j0 < n; j0 += kLanes) {
+        const int count = min(n - j0, kLanes);
+        float2 x = make_float2(-__builtin_inff(), 0.f);
+        if (lane < count) x = a.part_ml[slot(j0 + lane)];
+        float top = x.y != 0.f ? x.x : -__builtin_inff();  // no key was visible: nothing; a NaN goes on
 #pragma unroll
-    for (int k = 1; k < kLanes; k *= 2) m = fmaxf(m, __shfl_xor(m, k));
-    float l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
-    for (int j = 0; j < n; ++j) {
-        const float2 x = a.part_ml[slot(j)];
-        if (x.y == 0.f) continue;  // no key was visible; a NaN goes on
-        const float f = x.x == m ? 1.f : __builtin_amdgcn_exp2f(x.x - m);
-        l += f * x.y;
-        if (lane * 4 < P) {
-            const float4 v = *reinterpret_cast<const float4*>(a.part_o + (long long)slot(j) * P + lane * 4);
-            o[0] += f * v.x;
-            o[1] += f * v.y;
-            o[2] += f * v.z;
-            o[3] += f * v.w;
+        for (int k = 1; k < kLanes; k *= 2) top = fmaxf(top, __shfl_xor(top, k));
+        top = fmaxf(top, m);
+        const float keep = l == 0.f ? 0.f : m == top ? 1.f : __builtin_amdgcn_exp2f(m - top);
+        const float f = x.y == 0.f ? 0.f : x.x == top ? 1.f : __builtin_amdgcn_exp2f(x.x - top);
+        float sum = f * x.y;
+#pragma unroll
+        for (int k = 1; k < kLanes; k *= 2) sum += __shfl_xor(sum, k);
+        l = l * keep + sum;
+        o.x *= keep;
+        o.y *= keep;
+        o.z *= keep;
+        o.w *= keep;
+        m = top;
+        for (int j = 0; j < count; j += 8) {
+            float4 v[8];
+            float g[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const int at = min(j + k, count - 1);
+                const float fk = __shfl(f, at, kLanes);
+                g[k] = j + k < count ? fk : 0.f;
+                v[k] = *reinterpret_cast<const float4*>(a.part_o + slot(j0 + at) * P + (mine ? lane * 4 : 0));
+            }
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                if (g[k] == 0.f) continue;  // may hold anything
+                o.x += g[k] * v[k].x;
+                o.y += g[k] * v[k].y;
+                o.z += g[k] * v[k].z;
+                o.w += g[k] * v[k].w;
+            }
         }
     }
     const float inv = l == 0.f ? 0.f : 1.f / l;
-    T* out = (T*)a.o + (long long)row * a.o_row + (long long)h * a.o_head;
-#pragma unroll
-    for (int x = 0; x < 4; ++x)
-        if (lane * 4 + x < a.D) out[lane * 4 + x] = DT::from_float(o[x] * inv);
-    if (a.lse && lane == 0)
-        a.lse[i] = l == 0.f ? -__builtin_inff() : (m + __builtin_log2f(l)) * 0.69314718055994531f;
+    T* out = (T*)a.o + (long long)row * a.o_row + (long long)h * a.o_head + lane * 4;
+    const float f[4] = {o.x * inv, o.y * inv, o.z * inv, o.w * inv};
+    if (mine) store4f<DT>(out, a.D - lane * 4, a.o_vec, f);
+    if (a.lse && lane == 0) a.lse[i] = log_sum(m, l);
 }
 
 }  // namespace sgmv

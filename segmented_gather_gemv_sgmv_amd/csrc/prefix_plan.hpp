@@ -5,8 +5,10 @@
 // share a prefix over that prefix, or the rows of one sequence over its own tokens.  The
 // heads that share a K / V head lie on top of each other, so a stack has
 // M = rows * q_heads / kv_heads rows per K / V head.  An item is a tile of these rows (16, 32,
-// 64 or, with two tiles a wave, 128) over a chunk of the keys; its results go to the
-// workspace and are joined per row.
+// 64 or, with two tiles a wave, 128) over a chunk of the keys.  Where every sequence of a run fills the
+// largest tile (prompts), the prefix is put in front of each sequence's own tokens instead: the prefix is read
+// by each tile either way.  A row whose keys are one item's has its output from there; the results of the others
+// go to the workspace and are joined per row.
 #pragma once
 
 #include <stddef.h>
@@ -19,10 +21,18 @@ namespace sgmv {
 constexpr int kAttnWaves = 4;            // of an item's workgroup
 constexpr int kAttnThreads = 64 * kAttnWaves;
 constexpr int kAttnKeys = 64;            // keys of a wave's step
-constexpr int kAttnTarget = 768;        // items to aim at
-constexpr int kAttnLeast = 4;            // steps of an item, at least
-constexpr int kPlanHeader = 16;          // ints: items, slots, chunk
-constexpr int kStackInts = 8, kItemInts = 8;
+// Items to aim at: two workgroups a CU and some to even out.  A stack is cut into chunks of about
+// work / target, or not at all below 1.7 of that.  Work is counted in steps of 64 keys of a tile; a step of 64
+// or 128 rows takes about twice as long as one of up to 32.
+constexpr int kAttnTarget = 640;
+constexpr int kAttnLeast = 8;            // work of an item, at least
+constexpr int kPlanHeader = 16;          // ints: items, slots, work of a chunk
+
+// Records of the plan, in ints.
+enum { kStackRow0, kStackRows, kStackLen, kStackItem0, kStackChunks, kStackTiles, kStackTile, kStackSlot0,
+       kStackBlocks, kStackFront, kStackPrefix, kStackDone, kStackInts };
+enum { kItemTile, kItemHead, kItemM0, kItemBlk0, kItemBlk1, kItemSlot, kItemRow0, kItemM, kItemLen, kItemHidden,
+       kItemTable, kItemOwn, kItemFrontLen, kItemFrontTable, kItemFrontBlocks, kItemFinal, kItemInts };
 
 // Row tiles of 16 that a wave keeps at once: two halve the conversions of codes per
 // row, where the registers hold them (heads of up to 128; float32 has three terms of q).
@@ -39,16 +49,17 @@ inline AttnSizes attn_sizes(long long rows, long long seqs, long long prefixes, 
     const long long rep = q_heads / kv_heads, most = attn_tile_most(padded, dtype), stacks = seqs + prefixes;
     AttnSizes s;
     // Every row is in at most one prefix's stack and one sequence's.  A stack has one tile, or one
-    // more than M / most; chunks beyond a tile's first are at most the target.
+    // more than M / most.  A tile of work w has at most w / chunk + 0.3 chunks: beyond the first of each tile
+    // these are no more than the target.
     s.items = kAttnTarget + kv_heads * (stacks + 2 * rows * rep / most);
     s.slots = kAttnTarget * most + kv_heads * (16 * stacks + 4 * rows * rep);
-    s.plan_ints = (size_t)(kPlanHeader + kStackInts * stacks + kItemInts * s.items + rows + seqs);
+    s.plan_ints = (size_t)(kPlanHeader + kStackInts * stacks + kItemInts * s.items + rows + seqs + prefixes);
     return s;
 }
 
 // Offsets into the plan's ints.
 struct PlanLayout {
-    long long stacks, items, row_seq, seq_prefix;
+    long long stacks, items, row_seq, seq_prefix, apart;
 };
 inline PlanLayout plan_layout(long long rows, long long seqs, long long prefixes, long long items) {
     PlanLayout l;
@@ -56,6 +67,7 @@ inline PlanLayout plan_layout(long long rows, long long seqs, long long prefixes
     l.items = l.stacks + kStackInts * (seqs + prefixes);
     l.row_seq = l.items + kItemInts * items;
     l.seq_prefix = l.row_seq + rows;
+    l.apart = l.seq_prefix + seqs;
     return l;
 }
 
