@@ -105,8 +105,8 @@ extern "C" int prefix_attention(void* o, float* lse, const void* q, const sgmv_k
     if (const int e = check_shape(cache, num_rows, num_seqs, num_prefixes, q_heads, dtype, &s)) return e;
     if (pages_per_seq < 0 || pages_per_prefix < 0 || !(scale > 0.f) || scale > 3e38f) return SGMV_ERR_BAD_SHAPE;
     if (!table_fits(cache, pages_per_seq) || !table_fits(cache, pages_per_prefix) ||
-        (long long)cache->kv_heads * (cache->page_size / kKvBlock) > 0x7FFFFFFFll)
-        return SGMV_ERR_UNSUPPORTED;
+        (long long)cache->num_pages * (cache->page_size / kKvBlock) * cache->kv_heads >= 0xFFFFFFFFll)
+        return SGMV_ERR_UNSUPPORTED;  // blocks over all heads are counted in 32 bits
     if (num_rows == 0 || num_seqs == 0) return SGMV_OK;
     if (const int e = kv_check(cache)) return e;
     if (!o || !q || !plan || !strides || (pages_per_seq > 0 && !pages) ||

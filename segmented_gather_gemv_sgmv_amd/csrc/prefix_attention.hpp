@@ -205,26 +205,55 @@ __device__ __forceinline__ Item attn_item(const AttnArgs& a, const int* e) {
     return t;
 }
 
-// 16-token block `b` of some keys: its page's entry in the table and its place in the page.  Asked for a step
-// ahead of the loads that need it, in no branch and looked at only then, so that no step waits for it.
-struct KeyBlock {
-    int in, page;
+// Where a wave's next steps find their keys: steps `first`, first + stride, ... of the item, four 16-token blocks
+// each.  A lane looks up one block, so the wave knows 16 steps at a time; a step gets its blocks from
+// their lanes.  Page entries for the 16 steps after that are asked for by every step (from L1), so that
+// the load stands in no branch and no step waits for the one it has just issued.
+struct KeyWalk {
+    static constexpr uint32_t kNone = ~0u;
+    const AttnArgs& a;
+    const Item& it;
+    int lane, blk, stride;     // blk: of the group to come
+    uint32_t cur;              // blocks of the group at hand, counted over pages and heads; kNone: not there
+    int pos, page, in;
     bool there;
+    const int* entry;          // of the group to come
+
+    __device__ __forceinline__ KeyWalk(const AttnArgs& args, const Item& item, int l, int first, int step)
+        : a(args), it(item), lane(l), blk(first), stride(step) {
+        aim();
+        page = *entry;
+        turn();
+        page = *entry;
+    }
+    // The lane's block of the group that begins at step blk.
+    __device__ __forceinline__ void aim() {
+        const int s = blk + (lane >> 2) * stride;
+        const bool front = s < it.front_blocks;
+        const Keys keys = front || it.keys.len == 0 ? it.front : it.keys;
+        const int b = (front ? s : s - it.front_blocks) * 4 + (lane & 3);
+        there = b * kKvBlock < keys.len && s < it.blk1;
+        const uint32_t c = there ? (uint32_t)b : 0u;  // entry 0 where there is none: an item has a token
+        const uint32_t index = __umulhi(c, a.page_magic) + (c & a.page_one);
+        in = (int)(c - index * (uint32_t)a.blocks_per_page);
+        entry = keys.table + index;
+    }
+    __device__ __forceinline__ void turn() {
+        const bool ok = there && (unsigned)page < (unsigned)a.num_pages;
+        cur = ok ? (uint32_t)page * it.stride + it.base + (uint32_t)in : kNone;
+        pos = 0;
+        blk += 16 * stride;
+        aim();
+    }
+    // Of the next step, the block of K that the lane's token lies in and the lane's block of V.
+    __device__ __forceinline__ void next(int sub_k, int sub_v, uint32_t& k, uint32_t& v) {
+        if (pos == 16) turn();
+        page = *entry;
+        k = (uint32_t)__builtin_amdgcn_ds_bpermute((pos * 4 + sub_k) * 4, (int)cur);
+        v = (uint32_t)__builtin_amdgcn_ds_bpermute((pos * 4 + sub_v) * 4, (int)cur);
+        ++pos;
+    }
 };
-__device__ __forceinline__ KeyBlock key_block(const AttnArgs& a, const Keys& keys, int b) {
-    KeyBlock k;
-    k.there = b * kKvBlock < keys.len;
-    const uint32_t c = (uint32_t)max(min(b, (keys.len - 1) / kKvBlock), 0);  // any entry where there is none
-    const uint32_t index = __umulhi(c, a.page_magic) + (c & a.page_one);
-    k.in = (int)(c - index * (uint32_t)a.blocks_per_page);
-    k.page = keys.table[index];
-    return k;
-}
-// Where it lies, counted over pages and heads, and whether it is there (else some block of the cache).
-__device__ __forceinline__ uint64_t place_of(const AttnArgs& a, const Item& it, const KeyBlock& k, bool& ok) {
-    ok = k.there && (unsigned)k.page < (unsigned)a.num_pages;
-    return (uint64_t)(ok ? (uint32_t)k.page : 0u) * it.stride + (it.base + (uint32_t)k.in);
-}
 constexpr int kWaitLoads = 0x0F70;  // s_waitcnt: no load outstanding, LDS and scalars as they are
 
 // Keeps loads before it where they are written: without, a loop's loads for its next round are moved into that round.
@@ -459,29 +488,29 @@ __device__ __forceinline__ void attn_direct(const AttnArgs& a, const Item& it, u
     uint32_t kw[4][A::kPiece / 4], ks[A::kKGroups][4], vw[A::kLines][4], vs[A::kGroups][4];
     bool v_ok = false;
     const int g0 = BITS == 8 ? 0 : (lg * (P / 4)) >> 5;
-    // Where the next loads go.  Behind the last step they go on, to keys of the next chunk or to block 0 of a page:
-    // with loads in a branch every step would wait for all of them.
-    int next_k = blk * 4 + (lr >> 2), next_v = blk * 4 + lg;
-    KeyBlock at_k = key_block(a, it.keys, next_k), at_v = key_block(a, it.keys, next_v);
+    // Behind the last step loads go on, to block 0 of the cache: in a branch they would have every step wait for all.
+    KeyWalk walk(a, it, lane, blk, waves_k);
+    uint32_t block_v;
     auto load_k = [&] {
-        bool ok;
-        const uint64_t b = place_of(a, it, at_k, ok);
-        at_k = key_block(a, it.keys, next_k += 4 * waves_k);
-        const uint8_t* p = a.k + (b * 16 + (lr & 3)) * A::kRow + lg * A::kPiece;
+        uint32_t b;
+        walk.next(lr >> 2, lg, b, block_v);
+        b = b == KeyWalk::kNone ? 0u : b;
+        const uint8_t* p = a.k + ((lr & 3) * A::kRow + lg * A::kPiece) + (uint64_t)b * (16 * A::kRow);
 #pragma unroll
         for (int t = 0; t < 4; ++t) load_words<A::kPiece>(p + t * 4 * A::kRow, kw[t]);
+        const uint8_t* scales = a.k_scales + (uint64_t)b * (16 * A::kGroups);
 #pragma unroll
-        for (int g = 0; g < A::kKGroups; ++g)
-            load_words<16>(a.k_scales + (b * A::kGroups + min(g0 + g, A::kGroups - 1)) * 16, ks[g]);
+        for (int g = 0; g < A::kKGroups; ++g) load_words<16>(scales + min(g0 + g, A::kGroups - 1) * 16, ks[g]);
     };
     auto load_v = [&] {
-        const uint64_t b = place_of(a, it, at_v, v_ok);
-        at_v = key_block(a, it.keys, next_v += 4 * waves_k);
-        const uint8_t* p = a.v + (b * A::kRow + lr) * 16;
+        v_ok = block_v != KeyWalk::kNone;
+        const uint32_t b = v_ok ? block_v : 0u;
+        const uint8_t* p = a.v + lr * 16 + (uint64_t)b * (16 * A::kRow);
 #pragma unroll
         for (int i = 0; i < A::kLines; ++i) load_words<16>(p + i * 256, vw[i]);
+        const uint8_t* scales = a.v_scales + (uint64_t)b * (16 * A::kGroups);
 #pragma unroll
-        for (int g = 0; g < A::kGroups; ++g) load_words<16>(a.v_scales + (b * A::kGroups + g) * 16, vs[g]);
+        for (int g = 0; g < A::kGroups; ++g) load_words<16>(scales + g * 16, vs[g]);
     };
     // A step whose keys are not all seen by all rows.  V's scales of tokens that are not there may be
     // anything, and a NaN's must not meet rows that do not see it: both become 0, and the rows
@@ -636,36 +665,30 @@ __device__ __forceinline__ void attn_shared(const AttnArgs& a, const Item& it, u
 
     // Codes of the next step; vb: its scale bytes of V, one token a lane.
     uint32_t kw[A::kPiece / 4], vw[kMine][4], ks[A::kKGroups], vb[A::kGroups];
+    const uint8_t *v_bytes = nullptr, *v_bytes_now = nullptr;  // of the lane's block
     bool ok = false;
     const int g0 = BITS == 8 ? 0 : (lg * (P / 4)) >> 5;
-    // Where the next loads go; as in attn_direct they go on behind the last step.
-    int next = it.blk0;
-    KeyBlock at_k, at_v;
-    auto seek = [&] {
-        const bool front = next < it.front_blocks;
-        const Keys keys = front || it.keys.len == 0 ? it.front : it.keys;
-        const int b = (front ? next : next - it.front_blocks) * 4;
-        at_k = key_block(a, keys, b + (lr >> 2));
-        at_v = key_block(a, keys, b + lg);
-        ++next;
-    };
-    seek();
+    KeyWalk walk(a, it, lane, it.blk0, 1);  // as in attn_direct loads go on behind the last step
+    const int token = wave * 4 + (lr & 3);
     auto load = [&] {
-        bool there;
-        const uint64_t bk = place_of(a, it, at_k, there);
-        const uint64_t bv = place_of(a, it, at_v, ok);
-        seek();
-        const int token = wave * 4 + (lr & 3);
-        load_words<A::kPiece>(a.k + (bk * 16 + token) * A::kRow + lg * A::kPiece, kw);
+        uint32_t bk, bv;
+        walk.next(lr >> 2, lg, bk, bv);
+        ok = bv != KeyWalk::kNone;
+        bk = bk == KeyWalk::kNone ? 0u : bk;
+        bv = ok ? bv : 0u;
+        load_words<A::kPiece>(a.k + (token * A::kRow + lg * A::kPiece) + (uint64_t)bk * (16 * A::kRow), kw);
+        const uint8_t* k_scales = a.k_scales + token + (uint64_t)bk * (16 * A::kGroups);
 #pragma unroll
-        for (int g = 0; g < A::kKGroups; ++g)
-            ks[g] = a.k_scales[(bk * A::kGroups + min(g0 + g, A::kGroups - 1)) * 16 + token];
+        for (int g = 0; g < A::kKGroups; ++g) ks[g] = k_scales[min(g0 + g, A::kGroups - 1) * 16];
+        const uint8_t* p = a.v + (wave * 16 + lr) * 16 + (uint64_t)bv * (16 * A::kRow);
 #pragma unroll
         for (int i = 0; i < kMine; ++i)
             if (A::kLines % kAttnWaves == 0 || i * kAttnWaves + wave < A::kLines)
-                load_words<16>(a.v + (bv * A::kRow + (i * kAttnWaves + wave) * 16 + lr) * 16, vw[i]);
+                load_words<16>(p + i * kAttnWaves * 256, vw[i]);
+        const uint8_t* v_scales = a.v_scales + lr + (uint64_t)bv * (16 * A::kGroups);
 #pragma unroll
-        for (int g = 0; g < A::kGroups; ++g) vb[g] = a.v_scales[(bv * A::kGroups + g) * 16 + lr];
+        for (int g = 0; g < A::kGroups; ++g) vb[g] = v_scales[g * 16];
+        v_bytes = a.v_scales + (uint64_t)bv * (16 * A::kGroups);
     };
     // Exponents of the converted steps (biased), whether one of their tokens is a NaN, and whether the
     // lane's block of 16 tokens is there.
@@ -756,6 +779,7 @@ __device__ __forceinline__ void attn_shared(const AttnArgs& a, const Item& it, u
         load();
         convert(blk, stage);
         ok_now = ok;
+        v_bytes_now = v_bytes;
         nan = nan_next;
         load();
         do {
@@ -790,6 +814,7 @@ __device__ __forceinline__ void attn_shared(const AttnArgs& a, const Item& it, u
             eref = eref_next;
         }
         const bool ok_then = ok;
+        const uint8_t* v_bytes_then = v_bytes;
         convert(blk + 1, stage + (n ^ 1) * kStage);
         load();
         if (mine) {
@@ -831,11 +856,8 @@ __device__ __forceinline__ void attn_shared(const AttnArgs& a, const Item& it, u
             }
             if (__builtin_expect(nan, 0)) {
                 // A NaN's values went in as zeros: rows that see it are made NaN.
-                bool here;
-                const uint64_t b =
-                    place_of(a, it, key_block(a, front ? it.front : it.keys, key_of(blk) / kKvBlock + lg), here);
                 uint32_t w[4];
-                load_words<16>(a.v_scales + b * A::kGroups * 16, w);
+                load_words<16>(v_bytes_now, w);
 #pragma unroll
                 for (int r = 0; r < R; ++r) {
                     const int rem = rows.seen(r, first, there, front);
@@ -850,6 +872,7 @@ __device__ __forceinline__ void attn_shared(const AttnArgs& a, const Item& it, u
             }
         }
         ok_now = ok_then;
+        v_bytes_now = v_bytes_then;
         nan = nan_next;
         n ^= 1;
         } while (++blk < end);
