@@ -358,9 +358,8 @@ struct AttnRows {
         }
     }
 
-    // Scores to p; running maxima and sums.
-    __device__ __forceinline__ void soften(float c) {
-        // Maxima are moved only where p would pass 2^4.
+    // Running maxima, moved only where p would pass 2^4.
+    __device__ __forceinline__ void maxima(float c) {
         float mx[R];
         bool move = false;
 #pragma unroll
@@ -382,15 +381,16 @@ struct AttnRows {
                 for (int t = 0; t < A::kDTiles; ++t) o[r][t] *= f;
             }
         }
+    }
+
+    // Scores of half u of the lane's keys, tile r, to p; running sums.
+    __device__ __forceinline__ void soften(float c, int r, int u) {
+        const float m = (mref[r] == -__builtin_inff() ? 0.f : mref[r]) - HEAD;
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
-            const float m = (mref[r] == -__builtin_inff() ? 0.f : mref[r]) - HEAD;
-#pragma unroll
-            for (int t = 0; t < 16; ++t) {
-                const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(s[r][t / 4][t % 4], c, -m));
-                s[r][t / 4][t % 4] = p;
-                l[r] += p;
-            }
+        for (int t = 8 * u; t < 8 * u + 8; ++t) {
+            const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(s[r][t / 4][t % 4], c, -m));
+            s[r][t / 4][t % 4] = p;
+            l[r] += p;
         }
     }
 
@@ -557,7 +557,9 @@ __device__ __forceinline__ void attn_direct(const AttnArgs& a, const Item& it, u
         const int there = v_ok ? it.keys.len - first : 0;
         bool poison = false;
         if (!rows.all_seen(first, there, false)) poison = partial(first, there);
-        rows.soften(a.c);
+        rows.maxima(a.c);
+        rows.soften(a.c, 0, 0);
+        rows.soften(a.c, 0, 1);
         uint4 pf[2][kTerms];
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
@@ -640,6 +642,18 @@ __device__ __forceinline__ void attn_direct(const AttnArgs& a, const Item& it, u
 // others, and V scaled relative to the largest exponent that the item has met, which all waves follow alike;
 // a value below 2^-32 of the largest is lost.  When a larger exponent comes, O is scaled down.
 // ---------------------------------------------------------------------------
+// Asks for MFMAS matrix instructions with VALU others, WRITES LDS writes and TRANS exponentials behind each.
+template <int MFMAS, int VALU, int WRITES, int TRANS>
+__device__ __forceinline__ void interleave() {
+#pragma unroll
+    for (int i = 0; i < MFMAS; ++i) {
+        __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(0x2, VALU, 0);
+        if constexpr (TRANS > 0) __builtin_amdgcn_sched_group_barrier(0x400, TRANS, 0);
+        if constexpr (WRITES > 0) __builtin_amdgcn_sched_group_barrier(0x200, WRITES, 0);
+    }
+}
+
 constexpr int kAttnHead = 11;  // p 2^11 reaches 2^15 at most
 
 template <typename QT, int BITS, int P, int R>
@@ -789,22 +803,6 @@ __device__ __forceinline__ void attn_shared(const AttnArgs& a, const Item& it, u
         __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
         const uint4* from = stage + n * kStage + lane;
         const bool mine = blk < rows.blk_end;
-        if (mine) {
-            uint4 kf[2][A::kSteps];
-#pragma unroll
-            for (int x = 0; x < A::kSteps; ++x) kf[0][x] = from[x * 64];
-#pragma unroll
-            for (int t = 0; t < 4; ++t) {
-                if (t < 3) {
-#pragma unroll
-                    for (int x = 0; x < A::kSteps; ++x) kf[(t + 1) & 1][x] = from[((t + 1) * A::kSteps + x) * 64];
-                }
-                __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-                for (int x = 0; x < A::kSteps; ++x) rows.score(t, x, kf[t & 1][x]);
-                __builtin_amdgcn_sched_barrier(0);
-            }
-        }
         if (eref_next > eref) {  // this step's values are relative to a larger exponent
             const float f = __builtin_ldexpf(1.f, max(eref - eref_next, -126));
 #pragma unroll
@@ -815,43 +813,80 @@ __device__ __forceinline__ void attn_shared(const AttnArgs& a, const Item& it, u
         }
         const bool ok_then = ok;
         const uint8_t* v_bytes_then = v_bytes;
+        // Scores, K's operands a tile ahead of their products; behind the last operands the next step's codes are
+        // converted, between the products: a wave issues one instruction in about five cycles, a product takes 16.
+        uint4 kf[2][A::kSteps];
+        auto fetch_k = [&](int t) {
+#pragma unroll
+            for (int x = 0; x < A::kSteps; ++x) kf[t & 1][x] = from[(t * A::kSteps + x) * 64];
+        };
+        auto score = [&](int t) {
+#pragma unroll
+            for (int x = 0; x < A::kSteps; ++x) rows.score(t, x, kf[t & 1][x]);
+        };
+        fetch_k(0);
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            fetch_k(t + 1);
+            __builtin_amdgcn_sched_barrier(0);
+            score(t);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        fetch_k(3);
+        score(2);
+        score(3);
         convert(blk + 1, stage + (n ^ 1) * kStage);
+        interleave<2 * A::kSteps * R * A::kQTerms, 4, 1, 0>();
         load();
         if (mine) {
             const int first = key_of(blk) + lg * 16;
             const int there = ok_now ? len_of(blk) - first : 0;
             const bool front = blk < it.front_blocks;
             if (!rows.all_seen(first, there, front)) rows.mask(first, there, front);
-            // V's operands four pieces ahead of their products, the first ones across the exponentials.
+            // V's operands four pieces ahead of their products, the first ones across the exponentials; p of the
+            // second half of the keys between the products of the first.
             constexpr int kAhead = 4;
             uint4 vf[2][kAhead];
-            auto fetch = [&](int i, uint4* to) {  // pieces [i, i + kAhead) in the order of their use: half u, tile
+            auto fetch = [&](int i) {  // pieces [i, i + kAhead) in the order of their use: half u, tile
 #pragma unroll
                 for (int x = 0; x < kAhead; ++x)
-                    to[x] = from[(kKPieces + (i + x) % A::kDTiles * 2 + (i + x) / A::kDTiles) * 64];
+                    vf[(i / kAhead) & 1][x] = from[(kKPieces + (i + x) % A::kDTiles * 2 + (i + x) / A::kDTiles) * 64];
             };
             static_assert(A::kDTiles % 2 == 0 && kVPieces % kAhead == 0, "whole groups of pieces");
-            fetch(0, vf[0]);
-            rows.soften(a.c);
             uint4 pf[2][R][kTerms];
-#pragma unroll
-            for (int u = 0; u < 2; ++u)
+            auto weigh = [&](int u) {
 #pragma unroll
                 for (int r = 0; r < R; ++r) {
+                    rows.soften(a.c, r, u);
                     float w[8];
 #pragma unroll
                     for (int x = 0; x < 8; ++x) w[x] = rows.s[r][2 * u + x / 4][x % 4];
                     rows.split(w, pf[u][r]);
                 }
-#pragma unroll
-            for (int i = 0; i < kVPieces; i += kAhead) {
-                if (i + kAhead < kVPieces) fetch(i + kAhead, vf[(i / kAhead + 1) & 1]);
-                __builtin_amdgcn_sched_barrier(0);
+            };
+            auto products = [&](int i) {
 #pragma unroll
                 for (int x = 0; x < kAhead; ++x)
 #pragma unroll
                     for (int r = 0; r < R; ++r)
                         rows.product((i + x) % A::kDTiles, r, vf[(i / kAhead) & 1][x], pf[(i + x) / A::kDTiles][r]);
+            };
+            fetch(0);
+            rows.maxima(a.c);
+            weigh(0);
+            __builtin_amdgcn_sched_barrier(0);
+            weigh(1);
+#pragma unroll
+            for (int i = 0; i < A::kDTiles / kAhead * kAhead; i += kAhead) {
+                fetch(i + kAhead);
+                products(i);
+            }
+            interleave<A::kDTiles / kAhead * kAhead * R * kTerms, 4, 0, 1>();
+#pragma unroll
+            for (int i = A::kDTiles / kAhead * kAhead; i < kVPieces; i += kAhead) {
+                if (i + kAhead < kVPieces) fetch(i + kAhead);
+                __builtin_amdgcn_sched_barrier(0);
+                products(i);
                 __builtin_amdgcn_sched_barrier(0);
             }
             if (__builtin_expect(nan, 0)) {
