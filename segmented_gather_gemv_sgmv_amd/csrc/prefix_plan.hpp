@@ -21,10 +21,12 @@ namespace sgmv {
 constexpr int kAttnWaves = 4;            // of an item's workgroup
 constexpr int kAttnThreads = 64 * kAttnWaves;
 constexpr int kAttnKeys = 64;            // keys of a wave's step
-// Items to aim at: two workgroups a CU and some to even out.  A stack is cut into chunks of about
-// work / target, or not at all below 1.7 of that.  Work is counted in steps of 64 keys of a tile; a step of 64
-// or 128 rows takes about twice as long as one of up to 32.
-constexpr int kAttnTarget = 640;
+// Items to aim at, most of what two workgroups a CU can take: what is too much costs partial results, what is too
+// little leaves CUs waiting (64 sequences behind 16384 tokens, 32 / 8 heads of 128: 58, 56, 64, 68 us at
+// 384, 448, 640, 896).  A stack is cut into chunks of about work / target, or not at all below 1.7 of
+// that.  Work is counted in steps of 64 keys of a tile; a step of 64 or 128 rows takes about twice as long as
+// one of up to 32.
+constexpr int kAttnTarget = 448;
 constexpr int kAttnLeast = 8;            // work of an item, at least
 constexpr int kPlanHeader = 16;          // ints: items, slots, work of a chunk
 
