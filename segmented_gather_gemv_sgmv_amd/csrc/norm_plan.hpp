@@ -9,7 +9,7 @@ namespace sgmv {
 constexpr int kNormThreads = 256;
 constexpr int kNormMaxDim = 1024;    // of a head
 constexpr int kNormAngles = 512;     // of a workgroup's rows: rows x rot / 2
-constexpr int kNormGradBlocks = 1024;  // workgroups of the gradients, at most
+constexpr int kNormGradBlocks = 1024;  // workgroups of the gradients, at most: what 4 waves a SIMD can hold
 
 struct NormShape {
     int units, lanes, per_lane;  // units of a head, lanes that hold it, units of a lane (1, 2, 4 or 16)
@@ -34,11 +34,24 @@ inline int norm_rows_per_block(long long rows, int rotary_dim) {
     return (int)std::max(1ll, std::min(most, rows / 1024));
 }
 
-// Workgroups of the gradients: each takes the same number of blocks of rows, give or take one.
-inline int norm_grad_workgroups(long long rows, int rows_per_block) {
-    const long long blocks = (rows + rows_per_block - 1) / rows_per_block;
-    const long long turns = (blocks + kNormGradBlocks - 1) / kNormGradBlocks;
-    return turns ? (int)((blocks + turns - 1) / turns) : 0;
+// The gradients of one tensor: each of at most `most` workgroups takes ceil(rows / most) rows, in turns of as many as
+// its angles have room for.
+struct NormGradShape {
+    int block_rows, workgroups;
+};
+inline NormGradShape norm_grad_shape(long long rows, int rotary_dim, int most) {
+    const long long room = std::min(8, kNormAngles / (rotary_dim / 2));
+    const long long each = std::max(1ll, (rows + most - 1) / most);
+    const long long turns = (each + room - 1) / room;
+    NormGradShape s;
+    s.block_rows = (int)((each + turns - 1) / turns);
+    s.workgroups = (int)((rows + s.block_rows * turns - 1) / (s.block_rows * turns));
+    return s;
+}
+// The share of the workgroups that w (0: queries, 1: keys) gets.
+inline int norm_grad_share(int q_heads, int k_heads, int w) {
+    const int heads = w ? k_heads : q_heads;
+    return heads ? std::max(1, (int)((long long)kNormGradBlocks * heads / ((long long)q_heads + k_heads))) : 0;
 }
 
 // Heads of a workgroup in the forward pass: all of them once the blocks of rows fill the

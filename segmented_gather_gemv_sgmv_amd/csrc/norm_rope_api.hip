@@ -11,11 +11,21 @@ using namespace sgmv;
 template <typename DT, bool kVec, bool kGrad>
 void launch_norm(const NormRopeArgs& a, int per_lane, dim3 grid, hipStream_t st) {
     const dim3 block(kNormThreads);
-    auto go = [&](auto k) {
-        constexpr int K = decltype(k)::value;
+    auto go_lanes = [&](auto k, auto lanes) {
+        constexpr int K = decltype(k)::value, kLanes = decltype(lanes)::value;
         if constexpr (kGrad) launch(&norm_rope_grad_kernel<DT, kVec, K>, grid, block, st, a);
-        else launch(&norm_rope_kernel<DT, kVec, K>, grid, block, st, a);
+        else launch(&norm_rope_kernel<DT, kVec, K, kLanes>, grid, block, st, a);
     };
+    auto go = [&](auto k) { go_lanes(k, std::integral_constant<int, 0>{}); };
+    if constexpr (kVec && !kGrad) {  // whole heads of 64, 128 or 256, and 512 of 16 bits
+        const std::integral_constant<int, 1> k{};
+        const int lanes = a.units == a.lanes && a.rot == a.D && !a.interleaved ? a.lanes : 0;
+        if constexpr (DT::kBytes == 2)
+            if (lanes == 4) return go_lanes(k, std::integral_constant<int, 4>{});
+        if (lanes == 8) return go_lanes(k, std::integral_constant<int, 8>{});
+        if (lanes == 16) return go_lanes(k, std::integral_constant<int, 16>{});
+        if (lanes == 32) return go_lanes(k, std::integral_constant<int, 32>{});
+    }
     // 16-byte pieces of a head of at most 1024 elements: 128 units (16 bits) or 256 (float32)
     if (per_lane == 1) go(std::integral_constant<int, 1>{});
     else if (per_lane == 2) go(std::integral_constant<int, 2>{});
@@ -78,10 +88,6 @@ bool fill(NormRopeArgs& a, const void* const* in, const void* const* weight, con
     return vec;
 }
 
-int grad_workgroups(int32_t num_rows, int32_t rotary_dim) {
-    return norm_grad_workgroups(num_rows, norm_rows_per_block(num_rows, rotary_dim));
-}
-
 }  // namespace
 
 extern "C" int qk_norm_rope(void* q_out, void* k_out, const void* q, const void* k,
@@ -131,7 +137,8 @@ extern "C" size_t qk_norm_rope_backward_workspace_bytes(int32_t num_rows, int32_
     if (num_rows < 1 || head_dim < 1 || head_dim > kNormMaxDim || rotary_dim < 2 ||
         rotary_dim > head_dim)
         return 0;
-    return (size_t)grad_workgroups(num_rows, rotary_dim) * 2 * head_dim * sizeof(float);
+    // either tensor's workgroups are fewer with a share of them than with all
+    return (size_t)norm_grad_shape(num_rows, rotary_dim, kNormGradBlocks).workgroups * 2 * head_dim * sizeof(float);
 }
 
 extern "C" int qk_norm_rope_backward(void* dq, void* dk, void* dq_weight, void* dk_weight,
@@ -155,7 +162,7 @@ extern "C" int qk_norm_rope_backward(void* dq, void* dk, void* dq_weight, void* 
     if (sums && !empty && (!workspace || workspace_bytes < need || !aligned16(workspace)))
         return SGMV_ERR_WORKSPACE;
     const hipStream_t st = (hipStream_t)stream;
-    int n = 0;
+    int n[2] = {0, 0};
     if (!empty) {
         NormRopeArgs a{};
         const void* in[2] = {q, k};
@@ -184,15 +191,21 @@ extern "C" int qk_norm_rope_backward(void* dq, void* dk, void* dq_weight, void* 
         const NormShape s = norm_shape(head_dim, rotary_dim, interleaved != 0, vec ? V : 1);
         a.units = s.units;
         a.lanes = s.lanes;
-        n = grad_workgroups(num_rows, rotary_dim);
-        launch_norm<true>(a, dtype, vec, s.per_lane, dim3((unsigned)n), st);
+        for (int w = 0; w < 2; ++w) {
+            if (a.heads[w] == 0) continue;
+            const NormGradShape shape = norm_grad_shape(num_rows, rotary_dim, norm_grad_share(q_heads, k_heads, w));
+            a.grad_rows[w] = shape.block_rows;
+            n[w] = shape.workgroups;
+        }
+        a.split = n[0];
+        launch_norm<true>(a, dtype, vec, s.per_lane, dim3((unsigned)(n[0] + n[1])), st);
     }
     if (sums) {
-        const dim3 grid((unsigned)((head_dim + 63) / 64), 2), block(1024);
+        const dim3 grid((unsigned)((head_dim + 15) / 16), 2), block(1024);
         const float* p = (const float*)workspace;
-        if (dtype == SGMV_F32) launch(&norm_join_kernel<F32>, grid, block, st, p, dq_weight, dk_weight, n, head_dim);
-        else if (dtype == SGMV_F16) launch(&norm_join_kernel<F16>, grid, block, st, p, dq_weight, dk_weight, n, head_dim);
-        else launch(&norm_join_kernel<BF16>, grid, block, st, p, dq_weight, dk_weight, n, head_dim);
+        if (dtype == SGMV_F32) launch(&norm_join_kernel<F32>, grid, block, st, p, dq_weight, dk_weight, n[0], n[1], head_dim);
+        else if (dtype == SGMV_F16) launch(&norm_join_kernel<F16>, grid, block, st, p, dq_weight, dk_weight, n[0], n[1], head_dim);
+        else launch(&norm_join_kernel<BF16>, grid, block, st, p, dq_weight, dk_weight, n[0], n[1], head_dim);
     }
     return launch_status();
 }
