@@ -68,6 +68,7 @@ __device__ __forceinline__ long long block_scan64(long long v, long long* s, lon
 
 __global__ __launch_bounds__(kPlanThreads) void attn_plan_kernel(PlanArgs a) {
     __shared__ long long s_sum[kPlanThreads / 64];
+    __shared__ int s_key[kPlanThreads], s_order[kPlanThreads];
     const int n = a.prefixes + a.seqs, tid = threadIdx.x, lane = tid & 63, wave = tid / 64;
     constexpr int kWaves = kPlanThreads / 64;
     const int wide = 16 * a.tiles * kAttnWaves;
@@ -145,12 +146,30 @@ __global__ __launch_bounds__(kPlanThreads) void attn_plan_kernel(PlanArgs a) {
     items = block_sum64(items, s_sum);
     slots = block_sum64(slots, s_sum);
     const bool fits = items <= a.items && slots <= a.slots;
+    // Stacks of the longest items first, so that short ones even out the end (24 sequences of 1 to 2000 tokens
+    // behind 6000, 40 heads of 128 in 4 bits: 49 against 54 us).  More stacks than threads stay in their order: no
+    // one of so many is long against all.
+    const bool sorted = n <= kPlanThreads;
+    if (sorted) {
+        __syncthreads();
+        int key = 0;
+        if (tid < n) {
+            const int* r = record(tid);
+            key = r[kStackBlocks] * plan_weight(r[kStackTile]) / max(chunks_of(r), 1);
+        }
+        s_key[tid] = key;
+        __syncthreads();
+        int rank = 0;
+        for (int j = 0; j < n; ++j) rank += s_key[j] > key || (s_key[j] == key && j < tid);
+        if (tid < n) s_order[rank] = tid;
+        __syncthreads();
+    }
     // Where every stack's items and slots begin.
     long long item_base = 0, slot_base = 0;
     for (int base = 0; base < n; base += kPlanThreads) {
-        const int i = base + tid;
-        const bool live = i < n;
-        int* r = record(live ? i : 0);
+        const bool live = base + tid < n;
+        const int i = !live ? 0 : sorted ? s_order[tid] : base + tid;
+        int* r = record(i);
         const int chunks = live && fits ? chunks_of(r) : 0;
         const long long mine = live ? (long long)a.kv_heads * r[kStackTiles] * chunks : 0;
         const long long size = live ? mine * r[kStackTile] : 0;
