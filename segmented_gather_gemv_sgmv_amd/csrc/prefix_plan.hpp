@@ -27,7 +27,7 @@ constexpr int kAttnKeys = 64;            // keys of a wave's step
 // that.  Work is counted in steps of 64 keys of a tile; a step of 64 or 128 rows takes about twice as long as
 // one of up to 32.
 constexpr int kAttnTarget = 448;
-constexpr int kAttnLeast = 8;            // work of an item, at least
+constexpr int kAttnLeast = 6;            // work of an item, at least (40 short sequences, float32: 20, 19, 20, 23 us at 4, 6, 8, 12)
 constexpr int kPlanHeader = 16;          // ints: items, slots, work of a chunk
 
 // Records of the plan, in ints.
