@@ -13,7 +13,7 @@ import ctypes
 import math
 
 from . import _check, _need, _no_gradients, _stream_ptr, _torch, dtype_code, lib
-from .kv import KVCache, _Strides4
+from .kv import KVCache, _not_repeated, _Strides4
 from .rotary import _heads
 
 
@@ -126,6 +126,7 @@ def prefix_attention(q, cache: KVCache, plan: PrefixPlan, scale=None, out=None, 
         so = _heads(out, "out", dev, cache.dtype)
         if out.shape != shape:
             raise ValueError(f"out must be {shape}, got {tuple(out.shape)}")
+        _not_repeated(out)
     if lse is not None:
         _need(lse, "lse", dev, torch.float32, 2)
         if lse.shape != shape[:2]:

@@ -61,6 +61,13 @@ def kv_cache(num_pages: int, page_size: int, kv_heads: int, head_dim: int, dtype
     return KVCache(arrays, *sizes, dtype, kind)
 
 
+def _not_repeated(*outs):
+    """Refuses an out whose elements share memory by a stride of 0."""
+    for o in outs:
+        if o.numel() > 1 and any(s == 0 and n > 1 for s, n in zip(o.stride(), o.shape)):
+            raise ValueError("out must not repeat its own elements")
+
+
 def _rows(cache, t, name, n):
     st = _heads(t, name, cache.device, cache.dtype)
     if t.shape != (n, cache.kv_heads, cache.head_dim):
@@ -97,6 +104,7 @@ def kv_read(cache: KVCache, slots, out=None):
         out = tuple(_torch().empty(shape, dtype=cache.dtype, device=cache.device) for _ in range(2))
     else:
         _no_gradients("kv_read", *out)
+        _not_repeated(*out)
     k, v = out
     strides = _Strides4(*_rows(cache, k, "out k", n), *_rows(cache, v, "out v", n))
     _check(lib().kv_read(k.data_ptr(), v.data_ptr(), cache._ptr, slots.data_ptr(), slots.element_size(),

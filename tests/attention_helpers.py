@@ -105,7 +105,7 @@ def attend(q, k, v, scale):
     A score is a float32 sum of D products (of 3 terms for float32 q), scaled: off by d =
     (3 D + 8) roundings of the sum of its terms' magnitudes, and the exponential's argument and
     value by 4 more of the largest score and of 1.  p enters its product in float16
-    parts: 2^-12 of itself in one (bfloat16), 2^-22 in two, and what falls below 2^-35 of the
+    parts, of 10 fraction bits: half a step is at most 2^-11 of the value, so 2^-11 in one (bfloat16), 2^-22 in two, and what falls below 2^-35 of the
     largest value.  Sums over n keys in any order add n + 16 roundings, twice for
     the quotient."""
     dtype, n = q.dtype, k.shape[0]
@@ -119,7 +119,7 @@ def attend(q, k, v, scale):
     p = torch.softmax(s, -1)
     D = q.shape[-1]
     off = (3 * D + 8) * F32 * size.amax(-1, keepdim=True) + 4 * F32 * (1 + s.abs().amax(-1, keepdim=True))
-    part = 2.0 ** -12 if dtype == torch.bfloat16 else 2.0 ** -22
+    part = 2.0 ** -11 if dtype == torch.bfloat16 else 2.0 ** -22
     o = torch.matmul(p, vt)
     mass = torch.matmul(p, vt.abs())
     bound = mass * (2 * off + part + 2 * (n + 16) * F32) + vt.abs().amax(1, keepdim=True) * n * 2.0 ** -35
