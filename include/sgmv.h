@@ -361,11 +361,12 @@ int sgmv_group_rows(const int32_t* row_ids, int32_t num_rows, int32_t num_adapte
 
 /*
  * The projections around the adapters: a base model with 4-bit weights, the
- * gated feed-forward block, and rotary positions.  These calls follow the
+ * gated feed-forward block, rotary positions, and from the projections of q, k and v to attention over
+ * a quantized cache.  These calls follow the
  * conventions above (device pointers, row-major arrays of one dtype, float32
- * sums, enqueue-only); only gated_ffn_backward takes a workspace.  Outputs must
- * not overlap inputs, except that h may be gate_add or up_add itself and rope
- * works in place.
+ * sums, enqueue-only); a workspace is taken where one is named, and may hold anything.  Outputs must
+ * not overlap inputs, except that h may be gate_add or up_add itself and rope and qk_norm_rope
+ * work in place.
  */
 
 /*
@@ -564,13 +565,15 @@ int kv_read(void* k, void* v, const sgmv_kv_cache* cache, const void* slots, int
 /*
  * Attention of a batch over such a cache.  num_seqs sequences have tokens of
  * their own in the cache; runs of consecutive sequences may share a prefix, which is
- * read once for all of them.  Rows of sequence s, row_indptr[s] up to
+ * read for all of their rows together.  Rows of sequence s, row_indptr[s] up to
  * row_indptr[s + 1], are the last of its own tokens: row i of n sees the whole of its
  * run's prefix and the first lengths[s] - n + i + 1 of its own tokens,
  *     o = softmax(scale q K^T) V,   lse = log(sum of exp(scale q k)),
  * with float32 sums and maxima, rounded once.  q_heads / kv_heads consecutive heads of q share a
  * K / V head.  A row that sees no key gets zeros and an lse of minus infinity.  Rows of no
- * sequence are left as they are.  A visible NaN gives a row of NaN.
+ * sequence are left as they are.  A visible NaN gives a row of NaN; a score of minus infinity
+ * counts as a key that is not seen.  With many rows a V value whose scale lies 2^32 below the largest
+ * that the rows' tile meets may count as zero (caches of bfloat16 or float32 alone reach so far).
  *
  * Tables, int32 device arrays: lengths [num_seqs], tokens in the cache (a step's new
  * ones among them, written before); row_indptr [num_seqs + 1], or NULL for one row each (row s

@@ -22,12 +22,14 @@ constexpr int kAttnWaves = 4;            // of an item's workgroup
 constexpr int kAttnThreads = 64 * kAttnWaves;
 constexpr int kAttnKeys = 64;            // keys of a wave's step
 // Items to aim at, most of what two workgroups a CU can take: what is too much costs partial results, what is too
-// little leaves CUs waiting (64 sequences behind 16384 tokens, 32 / 8 heads of 128: 58, 56, 64, 68 us at
-// 384, 448, 640, 896).  A stack is cut into chunks of about work / target, or not at all below 1.7 of
+// little leaves CUs waiting (64 sequences behind 16384 tokens, 32 / 8 heads of 128: 50, 46, 50 us at
+// 384, 448, 512).  A stack is cut into chunks of about work / target, or not at all below 1.7 of
 // that.  Work is counted in steps of 64 keys of a tile; a step of 64 or 128 rows takes about twice as long as
 // one of up to 32.
 constexpr int kAttnTarget = 448;
-constexpr int kAttnLeast = 6;            // work of an item, at least (40 short sequences, float32: 20, 19, 20, 23 us at 4, 6, 8, 12)
+// Work of an item, at least (40 sequences behind 600 to 1300 tokens, 12 / 4 heads of 96, float32: 20, 19, 20, 23 us
+// with the join at 4, 6, 8, 12).
+constexpr int kAttnLeast = 6;
 constexpr int kPlanHeader = 16;          // ints: items, slots, work of a chunk
 
 // Records of the plan, in ints.
