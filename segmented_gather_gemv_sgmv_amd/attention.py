@@ -127,6 +127,8 @@ def prefix_attention(q, cache: KVCache, plan: PrefixPlan, scale=None, out=None, 
         if out.shape != shape:
             raise ValueError(f"out must be {shape}, got {tuple(out.shape)}")
         _not_repeated(out)
+        if out.data_ptr() == q.data_ptr() and q.numel():
+            raise ValueError("out must lie apart from q")
     if lse is not None:
         _need(lse, "lse", dev, torch.float32, 2)
         if lse.shape != shape[:2]:

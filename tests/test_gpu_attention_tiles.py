@@ -131,6 +131,22 @@ def test_lengths_past_the_table_in_wide_tiles():
     assert not bool(sg.prefix_attention(b.q, b.cache, b.plan())[:130].any())
 
 
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("kind", ["fp8", "fp4"])
+@pytest.mark.parametrize("power", [-100.0, 100.0])
+def test_very_small_and_large_values(kind, dt, power):
+    """Far from 1, yet of one magnitude: rows of wide and of narrow tiles."""
+    b = Batch([40, 1, 33, 5], [90, 60, 40, 9], [0, 2, 4], [100, 70], 4, 1, 64, 16, kind, dt, seed=37)
+    b.write(torch.cat(b.slots), b.k, (b.v.float() * 2.0 ** power).to(b.dt))
+    b.verify("power")
+
+
+def test_outputs_over_inputs_are_refused():
+    b = Batch([1, 1], [5, 9], [], [], 2, 2, 64, 16, "fp8", "f16", seed=36)
+    with pytest.raises(ValueError, match="apart"):
+        sg.prefix_attention(b.q, b.cache, b.plan(), out=b.q)
+
+
 def test_outputs_that_repeat_are_refused():
     b = Batch([1, 1], [5, 9], [], [], 2, 2, 64, 16, "fp8", "f16", seed=36)
     same = torch.zeros(1, 2, 64, device=DEV).half().expand(2, 2, 64)
