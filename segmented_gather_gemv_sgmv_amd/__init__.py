@@ -196,6 +196,15 @@ def _stream_ptr(device) -> int:
     return _raw_stream(_torch().cuda.current_device() if index is None else index)
 
 
+def _call_on(device, fn, *args) -> int:
+    """``fn(*args)`` with ``device`` the current one, as a launch on its default stream needs."""
+    cuda = _torch().cuda
+    if device.index is None or device.index == cuda.current_device():
+        return fn(*args)
+    with cuda.device(device):
+        return fn(*args)
+
+
 def _need(t, name, device, dtype=None, ndim=None):
     if not t.is_cuda or t.device != device:
         raise ValueError(f"{name} must be on {device}, got {t.device}")

@@ -12,7 +12,7 @@ from __future__ import annotations
 import ctypes
 import math
 
-from . import _check, _need, _no_gradients, _stream_ptr, _torch, dtype_code, lib
+from . import _call_on, _check, _need, _no_gradients, _stream_ptr, _torch, dtype_code, lib
 from .kv import KVCache, _not_repeated, _Strides4
 from .rotary import _heads
 
@@ -88,9 +88,9 @@ def prefix_plan(cache: KVCache, q_heads: int, pages, lengths, row_indptr=None, n
         raise ValueError(f"{rows} rows of {q_heads} heads over {S} sequences are more than a plan counts")
     table = torch.empty(nbytes, dtype=torch.uint8, device=dev)
     ptr = lambda t: None if t is None else t.data_ptr()
-    _check(lib().prefix_plan(table.data_ptr(), nbytes, cache._ptr, lengths.data_ptr(), ptr(row_indptr),
-                             pages.shape[1], ptr(prefix_lengths), ptr(prefix_indptr), prefix_width, *sizes,
-                             _stream_ptr(dev)), "prefix_plan")
+    _check(_call_on(dev, lib().prefix_plan, table.data_ptr(), nbytes, cache._ptr, lengths.data_ptr(),
+                    ptr(row_indptr), pages.shape[1], ptr(prefix_lengths), ptr(prefix_indptr), prefix_width,
+                    *sizes, _stream_ptr(dev)), "prefix_plan")
     return PrefixPlan(table, pages, prefix_pages, rows, S, G, q_heads, cache,
                       lib().prefix_attention_workspace_bytes(cache._ptr, *sizes),
                       row_indptr is not None or rows > S)
@@ -135,8 +135,8 @@ def prefix_attention(q, cache: KVCache, plan: PrefixPlan, scale=None, out=None, 
             raise ValueError(f"lse must be {shape[:2]}, got {tuple(lse.shape)}")
     ws = torch.empty(plan.workspace_bytes, dtype=torch.uint8, device=dev)
     pages, prefix_pages = plan.pages, plan.prefix_pages
-    _check(lib().prefix_attention(
-        out.data_ptr(), None if lse is None else lse.data_ptr(), q.data_ptr(), cache._ptr,
+    _check(_call_on(
+        dev, lib().prefix_attention, out.data_ptr(), None if lse is None else lse.data_ptr(), q.data_ptr(), cache._ptr,
         plan.table.data_ptr(), pages.data_ptr(), pages.shape[1],
         None if prefix_pages is None else prefix_pages.data_ptr(),
         0 if prefix_pages is None else prefix_pages.shape[1], plan.rows, plan.seqs, plan.prefixes,

@@ -13,7 +13,7 @@ from __future__ import annotations
 
 import ctypes
 
-from . import _check, _need, _no_gradients, _stream_ptr, _torch, dtype_code, lib
+from . import _call_on, _check, _need, _no_gradients, _stream_ptr, _torch, dtype_code, lib
 from .rotary import _heads, _position_types
 
 KINDS = {"fp8": 0, "fp4": 1}
@@ -91,8 +91,9 @@ def kv_write(cache: KVCache, k, v, slots) -> None:
     n = _slots(cache, slots)
     _no_gradients("kv_write", k, v)
     strides = _Strides4(*_rows(cache, k, "k", n), *_rows(cache, v, "v", n))
-    _check(lib().kv_write(cache._ptr, k.data_ptr(), v.data_ptr(), slots.data_ptr(), slots.element_size(),
-                          n, strides, dtype_code(cache.dtype), _stream_ptr(cache.device)), "kv_write")
+    _check(_call_on(cache.device, lib().kv_write, cache._ptr, k.data_ptr(), v.data_ptr(), slots.data_ptr(),
+                    slots.element_size(), n, strides, dtype_code(cache.dtype), _stream_ptr(cache.device)),
+           "kv_write")
 
 
 def kv_read(cache: KVCache, slots, out=None):
@@ -107,6 +108,7 @@ def kv_read(cache: KVCache, slots, out=None):
         _not_repeated(*out)
     k, v = out
     strides = _Strides4(*_rows(cache, k, "out k", n), *_rows(cache, v, "out v", n))
-    _check(lib().kv_read(k.data_ptr(), v.data_ptr(), cache._ptr, slots.data_ptr(), slots.element_size(),
-                         n, strides, dtype_code(cache.dtype), _stream_ptr(cache.device)), "kv_read")
+    _check(_call_on(cache.device, lib().kv_read, k.data_ptr(), v.data_ptr(), cache._ptr, slots.data_ptr(),
+                    slots.element_size(), n, strides, dtype_code(cache.dtype), _stream_ptr(cache.device)),
+           "kv_read")
     return k, v

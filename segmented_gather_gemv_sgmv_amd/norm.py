@@ -12,7 +12,7 @@ from __future__ import annotations
 
 import ctypes
 
-from . import _check, _need, _no_tangents, _stream_ptr, _torch, dtype_code, lib
+from . import _call_on, _check, _need, _no_tangents, _stream_ptr, _torch, dtype_code, lib
 from .rotary import RopePlan, _ABSENT, _heads, _one, _position_types, _Strides
 
 _GradStrides = ctypes.c_int64 * 12
@@ -61,10 +61,9 @@ def _run(q, k, q_weight, k_weight, positions, plan, eps, out):
     k2, ko, ki, ks, hk = _one(k, "k", ok, dev, dtype, R, D) if k is not None else _ABSENT
     wq = _weight(q_weight, "q_weight", q, D)
     wk = _weight(k_weight, "k_weight", k, D)
-    _check(lib().qk_norm_rope(qo, ko, qi, ki, wq, wk, positions.data_ptr(), positions.element_size(),
-                              plan.ptr, plan.magnitude, eps, R, hq, hk, D, plan.rotary_dim,
-                              _Strides(*qs, *ks), plan.interleaved, dtype_code(dtype),
-                              _stream_ptr(dev)), "qk_norm_rope")
+    _check(_call_on(dev, lib().qk_norm_rope, qo, ko, qi, ki, wq, wk, positions.data_ptr(),
+                    positions.element_size(), plan.ptr, plan.magnitude, eps, R, hq, hk, D, plan.rotary_dim,
+                    _Strides(*qs, *ks), plan.interleaved, dtype_code(dtype), _stream_ptr(dev)), "qk_norm_rope")
     return q2, k2
 
 
@@ -97,12 +96,11 @@ def qk_norm_rope_backward(dq, dk, q, k, q_weight, k_weight, positions, plan: Rop
     if gqw is not None or gkw is not None:
         ws_bytes = lib().qk_norm_rope_backward_workspace_bytes(R, D, plan.rotary_dim)
         ws = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
-    _check(lib().qk_norm_rope_backward(pq[0], pk[0], pq[1], pk[1], pq[2], pk[2], pq[3], pk[3], pq[4], pk[4],
-                                       positions.data_ptr(), positions.element_size(), plan.ptr,
-                                       plan.magnitude, eps, R, hq, hk, D, plan.rotary_dim,
-                                       _GradStrides(*sq, *sk), plan.interleaved, dtype_code(dtype),
-                                       None if ws is None else ws.data_ptr(), ws_bytes,
-                                       _stream_ptr(dev)), "qk_norm_rope_backward")
+    _check(_call_on(dev, lib().qk_norm_rope_backward, pq[0], pk[0], pq[1], pk[1], pq[2], pk[2], pq[3], pk[3],
+                    pq[4], pk[4], positions.data_ptr(), positions.element_size(), plan.ptr, plan.magnitude,
+                    eps, R, hq, hk, D, plan.rotary_dim, _GradStrides(*sq, *sk), plan.interleaved,
+                    dtype_code(dtype), None if ws is None else ws.data_ptr(), ws_bytes, _stream_ptr(dev)),
+           "qk_norm_rope_backward")
     return gq, gk, gqw, gkw
 
 
