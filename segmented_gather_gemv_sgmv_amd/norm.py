@@ -149,7 +149,8 @@ def qk_norm_rope(q, k, q_weight, k_weight, positions, plan: RopePlan, eps: float
     by the plan's magnitude; float32 in between (squares of elements past 1e19 overflow),
     rounded once.  q [R, q heads, D] and k [R, k heads, D], either may be None; weights [D] in
     their dtype, or None for ones; ``positions`` [R] int32 or int64.  ``out=(q, k)``
-    works in place (or into other tensors, which must not overlap the inputs)."""
+    works in place (or into other tensors, which must not overlap the inputs).  A backward pass may be
+    captured into a graph once no graph that eager calls recorded on the same leaves is alive."""
     if not isinstance(plan, RopePlan):
         raise TypeError("plan must be a RopePlan (see rope_plan)")
     eps = float(eps)

@@ -13,7 +13,7 @@ DEV = "cuda:0"
 SHAPES = [(1, 32, 8, 128, 128), (1, 1, 1, 2, 2), (7, 4, 2, 80, 32), (33, 3, 1, 96, 50), (5, 2, 2, 10, 6),
           (64, 32, 32, 128, 64), (300, 5, 5, 72, 72), (3, 7, 1, 256, 256), (9, 2, 1, 33, 32),
           (2, 1, 1, 1024, 1024), (2, 1, 2, 1024, 2), (2, 2, 1, 1023, 4), (2100, 4, 1, 64, 64),
-          (5000, 2, 1, 128, 96), (3, 40, 0, 128, 128), (3, 0, 2, 64, 32)]
+          (5000, 2, 1, 128, 96), (3, 40, 0, 128, 128), (3, 0, 2, 64, 32), (1300, 3, 1, 512, 512), (11, 2, 2, 32, 32)]
 
 
 def _inputs(R, Hq, Hk, D, dt, seed, weights=True):
@@ -165,6 +165,37 @@ def test_repeatable_graph_and_stream():
         torch.cuda.synchronize()
         want = sg.qk_norm_rope(q, k, wq, wk, pos, plan) + step()
         assert all(torch.equal(a, b) for a, b in zip(out, want))
+
+
+def test_captured_training_pass():
+    """Forward and backward through autograd in one graph: replays against eager passes, with eager
+    work between them.  No eager graph of the captured leaves is alive at the capture."""
+    q, k, wq, wk, pos, dq, dk = _inputs(130, 6, 2, 64, "bf16", 7)
+    plan = sg.rope_plan(64, device=DEV)
+    leaves = [t.detach().clone().requires_grad_() for t in (q, k, wq, wk)]
+    eager = [t.detach().clone().requires_grad_() for t in leaves]
+
+    def step(v):
+        y = sg.qk_norm_rope(*v, pos, plan)
+        return [t.detach() for t in y] + list(torch.autograd.grad(y, v, [dq, dk]))
+
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        step(leaves)
+    torch.cuda.current_stream().wait_stream(s)
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        got = step(leaves)
+    for _ in range(3):
+        with torch.no_grad():
+            for t, e in zip(leaves, eager):
+                t.mul_(-0.75)
+                e.copy_(t)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, step(eager)))
 
 
 def test_refusals():
