@@ -208,6 +208,13 @@ __device__ __forceinline__ Item attn_item(const AttnArgs& a, const int* e) {
     return t;
 }
 
+// End of the steps that row `m` sees, and with it all rows before it.  A row whose place lies before the first own
+// token (fewer tokens than rows) sees none of them, and all of a prefix in front.
+__device__ __forceinline__ int steps_seen(const AttnArgs& a, const Item& it, int m) {
+    const int keys = it.own ? max(it.hidden + m / a.rep + 1, 0) : it.keys.len;
+    return min(it.blk1, it.front_blocks + (keys + kAttnKeys - 1) / kAttnKeys);
+}
+
 // Where a wave's next steps find their keys: steps `first`, first + stride, ... of the item, four 16-token blocks
 // each.  A lane looks up one block, so the wave knows 16 steps at a time; a step gets its blocks from
 // their lanes.  Page entries for the 16 steps after that are asked for by every step (from L1), so that
@@ -283,8 +290,7 @@ struct AttnRows {
     __device__ __forceinline__ void init(const AttnArgs& a, const Item& it, int first, int lr, int lg) {
         m_first = first;
         const int last = min(first + 16 * R, it.M) - 1;
-        const int most = last < first ? -it.front_blocks * kAttnKeys : it.own ? it.hidden + last / a.rep + 1 : it.keys.len;
-        blk_end = min(it.blk1, it.front_blocks + (most + kAttnKeys - 1) / kAttnKeys);
+        blk_end = last < first ? 0 : steps_seen(a, it, last);
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             const int m = first + 16 * r + lr;
@@ -673,12 +679,7 @@ __device__ __forceinline__ void attn_shared(const AttnArgs& a, const Item& it, u
     const int lr = lane & 15, lg = lane >> 4;
     AttnRows<QT, BITS, P, R, F16, kTerms, kAttnHead> rows;
     rows.init(a, it, it.m0 + wave * 16 * R, lr, lg);
-    int end = 0;  // of the workgroup's rows
-    {
-        const int last = min(it.m0 + it.tile, it.M) - 1;
-        const int most = it.own ? it.hidden + last / a.rep + 1 : it.keys.len;
-        end = min(it.blk1, it.front_blocks + (most + kAttnKeys - 1) / kAttnKeys);
-    }
+    const int end = steps_seen(a, it, min(it.m0 + it.tile, it.M) - 1);  // of the workgroup's rows
 
     // Codes of the next step; vb: its scale bytes of V, one token a lane.
     uint32_t kw[A::kPiece / 4], vw[kMine][4], ks[A::kKGroups], vb[A::kGroups];
