@@ -1000,19 +1000,19 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a) {
         o.z *= keep;
         o.w *= keep;
         m = top;
+        // Results of no weight enter too: a visible NaN of V shows in them alone.
         for (int j = 0; j < count; j += 8) {
             float4 v[8];
             float g[8];
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
                 const int at = min(j + k, count - 1);
-                const float fk = __shfl(f, at, kLanes);
-                g[k] = j + k < count ? fk : 0.f;
+                g[k] = __shfl(f, at, kLanes);
                 v[k] = *reinterpret_cast<const float4*>(a.part_o + slot(j0 + at) * P + (mine ? lane * 4 : 0));
             }
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
-                if (g[k] == 0.f) continue;  // may hold anything
+                if (j + k >= count) continue;  // the last one again
                 o.x += g[k] * v[k].x;
                 o.y += g[k] * v[k].y;
                 o.z += g[k] * v[k].z;
