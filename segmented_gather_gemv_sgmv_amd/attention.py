@@ -9,12 +9,12 @@ prefix.  A row sees all of its run's prefix and its sequence's tokens up to itse
 """
 from __future__ import annotations
 
-import ctypes
 import math
 
 from . import _call_on, _check, _need, _no_gradients, _stream_ptr, _torch, dtype_code, lib
 from .kv import KVCache, _not_repeated, _Strides4
 from .rotary import _heads
+from .views import apart
 
 
 class PrefixPlan:
@@ -127,7 +127,7 @@ def prefix_attention(q, cache: KVCache, plan: PrefixPlan, scale=None, out=None, 
         if out.shape != shape:
             raise ValueError(f"out must be {shape}, got {tuple(out.shape)}")
         _not_repeated(out)
-        if out.data_ptr() == q.data_ptr() and q.numel():
+        if not apart(out, q):
             raise ValueError("out must lie apart from q")
     if lse is not None:
         _need(lse, "lse", dev, torch.float32, 2)

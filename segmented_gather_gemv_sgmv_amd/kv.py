@@ -15,6 +15,7 @@ import ctypes
 
 from . import _call_on, _check, _need, _no_gradients, _stream_ptr, _torch, dtype_code, lib
 from .rotary import _heads, _position_types
+from .views import apart, repeats
 
 KINDS = {"fp8": 0, "fp4": 1}
 
@@ -62,9 +63,9 @@ def kv_cache(num_pages: int, page_size: int, kv_heads: int, head_dim: int, dtype
 
 
 def _not_repeated(*outs):
-    """Refuses an out whose elements share memory by a stride of 0."""
+    """Refuses an out [rows, heads, head_dim] whose elements share memory."""
     for o in outs:
-        if o.numel() > 1 and any(s == 0 and n > 1 for s, n in zip(o.stride(), o.shape)):
+        if repeats(o):
             raise ValueError("out must not repeat its own elements")
 
 
@@ -98,16 +99,19 @@ def kv_write(cache: KVCache, k, v, slots) -> None:
 
 def kv_read(cache: KVCache, slots, out=None):
     """``(k, v)`` [rows, kv_heads, head_dim] of the slots [rows], in the cache's dtype; rows
-    whose slot lies outside the cache are zeros.  ``out=(k, v)`` receives them."""
-    n = _slots(cache, slots)
-    if out is None:
+    whose slot lies outside the cache are zeros.  ``out=(k, v)``, two tensors apart, receives them."""
+    n, given = _slots(cache, slots), out is not None
+    if not given:
         shape = (n, cache.kv_heads, cache.head_dim)
         out = tuple(_torch().empty(shape, dtype=cache.dtype, device=cache.device) for _ in range(2))
     else:
         _no_gradients("kv_read", *out)
-        _not_repeated(*out)
     k, v = out
     strides = _Strides4(*_rows(cache, k, "out k", n), *_rows(cache, v, "out v", n))
+    if given:
+        _not_repeated(k, v)
+        if not apart(k, v):
+            raise ValueError("out's k and v must lie apart")
     _check(_call_on(cache.device, lib().kv_read, k.data_ptr(), v.data_ptr(), cache._ptr, slots.data_ptr(),
                     slots.element_size(), n, strides, dtype_code(cache.dtype), _stream_ptr(cache.device)),
            "kv_read")

@@ -1,0 +1,48 @@
+"""Outputs that share elements with what a call still reads, or with each other, are refused; views that
+lie between each other in one buffer are not."""
+import pytest
+import torch
+
+import segmented_gather_gemv_sgmv_amd as sg
+from test_gpu_prefix_attention import Batch
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+
+
+def test_attention_into_its_queries():
+    b = Batch([3, 2], [20, 9], [0, 2], [70], 4, 2, 64, 16, "fp8", "f16", seed=70)
+    plan, T = b.plan(), b.T
+    want = sg.prefix_attention(b.q, b.cache, plan)
+    big = torch.zeros(T + 1, 9, 64, dtype=torch.float16, device=DEV)
+    q = big[:T, :4]
+    q.copy_(b.q)
+    before = big.clone()
+    for out in (q, big[1:, :4], big[:T, 1:5], big[:T, 3:7], big[1:, 2:6], big.flatten()[8:8 + T * 256].view(T, 4, 64)):
+        with pytest.raises(ValueError, match="apart"):
+            sg.prefix_attention(q, b.cache, plan, out=out)
+    assert torch.equal(big, before)  # refused ahead of any work
+    for out in (big[:T, 4:8], big[1:, 5:]):
+        assert torch.equal(sg.prefix_attention(q, b.cache, plan, out=out), want)
+        assert torch.equal(q, b.q)
+
+
+def test_outputs_of_a_read():
+    b = Batch([1, 1], [20, 9], [], [], 2, 2, 64, 16, "fp4", "bf16", seed=71)
+    slots = torch.cat(b.slots).to(DEV)
+    n = slots.numel()
+    want = sg.kv_read(b.cache, slots)
+    big = torch.zeros(n + 1, 5, 64, dtype=torch.bfloat16, device=DEV)
+    before = big.clone()
+    for out in ((big[:n, :2], big[:n, :2]), (big[:n, :2], big[:n, 1:3]), (big[:n, :2], big[1:, :2])):
+        with pytest.raises(ValueError, match="apart"):
+            sg.kv_read(b.cache, slots, out=out)
+    lying = big.flatten().as_strided((n, 2, 64), (96, 64, 1))  # rows run into each other
+    for out in ((lying, want[1]), (want[0], lying)):
+        with pytest.raises(ValueError, match="repeat"):
+            sg.kv_read(b.cache, slots, out=out)
+    assert torch.equal(big, before)
+    k, v = sg.kv_read(b.cache, slots, out=(big[:n, :2], big[:n, 2:4]))
+    assert torch.equal(k, want[0]) and torch.equal(v, want[1])
+    with pytest.raises(ValueError, match="out k must be"):
+        sg.kv_read(b.cache, slots, out=(big[:1, :2], big[:n, 2:4]))
