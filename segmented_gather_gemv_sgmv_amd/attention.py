@@ -14,7 +14,7 @@ import math
 from . import _call_on, _check, _need, _no_gradients, _stream_ptr, _torch, dtype_code, lib
 from .kv import KVCache, _not_repeated, _Strides4
 from .rotary import _heads
-from .views import apart
+from .views import apart, view
 
 
 class PrefixPlan:
@@ -127,7 +127,7 @@ def prefix_attention(q, cache: KVCache, plan: PrefixPlan, scale=None, out=None, 
         if out.shape != shape:
             raise ValueError(f"out must be {shape}, got {tuple(out.shape)}")
         _not_repeated(out)
-        if not apart(out, q):
+        if not apart(view(out), view(q), q.element_size()):
             raise ValueError("out must lie apart from q")
     if lse is not None:
         _need(lse, "lse", dev, torch.float32, 2)

@@ -15,7 +15,7 @@ import ctypes
 
 from . import _call_on, _check, _need, _no_gradients, _stream_ptr, _torch, dtype_code, lib
 from .rotary import _heads, _position_types
-from .views import apart, repeats
+from .views import apart, repeats, view
 
 KINDS = {"fp8": 0, "fp4": 1}
 
@@ -65,7 +65,7 @@ def kv_cache(num_pages: int, page_size: int, kv_heads: int, head_dim: int, dtype
 def _not_repeated(*outs):
     """Refuses an out [rows, heads, head_dim] whose elements share memory."""
     for o in outs:
-        if repeats(o):
+        if repeats(view(o)):
             raise ValueError("out must not repeat its own elements")
 
 
@@ -110,7 +110,7 @@ def kv_read(cache: KVCache, slots, out=None):
     strides = _Strides4(*_rows(cache, k, "out k", n), *_rows(cache, v, "out v", n))
     if given:
         _not_repeated(k, v)
-        if not apart(k, v):
+        if not apart(view(k), view(v), k.element_size()):
             raise ValueError("out's k and v must lie apart")
     _check(_call_on(cache.device, lib().kv_read, k.data_ptr(), v.data_ptr(), cache._ptr, slots.data_ptr(),
                     slots.element_size(), n, strides, dtype_code(cache.dtype), _stream_ptr(cache.device)),

@@ -5,7 +5,15 @@ import random
 import pytest
 import torch
 
-from segmented_gather_gemv_sgmv_amd.views import apart, repeats
+from segmented_gather_gemv_sgmv_amd.views import apart as _apart, repeats as _repeats, view
+
+
+def apart(a, b):
+    return _apart(view(a), view(b), a.element_size())
+
+
+def repeats(t):
+    return _repeats(view(t))
 
 
 def _elements(t):
