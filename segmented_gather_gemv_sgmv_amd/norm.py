@@ -14,6 +14,7 @@ import ctypes
 
 from . import _call_on, _check, _need, _no_tangents, _stream_ptr, _torch, dtype_code, lib
 from .rotary import RopePlan, _ABSENT, _heads, _one, _position_types, _Strides
+from .views import apart, repeats
 
 _GradStrides = ctypes.c_int64 * 12
 
@@ -51,16 +52,34 @@ def _common(q, k, q_weight, k_weight, positions, plan):
     return dev, dtype, R, D
 
 
+def _own_places(outs, ins, size):
+    """Refuses outputs (views, None for new tensors) that share elements with each other, or with an
+    input other than as that very view: workgroups read heads when others have written theirs."""
+    for i, o in enumerate(outs):
+        if o is None:
+            continue
+        if repeats(o):
+            raise ValueError("out must not repeat its own elements")
+        other = outs[1 - i]
+        if i == 0 and other is not None and not apart(o, other, size):
+            raise ValueError("out's q and k must lie apart")
+        for j, x in enumerate(ins):  # an output that is an input has been compared as one
+            if x is not None and not (o == x if j == i else other == x) and not apart(o, x, size):
+                raise ValueError("out must be its input itself or lie apart from the inputs")
+
+
 def _run(q, k, q_weight, k_weight, positions, plan, eps, out):
     dev, dtype, R, D = _common(q, k, q_weight, k_weight, positions, plan)
     oq, ok = out if out is not None else (None, None)
-    for o in (oq, ok):
-        if o is not None and any(s == 0 and n > 1 for s, n in zip(o.stride(), o.shape)):
-            raise ValueError("out must not repeat its own elements")
     q2, qo, qi, qs, hq = _one(q, "q", oq, dev, dtype, R, D) if q is not None else _ABSENT
     k2, ko, ki, ks, hk = _one(k, "k", ok, dev, dtype, R, D) if k is not None else _ABSENT
     wq = _weight(q_weight, "q_weight", q, D)
     wk = _weight(k_weight, "k_weight", k, D)
+    if out is not None:
+        ins = [None if x is None else (p, R, h, D, s[0], s[1]) for x, p, h, s in ((q, qi, hq, qs), (k, ki, hk, ks))]
+        outs = [None if x is None or o is None else (p, R, h, D, s[2], s[3])
+                for x, o, p, h, s in ((q, oq, qo, hq, qs), (k, ok, ko, hk, ks))]
+        _own_places(outs, ins, dtype.itemsize)
     _check(_call_on(dev, lib().qk_norm_rope, qo, ko, qi, ki, wq, wk, positions.data_ptr(),
                     positions.element_size(), plan.ptr, plan.magnitude, eps, R, hq, hk, D, plan.rotary_dim,
                     _Strides(*qs, *ks), plan.interleaved, dtype_code(dtype), _stream_ptr(dev)), "qk_norm_rope")

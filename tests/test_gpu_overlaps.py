@@ -46,3 +46,36 @@ def test_outputs_of_a_read():
     assert torch.equal(k, want[0]) and torch.equal(v, want[1])
     with pytest.raises(ValueError, match="out k must be"):
         sg.kv_read(b.cache, slots, out=(big[:1, :2], big[:n, 2:4]))
+
+
+def test_norm_into_its_inputs():
+    """In place, into places of their own in the inputs' buffer, or refused."""
+    gen = torch.Generator().manual_seed(72)
+    R, D = 9, 64
+    data = torch.randn(R + 1, 12, D, generator=gen).half().to(DEV)
+    w = torch.ones(D, dtype=torch.float16, device=DEV)
+    pos, plan = torch.arange(R, device=DEV), sg.rope_plan(D, device=DEV)
+    call = lambda q, k, out: sg.qk_norm_rope(q, k, w, w, pos, plan, out=out)
+    want = call(data[:R, :4], data[:R, 4:6], None)
+
+    big = data.clone()
+    q, k = big[:R, :4], big[:R, 4:6]
+    for out, match in (((q, q[:, :2]), "apart"), ((k.repeat(1, 2, 1), q[:, :2]), "apart"), ((big[1:, :4], k), "apart"),
+                       ((big[:R, 1:5], None), "apart"), ((None, big[:R, 5:7]), "apart"), ((big[:R, 6:10], big[:R, 9:11]), "apart"),
+                       ((big[:R, 2:6], k), "apart"), ((q, big[1:, 4:6]), "apart"),
+                       ((big.flatten().as_strided((R, 4, D), (D, D, 1), 8 * D), k), "repeat"),
+                       ((q, big[:1, 8:10].expand(R, 2, D)), "repeat")):
+        with pytest.raises(ValueError, match=match):
+            call(q, k, out)
+    with pytest.raises(ValueError, match="apart"):
+        call(q, q, (q, q))  # in place, twice
+    assert torch.equal(big, data)
+
+    for out in (lambda b: (b[:R, 6:10], b[:R, 10:12]), lambda b: (b[:R, :4], b[:R, 4:6]), lambda b: (b[:R, :4], None),
+                lambda b: (b[:R, 6:10], b[:R, 4:6]), lambda b: (None, b[1:, 7:9])):
+        big = data.clone()
+        a, b = call(big[:R, :4], big[:R, 4:6], out(big))
+        assert torch.equal(a, want[0]) and torch.equal(b, want[1])
+    big = data.clone()
+    a, _ = sg.qk_norm_rope(big[:R, :4], None, w, None, pos, plan, out=(big[:R, :4], None))
+    assert torch.equal(a, want[0]) and torch.equal(big[:R, 4:], data[:R, 4:])
