@@ -216,6 +216,13 @@ def _need(t, name, device, dtype=None, ndim=None):
         raise ValueError(f"{name} must have {ndim} dimensions, got {t.dim()}")
 
 
+def _counts(**sizes):
+    """Refuses sizes that the C ABI's 32-bit integers do not hold (ctypes would cut them off)."""
+    for name, n in sizes.items():
+        if not -0x80000000 <= n <= 0x7FFFFFFF:
+            raise ValueError(f"{name} must be below 2^31, got {n}")
+
+
 _forward_ad = None
 
 

@@ -11,7 +11,7 @@ from __future__ import annotations
 
 import math
 
-from . import _call_on, _check, _need, _no_gradients, _stream_ptr, _torch, dtype_code, lib
+from . import _call_on, _check, _counts, _need, _no_gradients, _stream_ptr, _torch, dtype_code, lib
 from .kv import KVCache, _not_repeated, _Strides4
 from .rotary import _heads
 from .views import apart, view
@@ -82,6 +82,8 @@ def prefix_plan(cache: KVCache, q_heads: int, pages, lengths, row_indptr=None, n
     elif G > 1:
         raise ValueError("several prefixes need prefix_indptr")
     dt = dtype_code(cache.dtype)
+    _counts(num_rows=rows, sequences=S, prefixes=G, q_heads=q_heads, pages_per_sequence=pages.shape[1],
+            pages_per_prefix=prefix_width)
     sizes = (rows, S, G, q_heads, dt)
     nbytes = lib().prefix_plan_bytes(cache._ptr, *sizes)
     if not nbytes:

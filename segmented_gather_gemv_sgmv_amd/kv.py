@@ -13,7 +13,7 @@ from __future__ import annotations
 
 import ctypes
 
-from . import _call_on, _check, _need, _no_gradients, _stream_ptr, _torch, dtype_code, lib
+from . import _call_on, _check, _counts, _need, _no_gradients, _stream_ptr, _torch, dtype_code, lib
 from .rotary import _heads, _position_types
 from .views import apart, repeats, view
 
@@ -53,6 +53,7 @@ def kv_cache(num_pages: int, page_size: int, kv_heads: int, head_dim: int, dtype
         raise ValueError(f"kind must be one of {', '.join(KINDS)}, got {kind!r}")
     dtype_code(dtype)
     sizes = (int(num_pages), int(page_size), int(kv_heads), int(head_dim))
+    _counts(num_pages=sizes[0], page_size=sizes[1], kv_heads=sizes[2], head_dim=sizes[3])
     codes = lib().kv_codes_bytes(*sizes, KINDS[kind])
     scales = lib().kv_scales_bytes(*sizes, KINDS[kind])
     if not codes:
@@ -82,7 +83,10 @@ def _slots(cache, slots):
     if slots.dtype not in _position_types():
         raise TypeError(f"slots must be int32 or int64, got {slots.dtype}")
     _need(slots, "slots", cache.device, None, 1)
-    return slots.shape[0]
+    n = slots.shape[0]
+    if n > 0x7FFFFFFF:
+        _counts(rows=n)
+    return n
 
 
 def kv_write(cache: KVCache, k, v, slots) -> None:

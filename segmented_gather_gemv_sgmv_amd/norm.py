@@ -12,7 +12,7 @@ from __future__ import annotations
 
 import ctypes
 
-from . import _call_on, _check, _need, _no_tangents, _stream_ptr, _torch, dtype_code, lib
+from . import _call_on, _check, _counts, _need, _no_tangents, _stream_ptr, _torch, dtype_code, lib
 from .rotary import RopePlan, _ABSENT, _heads, _one, _position_types, _Strides
 from .views import apart, repeats
 
@@ -39,7 +39,9 @@ def _common(q, k, q_weight, k_weight, positions, plan):
     dev, dtype = first.device, first.dtype
     if first.dim() != 3:
         raise ValueError(f"q and k must be [rows, heads, head_dim], got {tuple(first.shape)}")
-    R, _, D = first.shape
+    R, H, D = first.shape
+    if max(R, H, D) > 0x7FFFFFFF or (k is not None and k.dim() == 3 and k.shape[1] > 0x7FFFFFFF):
+        _counts(rows=R, heads=max(H, k.shape[1]) if k is not None else H, head_dim=D)
     if positions.dtype not in _position_types():
         raise TypeError(f"positions must be int32 or int64, got {positions.dtype}")
     _need(positions, "positions", dev, None, 1)
