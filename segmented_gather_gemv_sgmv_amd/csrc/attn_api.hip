@@ -26,9 +26,10 @@ int check_shape(const sgmv_kv_cache* cache, int32_t num_rows, int32_t num_seqs, 
         return SGMV_ERR_BAD_SHAPE;
     s->padded = kv_padded(cache->head_dim);
     s->sizes = attn_sizes(num_rows, num_seqs, num_prefixes, q_heads, cache->kv_heads, s->padded, dtype);
-    // Items, slots and (row, head) pairs are counted in 31 bits.
-    if (s->sizes.items > 0x7FFFFFFFll || s->sizes.slots > 0x7FFFFFFFll ||
-        (long long)num_rows * q_heads > 0x7FFFFFFFll || s->sizes.plan_ints > 0x7FFFFFFFull)
+    // Slots and (row, head) pairs are counted in 31 bits; both kernels have to be launchable.
+    const long long pairs = (long long)num_rows * q_heads;
+    if (s->sizes.slots > 0x7FFFFFFFll || pairs > 0x7FFFFFFFll || s->sizes.plan_ints > 0x7FFFFFFFull ||
+        !grid_fits(s->sizes.items, kAttnThreads) || !grid_fits(pairs + 256, attn_join_lanes(s->padded)))
         return SGMV_ERR_UNSUPPORTED;
     s->at = plan_layout(num_rows, num_seqs, num_prefixes, s->sizes.items);
     return SGMV_OK;

@@ -17,7 +17,7 @@ void run_attn_padded(const AttnArgs& a, int kind, int items, hipStream_t st) {
     const dim3 grid((unsigned)items), block(kAttnThreads);
     if (kind == SGMV_KV_FP8) launch(&attn_kernel<QT, 8, P, R>, grid, block, st, a);
     else launch(&attn_kernel<QT, 4, P, R>, grid, block, st, a);
-    constexpr int kLanes = P <= 64 ? 16 : P <= 128 ? 32 : 64;
+    constexpr int kLanes = attn_join_lanes(P);
     const long long pairs = (long long)a.rows * a.q_heads;
     launch(&attn_join_kernel<QT, P>, dim3((unsigned)((pairs + 256 / kLanes - 1) / (256 / kLanes))), dim3(256),
            st, a);

@@ -8,13 +8,14 @@ namespace {
 
 using namespace sgmv;
 
+// Rows of a workgroup: 64 leave whole 16-token lines between ragged ends; fewer where these
+// would leave CUs without work.
+int kv_row_tile(int rows, int heads) { return (rows + 63ll) / 64 * heads * 2 >= 512 ? 64 : 16; }
+
 template <bool kWrite, typename DT, int BITS, int P>
 void launch_kv(const KvArgs& a, hipStream_t st) {
-    // 64 rows a workgroup leave whole 16-token lines between ragged ends; fewer where these
-    // would leave CUs without work.
-    const long long tiles = (a.rows + 63ll) / 64 * a.heads * 2;
-    const int rt = tiles >= 512 ? 64 : 16;
-    const dim3 grid((unsigned)((a.rows + rt - 1) / rt), (unsigned)a.heads, 2), block(kKvThreads);
+    const int rt = kv_row_tile(a.rows, a.heads);
+    const dim3 grid((unsigned)((a.rows - 1ll + rt) / rt), (unsigned)a.heads, 2), block(kKvThreads);
     if constexpr (kWrite) {
         if (rt == 64) launch(&kv_write_kernel<DT, BITS, P, 64>, grid, block, st, a);
         else launch(&kv_write_kernel<DT, BITS, P, 16>, grid, block, st, a);
@@ -47,6 +48,8 @@ int run_kv(const sgmv_kv_cache* cache, const void* k, const void* v, const void*
     if (dtype != SGMV_F32 && dtype != SGMV_F16 && dtype != SGMV_BF16) return SGMV_ERR_BAD_DTYPE;
     if (num_rows < 0 || (slot_bytes != 4 && slot_bytes != 8)) return SGMV_ERR_BAD_SHAPE;
     if (const int e = kv_check(cache)) return e;
+    const int rt = kv_row_tile(num_rows, cache->kv_heads);
+    if (!grid_fits((num_rows - 1ll + rt) / rt, kKvThreads)) return SGMV_ERR_UNSUPPORTED;
     if (num_rows == 0) return SGMV_OK;
     if (!k || !v || !slots || !strides) return SGMV_ERR_NULL_PTR;
     KvArgs a{};

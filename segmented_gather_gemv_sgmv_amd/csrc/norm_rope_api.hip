@@ -84,7 +84,7 @@ bool fill(NormRopeArgs& a, const void* const* in, const void* const* weight, con
     a.rot = rotary_dim;
     a.interleaved = interleaved != 0;
     a.rows_per_block = norm_rows_per_block(num_rows, rotary_dim);
-    a.blocks = (num_rows + a.rows_per_block - 1) / a.rows_per_block;
+    a.blocks = (int)((num_rows - 1ll + a.rows_per_block) / a.rows_per_block);
     return vec;
 }
 
@@ -126,7 +126,7 @@ extern "C" int qk_norm_rope(void* q_out, void* k_out, const void* q, const void*
     a.lanes = s.lanes;
     a.heads_per_group = norm_heads_per_group(a.blocks, heads, s.lanes);
     a.groups = (int)((heads + a.heads_per_group - 1) / a.heads_per_group);
-    if ((long long)a.blocks * a.groups > 0x7FFFFFFFll) return SGMV_ERR_UNSUPPORTED;
+    if (!grid_fits((long long)a.blocks * a.groups, kNormThreads)) return SGMV_ERR_UNSUPPORTED;
     launch_norm<false>(a, dtype, vec, s.per_lane, dim3((unsigned)(a.blocks * a.groups)),
                        (hipStream_t)stream);
     return launch_status();

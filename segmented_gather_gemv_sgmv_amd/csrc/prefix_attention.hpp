@@ -943,7 +943,7 @@ __global__ __launch_bounds__(kAttnThreads, P <= 128 ? 2 : 1) void attn_kernel(At
 template <typename DT, int P>
 __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a) {
     using T = typename DT::storage;
-    constexpr int kLanes = P <= 64 ? 16 : P <= 128 ? 32 : 64;
+    constexpr int kLanes = attn_join_lanes(P);
     const int lane = threadIdx.x & (kLanes - 1);
     const long long i = (long long)blockIdx.x * (256 / kLanes) + threadIdx.x / kLanes;
     if (i >= (long long)a.rows * a.q_heads) return;

@@ -38,6 +38,9 @@ enum { kStackRow0, kStackRows, kStackLen, kStackItem0, kStackChunks, kStackTiles
 enum { kItemTile, kItemHead, kItemM0, kItemBlk0, kItemBlk1, kItemSlot, kItemRow0, kItemM, kItemLen, kItemHidden,
        kItemTable, kItemOwn, kItemFrontLen, kItemFrontTable, kItemFrontBlocks, kItemFinal, kItemInts };
 
+// Lanes that join a row's results, four elements each.
+constexpr int attn_join_lanes(int padded) { return padded <= 64 ? 16 : padded <= 128 ? 32 : 64; }
+
 // Row tiles of 16 that a wave keeps at once: two halve the conversions of codes per
 // row, where the registers hold them (heads of up to 128; float32 has three terms of q).
 inline int attn_tiles(int padded, int dtype) { return padded <= 128 && dtype != SGMV_F32 ? 2 : 1; }

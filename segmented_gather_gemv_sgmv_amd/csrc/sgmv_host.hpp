@@ -15,6 +15,9 @@ namespace sgmv {
 
 inline bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
 
+// Threads along a grid's dimension are counted in 32 bits by the hardware.
+inline bool grid_fits(long long blocks, int threads) { return blocks * threads <= 0xFFFFFFFFll; }
+
 // Launch bookkeeping: every launch goes through hipLaunchKernel, whose
 // return value describes that launch alone (hipGetLastError could also
 // report an older, unrelated error of the caller's).  The first failure of a
