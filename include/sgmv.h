@@ -592,7 +592,7 @@ int kv_read(void* k, void* v, const sgmv_kv_cache* cache, const void* slots, int
  * same sizes; the page tables are read by these calls themselves.  The cache's
  * arrays are not read by prefix_plan.  prefix_attention needs a workspace
  * (prefix_attention_workspace_bytes, 16-byte aligned, any contents; calls that may run
- * at the same time must not share one).  scale is positive.  strides: HOST array of
+ * at the same time must not share one).  scale is positive and at most 2e38.  strides: HOST array of
  * element strides q {row, head}, o {row, head}; lse [num_rows, q_heads] or NULL.  o must not
  * overlap q.  Where lse is NULL nothing else changes.
  */

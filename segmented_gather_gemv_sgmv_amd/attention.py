@@ -119,8 +119,8 @@ def prefix_attention(q, cache: KVCache, plan: PrefixPlan, scale=None, out=None, 
     if q.shape != shape:
         raise ValueError(f"q must be {shape}, got {tuple(q.shape)}")
     scale = 1 / math.sqrt(D) if scale is None else float(scale)
-    if not 0 < scale < math.inf:
-        raise ValueError(f"scale must be positive and finite, got {scale}")
+    if not 0 < scale <= 2e38:
+        raise ValueError(f"scale must be positive and at most 2e38, got {scale}")
     if out is None:
         out = (torch.zeros if plan.ragged else torch.empty)(shape, dtype=q.dtype, device=dev)
         so = (plan.q_heads * D, D)

@@ -42,6 +42,9 @@ bool table_fits(const sgmv_kv_cache* cache, int32_t width) {
     return blocks * kKvBlock <= 0x7FFFFFC0ll && blocks * per < (1ll << 32);
 }
 
+// Scores are taken times scale log2(e), which has to be finite.
+constexpr float kScaleMost = 2e38f;
+
 size_t part_bytes(const Shape& s) { return (size_t)s.sizes.slots * s.padded * sizeof(float); }
 
 }  // namespace
@@ -104,7 +107,8 @@ extern "C" int prefix_attention(void* o, float* lse, const void* q, const sgmv_k
                                 void* workspace, size_t workspace_bytes, void* stream) {
     Shape s;
     if (const int e = check_shape(cache, num_rows, num_seqs, num_prefixes, q_heads, dtype, &s)) return e;
-    if (pages_per_seq < 0 || pages_per_prefix < 0 || !(scale > 0.f) || scale > 3e38f) return SGMV_ERR_BAD_SHAPE;
+    if (pages_per_seq < 0 || pages_per_prefix < 0 || !(scale > 0.f) || !(scale <= kScaleMost))
+        return SGMV_ERR_BAD_SHAPE;
     if (!table_fits(cache, pages_per_seq) || !table_fits(cache, pages_per_prefix) ||
         (long long)cache->num_pages * (cache->page_size / kKvBlock) * cache->kv_heads >= 0xFFFFFFFFll)
         return SGMV_ERR_UNSUPPORTED;  // blocks over all heads are counted in 32 bits
