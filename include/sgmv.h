@@ -592,7 +592,10 @@ int kv_read(void* k, void* v, const sgmv_kv_cache* cache, const void* slots, int
  * same sizes; the page tables are read by these calls themselves.  The cache's
  * arrays are not read by prefix_plan.  prefix_attention needs a workspace
  * (prefix_attention_workspace_bytes, 16-byte aligned, any contents; calls that may run
- * at the same time must not share one).  scale is positive and at most 2e38.  strides: HOST array of
+ * at the same time must not share one).  It holds float32 results that are joined: without prefixes
+ * at most 36 MB, whatever the batch; with them about as much and, since lengths are not known on the
+ * host, room for two results of every row and head, 4 bytes an element of the padded head and 8 (578 MB
+ * for 16384 rows of 32 heads of 128).  scale is positive and at most 2e38.  strides: HOST array of
  * element strides q {row, head}, o {row, head}; lse [num_rows, q_heads] or NULL.  o must not
  * overlap q.  Where lse is NULL nothing else changes.
  */

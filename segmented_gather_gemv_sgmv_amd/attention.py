@@ -103,7 +103,9 @@ def prefix_attention(q, cache: KVCache, plan: PrefixPlan, scale=None, out=None, 
     ``scale`` 1 / sqrt(D) unless given.  q and ``out`` (optional, receives o, apart from q) may have any row
     and head strides; ``lse`` (optional, float32 [rows, q_heads]) receives the logarithms of the
     softmax's sums.  A row that sees no key is zeros, its lse minus infinity; rows of no sequence
-    are not written (an ``out`` made here holds zeros for them)."""
+    are not written (an ``out`` made here holds zeros for them).  A call allocates its workspace
+    (``plan.workspace_bytes``): at most 36 MB without prefixes, with them about 1 KB more for every row
+    and head of 128."""
     torch = _torch()
     if not isinstance(plan, PrefixPlan):
         raise TypeError("plan must be a PrefixPlan (see prefix_plan)")

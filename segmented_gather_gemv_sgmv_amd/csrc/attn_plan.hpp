@@ -95,7 +95,7 @@ __global__ __launch_bounds__(kPlanThreads) void attn_plan_kernel(PlanArgs a) {
     // The stacks and the work in all.
     long long work = 0;
     for (int i = tid; i < n; i += kPlanThreads) {
-        int row0, rows, len, front = 0, prefix = -1;
+        int row0, rows, len, front = 0, prefix = -1, only = 0;  // only: no other stack has keys of its rows
         if (i < a.prefixes) {
             int lo, hi;
             plan_run(a, i, lo, hi);
@@ -109,8 +109,9 @@ __global__ __launch_bounds__(kPlanThreads) void attn_plan_kernel(PlanArgs a) {
             rows = plan_rows(a, s, s + 1);
             len = plan_length(a.lengths[s], a.own_tokens);
             prefix = seq_prefix[s];
-            if (prefix >= 0 && !apart[prefix])
-                front = plan_length(a.prefix_lengths[prefix], a.prefix_tokens);
+            const int before = prefix >= 0 ? plan_length(a.prefix_lengths[prefix], a.prefix_tokens) : 0;
+            if (prefix >= 0 && !apart[prefix]) front = before;
+            only = front == before;
         }
         const int M = rows * a.rep;
         int tile = 16;
@@ -125,6 +126,7 @@ __global__ __launch_bounds__(kPlanThreads) void attn_plan_kernel(PlanArgs a) {
         r[kStackBlocks] = blocks;
         r[kStackFront] = front;
         r[kStackPrefix] = prefix;
+        r[kStackDone] = only;
         work += (long long)a.kv_heads * tiles * blocks * plan_weight(tile);
     }
     work = block_sum64(work, s_sum);
@@ -135,13 +137,16 @@ __global__ __launch_bounds__(kPlanThreads) void attn_plan_kernel(PlanArgs a) {
         const long long w = (long long)r[kStackBlocks] * plan_weight(r[kStackTile]);
         return (int)max(1ll, (10 * w + 3 * chunk) / (10 * chunk));
     };
+    // One chunk, and no prefix apart: the rows' outputs come from their items, and need no slots.
+    auto alone = [&](const int* r, int chunks) { return chunks == 1 && r[kStackDone] != 0; };
     // Row tables whose sequences overlap could ask for more than there is: no work then.
     long long items = 0, slots = 0;
     for (int i = tid; i < n; i += kPlanThreads) {
         const int* r = record(i);
-        const long long mine = (long long)a.kv_heads * r[kStackTiles] * chunks_of(r);
+        const int chunks = chunks_of(r);
+        const long long mine = (long long)a.kv_heads * r[kStackTiles] * chunks;
         items += mine;
-        slots += mine * r[kStackTile];
+        if (!alone(r, chunks)) slots += mine * r[kStackTile];
     }
     items = block_sum64(items, s_sum);
     slots = block_sum64(slots, s_sum);
@@ -172,19 +177,16 @@ __global__ __launch_bounds__(kPlanThreads) void attn_plan_kernel(PlanArgs a) {
         int* r = record(i);
         const int chunks = live && fits ? chunks_of(r) : 0;
         const long long mine = live ? (long long)a.kv_heads * r[kStackTiles] * chunks : 0;
-        const long long size = live ? mine * r[kStackTile] : 0;
+        const bool done = live && alone(r, chunks);
+        const long long size = live && !done ? mine * r[kStackTile] : 0;
         long long all_items, all_slots;
         const long long i1 = block_scan64(mine, s_sum, all_items);
         const long long s1 = block_scan64(size, s_sum, all_slots);
         if (live) {
-            // One chunk, and no prefix apart: the rows' outputs come from their items.
-            const int g = r[kStackPrefix];
-            const bool alone = i >= a.prefixes && chunks == 1 &&
-                               (g < 0 || !apart[g] || plan_length(a.prefix_lengths[g], a.prefix_tokens) == 0);
             r[kStackItem0] = (int)(item_base + i1 - mine);
             r[kStackChunks] = chunks;
             r[kStackSlot0] = (int)(slot_base + s1 - size);
-            r[kStackDone] = alone;
+            r[kStackDone] = done;
         }
         item_base += all_items;
         slot_base += all_slots;

@@ -47,9 +47,16 @@ inline int attn_tiles(int padded, int dtype) { return padded <= 128 && dtype != 
 inline int attn_tile_most(int padded, int dtype) { return 16 * attn_tiles(padded, dtype) * kAttnWaves; }
 
 struct AttnSizes {
-    long long items, slots;  // at most
+    long long items, slots;  // at most; a slot is a row's result of one item, to be joined
     size_t plan_ints;
 };
+
+// Slots of the first chunks of n stacks that share `rows` rows (of one K / V head), at most: a stack of M rows has
+// tiles of M + tile - 1 rows in all, and of 16 + 2 M.
+inline long long attn_first_slots(long long n, long long rows, long long tile) {
+    const long long a = rows + n * (tile - 1), b = 16 * n + 2 * rows;
+    return a < b ? a : b;
+}
 
 inline AttnSizes attn_sizes(long long rows, long long seqs, long long prefixes, int q_heads, int kv_heads,
                             int padded, int dtype) {
@@ -58,8 +65,15 @@ inline AttnSizes attn_sizes(long long rows, long long seqs, long long prefixes, 
     // Every row is in at most one prefix's stack and one sequence's.  A stack has one tile, or one
     // more than M / most.  A tile of work w has at most w / chunk + 0.3 chunks: beyond the first of each tile
     // these are no more than the target.
-    s.items = kAttnTarget + kv_heads * (stacks + 2 * rows * rep / most);
-    s.slots = kAttnTarget * most + kv_heads * (16 * stacks + 4 * rows * rep);
+    s.items = kAttnTarget + kv_heads * (stacks + (prefixes ? 2 : 1) * rows * rep / most);
+    long long tile = 16;  // of any stack, at most
+    while (tile < rows * rep && tile < most) tile *= 2;
+    s.slots = kAttnTarget * tile + kv_heads * (attn_first_slots(seqs, rows * rep, tile) +
+                                               (prefixes ? attn_first_slots(prefixes, rows * rep, tile) : 0));
+    // Without prefixes only stacks that are cut have slots: from a work of 1.7 chunks on, so c chunks stand for a
+    // work of c / (1 + 0.3 / 1.7) of them.
+    const long long cut = (kAttnTarget * 20 / 17 + 1) * tile;
+    if (prefixes == 0 && cut < s.slots) s.slots = cut;
     s.plan_ints = (size_t)(kPlanHeader + kStackInts * stacks + kItemInts * s.items + rows + seqs + prefixes);
     return s;
 }
