@@ -92,6 +92,8 @@ def _side(x, dy, w, want_x, want_w, name, dev, dtype, R, D):
     """One of q and k in the backward call: (gradients, pointers, strides, heads)."""
     if x is None or not (want_x or want_w):
         return None, None, (None, None, None, None, None), (0,) * 6, 0
+    if dy is None:
+        raise ValueError(f"d{name} must be given where a gradient of {name} or its weight is wanted")
     sx = _heads(x, name, dev, dtype)
     if dy.shape != x.shape:
         raise ValueError(f"d{name} must be {tuple(x.shape)}, got {tuple(dy.shape)}")
