@@ -251,12 +251,14 @@ __device__ __forceinline__ void norm_angles(const NormRopeArgs& a, int row0, int
         const int r = i / half, j = i - r * half;
         const double pos = a.wide_positions ? (double)((const long long*)a.positions)[row0 + r]
                                             : (double)((const int*)a.positions)[row0 + r];
-        // fraction of a turn in [-1/2, 1/2], times 2: sincospi's argument
-        const double t = pos * a.freq[j] * 0.15915494309189533577;
+        // fraction of a turn in [-1/2, 1/2], times 2: sincospi's argument.  In float32 it is off by up to 2^-26, 1e-7
+        // of the angle, which enters to first order: 2 pi cos of it into the sine and the reverse.
+        const double t = pos * a.freq[j] * 0.15915494309189533577, turn = t - rint(t);
+        const float near = (float)turn, off = 6.2831853f * (float)(turn - near);
         float sn, cs;
-        sincospif(2.f * (float)(t - rint(t)), &sn, &cs);
-        s_cos[i] = cs * a.mag;
-        s_sin[i] = sn * a.mag;
+        sincospif(2.f * near, &sn, &cs);
+        s_cos[i] = __builtin_fmaf(-sn, off, cs) * a.mag;
+        s_sin[i] = __builtin_fmaf(cs, off, sn) * a.mag;
     }
 }
 
