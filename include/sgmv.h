@@ -572,10 +572,12 @@ int kv_read(void* k, void* v, const sgmv_kv_cache* cache, const void* slots, int
  * with float32 sums and maxima, rounded once.  q_heads / kv_heads consecutive heads of q share a
  * K / V head.  A row that sees no key gets zeros and an lse of minus infinity.  Rows of no
  * sequence are left as they are.  A visible NaN gives a row of NaN, whatever its weight; but for
- * that a score of minus infinity counts as a key that is not seen.  With many rows a V value whose
- * scale lies 2^32 below the largest that the rows' tile meets may count as zero (caches of bfloat16
- * or float32 alone reach so far); sums of weights up to 2^4 times V have to stay within float32, so V
- * within about 1e37 over the keys.
+ * that a score of minus infinity counts as a key that is not seen.  Weights
+ * meet V with 11 bits or more where o is bfloat16, with 16 or more where it is float16 and with 22
+ * or more where it is float32.  With many rows V is held in steps of 2^-31 of the largest scale that the
+ * rows' tile meets, also of keys that a row does not see: exact over scales of 2^22, zero from 2^32 below it
+ * on (caches of bfloat16 or float32 alone reach so far).  Sums of weights up to 2^4 times V have to
+ * stay within float32, so V within about 1e37 over the keys.
  *
  * Tables, int32 device arrays: lengths [num_seqs], tokens in the cache (a step's new
  * ones among them, written before); row_indptr [num_seqs + 1], or NULL for one row each (row s

@@ -29,7 +29,7 @@ inline NormShape norm_shape(int head_dim, int rotary_dim, bool interleaved, int 
 
 // Rows a workgroup takes at once: as many as give its threads an angle each and whole
 // passes over heads, but no more than leave the chip without work (4 workgroups per CU), and no
-// fewer than make one round of them (1400 rows of 12 + 4 heads of 64, float16: 4.4 us, with one row each 5.5).
+// fewer than make one round of them (1400 rows of 12 + 4 heads of 64, float16: 5.3 us, with one row each 6.4).
 inline int norm_rows_per_block(long long rows, int rotary_dim) {
     const long long most = std::min(8, kNormAngles / (rotary_dim / 2));
     return (int)std::min(most, (rows + 1023) / 1024);
@@ -56,7 +56,7 @@ inline int norm_grad_share(int q_heads, int k_heads, int w) {
 }
 
 // Heads of a workgroup in the forward pass: all of them once the blocks of rows are half a round, else
-// split down to one pass (1003 rows of 5 + 5 heads of 80, float32: 5.2 us, in two groups 7.3).
+// split down to one pass (1003 rows of 5 + 5 heads of 80, float32: 6.5 us, in two groups 8.8).
 inline int norm_heads_per_group(long long blocks, long long heads, int lanes) {
     const long long pass = std::max(1, kNormThreads / lanes);
     const long long want = std::max(1ll, 1024 / blocks);

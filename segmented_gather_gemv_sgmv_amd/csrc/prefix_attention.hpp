@@ -10,7 +10,7 @@
 // Bound: HBM for decode batches (every code is read once per tile of rows), exponentials
 // and conversions of codes beside the matrix cores for prompts and wide prefixes.  Measured (kernel + join; heads
 // of 128): 64 sequences of up to 1200 tokens behind 16384, 32 / 8 heads, 8 bits, bfloat16, 47 + 7 us (133 MB: 26
-// at a copy's rate); 24 of up to 2000 behind 6000, 40 heads, 4 bits, float16, 48 + 5 (164 MB: 32); 5 prompts
+// at a copy's rate); 24 of up to 2000 behind 6000, 40 heads, 4 bits, float16, 49 + 5 (164 MB: 32); 5 prompts
 // of 1556 rows behind 2048, 32 / 8 heads, 8 bits, bfloat16, 126 + 5 (70 GFLOP: 50 at a library product's rate).
 //
 // A wave takes 64 keys a step and R tiles of 16 rows.  Both products run on
@@ -647,8 +647,9 @@ __device__ __forceinline__ void attn_direct(const AttnArgs& a, const Item& it, u
 // into LDS, in the order in which lanes read them as operands (piece after piece of 16
 // bytes a lane: no bank is met twice), one step ahead of the products.
 //
-// Operands of the second product are float16: p in one term (11 bits) for bfloat16 outputs, in two (22) for the
-// others, and V scaled relative to the largest exponent that the item has met, which all waves follow alike;
+// Operands of the second product are float16: p in one term (11 bits) for bfloat16 outputs, an eighth of what their
+// own rounding loses (a second term: prompts 124 -> 157 us, 64 sequences behind 16384 tokens 47 -> 54), in two (22)
+// for the others, and V scaled relative to the largest exponent that the item has met, which all waves follow alike;
 // a value below 2^-32 of the largest is lost.  When a larger exponent comes, O is scaled down.
 // ---------------------------------------------------------------------------
 // Asks for MFMAS matrix instructions with VALU others, WRITES LDS writes and TRANS exponentials behind each.

@@ -22,13 +22,16 @@ constexpr int kAttnWaves = 4;            // of an item's workgroup
 constexpr int kAttnThreads = 64 * kAttnWaves;
 constexpr int kAttnKeys = 64;            // keys of a wave's step
 // Items to aim at, most of what two workgroups a CU can take: what is too much costs partial results, what is too
-// little leaves CUs waiting (64 sequences behind 16384 tokens, 32 / 8 heads of 128: 50, 46, 50 us at
-// 384, 448, 512).  A stack is cut into chunks of about work / target, or not at all below 1.7 of
+// little leaves CUs waiting.  Kernel and join at 384, 448, 512: 64 sequences behind 16384 tokens, 32 / 8 heads of
+// 128: 60, 55, 61 us; 24 behind 6000, 40 heads of 128, 4 bits: 54, 54, 54; 32 of up to 4000 tokens without a prefix,
+// 32 / 8 heads of 128: 45, 42, 40; four prompts of up to 600 rows, 16 / 4 heads of 128, 4 bits: 51, 48, 47.
+// A stack is cut into chunks of about work / target, or not at all below 1.7 of
 // that.  Work is counted in steps of 64 keys of a tile; a step of 64 or 128 rows takes about twice as long as
 // one of up to 32.
 constexpr int kAttnTarget = 448;
-// Work of an item, at least (40 sequences behind 600 to 1300 tokens, 12 / 4 heads of 96, float32: 20, 19, 20, 23 us
-// with the join at 4, 6, 8, 12).
+// Work of an item, at least.  Kernel and join at 4, 6, 8: 40 sequences behind 450 to 1350 tokens, 12 / 4 heads of 96,
+// float32: 19.5, 18.4, 19.1 us; 12 of up to 800 behind 250 to 750, 16 / 4 heads of 64, bfloat16: 13.2, 14.0, 14.3;
+// 16 of up to 2000 behind 1500, 8 / 2 heads of 256, float16: 24, 25, 27; three short ones: 10.8 at each.
 constexpr int kAttnLeast = 6;
 constexpr int kPlanHeader = 16;          // ints: items, slots, work of a chunk
 
