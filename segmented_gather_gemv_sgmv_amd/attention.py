@@ -82,8 +82,9 @@ def prefix_plan(cache: KVCache, q_heads: int, pages, lengths, row_indptr=None, n
     elif G > 1:
         raise ValueError("several prefixes need prefix_indptr")
     dt = dtype_code(cache.dtype)
-    _counts(num_rows=rows, sequences=S, prefixes=G, q_heads=q_heads, pages_per_sequence=pages.shape[1],
-            pages_per_prefix=prefix_width)
+    if max(rows, S, G, q_heads, pages.shape[1], prefix_width) > 0x7FFFFFFF:
+        _counts(num_rows=rows, sequences=S, prefixes=G, q_heads=q_heads, pages_per_sequence=pages.shape[1],
+                pages_per_prefix=prefix_width)
     sizes = (rows, S, G, q_heads, dt)
     nbytes = lib().prefix_plan_bytes(cache._ptr, *sizes)
     if not nbytes:

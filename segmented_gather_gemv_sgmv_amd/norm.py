@@ -40,8 +40,8 @@ def _common(q, k, q_weight, k_weight, positions, plan):
     if first.dim() != 3:
         raise ValueError(f"q and k must be [rows, heads, head_dim], got {tuple(first.shape)}")
     R, H, D = first.shape
-    if max(R, H, D) > 0x7FFFFFFF or (k is not None and k.dim() == 3 and k.shape[1] > 0x7FFFFFFF):
-        _counts(rows=R, heads=max(H, k.shape[1]) if k is not None else H, head_dim=D)
+    if R > 0x7FFFFFFF or H > 0x7FFFFFFF or D > 0x7FFFFFFF:
+        _counts(rows=R, heads=H, head_dim=D)
     if positions.dtype not in _position_types():
         raise TypeError(f"positions must be int32 or int64, got {positions.dtype}")
     _need(positions, "positions", dev, None, 1)
@@ -75,6 +75,8 @@ def _run(q, k, q_weight, k_weight, positions, plan, eps, out):
     oq, ok = out if out is not None else (None, None)
     q2, qo, qi, qs, hq = _one(q, "q", oq, dev, dtype, R, D) if q is not None else _ABSENT
     k2, ko, ki, ks, hk = _one(k, "k", ok, dev, dtype, R, D) if k is not None else _ABSENT
+    if hk > 0x7FFFFFFF:
+        _counts(heads=hk)
     wq = _weight(q_weight, "q_weight", q, D)
     wk = _weight(k_weight, "k_weight", k, D)
     if out is not None:
@@ -115,6 +117,8 @@ def qk_norm_rope_backward(dq, dk, q, k, q_weight, k_weight, positions, plan: Rop
     dev, dtype, R, D = _common(q, k, q_weight, k_weight, positions, plan)
     gq, gqw, pq, sq, hq = _side(q, dq, q_weight, need[0], need[2] and q_weight is not None, "q", dev, dtype, R, D)
     gk, gkw, pk, sk, hk = _side(k, dk, k_weight, need[1], need[3] and k_weight is not None, "k", dev, dtype, R, D)
+    if hk > 0x7FFFFFFF:
+        _counts(heads=hk)
     ws, ws_bytes = None, 0
     if gqw is not None or gkw is not None:
         ws_bytes = lib().qk_norm_rope_backward_workspace_bytes(R, D, plan.rotary_dim)

@@ -22,7 +22,8 @@ def _starts(v):
     """Sorted distances in elements of the heads from the view's first."""
     torch = _torch()
     _, R, H, _, row, head = v
-    return (torch.arange(R)[:, None] * row + torch.arange(H)[None, :] * head).flatten().sort().values
+    count = lambda n: torch.arange(n, device="cpu")
+    return (count(R)[:, None] * row + count(H)[None, :] * head).flatten().sort().values
 
 
 def repeats(v) -> bool:

@@ -25,7 +25,7 @@ def _shape(*shape):
 
 
 def test_rows(monkeypatch):
-    cache = sg.kv_cache(2, 16, 1, 64, torch.float32, device="cpu")
+    cache, one_head = sg.kv_cache(2, 16, 1, 64, torch.float32, device="cpu"), torch.zeros(1, 1, 2)
     for module in (kv, norm, attention):
         monkeypatch.setattr(module, "_need", lambda *a: None)
     with pytest.raises(ValueError, match="rows must be below"):
@@ -34,8 +34,15 @@ def test_rows(monkeypatch):
     for shape, name in (((2 ** 32 + 1, 1, 2), "rows"), ((1, 2 ** 32 + 1, 2), "heads"), ((1, 1, 2 ** 32 + 2), "head_dim")):
         with pytest.raises(ValueError, match=f"{name} must be below"):
             norm._common(_shape(*shape), None, None, None, _shape(shape[0]), None)
+    many = (None, 0, 0, (0, 0, 0, 0), 2 ** 32 + 1)  # heads of k, which _common does not look at
+    monkeypatch.setattr(norm, "_common", lambda *a: (CPU, torch.float32, 1, 2))
+    monkeypatch.setattr(norm, "_one", lambda t, name, *a: many if name == "k" else (None, 0, 0, (0, 0, 0, 0), 1))
     with pytest.raises(ValueError, match="heads must be below"):
-        norm._common(_shape(1, 1, 2), _shape(1, 2 ** 32 + 1, 2), None, None, _shape(1), None)
+        norm._run(one_head, one_head, None, None, None, None, 0.0, None)
+    monkeypatch.setattr(norm, "_side", lambda x, dy, w, want_x, want_w, name, *a: (
+        None, None, (None,) * 5, (0,) * 6, 2 ** 32 + 1 if name == "k" else 1))
+    with pytest.raises(ValueError, match="heads must be below"):
+        norm.qk_norm_rope_backward(one_head, one_head, one_head, one_head, None, None, None, None)
     one, table = torch.zeros(1, dtype=torch.int32), torch.zeros(1, 1, dtype=torch.int32)
     with pytest.raises(ValueError, match="num_rows must be below"):
         sg.prefix_plan(cache, 1, table, one, num_rows=2 ** 32 + 1)

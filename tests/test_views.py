@@ -56,3 +56,20 @@ def test_views_of_a_fused_buffer():
     assert apart(turned[:, :8], turned[:, 8:]) and not apart(turned[:, :8], turned[:, 7:]) and not repeats(turned)
     assert apart(qkv[..., :32], qkv[..., 32:]) and not apart(qkv[..., :33], qkv[..., 32:])
     assert repeats(qkv[:1].expand(5, 12, 64)) and not repeats(qkv[:1])
+
+
+def test_on_the_host_alone():
+    """Addresses are compared on the CPU whatever torch's default device is: a call may be under capture."""
+    made = []
+
+    class Mode(torch.overrides.TorchFunctionMode):
+        def __torch_function__(self, func, types, args=(), kwargs=None):
+            if func is torch.arange:
+                made.append((kwargs or {}).get("device"))
+            return func(*args, **(kwargs or {}))
+
+    buf = torch.zeros(100)
+    a, b = buf.as_strided((3, 2, 4), (8, 12, 1)), buf.as_strided((3, 2, 4), (9, 12, 1), 4)
+    with Mode():
+        apart(a, b), repeats(a)
+    assert made and set(made) == {"cpu"}
