@@ -1,6 +1,5 @@
 """How prefix_plan cuts a step into items, in plain Python, and what the C ABI reserves for it."""
 import ctypes
-import random
 
 TARGET, LEAST, KEYS = 448, 6, 64
 

@@ -1,7 +1,6 @@
 """Calls whose grids would pass 2^32 threads are refused before anything is enqueued (CPU)."""
 import ctypes
 
-import segmented_gather_gemv_sgmv_amd as sg
 from test_attention_host import FAKE, _cache, lib  # noqa: F401 (fixture)
 
 UNSUPPORTED = 4
